@@ -284,7 +284,7 @@ def prepare(case, seed):
     if own:
         st["cache"] = _handle(st)
         if case["kind"] == "cached":
-            n = _planner().attention_kv8_workspace(st["cache"], case["batch"], case["tq"], hq)
+            n = _planner().attention_kv8_workspace(st["cache"])
             st["work"] = torch.empty(n, dtype=torch.uint8, device="cuda")
     return st
 
@@ -446,8 +446,8 @@ def run(state):
         p.kv8_read(st["cache"], st["cu_window"], st["first"], st["k_read"], st["v_read"])
         return {"q": st["q_out"], "k": st["k_read"], "v": st["v_read"]}
     if kind == "cached":
-        p.attention_kv8(st["q"], st["cache"], st["kv_len"], st["out"], case["dim"] ** -0.5, causal=case["causal"],
-                        lse=st["lse"], workspace=st["work"])
+        p.attention_kv8(st["q"], st["cache"], st["kv_len"], st["out"], case["dim"] ** -0.5, st["work"],
+                        causal=case["causal"], lse=st["lse"])
     else:
         p.attention_packed(st["q"], st["k"], st["v"], st["cu_q"], st["cu_k"], st["out"], case["dim"] ** -0.5,
                            frame=case["frame"], lse=st["lse"])
