@@ -29,7 +29,8 @@ EXPORTS = ("jepa_create", "jepa_destroy", "jepa_last_error", "jepa_status_string
            "jepa_attention_bf16", "jepa_cem_warm_start", "jepa_world_model_step",
            "jepa_cem_closed_loop", "jepa_linear_fp8", "jepa_quantize_rows_fp8",
            "jepa_set_use_graphs", "jepa_selftest_bounded_wait", "jepa_linear_resid_bf16",
-           "jepa_linear_qkv_bf16")
+           "jepa_linear_qkv_bf16", "jepa_rope_table", "jepa_rope_append_kv8", "jepa_kv8_read",
+           "jepa_attention_kv8_workspace", "jepa_attention_kv8", "jepa_attention_packed")
 
 
 class JepaError(RuntimeError):
@@ -56,6 +57,14 @@ class Trace(ctypes.Structure):
                 ("winner", ctypes.c_void_p)]
 
 
+class Kv8Struct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 def load(path: str = _LIB_PATH):
     """Load the library (once) and declare its signatures."""
     global _lib
@@ -65,6 +74,7 @@ def load(path: str = _LIB_PATH):
         raise RuntimeError(f"{path} is missing: build it first (__graft_entry__.build())")
     lib = ctypes.CDLL(path)
     P, I, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_float
+    I64, D, Z, CACHE = ctypes.c_int64, ctypes.c_double, ctypes.c_size_t, ctypes.POINTER(Kv8Struct)
     sig = {
         "jepa_create": ([ctypes.POINTER(Config), I, ctypes.POINTER(P)], I),
         "jepa_destroy": ([P], None),
@@ -92,6 +102,14 @@ def load(path: str = _LIB_PATH):
         "jepa_cem_closed_loop": ([P, P, P, P, P, P, I, I, I, I, I, I, I, U64, P, P, P], I),
         "jepa_linear_fp8": ([P, P, P, P, P, P, I, I, I, I, P, P], I),
         "jepa_quantize_rows_fp8": ([P, P, I, I, P, P, P], I),
+        "jepa_rope_table": ([P, I, I, D, D, P, P], I),
+        "jepa_rope_append_kv8": ([P, CACHE, P, I64, P, I64, P, I64, I, I, P, P, F, P, I, I, I, P, P,
+                                  P, P, P], I),
+        "jepa_kv8_read": ([P, CACHE, P, P, I, P, P, P], I),
+        "jepa_attention_kv8_workspace": ([P, CACHE, ctypes.POINTER(Z)], I),
+        "jepa_attention_kv8": ([P, CACHE, P, I, I, P, F, I, P, P, P, Z, P], I),
+        "jepa_attention_packed": ([P, P, I64, P, I64, P, I64, I, I, I, I, I, I, P, P, F, I, P, P, P],
+                                  I),
         "jepa_set_use_graphs": ([P, I], I),
         "jepa_selftest_bounded_wait": ([P, P], I),
     }
@@ -164,10 +182,61 @@ def _arg(t, name: str, kind: str, numel: int, host_ok: bool = False,
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _rows(t, name: str):
+    """(address, elements between tokens) of token rows [tokens, heads, head_dim]: a bf16 CUDA
+    tensor whose heads lie back to back (a slice of a wider projection's rows is fine)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise JepaError(1, f"{name}: expected a tensor [tokens, heads, head_dim]")
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise JepaError(1, f"{name}: dtype {t.dtype} where bf16 is required")
+    n, heads, dim = t.shape
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise JepaError(1, f"{name}: the heads of a token must be contiguous")
+    if not t.is_cuda:
+        raise JepaError(1, f"{name} must be a CUDA tensor")
+    return t.data_ptr(), (st[0] if n > 1 else heads * dim)
+
+
+class KvCache8:
+    """One layer's 8-bit paged key/value cache (jepa_kv8_cache of the C header) over tensors that
+    the caller owns; the handle keeps them alive and checks them once.
+
+    k, v: uint8 or float8_e4m3fn [num_pages, kv_heads, page_size, head_dim]; k_scale, v_scale:
+    float32 [num_pages, kv_heads]; page_table: int32 [batch, max_pages]."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table):
+        if getattr(k, "ndim", 0) != 4 or getattr(page_table, "ndim", 0) != 2:
+            raise JepaError(1, "KvCache8: k must be [num_pages, kv_heads, page_size, head_dim] and "
+                               "page_table [batch, max_pages]")
+        pages, heads, page, dim = k.shape
+        if tuple(v.shape) != tuple(k.shape):
+            raise JepaError(1, f"KvCache8: v has shape {tuple(v.shape)}, k {tuple(k.shape)}")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if tuple(s.shape) != (pages, heads):
+                raise JepaError(1, f"KvCache8: {name} must be [{pages}, {heads}]")
+        if dim not in (64, 128) or page not in (16, 32, 64, 128):
+            raise JepaError(2, "KvCache8: head_dim must be 64 or 128, page_size 16, 32, 64 or 128")
+        self.tensors = (k, v, k_scale, v_scale, page_table)
+        if len({t.device for t in self.tensors}) != 1:
+            raise JepaError(1, "KvCache8: all tensors must be on one device")
+        n = pages * heads
+        batch, max_pages = page_table.shape
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.batch, self.max_pages, self.device = batch, max_pages, k.device
+        self.struct = Kv8Struct(
+            _arg(k, "k", "u8", n * page * dim), _arg(v, "v", "u8", n * page * dim),
+            _arg(k_scale, "k_scale", "f32", n), _arg(v_scale, "v_scale", "f32", n),
+            _arg(page_table, "page_table", "i32", batch * max_pages), pages, page, heads, dim, batch,
+            max_pages)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _stream(stream, device=None) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -196,6 +265,7 @@ class Planner:
                  max_chunk: int = 0):
         self.lib = load()
         self.pc = pc
+        self.device = device
         self.cfg = make_config(pc, max_horizon, max_chunk)
         h = ctypes.c_void_p()
         st = self.lib.jepa_create(ctypes.byref(self.cfg), device, ctypes.byref(h))
@@ -380,6 +450,114 @@ class Planner:
             self.h, _arg(q, "q", "bf16", ncand * T * d), _arg(kv, "kv", "bf16", ncand * kv_rows * 2 * d),
             _arg(out, "out", "bf16", ncand * T * d), ncand, T, Lk, kv_rows, heads, d,
             _stream(stream)), "attention_bf16")
+
+    # ---- 8-bit paged key/value cache and the attention around it (see the C header) ----
+
+    def _on(self, **tensors):
+        """Tensors (or None) that must live on this planner's device."""
+        for name, t in tensors.items():
+            if t is not None and t.device.index != self.device:
+                raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{self.device}")
+
+    def rope_table(self, positions, rot, base=10000.0, factor=1.0, table=None, stream=None):
+        """cos / sin table [positions, rot] for rope_append_kv8 (allocated when not given)."""
+        self._dims(positions=positions, rot=rot)
+        if table is None:
+            import torch
+            table = torch.empty(positions, rot, device=f"cuda:{self.device}")
+        self._on(table=table)
+        self._check(self.lib.jepa_rope_table(self.h, positions, rot, base, factor,
+                                             _arg(table, "table", "f32", positions * rot),
+                                             _stream(stream, self.device)), "rope_table")
+        return table
+
+    def rope_append_kv8(self, q, k, v, rope_table, cu, start, cache: KvCache8, q_out, q_norm=None,
+                        k_norm=None, norm_eps=1e-6, interleaved=False, k_out=None, stream=None):
+        """Norm, rotate and append packed tokens: q [tokens, q_heads, head_dim] (or None with
+        q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None."""
+        kp, ks = _rows(k, "k")
+        vp, vs = _rows(v, "v")
+        tokens, heads, dim = k.shape
+        if v.shape != k.shape or heads != cache.kv_heads or dim != cache.head_dim:
+            raise JepaError(1, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit the cache's "
+                               f"{cache.kv_heads} heads of {cache.head_dim}")
+        if (q is None) != (q_out is None):
+            raise JepaError(1, "q and q_out are given together")
+        qp, qs, q_heads = None, 0, 0
+        if q is not None:
+            qp, qs = _rows(q, "q")
+            q_heads = q.shape[1]
+            if q.shape[0] != tokens or q.shape[2] != dim:
+                raise JepaError(1, f"q {tuple(q.shape)} does not fit k {tuple(k.shape)}")
+        positions, rot = (0, 0) if rope_table is None else rope_table.shape
+        self._on(q=q, k=k, v=v, rope_table=rope_table, cu=cu, start=start, cache=cache, q_out=q_out,
+                 q_norm=q_norm, k_norm=k_norm, k_out=k_out)
+        self._dims(tokens=tokens)
+        self._check(self.lib.jepa_rope_append_kv8(
+            self.h, cache.ref, qp, qs, kp, ks, vp, vs, tokens, q_heads,
+            _arg(q_norm, "q_norm", "f32", dim, optional=True),
+            _arg(k_norm, "k_norm", "f32", dim, optional=True), norm_eps,
+            _arg(rope_table, "rope_table", "f32", positions * rot, optional=True), positions, rot,
+            int(interleaved), _arg(cu, "cu", "i32", cache.batch + 1),
+            _arg(start, "start", "i32", cache.batch),
+            _arg(q_out, "q_out", "bf16", tokens * q_heads * dim, optional=True),
+            _arg(k_out, "k_out", "bf16", tokens * heads * dim, optional=True),
+            _stream(stream, self.device)), "rope_append_kv8")
+
+    def kv8_read(self, cache: KvCache8, cu, first, k_out, v_out, stream=None):
+        """Cached tokens as bf16 into k_out, v_out [tokens, kv_heads, head_dim]."""
+        tokens = k_out.shape[0]
+        self._dims(tokens=tokens)
+        n = tokens * cache.kv_heads * cache.head_dim
+        self._on(cache=cache, cu=cu, first=first, k_out=k_out, v_out=v_out)
+        self._check(self.lib.jepa_kv8_read(
+            self.h, cache.ref, _arg(cu, "cu", "i32", cache.batch + 1),
+            _arg(first, "first", "i32", cache.batch), tokens, _arg(k_out, "k_out", "bf16", n),
+            _arg(v_out, "v_out", "bf16", n), _stream(stream, self.device)), "kv8_read")
+
+    def attention_kv8_workspace(self, cache: KvCache8) -> int:
+        """Bytes of workspace that attention_kv8 needs."""
+        n = ctypes.c_size_t()
+        self._check(self.lib.jepa_attention_kv8_workspace(self.h, cache.ref, ctypes.byref(n)),
+                    "attention_kv8_workspace")
+        return n.value
+
+    def attention_kv8(self, q, cache: KvCache8, kv_len, out, scale, workspace, causal=True, lse=None,
+                      stream=None):
+        """Attention of q [batch, q_tokens, q_heads, head_dim] over the cache; workspace: a uint8
+        tensor of attention_kv8_workspace bytes, one for each call that may run at a time."""
+        if getattr(q, "ndim", 0) != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
+            raise JepaError(1, f"q must be [{cache.batch}, q_tokens, q_heads, {cache.head_dim}]")
+        batch, q_tokens, q_heads, dim = q.shape
+        rows = batch * q_tokens * q_heads
+        self._dims(q_tokens=q_tokens, q_heads=q_heads)
+        self._on(q=q, cache=cache, kv_len=kv_len, out=out, workspace=workspace, lse=lse)
+        self._check(self.lib.jepa_attention_kv8(
+            self.h, cache.ref, _arg(q, "q", "bf16", rows * dim), q_tokens, q_heads,
+            _arg(kv_len, "kv_len", "i32", batch), scale, int(causal),
+            _arg(out, "out", "bf16", rows * dim), _arg(lse, "lse", "f32", rows, optional=True),
+            _arg(workspace, "workspace", "u8", 0), workspace.numel(),
+            _stream(stream, self.device)), "attention_kv8")
+
+    def attention_packed(self, q, k, v, cu_q, cu_k, out, scale, frame=1, lse=None, stream=None):
+        """Attention of packed prompts: q [tokens_q, q_heads, head_dim], k and v [tokens_k,
+        kv_heads, head_dim]; cu_q, cu_k [batch + 1]."""
+        qp, qs = _rows(q, "q")
+        kp, ks = _rows(k, "k")
+        vp, vs = _rows(v, "v")
+        tokens_q, q_heads, dim = q.shape
+        tokens_k, kv_heads, k_dim = k.shape
+        if v.shape != k.shape or k_dim != dim:
+            raise JepaError(1, f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+        batch = cu_q.numel() - 1
+        self._dims(tokens_q=tokens_q, tokens_k=tokens_k, batch=batch)
+        self._on(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+        self._check(self.lib.jepa_attention_packed(
+            self.h, qp, qs, kp, ks, vp, vs, tokens_q, tokens_k, batch, q_heads, kv_heads, dim,
+            _arg(cu_q, "cu_q", "i32", batch + 1), _arg(cu_k, "cu_k", "i32", batch + 1), scale, frame,
+            _arg(out, "out", "bf16", tokens_q * q_heads * dim),
+            _arg(lse, "lse", "f32", tokens_q * q_heads, optional=True),
+            _stream(stream, self.device)), "attention_packed")
 
     def set_use_graphs(self, on: bool):
         self._check(self.lib.jepa_set_use_graphs(self.h, int(on)), "set_use_graphs")

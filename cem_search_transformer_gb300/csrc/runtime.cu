@@ -8,6 +8,7 @@
 // point out that rounds which must run one after another bound the latency from below).
 #include "jepa_cem.h"
 #include "common.cuh"
+#include "kv8.cuh"
 
 #include <cmath>
 #include <cstdarg>
@@ -1247,6 +1248,191 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
   return JEPA_OK;
 }
 
+// ---- 8-bit paged cache and the attention around it ----
+
+// Runs the rest of a call on the context's device and leaves the caller's current device as it
+// was.
+struct OnDevice {
+  int before = -1;
+  cudaError_t status;
+  explicit OnDevice(int device) {
+    status = cudaGetDevice(&before);
+    if (status == cudaSuccess && before != device) status = cudaSetDevice(device);
+    if (before == device) before = -1;
+  }
+  ~OnDevice() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+static bool aligned(const void* p, size_t n) { return (((uintptr_t)p) & (n - 1)) == 0; }
+
+static jepa_status kv8_view(jepa_ctx* ctx, const char* what, const jepa_kv8_cache* c, Kv8View* out) {
+  if (!bf16_mode(ctx)) return fail(ctx, JEPA_ERR_UNSUPPORTED, "%s needs a bf16 context", what);
+  if (!c || bad_ptr(c->k) || bad_ptr(c->v) || bad_ptr(c->k_scale) || bad_ptr(c->v_scale) ||
+      bad_ptr(c->page_table))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: null cache or pointer in it", what);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+      !aligned(c->v_scale, 4) || !aligned(c->page_table, 4))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: misaligned cache buffer", what);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(ctx, JEPA_ERR_SHAPE, "%s: head_dim must be 64 or 128", what);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(ctx, JEPA_ERR_SHAPE, "%s: page_size must be 16, 32, 64 or 128", what);
+  if (c->num_pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024 || c->batch < 1 ||
+      c->batch > 65535 || c->max_pages < 1 ||
+      (long long)c->max_pages * c->page_size > (1LL << 30))
+    return fail(ctx, JEPA_ERR_SHAPE, "%s: cache sizes out of range", what);
+  *out = Kv8View{c->k, c->v, c->k_scale, c->v_scale, c->page_table, c->num_pages, c->page_size,
+                 c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7,
+                 c->kv_heads, c->head_dim, c->batch, c->max_pages};
+  return JEPA_OK;
+}
+
+static bool bad_rows(const void* p, int64_t stride, int heads, int dim) {
+  return bad_ptr(p) || !aligned(p, 16) || stride < (int64_t)heads * dim || stride % 8 ||
+         stride > (1LL << 31);
+}
+
+jepa_status jepa_rope_table(jepa_ctx* ctx, int positions, int rot, double base, double factor,
+                            float* table, void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  if (bad_ptr(table) || !aligned(table, 16) || positions < 1 || rot < 16 || rot % 16 ||
+      rot > 1024 || !(base > 0) || !(factor > 0) || !std::isfinite(base) || !std::isfinite(factor))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_table: bad argument");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(rope_table(positions, rot, base, factor, table, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                 const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
+                                 const float* q_norm, const float* k_norm, float norm_eps,
+                                 const float* rope_table, int positions, int rot, int interleaved,
+                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
+                                 uint16_t* k_out, void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv8View c;
+  const jepa_status st = kv8_view(ctx, "rope_append_kv8", cache, &c);
+  if (st) return st;
+  if (tokens < 1 || bad_ptr(cu) || bad_ptr(start) || bad_rows(k, k_stride, c.heads, c.dim) ||
+      bad_rows(v, v_stride, c.heads, c.dim) || (q == nullptr) != (q_out == nullptr) ||
+      !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
+      (interleaved != 0 && interleaved != 1) || !(norm_eps >= 0.f))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: bad argument");
+  if (q && (q_heads < 1 || q_heads % c.heads || q_heads > 65535 || bad_rows(q, q_stride, q_heads, c.dim)))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: bad queries");
+  if (rot < 0 || rot % 16 || rot > c.dim || (rot > 0 && (bad_ptr(rope_table) || !aligned(rope_table, 16) || positions < 1)))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: bad rotary table");
+  // in place only where the rows are dense: a thread then writes the row that it read
+  if ((q && q == q_out && q_stride != (int64_t)q_heads * c.dim) ||
+      (k == k_out && k_stride != (int64_t)c.heads * c.dim))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: in place needs dense rows");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  AppendArgs a;
+  a.q = (const bf16*)q;
+  a.k = (const bf16*)k;
+  a.v = (const bf16*)v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.eps = norm_eps;
+  a.rope = rope_table;
+  a.positions = rot > 0 ? positions : 1 << 30;
+  a.rot = rot;
+  a.interleaved = interleaved;
+  a.cu = cu;
+  a.start = start;
+  a.q_out = (bf16*)q_out;
+  a.k_out = (bf16*)k_out;
+  CK(rope_append_kv8(c, a, ctx->dev_err, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_kv8_read(jepa_ctx* ctx, const jepa_kv8_cache* cache, const int32_t* cu,
+                          const int32_t* first, int tokens, uint16_t* k_out, uint16_t* v_out,
+                          void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv8View c;
+  const jepa_status st = kv8_view(ctx, "kv8_read", cache, &c);
+  if (st) return st;
+  if (tokens < 1 || bad_ptr(cu) || bad_ptr(first) || bad_ptr(k_out) || bad_ptr(v_out) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "kv8_read: bad argument");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(kv8_read(c, cu, first, tokens, (bf16*)k_out, (bf16*)v_out, ctx->dev_err, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_attention_kv8_workspace(jepa_ctx* ctx, const jepa_kv8_cache* cache, size_t* bytes) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv8View c;
+  const jepa_status st = kv8_view(ctx, "attention_kv8_workspace", cache, &c);
+  if (st) return st;
+  if (bad_ptr(bytes)) return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv8_workspace: null bytes");
+  *bytes = attention_kv8_workspace(c.dim, ctx->num_sms);
+  return JEPA_OK;
+}
+
+jepa_status jepa_attention_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
+                               int q_tokens, int q_heads, const int32_t* kv_len, float scale,
+                               int causal, uint16_t* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv8View c;
+  const jepa_status st = kv8_view(ctx, "attention_kv8", cache, &c);
+  if (st) return st;
+  if (bad_ptr(q) || bad_ptr(out) || bad_ptr(kv_len) || bad_ptr(workspace) || !aligned(q, 16) ||
+      !aligned(out, 16) || !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(kv_len, 4) ||
+      q_tokens < 1 || q_heads < 1 || q_heads % c.heads || (causal != 0 && causal != 1) ||
+      !(scale > 0.f) || !std::isfinite(scale))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv8: bad argument");
+  if ((long long)q_tokens * (q_heads / c.heads) > 65536 ||
+      (long long)c.batch * q_tokens * q_heads > (1LL << 30))
+    return fail(ctx, JEPA_ERR_SHAPE, "attention_kv8: too many query rows");
+  if (workspace_bytes < attention_kv8_workspace(c.dim, ctx->num_sms))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv8: the workspace is too small");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(attention_kv8(c, (const bf16*)q, q_tokens, q_heads, kv_len, scale, causal, (bf16*)out, lse,
+                   workspace, ctx->dev_err, ctx->num_sms, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_stride,
+                                  const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                  int64_t v_stride, int tokens_q, int tokens_k, int batch,
+                                  int q_heads, int kv_heads, int head_dim, const int32_t* cu_q,
+                                  const int32_t* cu_k, float scale, int frame, uint16_t* out,
+                                  float* lse, void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  if (!bf16_mode(ctx)) return fail(ctx, JEPA_ERR_UNSUPPORTED, "attention_packed needs a bf16 context");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(ctx, JEPA_ERR_SHAPE, "attention_packed: head_dim must be 64 or 128");
+  if (tokens_q < 1 || tokens_k < 1 || batch < 1 || batch > 65535 || q_heads < 1 || kv_heads < 1 ||
+      q_heads % kv_heads || q_heads > 65535 || bad_rows(q, q_stride, q_heads, head_dim) ||
+      bad_rows(k, k_stride, kv_heads, head_dim) || bad_rows(v, v_stride, kv_heads, head_dim) ||
+      bad_ptr(cu_q) || bad_ptr(cu_k) || bad_ptr(out) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !(scale > 0.f) || !std::isfinite(scale) || frame < 1)
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_packed: bad argument");
+  if (q_heads / kv_heads > 128 || tokens_q > (1 << 30) || tokens_k > (1 << 30))
+    return fail(ctx, JEPA_ERR_SHAPE, "attention_packed: more than 128 heads a group, or too many tokens");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(attention_packed((const bf16*)q, q_stride, (const bf16*)k, k_stride, (const bf16*)v, v_stride,
+                      tokens_q, tokens_k, batch, q_heads, kv_heads, head_dim, cu_q, cu_k, scale,
+                      frame, (bf16*)out, lse, ctx->dev_err, ctx->num_sms, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
 jepa_status jepa_set_use_graphs(jepa_ctx* ctx, int enable) {
   if (!ctx) return JEPA_ERR_INVALID_ARG;
   ctx->use_graphs = enable != 0;
@@ -1292,6 +1478,9 @@ jepa_status jepa_sync_check(jepa_ctx* ctx, void* stream) {
   CK(cudaMemcpy(&flag, ctx->dev_err, sizeof(int), cudaMemcpyDeviceToHost));
   if (flag) {
     CK(cudaMemset(ctx->dev_err, 0, sizeof(int)));
+    if (!(flag & DEV_ERR_TIMEOUT))
+      return fail(ctx, JEPA_ERR_INVALID_ARG,
+                  "a page index, position, length or offset on the device lies outside its buffer");
     return fail(ctx, JEPA_ERR_TIMEOUT, "a bounded device wait expired (kernel returned early)");
   }
   return JEPA_OK;

@@ -286,6 +286,115 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
                                 int ncand, int T, int Lk, int kv_rows, int heads, int d,
                                 void* stream);
 
+/* ---- 8-bit paged key/value cache, and attention over it and over packed prompts ----
+ *
+ * For histories longer than the planner's dense per-candidate caches hold well: sequences of
+ * different lengths share one pool of pages, keys and values take a byte an element, and
+ * sequences with a common context may name the same pages. Serving only (no gradients). All of
+ * these entry points need a bf16 (or fp8) context and no weights, enqueue on `stream`, allocate
+ * nothing, and can be captured into a CUDA graph; what they read from the device (offsets,
+ * lengths, page tables) is read when the graph runs. Tensors are bf16 bit patterns (uint16).
+ * Token rows are [tokens][heads][head_dim] with `*_stride` elements between tokens (at least
+ * heads * head_dim, a multiple of 8), so q, k and v may be slices of one projection's rows.
+ *
+ * Packed sequences: `cu` [batch + 1] int32 dev, ascending; sequence b owns packed tokens cu[b] ..
+ * cu[b+1] - 1 (none is fine). Output rows behind the last sequence are left as they were.
+ *
+ * A page index, position, length or offset on the device that lies outside its buffer is never
+ * followed: what depends on it is skipped or read as zero (those outputs are unspecified), and
+ * the next jepa_sync_check reports JEPA_ERR_INVALID_ARG. */
+
+/* One layer's cache. k, v [num_pages][kv_heads][page_size][head_dim] e4m3 codes; k_scale,
+ * v_scale [num_pages][kv_heads] float32: an element stands for code * scale. page_table
+ * [batch][max_pages] int32: token t of sequence b lies in page page_table[b][t / page_size],
+ * slot t % page_size; entries past a sequence's length are not read. head_dim 64 or 128,
+ * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30; k and v 16-byte aligned. Scales
+ * lie in [2^-40, 2^40] (others are read as the nearer end); those written here are powers of
+ * two. The codes and scales of fresh pages need no initial values. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int32_t num_pages, page_size, kv_heads, head_dim, batch, max_pages;
+} jepa_kv8_cache;
+
+/* Rotary table [positions][rot] float32, 16-byte aligned: cos of the angles in columns
+ * [0, rot/2), sin in [rot/2, rot); angle = position / factor * base^(-2 i / rot), evaluated in
+ * 64 bits (factor > 1 stretches positions for contexts longer than those trained on; a table
+ * of another rule may be passed to jepa_rope_append_kv8 just as well). rot a multiple of 16. */
+jepa_status jepa_rope_table(jepa_ctx* ctx, int positions, int rot, double base, double factor,
+                            float* table, void* stream);
+
+/* Append new tokens to the cache, with the queries' and keys' per-head norm and rotation on the
+ * way. Token i of sequence b has position p = start[b] + i - cu[b]. For each head row x of q, k:
+ *   x <- x * w / sqrt(mean(x^2) + norm_eps)      where w (q_norm / k_norm) is given;
+ *   (x_i, x_j) <- (x_i cos - x_j sin, x_j cos + x_i sin) with the table's row p, for the pairs
+ *   (i, i + rot/2), or (2i, 2i + 1) where interleaved, i < rot/2; elements past rot stay.
+ * q_out = bf16 of the rotated q; the rotated k and v are quantised from fp32: scale of a (page,
+ * head) = 2^e, the least e in [-40, 40] with max|x| <= 448 * 2^e over the page's new tokens,
+ * codes = e4m3(x / scale), nearest even, saturating (infinities too; NaN stays NaN and does not
+ * enter the maximum). Where a page holds earlier tokens its scale never shrinks, and where it
+ * grows their codes are rounded to the new scale. Appending the same tokens again changes nothing.
+ *   q [tokens][q_heads][head_dim] and q_out (dense) dev, or both NULL; k, v
+ *   [tokens][kv_heads][head_dim] dev; k_out (dense, the rotated keys as bf16, as
+ *   jepa_attention_packed wants them) dev or NULL; q_norm, k_norm [head_dim] float32 dev or NULL;
+ *   rope_table [positions][rot]; cu [batch + 1], start [batch] int32 dev.
+ *   q_heads a multiple of kv_heads; rot a multiple of 16, 0 <= rot <= head_dim (0: no rotation);
+ *   q_out may be q and k_out may be k where those rows are dense; no other overlap.
+ * A page that receives tokens belongs to one sequence of the batch (shared pages are full). */
+jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                 const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
+                                 const float* q_norm, const float* k_norm, float norm_eps,
+                                 const float* rope_table, int positions, int rot, int interleaved,
+                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
+                                 uint16_t* k_out, void* stream);
+
+/* Read cached tokens back as bf16 (exact for power-of-two scales): row cu[b] + i of k_out, v_out
+ * [tokens][kv_heads][head_dim] (dense) = token first[b] + i of sequence b. With
+ * jepa_attention_packed this serves a prompt whose beginning is already cached. */
+jepa_status jepa_kv8_read(jepa_ctx* ctx, const jepa_kv8_cache* cache, const int32_t* cu,
+                          const int32_t* first, int tokens, uint16_t* k_out, uint16_t* v_out,
+                          void* stream);
+
+/* Bytes of jepa_attention_kv8's workspace for this cache's head_dim (the same for every batch,
+ * length and head count). */
+jepa_status jepa_attention_kv8_workspace(jepa_ctx* ctx, const jepa_kv8_cache* cache, size_t* bytes);
+
+/* Attention of the newest q_tokens tokens of each sequence over its cached tokens (their own
+ * keys and values, appended before, included): with n = kv_len[b], query t sees cached tokens
+ * [0, n - q_tokens + t + 1) where causal, all n otherwise;
+ *   out[b, t, h] = sum_j softmax_j(scale * q[b, t, h] . K_j) V_j,  key / value head
+ *   h / (q_heads / kv_heads); lse[b, t, h] = ln sum_j exp(scale * q . K_j).
+ * A query that sees nothing gives zeros and lse -inf; what it does not see does not reach it,
+ * whatever it holds.
+ *   q, out [batch][q_tokens][q_heads][head_dim], 16-byte aligned, dev; kv_len [batch] int32
+ *   dev; lse [batch][q_tokens][q_heads] float32 dev or NULL; workspace: device memory of the
+ *   size above, 256-byte aligned, its contents between calls without meaning. Calls that may
+ *   overlap on the device (streams, graphs) need a workspace each. scale finite, > 0. */
+jepa_status jepa_attention_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
+                               int q_tokens, int q_heads, const int32_t* kv_len, float scale,
+                               int causal, uint16_t* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Attention of whole packed prompts. Sequence b has nq = cu_q[b+1] - cu_q[b] queries and nk =
+ * cu_k[b+1] - cu_k[b] keys; query i stands at position p = i + nk - nq and sees keys
+ * [0, min(nk, (p / frame + 1) * frame)), none where p < 0: frame 1 is causal, frame T is causal
+ * over frames of T tokens (the predictor's mask), frame >= nk sees everything.
+ *   q [tokens_q][q_heads][head_dim], k, v [tokens_k][kv_heads][head_dim] with strides, 16-byte
+ *   aligned, dev; cu_q, cu_k [batch + 1]; out [tokens_q][q_heads][head_dim] dense, 16-byte
+ *   aligned; lse [tokens_q][q_heads] float32 or NULL, as in jepa_attention_kv8, whose promises
+ *   for unseen keys and empty rows hold here too. head_dim 64 or 128, q_heads a multiple of
+ *   kv_heads with at most 128 per key/value head, scale finite and > 0, frame >= 1. */
+jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_stride,
+                                  const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                  int64_t v_stride, int tokens_q, int tokens_k, int batch,
+                                  int q_heads, int kv_heads, int head_dim, const int32_t* cu_q,
+                                  const int32_t* cu_k, float scale, int frame, uint16_t* out,
+                                  float* lse, void* stream);
+
 /* enable = 0: jepa_cem_plan launches the kernels of its captured graph one by one on the
  * stream instead of replaying the graph (same kernels, same results; for measuring what the
  * graph saves). enable != 0 (the default): graph replay. */
@@ -330,7 +439,9 @@ jepa_status jepa_energy_l1_noalloc(const float* z_pred, const float* goal, int B
 jepa_status jepa_selftest_bounded_wait(jepa_ctx* ctx, void* stream);
 
 /* Synchronise `stream`, then report JEPA_ERR_TIMEOUT if a bounded device-side wait in
- * any kernel of this context gave up since the last check (the flag is then cleared). */
+ * any kernel of this context gave up since the last check, or else JEPA_ERR_INVALID_ARG if a
+ * kernel met a page index, position, length or offset outside its buffer (the flag is then
+ * cleared). */
 jepa_status jepa_sync_check(jepa_ctx* ctx, void* stream);
 
 #ifdef __cplusplus
