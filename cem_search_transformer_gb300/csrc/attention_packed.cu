@@ -10,18 +10,23 @@
 // and short prompts still fill the rows; groups that do not divide 128 leave a few rows unused.
 // Warps:
 //   0-3, 4-7  softmax of tile 0 and 1, a row a thread: read S from TMEM, running maximum and sum,
-//             P (bf16) over S, rescale O in TMEM when the maximum moved by more than 2^8, and at
-//             the end normalise and store;
+//             P (bf16) over the read scores, rescale O in TMEM when the maximum moved by more than
+//             2^8, and at the end normalise and store;
 //   8         MMA issuer: S_w = Q_w K^T, O_w += P_w V (P from TMEM, V MN-major from its TMA tile).
 //             The two tiles alternate, so that one tile's products run under the other's softmax;
-//   9         TMA producer: the Q tiles, then K_0, V_0, K_1, V_1, ... through one ring;
-//   10, 11    nothing (registers are handed over by warpgroups of four).
+//   9         scheduler and TMA producer: the next item, its Q tiles, then K_0, V_0, K_1, V_1, ...
+//             through one ring that runs on across items;
+//   10, 11    cleaning of V (below).
+// The grid has a CTA for every item there can be, the heaviest of a sequence first. A running CTA
+// takes over items whose CTA has not begun (cluster launch control), so that loads and scores of
+// the next item run under the present one's last products and read-out, and SMs that finish early
+// take more.
 // A barrier on S_w of key tile j also says that O_w += P_w V of tile j - 1 is complete: tensor-core
 // operations of one thread complete in order, and the commit follows both.
 // What lies behind a sequence's last key in its last tile is another sequence's (or nothing), and
 // a masked probability of 0 times an infinity or NaN there is NaN. So in tiles where some row's
-// limit ends, the softmax warps zero V rows past the sequence and any non-finite value before
-// they hand over P; the (rare) latter are added to the rows that see them in the epilogue.
+// limit ends, two warps zero V rows past the sequence and any non-finite value before the product
+// reads them; the (rare) latter are added to the rows that see them in the read-out.
 // All waits are bounded.
 #include "kv8.cuh"
 #include "tc_common.cuh"
@@ -34,9 +39,10 @@ using namespace tc;
 
 constexpr int TQ = 128;            // rows of a query tile (MMA M)
 constexpr int TK = 128;            // keys of a tile
-constexpr int P_THREADS = 384;
-// Registers a thread after setmaxnreg. The block launches with 168 each (384 threads); the two
-// softmax warpgroups draw what the third returns: 256 * 208 + 128 * 88 = 384 * 168.
+constexpr int P_THREADS = 384;     // 8 warps of softmax, then issuer, producer, two cleaning
+constexpr int W_MMA = 8, W_TMA = 9, W_CLEAN = 10;
+// Registers a thread after setmaxnreg. The block launches with 168 each; the softmax warpgroups
+// draw what the last one returns.
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == P_THREADS * 168, "register split");
 constexpr uint32_t P_TMEM = 512;
@@ -48,10 +54,14 @@ struct PShape {
   static constexpr int TILE = NB * BLK;             // bytes of a Q, K or V tile
   static constexpr int STAGES = D == 128 ? 4 : 6;
   static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
-  // q_full, kv_full[STAGES], kv_empty[STAGES], s_full[2], p_full[2], o_full[2], teardown
-  static constexpr int NUM_BARS = 1 + 2 * STAGES + 6 + 1;
-  static constexpr int SMEM = OFF_BAR + NUM_BARS * 8 + 64 + 1024;
+  static constexpr int OFF_OUT = OFF_RING + STAGES * TILE;   // read-out: 32 rows x 64 B a warp
+  static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
+  // kv_full[STAGES], kv_empty[STAGES], edge_full[STAGES], q_full[2], q_empty[2], s_full[2],
+  // p_half[2], p_full[2], o_full[2], item_full[2], item_empty[2], next, teardown
+  static constexpr int NUM_BARS = 3 * STAGES + 18;
+  static constexpr int OFF_TAIL = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM = OFF_TAIL + 160 + 1024;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 struct PArgs {
@@ -64,12 +74,21 @@ struct PArgs {
   float scale_log2;
 };
 
-// What a CTA works on.
+// What a CTA works on next.
 struct Item {
-  int valid;
+  int valid;           // 0: nothing is left
   int head;            // key / value head
   int q0, nq, k0, nk;  // the sequence's first packed row and length
   int t0;              // first token of tile 0 within the sequence
+  int nt[2];           // key tiles of each query tile (0: no rows, or none that sees a key)
+  int first_edge;      // the first key tile in which some row's limit ends
+  int dirty;           // a non-finite V was taken out of one of its tiles
+  int pad;
+};
+// Where the search for an item goes on: items come in ascending order as a rule.
+struct Cursor {
+  int s0;
+  long long base;
 };
 
 __device__ __forceinline__ float p_ex2(float x) {
@@ -108,6 +127,33 @@ __device__ __forceinline__ bool p_wait(uint32_t bar, uint32_t parity, volatile i
     }
   }
 }
+__device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
+  float part[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t* x = &r[8 * q];
+    part[q] = p_max3(p_max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2])),
+                     p_max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5])),
+                     fmaxf(__uint_as_float(x[6]), __uint_as_float(x[7])));
+  }
+  return fmaxf(p_max3(part[0], part[1], part[2]), part[3]);
+}
+// 32 lanes x 16 columns TMEM store (thread i -> lane i).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
 // MN-major operand of two 64-wide blocks: the leading byte offset is the distance between them.
 __device__ __forceinline__ uint64_t desc_mn_blocks(uint32_t saddr) {
   return (desc_sw128_mn(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(BLK >> 4) << 16);
@@ -117,16 +163,20 @@ __device__ __forceinline__ uint64_t desc_mn_blocks(uint32_t saddr) {
 __device__ __forceinline__ int limit_of(const Item& it, int i, int frame) {
   const int p = i + it.nk - it.nq;
   if (p < 0) return 0;
+  if (frame == 1) return p + 1;
   const long long lim = ((long long)(p / frame) + 1) * frame;
   return lim < it.nk ? (int)lim : it.nk;
 }
 
 // The `index`-th 256-row item; sequences in order, within one the last rows (most keys) first.
-__device__ __forceinline__ void find_item(const PArgs& a, long long index, Item& it, int* err_flag) {
+__device__ __forceinline__ void find_item(const PArgs& a, long long index, Cursor& cur, Item& it,
+                                          int* err_flag) {
   const int lane = threadIdx.x & 31, span = 2 * a.per_tile;
-  long long base = 0;
+  if (index < cur.base) cur = Cursor{0, 0};   // not in order after all
+  long long base = cur.base;
   it.valid = 0;
-  for (int s0 = 0; s0 < a.batch; s0 += 32) {
+  it.dirty = 0;
+  for (int s0 = cur.s0; s0 < a.batch; s0 += 32) {
     const int s = s0 + lane;
     int q0 = 0, nq = 0, k0 = 0, nk = 0;
     if (s < a.batch) {
@@ -160,10 +210,41 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Item&
       it.nq = __shfl_sync(0xffffffffu, nq, src);
       it.k0 = __shfl_sync(0xffffffffu, k0, src);
       it.nk = __shfl_sync(0xffffffffu, nk, src);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int t = it.t0 + w * a.per_tile, last = min(it.nq, t + a.per_tile) - 1;
+        it.nt[w] = t < it.nq ? (limit_of(it, last, a.frame) + TK - 1) / TK : 0;
+      }
+      it.first_edge = limit_of(it, it.t0, a.frame) / TK;
+      cur.s0 = s0;
+      cur.base = base;
       return;
     }
     base += __shfl_sync(0xffffffffu, incl, 31) * a.kv_heads;
   }
+}
+
+// Asks for the next CTA of the grid that has not begun to run to be given to this one instead (16
+// bytes at `dst`, announced at `bar`); clc_index reads the answer: its index, or -1 for none.
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      ::"r"(dst), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ int clc_index(uint32_t src) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 answer;\n\t.reg .pred given;\n\t.reg .b32 y, z;\n\t"
+      "ld.shared.b128 answer, [%1];\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 given, answer;\n\t"
+      "@given clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, answer;\n\t"
+      "}"
+      : "=r"(x)
+      : "r"(src)
+      : "memory");
+  return x;
 }
 
 template <int D>
@@ -174,305 +255,439 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(smem);
-  const uint32_t q_full = sb + S::OFF_BAR;
-  auto kv_full = [&](int s) { return q_full + 8u * (1 + s); };
-  auto kv_empty = [&](int s) { return q_full + 8u * (1 + S::STAGES + s); };
-  const uint32_t s_full0 = q_full + 8u * (1 + 2 * S::STAGES);
-  auto s_full = [&](int w) { return s_full0 + 8u * w; };
-  auto p_full = [&](int w) { return s_full0 + 16 + 8u * w; };
-  auto o_full = [&](int w) { return s_full0 + 32 + 8u * w; };
-  const uint32_t teardown = s_full0 + 48;
-  uint8_t* tail = smem + S::OFF_BAR + S::NUM_BARS * 8;
-  uint32_t* tmem_slot = (uint32_t*)tail;
-  volatile int* abort_flag = (volatile int*)(tail + 4);
-  volatile int* dirty = (volatile int*)(tail + 8);   // a non-finite V was taken out of a tile
-  Item* item_slot = (Item*)(tail + 16);
-  static_assert(sizeof(Item) <= 48, "the item fits behind the barriers");
+  const uint32_t bars = sb + S::OFF_BAR;
+  auto kv_full = [&](int s) { return bars + 8u * s; };
+  auto kv_empty = [&](int s) { return bars + 8u * (S::STAGES + s); };
+  auto edge_full = [&](int s) { return bars + 8u * (2 * S::STAGES + s); };
+  const uint32_t rest = bars + 24u * S::STAGES;
+  auto q_full = [&](int w) { return rest + 8u * w; };
+  auto q_empty = [&](int w) { return rest + 16 + 8u * w; };
+  auto s_full = [&](int w) { return rest + 32 + 8u * w; };
+  auto p_half = [&](int w) { return rest + 48 + 8u * w; };
+  auto p_full = [&](int w) { return rest + 64 + 8u * w; };
+  auto o_full = [&](int w) { return rest + 80 + 8u * w; };
+  auto item_full = [&](int b) { return rest + 96 + 8u * b; };
+  auto item_empty = [&](int b) { return rest + 112 + 8u * b; };
+  const uint32_t next_full = rest + 128, teardown = rest + 136;
+  uint8_t* tail = smem + ((S::OFF_TAIL + 15) & ~15);
+  Item* items = (Item*)tail;                              // two slots
+  const uint32_t next_slot = smem_u32(tail + 2 * sizeof(Item));   // 16 bytes, 16-byte aligned
+  uint32_t* tmem_slot = (uint32_t*)(tail + 2 * sizeof(Item) + 16);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  static_assert(2 * sizeof(Item) + 16 + 8 + 15 <= 160 && sizeof(Item) % 16 == 0, "tail");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 9) {
+  const int span = a.per_tile;
+  Cursor cursor{0, 0};
+  if (warp == W_TMA) {
     Item it;
-    find_item(a, blockIdx.x, it, err_flag);
-    if (lane == 0) *item_slot = it;
+    find_item(a, blockIdx.x, cursor, it, err_flag);
+    if (lane == 0) items[0] = it;
   }
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(kv_full(s), 1);
+      mbar_init(kv_full(s), 2);   // the producer twice, or each cleaning warp
       mbar_init(kv_empty(s), 1);
+      mbar_init(edge_full(s), 1);
     }
     for (int w = 0; w < 2; ++w) {
+      mbar_init(q_full(w), 1);
+      mbar_init(q_empty(w), 1);
       mbar_init(s_full(w), 1);
+      mbar_init(p_half(w), 4);
       mbar_init(p_full(w), 4);
       mbar_init(o_full(w), 1);
+      mbar_init(item_full(w), 1);
+      mbar_init(item_empty(w), 11);   // all warps but the producer
     }
+    mbar_init(next_full, 1);
     mbar_init(teardown, 1);
     *abort_flag = 0;
-    *dirty = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
   __syncthreads();
-  const Item it = *item_slot;
-  if (!it.valid) return;
-  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), P_TMEM);
+  if (!items[0].valid) return;       // a surplus CTA
+  if (warp == W_MMA) tmem_alloc(smem_u32(tmem_slot), P_TMEM);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto tS = [&](int w) { return tmem + 128u * w; };
   auto tO = [&](int w) { return tmem + 256u + 128u * w; };
-
-  // key tiles of each query tile (0: it has no rows, or none that sees a key)
-  const int span = a.per_tile;
-  int nt[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int first = it.t0 + w * span, last = min(it.nq, first + span) - 1;
-    nt[w] = first < it.nq ? (limit_of(it, last, a.frame) + TK - 1) / TK : 0;
-  }
-  const int n_tiles = max(nt[0], nt[1]);
-  // the first key tile in which some row's limit ends
-  const int first_edge = limit_of(it, it.t0, a.frame) / TK;
-
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-  if (warp == 9) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
+  if (warp >= W_MMA) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    if (warp == W_TMA) {
+      // ---------------- scheduler and TMA producer ----------------
       const int box = a.per_tile * a.group * 128;
-      if (n_tiles > 0) {
-        mbar_expect_tx(q_full, (uint32_t)(S::NB * box * ((nt[0] > 0) + (nt[1] > 0))));
-        for (int w = 0; w < 2; ++w)
-          if (nt[w] > 0)
+      int n = 0, qn[2] = {0, 0};   // tiles through the ring, items that loaded Q_w
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        Item it;
+        if (i == 0) {
+          it = items[0];
+        } else {
+          ok = __all_sync(0xffffffffu, p_wait(next_full, (i - 1) & 1, abort_flag, err_flag));
+          if (!ok) break;
+          const int index = clc_index(next_slot);
+          __syncwarp();
+          it.valid = 0;
+          if (index >= 0) find_item(a, index, cursor, it, err_flag);
+          if (i >= 2) {
+            ok = __all_sync(0xffffffffu, p_wait(item_empty(i & 1), ((i >> 1) - 1) & 1, abort_flag, err_flag));
+            if (!ok) break;
+          }
+          if (lane == 0) items[i & 1] = it;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_full(i & 1));
+        if (!it.valid) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();   // the slot's last answer has been read
+          mbar_expect_tx(next_full, 16);
+          clc_request(next_slot, next_full);
+          const int n_tiles = max(it.nt[0], it.nt[1]);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || it.nt[w] == 0) continue;
+            ok = qn[w] == 0 || p_wait(q_empty(w), (qn[w] - 1) & 1, abort_flag, err_flag);
+            if (!ok) continue;
+            ++qn[w];
+            mbar_expect_tx(q_full(w), (uint32_t)(S::NB * box));
             for (int b = 0; b < S::NB; ++b)
               tma_load_3d(sb + w * S::TILE + b * BLK, &tmQ, 64 * b, it.head * a.group,
-                          it.q0 + it.t0 + w * span, q_full);
+                          it.q0 + it.t0 + w * span, q_full(w));
+          }
+          for (int j = 0; j < 2 * n_tiles && ok; ++j, ++n) {
+            const int st = n % S::STAGES;
+            ok = n < S::STAGES || p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag);
+            if (!ok) break;
+            const uint32_t dst = sb + S::OFF_RING + st * S::TILE;
+            // V tiles with an edge land at the cleaning warps, which pass them on to the issuer
+            const bool edge = (j & 1) && (j >> 1) >= it.first_edge;
+            const uint32_t at = edge ? edge_full(st) : kv_full(st);
+            mbar_expect_tx(at, S::TILE);
+            if (!edge) mbar_arrive(at);
+            for (int b = 0; b < S::NB; ++b)
+              tma_load_3d(dst + b * BLK, (j & 1) ? &tmV : &tmK, 64 * b, it.head, it.k0 + (j >> 1) * TK, at);
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
       }
-      for (int n = 0; n < 2 * n_tiles; ++n) {
-        const int st = n % S::STAGES;
-        if (n >= S::STAGES &&
-            !p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag))
-          break;
-        const uint32_t dst = sb + S::OFF_RING + st * S::TILE;
-        mbar_expect_tx(kv_full(st), S::TILE);
-        for (int b = 0; b < S::NB; ++b)
-          tma_load_3d(dst + b * BLK, (n & 1) ? &tmV : &tmK, 64 * b, it.head, it.k0 + (n >> 1) * TK,
-                      kv_full(st));
-      }
-      if (*abort_flag) {
+      if (*abort_flag && lane == 0) {
         // give copies still in flight into this CTA's shared memory time to land
         const unsigned long long t0 = globaltimer();
         while (globaltimer() - t0 < 2000000ull) {
         }
       }
-    }
-  } else if (warp == 8) {
-    if (lane == 0 && n_tiles > 0) {
+    } else if (warp == W_MMA) {
       // ---------------- MMA issuer ----------------
+      // The whole warp walks the loop so that addresses and descriptors stay in uniform registers
+      // (a lone thread's would be moved there one by one, ahead of every MMA); one elected lane
+      // issues.
       constexpr uint32_t idS = idesc_bf16(TQ, TK, false);
       constexpr uint32_t idO = idesc_bf16(TQ, D, true);
-      auto slot = [&](int n) { return sb + S::OFF_RING + (n % S::STAGES) * S::TILE; };
-      auto landed = [&](int n) {
-        return p_wait(kv_full(n % S::STAGES), (n / S::STAGES) & 1, abort_flag, err_flag);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
       };
-      auto scores = [&](int w, int j) {
-        const uint64_t qd = desc_sw128(sb + w * S::TILE), kd = desc_sw128(slot(2 * j));
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t at = (uint64_t)((kk >> 2) * (BLK >> 4) + 2 * (kk & 3));
-          mma_bf16_ss(tS(w), qd + at, kd + at, idS, kk > 0);
+      const uint64_t q_desc = desc_sw128(sb), ring_k = desc_sw128(sb + S::OFF_RING);
+      const uint64_t ring_v =
+          D == 128 ? desc_mn_blocks(sb + S::OFF_RING) : desc_sw128_mn(sb + S::OFF_RING);
+      constexpr uint64_t STEP = S::TILE >> 4;     // of a tile, in descriptor units
+      int ks = 0, k_phase = 0;       // ring stage and lap of the next K tile the issuer meets
+      auto advance = [&](int& st, int& phase, int by) {
+        st += by;
+        if (st >= S::STAGES) {
+          st -= S::STAGES;
+          phase ^= 1;
         }
-        mma_commit(s_full(w));
       };
-      auto product = [&](int w, int j) {
-        const uint64_t vd = D == 128 ? desc_mn_blocks(slot(2 * j + 1)) : desc_sw128_mn(slot(2 * j + 1));
+      uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        ok = wait(item_full(i & 1), (i >> 1) & 1);
+        if (!ok) break;
+        const Item it = items[i & 1];
+        const int valid = __shfl_sync(0xffffffffu, it.valid, 0);
+        const int nt[2] = {__shfl_sync(0xffffffffu, it.nt[0], 0), __shfl_sync(0xffffffffu, it.nt[1], 0)};
+        const int n_tiles = max(nt[0], nt[1]);
+        if (lane == 0) mbar_arrive(item_empty(i & 1));
+        if (!valid) break;
+        auto scores = [&](int w, int st, bool last) {
+          const uint64_t qd = q_desc + w * STEP, kd = ring_k + st * STEP;
+          if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < TK / 16; ++kk)
-          mma_bf16_ts(tO(w), tS(w) + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)), idO,
-                      (j > 0) || (kk > 0));
-        if (j + 1 == nt[w]) mma_commit(o_full(w));
-      };
-      bool ok = p_wait(q_full, 0, abort_flag, err_flag) && landed(0);
-      if (ok) {
-        tc_fence_after();
-        if (nt[0] > 0) scores(0, 0);
-        if (nt[1] > 0) scores(1, 0);
-        mma_commit(kv_empty(0));
-      }
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        ok = landed(2 * j + 1);
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (j < nt[w]) {
-            ok = p_wait(p_full(w), j & 1, abort_flag, err_flag);
-            if (!ok) break;
-            tc_fence_after();
-            product(w, j);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t at = (uint64_t)((kk >> 2) * (BLK >> 4) + 2 * (kk & 3));
+              mma_bf16_ss(tS(w), qd + at, kd + at, idS, kk > 0);
+            }
+            mma_commit(s_full(w));
+            if (last) mma_commit(q_empty(w));
           }
-          if (w == 1) mma_commit(kv_empty((2 * j + 1) % S::STAGES));
-          if (j + 1 < n_tiles && w == 0) ok = landed(2 * j + 2);
-          if (ok && j + 1 < nt[w]) {
-            tc_fence_after();
-            scores(w, j + 1);
+          __syncwarp();
+        };
+        auto product = [&](int w, int st, int half, bool fresh) {
+          const uint64_t vd = ring_v + st * STEP;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < TK / 32; ++k) {
+              const int kk = half * (TK / 32) + k;
+              mma_bf16_ts(tO(w), tS(w) + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)), idO,
+                          !fresh || (kk > 0));
+            }
           }
-          if (w == 1 && j + 1 < n_tiles) mma_commit(kv_empty((2 * j + 2) % S::STAGES));
+          __syncwarp();
+        };
+        auto release = [&](uint32_t bar) {
+          if (elect_one()) mma_commit(bar);
+          __syncwarp();
+        };
+        if (n_tiles > 0) {
+          ok = wait(kv_full(ks), k_phase);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || nt[w] == 0) continue;
+            ok = wait(q_full(w), q_phase[w]);
+            q_phase[w] ^= 1;
+            tc_fence_after();
+            if (ok) scores(w, ks, nt[w] == 1);
+          }
+          release(kv_empty(ks));
+          advance(ks, k_phase, 1);
+        }
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          // V_j at (vs, v_phase), K_{j+1} behind it
+          const int vs = ks;
+          ok = wait(kv_full(vs), k_phase);
+          advance(ks, k_phase, 1);
+          const bool more = j + 1 < n_tiles;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (ok && j < nt[w]) {
+              ok = wait(p_half(w), p_phase[w]);
+              tc_fence_after();
+              if (ok) product(w, vs, 0, j == 0);
+              ok = ok && wait(p_full(w), p_phase[w]);
+              p_phase[w] ^= 1;
+              tc_fence_after();
+              if (ok) product(w, vs, 1, j == 0);
+              if (j + 1 == nt[w]) release(o_full(w));
+            }
+            if (w == 1) release(kv_empty(vs));
+            if (w == 0 && more) ok = ok && wait(kv_full(ks), k_phase);
+            if (ok && j + 1 < nt[w]) {
+              tc_fence_after();
+              scores(w, ks, j + 2 == nt[w]);
+            }
+          }
+          if (more) {
+            release(kv_empty(ks));
+            advance(ks, k_phase, 1);
+          }
         }
       }
-      mma_commit(teardown);
+      if (elect_one()) mma_commit(teardown);
+      __syncwarp();
       const unsigned long long t0 = globaltimer();
       while (!mbar_try_wait(teardown, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
       }
+    } else {
+      // ---------------- cleaning of V in tiles where some row's limit ends ----------------
+      int n0 = 0;
+      uint32_t phase = 0;            // a bit for each stage
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, p_wait(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
+        if (!ok) break;
+        const Item it = items[i & 1];
+        if (!it.valid) break;
+        const int n_tiles = max(it.nt[0], it.nt[1]);
+        for (int j = it.first_edge; j < n_tiles && ok; ++j) {
+          const int st = (n0 + 2 * j + 1) % S::STAGES;
+          ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
+          if (!ok) break;
+          phase ^= 1u << st;
+#pragma unroll 1
+          for (int row = (warp - W_CLEAN) * 32 + lane; row < TK; row += 64) {   // thread = key
+            uint8_t* v_row = smem + S::OFF_RING + st * S::TILE + row * 128;
+            const bool behind = j * TK + row >= it.nk;
+            uint32_t odd = 0;
+            if (!behind) {
+#pragma unroll 8
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(v_row + (c >> 3) * BLK + 16 * ((c & 7) ^ (row & 7)));
+                odd |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                       ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+              }
+              odd &= 0x80008000u;
+            }
+            if (behind || odd) {
+              if (odd) *(volatile int*)&items[i & 1].dirty = 1;
+#pragma unroll 1
+              for (int c = 0; c < D / 8; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(v_row + (c >> 3) * BLK + 16 * ((c & 7) ^ (row & 7)));
+                uint32_t x[4] = {0, 0, 0, 0};
+                if (!behind) {
+                  const uint4 y = *at;
+                  x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u;
+                    if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0x0000ffffu;
+                  }
+                }
+                *at = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_full(st));
+        }
+        n0 += 2 * n_tiles;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty(i & 1));
+      }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
-    // ---------------- softmax (thread = row) ----------------
+    // ---------------- softmax: thread = row ----------------
     const int w = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const int tok = it.t0 + w * span + row / a.group;       // within the sequence
-    const bool mine = row < span * a.group && tok < it.nq;
-    const int lim = mine ? limit_of(it, tok, a.frame) : 0x7fffffff;
-    const int lim_min = __reduce_min_sync(0xffffffffu, lim);
-    const bool active = __any_sync(0xffffffffu, mine);
     const uint32_t tSw = tS(w) + lane_off, tOw = tO(w) + lane_off;
     const float scale_log2 = a.scale_log2;
+    const float inv_group = 1.0f / a.group;
+    const int row_tok = row / a.group, row_head = row % a.group;
+    uint8_t* stage = smem + S::OFF_OUT + warp * 2048;
     // a warp goes on, or gives up, as one: what follows a wait are warp-wide instructions
     auto all_wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
     };
-    float m = -INFINITY, l = 0.f;
+    int sn = 0, on = 0;    // score tiles and outputs so far
     bool ok = true;
-    for (int j = 0; j < nt[w]; ++j) {
-      if (!all_wait(s_full(w), j & 1)) {
-        ok = false;
-        break;
+    for (int i = 0; ok; ++i) {
+      ok = all_wait(item_full(i & 1), (i >> 1) & 1);
+      if (!ok) break;
+      const volatile Item* slot = &items[i & 1];
+      if (!slot->valid) break;
+      const int ntw = slot->nt[w];
+      int lim = 0x7fffffff;
+      bool mine;
+      {
+        const Item it = items[i & 1];
+        const int tok = it.t0 + w * span + row_tok;             // within the sequence
+        mine = row < span * a.group && tok < it.nq;
+        if (mine) lim = limit_of(it, tok, a.frame);
       }
-      tc_fence_after();
-      if (active) {
-        uint32_t r[4][32];
+      const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+      const bool active = __any_sync(0xffffffffu, mine);
+      // scores of 32 keys from key0 on, those past the row's limit to -inf
+      auto hide = [&](uint32_t (&r)[32], int key0) {
+        if (key0 + 32 <= lim_min) return;                       // seen by all rows of the warp
+        const int left = lim - key0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32_async(tSw + 32 * q, r[q]);
+        for (int c = 0; c < 32; ++c)
+          if (c >= left) r[c] = __float_as_uint(-INFINITY);
+      };
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < ntw; ++j, ++sn) {
+        ok = all_wait(s_full(w), sn & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float alpha = 1.f, ms = 0.f;
+        uint32_t r0[32], r1[32];
+        if (active) {
+          // Two reads of the scores, one for the maximum and one for the exponentials: 128 values
+          // held in between would push the loop's state out of the registers.
+          float part[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_wait(r[q]);
-        if ((j + 1) * TK > lim_min) {
-          const int left = lim - j * TK;
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32_async(tSw + 64 * h, r0);
+            tmem_ld32_async(tSw + 64 * h + 32, r1);
+            tmem_wait(r0);
+            tmem_wait(r1);
+            hide(r0, j * TK + 64 * h);
+            hide(r1, j * TK + 64 * h + 32);
+            part[2 * h] = max32(r0);
+            part[2 * h + 1] = max32(r1);
+          }
+          tmem_ld32_async(tSw, r0);
+          const float cmax = fmaxf(p_max3(part[0], part[1], part[2]), part[3]);
+          // the exponent's reference moves only when the maximum grew by more than 2^8: the same
+          // reference scales O and the sum, so the result is unchanged
+          const bool bump = cmax > m && (m == -INFINITY || (cmax - m) * scale_log2 > 8.0f);
+          const float mnew = bump ? cmax : m;
+          alpha = bump ? p_ex2((m - mnew) * scale_log2) : 1.f;
+          ms = mnew == -INFINITY ? 0.f : mnew * scale_log2;
+          m = mnew;
+          if (j > 0 && __any_sync(0xffffffffu, bump)) {
+            // O holds the products of tile j - 1 and before (see the head of the file)
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t ov[32];
+              tmem_ld32_async(tOw + 32 * q, ov);
+              tmem_wait(ov);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (32 * q + c >= left) r[q][c] = __float_as_uint(-INFINITY);
-        }
-        float part[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const uint32_t* x = &r[q >> 2][8 * (q & 3)];
-          part[q] = p_max3(p_max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2])),
-                           p_max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5])),
-                           fmaxf(__uint_as_float(x[6]), __uint_as_float(x[7])));
-        }
-        const float cmax =
-            fmaxf(p_max3(p_max3(part[0], part[1], part[2]), p_max3(part[3], part[4], part[5]),
-                         p_max3(part[6], part[7], part[8])),
-                  p_max3(p_max3(part[9], part[10], part[11]), p_max3(part[12], part[13], part[14]),
-                         part[15]));
-        // the exponent's reference moves only when the maximum grew by more than 2^8: the same
-        // reference scales O and the sum, so the result is unchanged
-        const bool bump = cmax > m && (m == -INFINITY || (cmax - m) * scale_log2 > 8.0f);
-        const float mnew = bump ? cmax : m;
-        const float alpha = bump ? p_ex2((m - mnew) * scale_log2) : 1.f;
-        const float ms = mnew == -INFINITY ? 0.f : mnew * scale_log2;
-        m = mnew;
-        if (j > 0 && __any_sync(0xffffffffu, bump)) {
-          // O holds the product of tile j - 1 and before (see the head of the file)
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t ov[32];
-            tmem_ld32_async(tOw + 32 * q, ov);
-            tmem_wait(ov);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
-            tmem_st32(tOw + 32 * q, ov);
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+              tmem_st32(tOw + 32 * q, ov);
+            }
           }
         }
+        // P in two halves of 64 keys: the first one's product runs under the second's exponentials
         const unsigned long long sc2 = f2_pack(scale_log2, scale_log2), nms2 = f2_pack(-ms, -ms);
         unsigned long long sum2[2] = {0, 0};
+        auto exponentials = [&](const uint32_t (&r)[32], uint32_t to) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t* x = &r[2 * h + (c >> 4)][2 * (c & 15)];
+          for (int c = 0; c < 16; ++c) {
             const float2 e = f2_unpack(
-                f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, nms2));
+                f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sc2, nms2));
             const float p0 = p_ex2(e.x), p1 = p_ex2(e.y);
             sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
             const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
             pk[c] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_st32(tSw + 32 * h, pk);
+          tmem_st16(to, pk);
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (active) {
+            tmem_wait(r0);
+            tmem_ld32_async(tSw + 64 * h + 32, r1);
+            hide(r0, j * TK + 64 * h);
+            exponentials(r0, tSw + 32 * h);
+            tmem_wait(r1);
+            if (h == 0) tmem_ld32_async(tSw + 64, r0);
+            hide(r1, j * TK + 64 * h + 32);
+            exponentials(r1, tSw + 32 * h + 16);
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(h == 0 ? p_half(w) : p_full(w));
         }
         const float2 sm = f2_unpack(f2_add(sum2[0], sum2[1]));
         l = l * alpha + (sm.x + sm.y);
-        tmem_st_wait();
       }
-      if (j >= first_edge && w == (j < nt[0] ? 0 : 1)) {
-        // this tile's V is about to be used for the first time: thread = key
-        const int n = 2 * j + 1;
-        if (!all_wait(kv_full(n % S::STAGES), (n / S::STAGES) & 1)) {
-          ok = false;
-          break;
-        }
-        uint8_t* v_row = smem + S::OFF_RING + (n % S::STAGES) * S::TILE + row * 128;
-        const bool behind = j * TK + row >= it.nk;
-        uint32_t odd = 0;
-        if (!behind) {
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(v_row + (c >> 3) * BLK + 16 * ((c & 7) ^ (row & 7)));
-            odd |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
-          }
-          odd &= 0x80008000u;
-        }
-        if (behind || odd) {
-          if (odd) *dirty = 1;
-          for (int c = 0; c < D / 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(v_row + (c >> 3) * BLK + 16 * ((c & 7) ^ (row & 7)));
-            uint32_t x[4] = {0, 0, 0, 0};
-            if (!behind) {
-              const uint4 y = *at;
-              x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((x[i] & 0x7f80u) == 0x7f80u) x[i] &= 0xffff0000u;
-                if ((x[i] & 0x7f800000u) == 0x7f800000u) x[i] &= 0x0000ffffu;
-              }
-            }
-            *at = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(w));
-    }
-    if (ok && active) {
-      const long long at = ((long long)(it.q0 + tok) * a.q_heads + it.head * a.group + row % a.group);
-      const bool any = nt[w] > 0;
-      if (any) {
-        ok = all_wait(o_full(w), 0);
+      if (!ok) break;
+      if (ntw > 0) {
+        ok = all_wait(o_full(w), on & 1);
+        if (!ok) break;
+        ++on;
         tc_fence_after();
       }
-      if (ok) {
+      if (active) {
+        // the item is read again here: its fields need not live through the loop above
+        const int q0 = slot->q0, t0 = slot->t0 + w * span, left = slot->nq - t0, head = slot->head;
         const bool empty = l == 0.f;
         const float inv = empty ? 0.f : 1.f / l;
-        const bool fix = any && *dirty != 0;
+        const bool fix = ntw > 0 && slot->dirty != 0;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
+          const int col = 32 * q;
           uint32_t ov[32];
-          if (any) {
+          if (ntw > 0) {
             tmem_ld32_async(tOw + 32 * q, ov);
             tmem_wait(ov);
           }
@@ -480,8 +695,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           for (int c = 0; c < 32; ++c)
             ov[c] = __float_as_uint(empty ? 0.f : __uint_as_float(ov[c]) * inv);
           if (fix && mine) {
-            for (int key = first_edge * TK; key < lim; ++key) {
-              const bf16* vr = a.v + (long long)(it.k0 + key) * a.v_stride + (long long)it.head * D + 32 * q;
+#pragma unroll 1
+            for (int key = slot->first_edge * TK; key < lim; ++key) {
+              const bf16* vr = a.v + (long long)(slot->k0 + key) * a.v_stride + (long long)head * D + col;
 #pragma unroll
               for (int c = 0; c < 32; ++c) {
                 const float x = __bfloat162float(vr[c]);
@@ -489,30 +705,47 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               }
             }
           }
-          if (mine) {
-            bf16* to = a.out + at * D + 32 * q;
+          // 32 columns at a time through shared memory: a row's 64 bytes then leave by four lanes
+          // together
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-              uint32_t u[4];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(ov[c + 2 * i]),
-                                                               __uint_as_float(ov[c + 2 * i + 1]));
-                u[i] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              *reinterpret_cast<uint4*>(to + c) = make_uint4(u[0], u[1], u[2], u[3]);
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(ov[8 * c + 2 * k]),
+                                                             __uint_as_float(ov[8 * c + 2 * k + 1]));
+              u[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (c ^ ((lane >> 1) & 3))) =
+                make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int rr = 8 * g + (lane >> 2), chunk = lane & 3;
+            const int R = quarter * 32 + rr, rt = (int)((R + 0.5f) * inv_group);   // R / group
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 64 + 16 * (chunk ^ ((rr >> 1) & 3)));
+            if (rt < span && rt < left) {
+              const long long to = (long long)(q0 + t0 + rt) * a.q_heads + head * a.group + (R - rt * a.group);
+              *reinterpret_cast<uint4*>(a.out + to * D + col + 8 * chunk) = x;
             }
           }
+          __syncwarp();
         }
         if (mine && a.lse)
-          a.lse[at] = empty ? -INFINITY
-                            : ((m == -INFINITY ? 0.f : m * scale_log2) + log2f(l)) * 0.69314718055994531f;
+          a.lse[(long long)(q0 + t0 + row_tok) * a.q_heads + head * a.group + row_head] =
+              empty ? -INFINITY
+                    : ((m == -INFINITY ? 0.f : m * scale_log2) + log2f(l)) * 0.69314718055994531f;
       }
+      // O is read out: the next item's first hand-over of P tells the issuer so
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty(i & 1));
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == W_MMA) {
     tc_fence_after();
     __syncwarp();
     tmem_dealloc(tmem, P_TMEM);
