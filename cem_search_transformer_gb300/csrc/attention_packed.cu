@@ -12,20 +12,23 @@
 //   0-3, 4-7  softmax of tile 0 and 1, a row a thread: read S from TMEM, running maximum and sum,
 //             P (bf16) over the read scores, rescale O in TMEM when the maximum moved by more than
 //             2^8, and at the end normalise and store;
-//   8         MMA issuer: S_w = Q_w K^T, O_w += P_w V (P from TMEM, V MN-major from its TMA tile).
-//             The two tiles alternate, so that one tile's products run under the other's softmax;
-//   9         scheduler and TMA producer: the next item, its Q tiles, then K_0, V_0, K_1, V_1, ...
+//   8, 9      MMA issuers of tile 0 and 1: S_w = Q_w K^T, O_w += P_w V (P from TMEM, V MN-major from
+//             its TMA tile). One warp for both spent its time on issuing: an MMA of 64 columns takes
+//             32 cycles, its issue 40 to 60;
+//   10        scheduler and TMA producer: the next item, its Q tiles, then K_0, K_1, V_0, K_2, V_1, ...
 //             through one ring that runs on across items;
-//   10, 11    cleaning of V (below).
+//   11        cleaning of V (below).
 // The grid has a CTA for every item there can be, the heaviest of a sequence first. A running CTA
 // takes over items whose CTA has not begun (cluster launch control), so that loads and scores of
 // the next item run under the present one's last products and read-out, and SMs that finish early
 // take more.
-// A barrier on S_w of key tile j also says that O_w += P_w V of tile j - 1 is complete: tensor-core
-// operations of one thread complete in order, and the commit follows both.
+// Key tiles are 64 wide and each query tile has two score buffers, so that the scores of tile j + 1
+// are there when the softmax is done with tile j: with one buffer of 128 keys a tile waited about
+// 1200 cycles for its P V and the next scores after 2200 of softmax (D = 128). The price is 64-key
+// scores MMAs, which read Q from shared memory twice as often.
 // What lies behind a sequence's last key in its last tile is another sequence's (or nothing), and
 // a masked probability of 0 times an infinity or NaN there is NaN. So in tiles where some row's
-// limit ends, two warps zero V rows past the sequence and any non-finite value before the product
+// limit ends, a warp zeroes V rows past the sequence and any non-finite value before the product
 // reads them; the (rare) latter are added to the rows that see them in the read-out.
 // All waits are bounded.
 #include "kv8.cuh"
@@ -38,27 +41,28 @@ namespace {
 using namespace tc;
 
 constexpr int TQ = 128;            // rows of a query tile (MMA M)
-constexpr int TK = 128;            // keys of a tile
-constexpr int P_THREADS = 384;     // 8 warps of softmax, then issuer, producer, two cleaning
-constexpr int W_MMA = 8, W_TMA = 9, W_CLEAN = 10;
+constexpr int TK = 64;             // keys of a tile
+constexpr int P_THREADS = 384;     // 8 warps of softmax, then two issuers, producer, cleaning
+constexpr int W_MMA = 8, W_TMA = 10, W_CLEAN = 11;   // issuers: W_MMA and the next
 // Registers a thread after setmaxnreg. The block launches with 168 each; the softmax warpgroups
 // draw what the last one returns.
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == P_THREADS * 168, "register split");
 constexpr uint32_t P_TMEM = 512;
-constexpr int BLK = TQ * 128;      // bytes of 128 rows x 64 bf16 (one swizzled block)
+constexpr int BLK = TQ * 128;      // bytes of 128 rows x 64 bf16 (one swizzled block of Q)
+constexpr int KBLK = TK * 128;     // the same of K or V
 
 template <int D>
 struct PShape {
   static constexpr int NB = D / 64;                 // 64-column blocks
-  static constexpr int TILE = NB * BLK;             // bytes of a Q, K or V tile
-  static constexpr int STAGES = D == 128 ? 4 : 6;
-  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int QTILE = NB * BLK, TILE = NB * KBLK;   // bytes of a Q tile, of K or V
+  static constexpr int STAGES = 8;
+  static constexpr int OFF_RING = 2 * QTILE;
   static constexpr int OFF_OUT = OFF_RING + STAGES * TILE;   // read-out: 32 rows x 64 B a warp
   static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
-  // kv_full[STAGES], kv_empty[STAGES], edge_full[STAGES], q_full[2], q_empty[2], s_full[2],
-  // p_half[2], p_full[2], o_full[2], item_full[2], item_empty[2], next, teardown
-  static constexpr int NUM_BARS = 3 * STAGES + 18;
+  // kv_full[STAGES], kv_empty[STAGES], edge_full[STAGES], q_full[2], q_empty[2], s_full[2][2],
+  // p_full[2][2], pv[2][2], item_full[2], item_empty[2], next, teardown
+  static constexpr int NUM_BARS = 3 * STAGES + 22;
   static constexpr int OFF_TAIL = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM = OFF_TAIL + 160 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -138,15 +142,6 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
   }
   return fmaxf(p_max3(part[0], part[1], part[2]), part[3]);
 }
-// 32 lanes x 16 columns TMEM store (thread i -> lane i).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
   asm volatile(
@@ -156,9 +151,24 @@ __device__ __forceinline__ bool elect_one() {
 }
 // MN-major operand of two 64-wide blocks: the leading byte offset is the distance between them.
 __device__ __forceinline__ uint64_t desc_mn_blocks(uint32_t saddr) {
-  return (desc_sw128_mn(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(BLK >> 4) << 16);
+  return (desc_sw128_mn(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(KBLK >> 4) << 16);
 }
 
+
+// MMAs and commits of a whole warp, of which the elected lane's counts: the predicate is inside, so
+// that the code around stays convergent and its addresses in uniform registers.
+__device__ __forceinline__ void w_mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc, uint32_t leader) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\t" "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void w_mma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, uint32_t acc, uint32_t leader) {
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\t" "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bd), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void w_commit(uint32_t bar, uint32_t leader) {
+  asm volatile("{\n\t.reg .pred q;\n\t" "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader) : "memory");
+}
 // Keys that token i of a sequence sees.
 __device__ __forceinline__ int limit_of(const Item& it, int i, int frame) {
   const int p = i + it.nk - it.nq;
@@ -262,13 +272,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const uint32_t rest = bars + 24u * S::STAGES;
   auto q_full = [&](int w) { return rest + 8u * w; };
   auto q_empty = [&](int w) { return rest + 16 + 8u * w; };
-  auto s_full = [&](int w) { return rest + 32 + 8u * w; };
-  auto p_half = [&](int w) { return rest + 48 + 8u * w; };
-  auto p_full = [&](int w) { return rest + 64 + 8u * w; };
-  auto o_full = [&](int w) { return rest + 80 + 8u * w; };
-  auto item_full = [&](int b) { return rest + 96 + 8u * b; };
-  auto item_empty = [&](int b) { return rest + 112 + 8u * b; };
-  const uint32_t next_full = rest + 128, teardown = rest + 136;
+  // of query tile w and score buffer b
+  auto s_full = [&](int w, int b) { return rest + 32 + 16u * w + 8u * b; };
+  auto p_full = [&](int w, int b) { return rest + 64 + 16u * w + 8u * b; };
+  auto pv_done = [&](int w, int b) { return rest + 96 + 16u * w + 8u * b; };
+  auto item_full = [&](int b) { return rest + 128 + 8u * b; };
+  auto item_empty = [&](int b) { return rest + 144 + 8u * b; };
+  const uint32_t next_full = rest + 160, teardown = rest + 168;
   uint8_t* tail = smem + ((S::OFF_TAIL + 15) & ~15);
   Item* items = (Item*)tail;                              // two slots
   const uint32_t next_slot = smem_u32(tail + 2 * sizeof(Item));   // 16 bytes, 16-byte aligned
@@ -286,22 +296,23 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(kv_full(s), 2);   // the producer twice, or each cleaning warp
-      mbar_init(kv_empty(s), 1);
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 2);   // both issuers
       mbar_init(edge_full(s), 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(q_full(w), 1);
       mbar_init(q_empty(w), 1);
-      mbar_init(s_full(w), 1);
-      mbar_init(p_half(w), 4);
-      mbar_init(p_full(w), 4);
-      mbar_init(o_full(w), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(s_full(w, b), 1);
+        mbar_init(p_full(w, b), 4);
+        mbar_init(pv_done(w, b), 1);
+      }
       mbar_init(item_full(w), 1);
       mbar_init(item_empty(w), 11);   // all warps but the producer
     }
     mbar_init(next_full, 1);
-    mbar_init(teardown, 1);
+    mbar_init(teardown, 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -312,8 +323,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  auto tS = [&](int w) { return tmem + 128u * w; };
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  auto tS = [&](int w, int b) { return tmem + 128u * w + 64u * b; };
   auto tO = [&](int w) { return tmem + 256u + 128u * w; };
   if (warp >= W_MMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
@@ -355,21 +366,27 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             ++qn[w];
             mbar_expect_tx(q_full(w), (uint32_t)(S::NB * box));
             for (int b = 0; b < S::NB; ++b)
-              tma_load_3d(sb + w * S::TILE + b * BLK, &tmQ, 64 * b, it.head * a.group,
+              tma_load_3d(sb + w * S::QTILE + b * BLK, &tmQ, 64 * b, it.head * a.group,
                           it.q0 + it.t0 + w * span, q_full(w));
           }
-          for (int j = 0; j < 2 * n_tiles && ok; ++j, ++n) {
+          // K_0, K_1, V_0, K_2, V_1, ...: the order in which the issuer takes them
+          auto load = [&](bool is_v, int j) {
             const int st = n % S::STAGES;
-            ok = n < S::STAGES || p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag);
-            if (!ok) break;
+            ok = ok && (n < S::STAGES ||
+                        p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag));
+            if (!ok) return;
+            ++n;
             const uint32_t dst = sb + S::OFF_RING + st * S::TILE;
-            // V tiles with an edge land at the cleaning warps, which pass them on to the issuer
-            const bool edge = (j & 1) && (j >> 1) >= it.first_edge;
-            const uint32_t at = edge ? edge_full(st) : kv_full(st);
+      // V tiles with an edge land at the cleaning warp, which passes them on to the issuers
+            const uint32_t at = is_v && j >= it.first_edge ? edge_full(st) : kv_full(st);
             mbar_expect_tx(at, S::TILE);
-            if (!edge) mbar_arrive(at);
             for (int b = 0; b < S::NB; ++b)
-              tma_load_3d(dst + b * BLK, (j & 1) ? &tmV : &tmK, 64 * b, it.head, it.k0 + (j >> 1) * TK, at);
+              tma_load_3d(dst + b * KBLK, is_v ? &tmV : &tmK, 64 * b, it.head, it.k0 + j * TK, at);
+          };
+          for (int j = 0; j < min(2, n_tiles); ++j) load(false, j);
+          for (int j = 0; j < n_tiles && ok; ++j) {
+            load(true, j);
+            if (j + 2 < n_tiles) load(false, j + 2);
           }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -380,114 +397,92 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         while (globaltimer() - t0 < 2000000ull) {
         }
       }
-    } else if (warp == W_MMA) {
-      // ---------------- MMA issuer ----------------
-      // The whole warp walks the loop so that addresses and descriptors stay in uniform registers
-      // (a lone thread's would be moved there one by one, ahead of every MMA); one elected lane
-      // issues.
+    } else if (warp < W_TMA) {
+      // ---------------- MMA issuers, one for each query tile ----------------
+      // The whole warp walks the loop, so that addresses and descriptors stay in uniform registers;
+      // one lane's MMAs count. Each issuer's order of S and P V is that of its tile's chain.
       constexpr uint32_t idS = idesc_bf16(TQ, TK, false);
       constexpr uint32_t idO = idesc_bf16(TQ, D, true);
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
       };
-      const uint64_t q_desc = desc_sw128(sb), ring_k = desc_sw128(sb + S::OFF_RING);
+      const int w = __shfl_sync(0xffffffffu, warp - W_MMA, 0);
+      const uint32_t leader = elect_one();
+      const uint64_t q_desc = desc_sw128(sb + w * S::QTILE), ring_k = desc_sw128(sb + S::OFF_RING);
       const uint64_t ring_v =
           D == 128 ? desc_mn_blocks(sb + S::OFF_RING) : desc_sw128_mn(sb + S::OFF_RING);
       constexpr uint64_t STEP = S::TILE >> 4;     // of a tile, in descriptor units
-      int ks = 0, k_phase = 0;       // ring stage and lap of the next K tile the issuer meets
-      auto advance = [&](int& st, int& phase, int by) {
-        st += by;
-        if (st >= S::STAGES) {
-          st -= S::STAGES;
-          phase ^= 1;
+      int ks = 0, k_phase = 0;       // ring stage and lap of the next tile
+      auto advance = [&]() {
+        if (++ks == S::STAGES) {
+          ks = 0;
+          k_phase ^= 1;
         }
       };
-      uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+      int step = 0;                  // key tiles that the query tile has behind it
+      uint32_t q_phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
         ok = wait(item_full(i & 1), (i >> 1) & 1);
         if (!ok) break;
-        const Item it = items[i & 1];
-        const int valid = __shfl_sync(0xffffffffu, it.valid, 0);
-        const int nt[2] = {__shfl_sync(0xffffffffu, it.nt[0], 0), __shfl_sync(0xffffffffu, it.nt[1], 0)};
-        const int n_tiles = max(nt[0], nt[1]);
+        const volatile Item* slot = &items[i & 1];
+        const int valid = __shfl_sync(0xffffffffu, slot->valid, 0);
+        const int nt = __shfl_sync(0xffffffffu, slot->nt[w], 0);
+        const int n_tiles = __shfl_sync(0xffffffffu, max(slot->nt[0], slot->nt[1]), 0);
         if (lane == 0) mbar_arrive(item_empty(i & 1));
+        __syncwarp();
         if (!valid) break;
-        auto scores = [&](int w, int st, bool last) {
-          const uint64_t qd = q_desc + w * STEP, kd = ring_k + st * STEP;
-          if (elect_one()) {
+        auto scores = [&](int j) {
+          const uint64_t kd = ring_k + ks * STEP;
+          const int b = (step + j) & 1;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t at = (uint64_t)((kk >> 2) * (BLK >> 4) + 2 * (kk & 3));
-              mma_bf16_ss(tS(w), qd + at, kd + at, idS, kk > 0);
-            }
-            mma_commit(s_full(w));
-            if (last) mma_commit(q_empty(w));
-          }
-          __syncwarp();
+          for (int kk = 0; kk < D / 16; ++kk)
+            w_mma_ss(tS(w, b), q_desc + (uint64_t)((kk >> 2) * (BLK >> 4) + 2 * (kk & 3)),
+                     kd + (uint64_t)((kk >> 2) * (KBLK >> 4) + 2 * (kk & 3)), idS, kk > 0, leader);
+          w_commit(s_full(w, b), leader);
+          if (j + 1 == nt) w_commit(q_empty(w), leader);
         };
-        auto product = [&](int w, int st, int half, bool fresh) {
-          const uint64_t vd = ring_v + st * STEP;
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < TK / 32; ++k) {
-              const int kk = half * (TK / 32) + k;
-              mma_bf16_ts(tO(w), tS(w) + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)), idO,
-                          !fresh || (kk > 0));
-            }
-          }
-          __syncwarp();
-        };
-        auto release = [&](uint32_t bar) {
-          if (elect_one()) mma_commit(bar);
-          __syncwarp();
-        };
-        if (n_tiles > 0) {
+        // K_0, K_1, then V_j and K_{j+2} in turn
+        for (int j = 0; j < min(2, n_tiles) && ok; ++j) {
           ok = wait(kv_full(ks), k_phase);
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (!ok || nt[w] == 0) continue;
-            ok = wait(q_full(w), q_phase[w]);
-            q_phase[w] ^= 1;
-            tc_fence_after();
-            if (ok) scores(w, ks, nt[w] == 1);
+          if (ok && j == 0 && nt > 0) {
+            ok = wait(q_full(w), q_phase);
+            q_phase ^= 1;
           }
-          release(kv_empty(ks));
-          advance(ks, k_phase, 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (j < nt) scores(j);
+          w_commit(kv_empty(ks), leader);
+          advance();
         }
         for (int j = 0; j < n_tiles && ok; ++j) {
-          // V_j at (vs, v_phase), K_{j+1} behind it
-          const int vs = ks;
-          ok = wait(kv_full(vs), k_phase);
-          advance(ks, k_phase, 1);
-          const bool more = j + 1 < n_tiles;
+          ok = wait(kv_full(ks), k_phase);
+          if (ok && j < nt) {
+            const int at = step + j, b = at & 1;
+            ok = wait(p_full(w, b), (at >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = ring_v + ks * STEP;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (ok && j < nt[w]) {
-              ok = wait(p_half(w), p_phase[w]);
-              tc_fence_after();
-              if (ok) product(w, vs, 0, j == 0);
-              ok = ok && wait(p_full(w), p_phase[w]);
-              p_phase[w] ^= 1;
-              tc_fence_after();
-              if (ok) product(w, vs, 1, j == 0);
-              if (j + 1 == nt[w]) release(o_full(w));
-            }
-            if (w == 1) release(kv_empty(vs));
-            if (w == 0 && more) ok = ok && wait(kv_full(ks), k_phase);
-            if (ok && j + 1 < nt[w]) {
-              tc_fence_after();
-              scores(w, ks, j + 2 == nt[w]);
-            }
+            for (int kk = 0; kk < TK / 16; ++kk)
+              w_mma_ts(tO(w), tS(w, b) + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)), idO,
+                       (j > 0) || (kk > 0), leader);
+            w_commit(pv_done(w, b), leader);
           }
-          if (more) {
-            release(kv_empty(ks));
-            advance(ks, k_phase, 1);
+          w_commit(kv_empty(ks), leader);
+          advance();
+          if (j + 2 < n_tiles) {
+            ok = ok && wait(kv_full(ks), k_phase);
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 2 < nt) scores(j + 2);
+            w_commit(kv_empty(ks), leader);
+            advance();
           }
         }
+        step += nt;
       }
-      if (elect_one()) mma_commit(teardown);
-      __syncwarp();
+      w_commit(teardown, leader);
       const unsigned long long t0 = globaltimer();
       while (!mbar_try_wait(teardown, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
       }
@@ -503,19 +498,21 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (!it.valid) break;
         const int n_tiles = max(it.nt[0], it.nt[1]);
         for (int j = it.first_edge; j < n_tiles && ok; ++j) {
-          const int st = (n0 + 2 * j + 1) % S::STAGES;
+          // tiles of the item ahead of V_j in the ring
+          const int ahead = min(2, n_tiles) + j + max(0, min(j, n_tiles - 2));
+          const int st = (n0 + ahead) % S::STAGES;
           ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
           if (!ok) break;
           phase ^= 1u << st;
 #pragma unroll 1
-          for (int row = (warp - W_CLEAN) * 32 + lane; row < TK; row += 64) {   // thread = key
+          for (int row = lane; row < TK; row += 32) {   // thread = key
             uint8_t* v_row = smem + S::OFF_RING + st * S::TILE + row * 128;
             const bool behind = j * TK + row >= it.nk;
             uint32_t odd = 0;
             if (!behind) {
 #pragma unroll 8
               for (int c = 0; c < D / 8; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4*>(v_row + (c >> 3) * BLK + 16 * ((c & 7) ^ (row & 7)));
+                const uint4 x = *reinterpret_cast<const uint4*>(v_row + (c >> 3) * KBLK + 16 * ((c & 7) ^ (row & 7)));
                 odd |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
                        ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
               }
@@ -525,7 +522,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               if (odd) *(volatile int*)&items[i & 1].dirty = 1;
 #pragma unroll 1
               for (int c = 0; c < D / 8; ++c) {
-                uint4* at = reinterpret_cast<uint4*>(v_row + (c >> 3) * BLK + 16 * ((c & 7) ^ (row & 7)));
+                uint4* at = reinterpret_cast<uint4*>(v_row + (c >> 3) * KBLK + 16 * ((c & 7) ^ (row & 7)));
                 uint32_t x[4] = {0, 0, 0, 0};
                 if (!behind) {
                   const uint4 y = *at;
@@ -555,7 +552,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const int w = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tSw = tS(w) + lane_off, tOw = tO(w) + lane_off;
+    const uint32_t tOw = tO(w) + lane_off;
     const float scale_log2 = a.scale_log2;
     const float inv_group = 1.0f / a.group;
     const int row_tok = row / a.group, row_head = row % a.group;
@@ -564,7 +561,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     auto all_wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
     };
-    int sn = 0, on = 0;    // score tiles and outputs so far
+    int sn = 0;            // key tiles so far
     bool ok = true;
     for (int i = 0; ok; ++i) {
       ok = all_wait(item_full(i & 1), (i >> 1) & 1);
@@ -592,37 +589,33 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       };
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < ntw; ++j, ++sn) {
-        ok = all_wait(s_full(w), sn & 1);
+        const int b = sn & 1;
+        const uint32_t tSw = tS(w, b) + lane_off;
+        ok = all_wait(s_full(w, b), (sn >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        float alpha = 1.f, ms = 0.f;
-        uint32_t r0[32], r1[32];
         if (active) {
-          // Two reads of the scores, one for the maximum and one for the exponentials: 128 values
-          // held in between would push the loop's state out of the registers.
-          float part[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld32_async(tSw + 64 * h, r0);
-            tmem_ld32_async(tSw + 64 * h + 32, r1);
-            tmem_wait(r0);
-            tmem_wait(r1);
-            hide(r0, j * TK + 64 * h);
-            hide(r1, j * TK + 64 * h + 32);
-            part[2 * h] = max32(r0);
-            part[2 * h + 1] = max32(r1);
-          }
+          uint32_t r0[32], r1[32];
           tmem_ld32_async(tSw, r0);
-          const float cmax = fmaxf(p_max3(part[0], part[1], part[2]), part[3]);
+          tmem_ld32_async(tSw + 32, r1);
+          tmem_wait(r0);
+          tmem_wait(r1);
+          hide(r0, j * TK);
+          hide(r1, j * TK + 32);
+          const float cmax = fmaxf(max32(r0), max32(r1));
           // the exponent's reference moves only when the maximum grew by more than 2^8: the same
           // reference scales O and the sum, so the result is unchanged
           const bool bump = cmax > m && (m == -INFINITY || (cmax - m) * scale_log2 > 8.0f);
           const float mnew = bump ? cmax : m;
-          alpha = bump ? p_ex2((m - mnew) * scale_log2) : 1.f;
-          ms = mnew == -INFINITY ? 0.f : mnew * scale_log2;
+          const float alpha = bump ? p_ex2((m - mnew) * scale_log2) : 1.f;
+          const float ms = mnew == -INFINITY ? 0.f : mnew * scale_log2;
           m = mnew;
           if (j > 0 && __any_sync(0xffffffffu, bump)) {
-            // O holds the products of tile j - 1 and before (see the head of the file)
+            // the last product must be complete (those before it are: the issuer began this
+            // tile's scores after them)
+            ok = all_wait(pv_done(w, b ^ 1), ((sn - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               uint32_t ov[32];
@@ -633,48 +626,35 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               tmem_st32(tOw + 32 * q, ov);
             }
           }
-        }
-        // P in two halves of 64 keys: the first one's product runs under the second's exponentials
-        const unsigned long long sc2 = f2_pack(scale_log2, scale_log2), nms2 = f2_pack(-ms, -ms);
-        unsigned long long sum2[2] = {0, 0};
-        auto exponentials = [&](const uint32_t (&r)[32], uint32_t to) {
-          uint32_t pk[16];
+          const unsigned long long sc2 = f2_pack(scale_log2, scale_log2), nms2 = f2_pack(-ms, -ms);
+          unsigned long long sum2[2] = {0, 0};
+          uint32_t pk[32];
+          auto exponentials = [&](const uint32_t (&r)[32], uint32_t* to) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float2 e = f2_unpack(
-                f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sc2, nms2));
-            const float p0 = p_ex2(e.x), p1 = p_ex2(e.y);
-            sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-            pk[c] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          tmem_st16(to, pk);
-        };
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (active) {
-            tmem_wait(r0);
-            tmem_ld32_async(tSw + 64 * h + 32, r1);
-            hide(r0, j * TK + 64 * h);
-            exponentials(r0, tSw + 32 * h);
-            tmem_wait(r1);
-            if (h == 0) tmem_ld32_async(tSw + 64, r0);
-            hide(r1, j * TK + 64 * h + 32);
-            exponentials(r1, tSw + 32 * h + 16);
-            tmem_st_wait();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(h == 0 ? p_half(w) : p_full(w));
+            for (int c = 0; c < 16; ++c) {
+              const float2 e = f2_unpack(
+                  f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sc2, nms2));
+              const float p0 = p_ex2(e.x), p1 = p_ex2(e.y);
+              sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
+              const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+              to[c] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          };
+          exponentials(r0, pk);
+          exponentials(r1, pk + 16);
+          tmem_st32(tSw, pk);              // P over the first half of the scores' columns
+          const float2 sm = f2_unpack(f2_add(sum2[0], sum2[1]));
+          l = l * alpha + (sm.x + sm.y);
+          tmem_st_wait();
         }
-        const float2 sm = f2_unpack(f2_add(sum2[0], sum2[1]));
-        l = l * alpha + (sm.x + sm.y);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(w, b));
       }
       if (!ok) break;
       if (ntw > 0) {
-        ok = all_wait(o_full(w), on & 1);
+        ok = all_wait(pv_done(w, (sn - 1) & 1), ((sn - 1) >> 1) & 1);
         if (!ok) break;
-        ++on;
         tc_fence_after();
       }
       if (active) {
