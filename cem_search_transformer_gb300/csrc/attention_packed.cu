@@ -43,10 +43,10 @@ using namespace tc;
 constexpr int TQ = 128;            // rows of a query tile (MMA M)
 constexpr int TK = 64;             // keys of a tile
 constexpr int P_THREADS = 384;     // 8 warps of softmax, then two issuers, producer, cleaning
-constexpr int W_MMA = 8, W_TMA = 10, W_CLEAN = 11;   // issuers: W_MMA and the next
+constexpr int W_MMA = 8, W_TMA = 10;   // issuers: W_MMA and the next; cleaning: the last
 // Registers a thread after setmaxnreg. The block launches with 168 each; the softmax warpgroups
 // draw what the last one returns.
-constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
+constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == P_THREADS * 168, "register split");
 constexpr uint32_t P_TMEM = 512;
 constexpr int BLK = TQ * 128;      // bytes of 128 rows x 64 bf16 (one swizzled block of Q)
@@ -588,33 +588,35 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           if (c >= left) r[c] = __float_as_uint(-INFINITY);
       };
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < ntw; ++j, ++sn) {
-        const int b = sn & 1;
-        const uint32_t tSw = tS(w, b) + lane_off;
-        ok = all_wait(s_full(w, b), (sn >> 1) & 1);
-        if (!ok) break;
+      auto scores_of = [&](int n) { return tS(w, n & 1) + lane_off; };
+      auto ready = [&](int n) {
+        const bool there = all_wait(s_full(w, n & 1), (n >> 1) & 1);
         tc_fence_after();
-        if (active) {
-          uint32_t r0[32], r1[32];
-          tmem_ld32_async(tSw, r0);
-          tmem_ld32_async(tSw + 32, r1);
-          tmem_wait(r0);
-          tmem_wait(r1);
-          hide(r0, j * TK);
-          hide(r1, j * TK + 32);
-          const float cmax = fmaxf(max32(r0), max32(r1));
-          // the exponent's reference moves only when the maximum grew by more than 2^8: the same
-          // reference scales O and the sum, so the result is unchanged
-          const bool bump = cmax > m && (m == -INFINITY || (cmax - m) * scale_log2 > 8.0f);
+        return there;
+      };
+      auto tile = [&](int j) {
+        const int b = sn & 1;
+        if (!ready(sn)) return false;
+        uint32_t r0[32], r1[32];
+        tmem_ld32_async(scores_of(sn), r0);
+        tmem_ld32_async(scores_of(sn) + 32, r1);
+        tmem_wait(r0);
+        tmem_wait(r1);
+        hide(r0, j * TK);
+        hide(r1, j * TK + 32);
+        const float cmax = fmaxf(max32(r0), max32(r1));
+        // the exponent's reference moves only when the maximum grew by more than 2^8: the same
+        // reference scales O and the sum, so the result is unchanged
+        const bool bump = cmax > m && (m == -INFINITY || (cmax - m) * scale_log2 > 8.0f);
+        if (__any_sync(0xffffffffu, bump)) {
           const float mnew = bump ? cmax : m;
           const float alpha = bump ? p_ex2((m - mnew) * scale_log2) : 1.f;
-          const float ms = mnew == -INFINITY ? 0.f : mnew * scale_log2;
           m = mnew;
-          if (j > 0 && __any_sync(0xffffffffu, bump)) {
+          l *= alpha;
+          if (j > 0) {
             // the last product must be complete (those before it are: the issuer began this
             // tile's scores after them)
-            ok = all_wait(pv_done(w, b ^ 1), ((sn - 1) >> 1) & 1);
-            if (!ok) break;
+            if (!all_wait(pv_done(w, b ^ 1), ((sn - 1) >> 1) & 1)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -626,30 +628,43 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               tmem_st32(tOw + 32 * q, ov);
             }
           }
-          const unsigned long long sc2 = f2_pack(scale_log2, scale_log2), nms2 = f2_pack(-ms, -ms);
-          unsigned long long sum2[2] = {0, 0};
-          uint32_t pk[32];
-          auto exponentials = [&](const uint32_t (&r)[32], uint32_t* to) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float2 e = f2_unpack(
-                  f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sc2, nms2));
-              const float p0 = p_ex2(e.x), p1 = p_ex2(e.y);
-              sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
-              const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-              to[c] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-          };
-          exponentials(r0, pk);
-          exponentials(r1, pk + 16);
-          tmem_st32(tSw, pk);              // P over the first half of the scores' columns
-          const float2 sm = f2_unpack(f2_add(sum2[0], sum2[1]));
-          l = l * alpha + (sm.x + sm.y);
-          tmem_st_wait();
         }
+        const float ms = m == -INFINITY ? 0.f : m * scale_log2;
+        const unsigned long long sc2 = f2_pack(scale_log2, scale_log2), nms2 = f2_pack(-ms, -ms);
+        unsigned long long sum2[2] = {0, 0};
+        uint32_t pk[32];
+        auto exponentials = [&](const uint32_t (&r)[32], uint32_t* to) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 e = f2_unpack(
+                f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sc2, nms2));
+            const float p0 = p_ex2(e.x), p1 = p_ex2(e.y);
+            sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+            to[c] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        };
+        exponentials(r0, pk);
+        exponentials(r1, pk + 16);
+        tmem_st32(scores_of(sn), pk);      // P over the first half of the scores' columns
+        const float2 sm = f2_unpack(f2_add(sum2[0], sum2[1]));
+        l += sm.x + sm.y;
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(w, b));
+        ++sn;
+        return true;
+      };
+      if (active) {
+        for (int j = 0; j < ntw && ok; ++j) ok = tile(j);
+      } else {
+        for (int j = 0; j < ntw && ok; ++j, ++sn) {   // none of the warp's rows is in use
+          ok = ready(sn);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(p_full(w, sn & 1));
+        }
       }
       if (!ok) break;
       if (ntw > 0) {
