@@ -4,23 +4,28 @@
 //
 // for the rows r = (new token, head of the group) that share a key/value head. Bound by the HBM
 // bytes of the codes (2 kv_heads * dim a cached token), so the codes go from shared memory
-// straight into mma.sync fragments: e4m3 -> f16 is exact, 64 conversions a 16-key step, and 16
-// rows cost the same as one.
-//   * Work: items (sequence, head, tile of 16 rows), each cut into units of 4 warps * KS keys.
+// straight into mma.sync fragments: e4m3 -> f16 is exact, 64 conversions a warp's 16 keys.
+//   * The products are transposed, S^T = K Q^T and O^T = V^T P^T: codes are the 16-row operand and
+//     query rows the 8-wide one, so that up to 8 rows (one new token, groups up to 8) cost 8 + 8
+//     MMAs a 16-key step; 9 to 16 rows take two 8-wide tiles over the same converted codes. With
+//     the query rows as the 16-row operand one row cost as much as 16, and the kernel 530
+//     instructions a step: it was bound by issue, not by HBM.
+//   * Work: items (sequence, head, tile of rows), each cut into units of 4 warps * KS keys.
 //     All units of the call in one line are shared out evenly over the CTAs, so ragged lengths
 //     and few long sequences fill the machine alike; an item that crosses CTAs leaves partial
-//     (max, sum, output) rows in the workspace, which k_combine joins in a fixed order.
+//     (max, sum, output) rows in the workspace, which k_combine joins in a fixed order. Where all
+//     sequences are short, items stay whole.
 //   * A warp owns KS keys of each unit and its own ring of NST stages filled with cp.async
 //     (zero-filled past the sequence's end, so stale codes there never meet the tensor cores).
 //   * q is scaled per row by a power of two into f16's range; the exact scores are fp32. The
 //     probabilities enter the second product as f16 (2^-12 relative, finer than bf16's 2^-9).
 //   * Scores are exponentiated against a reference that moves only when the maximum grows by
 //     more than 2^8, so that most steps leave the accumulators alone.
-//   * Fragment layouts. A lane (g = lane / 4, t = lane % 4) takes bytes [t D/4, (t+1) D/4) of key
-//     g for Q K^T, and bytes [g D/8, (g+1) D/8) of keys 2t, 2t+1, 2t+8, 2t+9 for P V: the order
-//     of the summed index is free, and so is the naming of output columns. Both are wide loads
-//     without bank conflicts under the XOR swizzle (dim 64: two-way for V), and a lane ends with
-//     D/4 consecutive outputs of two rows.
+//   * Fragment layouts. A lane (g = lane / 4, t = lane % 4) takes bytes [t D/4, (t+1) D/4) of keys
+//     g and g + 8 for K Q^T, and bytes [g D/8, (g+1) D/8) of keys 2t, 2t+1, 2t+8, 2t+9 for V^T P^T:
+//     the order of the summed index is free, and so is the naming of output rows. Both are wide
+//     loads without bank conflicts under the XOR swizzle (dim 64: two-way for V), and a lane ends
+//     with D/8 consecutive outputs of two query rows.
 #include "kv8.cuh"
 
 #include <cuda_fp16.h>
@@ -32,23 +37,24 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int NST = 4;              // cp.async stages of a warp
-constexpr int ROWS = 16;            // query rows of an item
 constexpr int CTAS_PER_SM = 3;
-constexpr int MIN_UNITS = 2;        // units a CTA takes at least
+constexpr int MIN_UNITS = 4;        // units a CTA takes at least where items are split
+constexpr int WHOLE_UNITS = 8;      // items up to this many units are not split
 
 // Probabilities are 2^(s - m + P_SHIFT) for the running reference m, which trails the maximum by
 // P_SLACK at most: up to 2^15 as f16, so that the many small weights of a long context keep
 // their bits (f16 ends at 2^-24, here 2^-31 of the largest).
 constexpr float P_SHIFT = 7.f, P_SLACK = 8.f;
 
-template <int D>
+template <int D, int NR>
 struct Shape {
+  static constexpr int ROWS = 8 * NR;              // query rows of an item
   static constexpr int KS = 2048 / D;              // keys a warp takes in a step
   static constexpr int GROUPS = KS / 16;           // 16-key groups of P V
   static constexpr int UNIT = WARPS * KS;          // keys of a unit
-  static constexpr int NT = KS / 8;                // score tiles (8 keys)
   static constexpr int KW = D / 16;                // 32-bit words of a key a lane takes
-  static constexpr int VN = D / 8;                 // output tiles = values of a V row a lane takes
+  static constexpr int VN = D / 8;                 // values of a V row a lane takes
+  static constexpr int MT = D / 16;                // output tiles of 16 columns
   static constexpr int STAGE = 2 * KS * D;         // K and V codes
   static constexpr int OFF_SCALE = WARPS * NST * STAGE;
   static constexpr int SMEM = OFF_SCALE + WARPS * NST * 16;
@@ -105,12 +111,20 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// 8 x 8 f16 matrix (lane (g, t) holds row g, columns 2t, 2t + 1) transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 struct Args {
   const bf16* q;
   const int* kv_len;
   bf16* out;
   float* lse;
-  float* part;       // workspace: [CTA][2][ROWS][D + 2]
+  int4* split;       // workspace: [CTA] (sequence, item, last CTA, 1) of an item begun and split
+  float* part;       // workspace: [CTA][2][ROWS * (D + 2)]
   float scale_log2;
   int q_tokens, q_heads, group, tiles, causal;
 };
@@ -175,91 +189,123 @@ __device__ __forceinline__ void seek(const Kv8View& c, const Args& a, int unit, 
   at.s = c.batch;
 }
 
-// CTAs that take part: each has MIN_UNITS units at least.
+// CTAs that take part in a split line: each has MIN_UNITS units at least.
 __device__ __forceinline__ int workers_of(long long total, int grid) {
   const long long w = (total + MIN_UNITS - 1) / MIN_UNITS;
   return w < grid ? (int)w : grid;
 }
 
-template <int D>
+template <int D, int NR>
 __device__ __forceinline__ float* part_of(const Args& a, int cta, int which) {
-  return a.part + ((long long)cta * 2 + which) * (ROWS * (D + 2));
+  return a.part + ((long long)cta * 2 + which) * (Shape<D, NR>::ROWS * (D + 2));
 }
 
-template <int D>
+// Row r of an item's tile as an index into [batch][q_tokens][q_heads].
+__device__ __forceinline__ long long row_at(const Args& a, int s, int head, int r) {
+  const int tok = r / a.group;
+  return ((long long)s * a.q_tokens + tok) * a.q_heads + head * a.group + (r - tok * a.group);
+}
+
+template <int D, int NR>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-    k_attention_kv8(Kv8View c, Args a, int* err_flag) {
-  using S = Shape<D>;
+    k_attention_kv8(Kv8View c, Args a, int whole, int* err_flag) {
+  using S = Shape<D, NR>;
+  constexpr int ROWS = S::ROWS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");   // k_combine may be set up meanwhile
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (NST * S::STAGE);
   const uint8_t* ring_ptr = smem + warp * (NST * S::STAGE);
   const uint32_t ring_sc =
       (uint32_t)__cvta_generic_to_shared(smem) + S::OFF_SCALE + warp * (NST * 16);
   const float* ring_sc_ptr = reinterpret_cast<const float*>(smem + S::OFF_SCALE) + warp * NST * 4;
 
-  const long long total = total_units(c, a, S::UNIT, blockIdx.x == 0 ? err_flag : nullptr);
-  const int workers = workers_of(total, gridDim.x);
-  if ((int)blockIdx.x >= workers) return;
-  const long long u_begin = kv8_share(total, workers, blockIdx.x);
-  const long long u_end = kv8_share(total, workers, blockIdx.x + 1);
+  int* const flag0 = blockIdx.x == 0 ? err_flag : nullptr;
+  long long u_begin, u_end, total = 0;
+  int workers = 0;
+  if (whole) {
+    // items in equal numbers; `units` below then count items of one unit each
+    const long long items = (long long)c.batch * c.heads * a.tiles;
+    u_begin = kv8_share(items, gridDim.x, blockIdx.x);
+    u_end = kv8_share(items, gridDim.x, blockIdx.x + 1);
+    if (flag0 && warp == 0) total_units(c, a, S::UNIT, flag0);   // reports lengths out of range
+  } else {
+    total = total_units(c, a, S::UNIT, flag0);
+    workers = workers_of(total, gridDim.x);
+    if ((int)blockIdx.x >= workers) {
+      if (threadIdx.x == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
+    u_begin = kv8_share(total, workers, blockIdx.x);
+    u_end = kv8_share(total, workers, blockIdx.x + 1);
+  }
+  int4 begun = make_int4(0, 0, 0, 0);
   Cursor cur{0, 0, 0, 0};
   const int rows = a.q_tokens * a.group;
+  const long long v_ahead = c.v - c.k;         // bytes from a key's codes to its value's
 
   for (long long u = u_begin; u < u_end;) {
-    seek(c, a, S::UNIT, u, cur);
-    const long long in = u - cur.base;
-    const int item = (int)(in / cur.n), k0 = (int)(in % cur.n);
-    const int k1 = (int)min((long long)cur.n, k0 + (u_end - u));   // units [k0, k1) of the item
+    int item, k0, k1;                          // units [k0, k1) of the item
+    if (whole) {
+      const int per = c.heads * a.tiles;
+      cur.s = (int)(u / per);
+      item = (int)(u % per);
+      cur.len = length_of(c, a, cur.s, nullptr);
+      cur.n = units_of(cur.len, S::UNIT);
+      k0 = 0;
+      k1 = cur.n;
+    } else {
+      seek(c, a, S::UNIT, u, cur);
+      const long long in = u - cur.base;
+      item = (int)(in / cur.n);
+      k0 = (int)(in % cur.n);
+      k1 = (int)min((long long)cur.n, k0 + (u_end - u));
+    }
     const int head = item / a.tiles, r0 = (item % a.tiles) * ROWS;
     const int s = cur.s, len = cur.len;
-    const long long table0 = (long long)s * c.max_pages;
+    const int* const table = c.table + (long long)s * c.max_pages;
 
     // ---- the warp's share of the keys: steps k0 .. k1 - 1, KS keys each ----
     const int steps = k1 - k0;
-    auto key_of = [&](int i) { return (k0 + i) * S::UNIT + warp * S::KS; };
-    // page of the 16-key group `grp` of step i (-1: none, or out of range)
-    auto page_of = [&](int i, int grp) {
-      const int key = key_of(i) + 16 * grp;
-      if (i >= steps || key >= len) return -1;
-      return __ldg(c.table + table0 + (key >> c.page_log2));
-    };
-    int pg_next[S::GROUPS];
+    const int key_first = k0 * S::UNIT + warp * S::KS;
+    constexpr int CPR = D / 16;                // 16-byte chunks of a row
+    constexpr int RPI = 32 / CPR;              // rows a warp copies in one instruction
+    const int chunk = lane % CPR, sub = lane / CPR;
+    int pg_next[S::GROUPS];                    // pages of the step that is issued next
     auto fetch_pages = [&](int i) {
 #pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) pg_next[p] = page_of(i, p);
+      for (int p = 0; p < S::GROUPS; ++p) {
+        const int key = key_first + i * S::UNIT + 16 * p;
+        pg_next[p] = i < steps && key < len ? __ldg(table + (key >> c.page_log2)) : -1;
+      }
     };
-    auto issue = [&](int i) {   // step i into stage i % NST; pg_next holds its pages
+    auto issue = [&](int i) {   // step i into stage i % NST
       const uint32_t st = ring + (i % NST) * S::STAGE;
-      const int key0 = key_of(i);
+      const int key0 = key_first + i * S::UNIT;
       if (i < steps && key0 < len) {
-        constexpr int CPR = D / 16;                // 16-byte chunks of a row
-        constexpr int RPI = 32 / CPR;              // rows a warp copies in one instruction
-        const int chunk = lane % CPR, sub = lane / CPR;
 #pragma unroll
-        for (int q = 0; q < S::KS / RPI; ++q) {
-          const int row = q * RPI + sub, key = key0 + row;
-          const int grp = (q * RPI) / 16;          // RPI divides 16
-          int pg = pg_next[grp];
-          const bool there = pg >= 0 && pg < c.num_pages && key < len;
-          if (!there) pg = 0;
-          const long long from =
-              (((long long)pg * c.heads + head) * c.page + (key & (c.page - 1))) * D + 16 * chunk;
-          const int sw = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-          const uint32_t to = st + row * D + 16 * sw;
-          cp16(to, c.k + from, there ? 16 : 0);
-          cp16(to + S::KS * D, c.v + from, there ? 16 : 0);
-        }
-        if (lane < 2 * S::GROUPS) {
-          int pg = S::GROUPS == 1 || lane < 2 ? pg_next[0] : pg_next[S::GROUPS - 1];
-          const bool named = key0 + 16 * (lane >> 1) < len;
-          const bool there = pg >= 0 && pg < c.num_pages && named;
-          if (!there && named) atomicOr(err_flag, DEV_ERR_INDEX);
-          if (!there) pg = 0;
-          cp4(ring_sc + (i % NST) * 16 + lane * 4,
-              ((lane & 1) ? c.v_scale : c.k_scale) + (long long)pg * c.heads + head,
-              there ? 4 : 0);
+        for (int p = 0; p < S::GROUPS; ++p) {
+          const bool page_ok = pg_next[p] >= 0 && pg_next[p] < c.num_pages;
+          const int pg = page_ok ? pg_next[p] : 0, key_p = key0 + 16 * p;
+          const int keys = page_ok ? min(16, len - key_p) : 0;      // of this group that are there
+          const long long block = (long long)pg * c.heads + head;
+          const uint8_t* from =
+              c.k + (block * c.page + (key_p & (c.page - 1)) + sub) * D + 16 * chunk;
+#pragma unroll
+          for (int q = 0; q < 16 / RPI; ++q) {
+            const int row = 16 * p + q * RPI + sub;
+            const int sw = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+            const uint32_t to = st + row * D + 16 * sw;
+            const uint32_t bytes = q * RPI + sub < keys ? 16 : 0;
+            cp16(to, from + q * RPI * D, bytes);
+            cp16(to + S::KS * D, from + v_ahead + q * RPI * D, bytes);
+          }
+          if (lane < 2) {
+            if (!page_ok && key_p < len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+            cp4(ring_sc + (i % NST) * 16 + (2 * p + lane) * 4, (lane ? c.v_scale : c.k_scale) + block,
+                page_ok ? 4 : 0);
+          }
         }
       }
       cp_commit();
@@ -271,17 +317,17 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       fetch_pages(i + 1);
     }
 
-    // ---- queries: rows g and g + 8 of the tile as f16, times 2^-e so that |q| < 2^15 ----
-    uint32_t qf[S::KW][4];
-    float qs[2];        // 2^e * softmax scale * log2(e)
-    int lim[2];         // keys a row sees
+    // ---- queries: row g of each 8-row tile as f16, times 2^-e so that |q| < 2^15 ----
+    uint32_t qf[NR][S::KW][2];
+    float qs[NR][2];       // of rows 2t, 2t + 1: 2^e * softmax scale * log2(e)
+    int lim[NR][2];        // keys that they see
+    int lim_g[NR];         // keys that row g sees
     int lim_min = len;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = r0 + g + 8 * hf;
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = r0 + 8 * nr + g;
       const bool valid = r < rows;
-      const int tok = valid ? r / a.group : 0, hd = head * a.group + (valid ? r % a.group : 0);
-      const bf16* src = a.q + (((long long)s * a.q_tokens + tok) * a.q_heads + hd) * D + t * (D / 4);
+      const bf16* src = a.q + row_at(a, s, head, valid ? r : 0) * D + t * (D / 4);
       uint32_t w[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -297,123 +343,155 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       int e = (int)(top >> 7) - 127 - 14;
       e = max(-126, min(e, 113));
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      qs[hf] = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const float lo = __uint_as_float(w[i] << 16) * down;
-        const float hi = __uint_as_float(w[i] & 0xffff0000u) * down;
-        qf[i >> 1][(i & 1) * 2 + hf] = pack_f16(lo, hi);
+      for (int i = 0; i < D / 8; ++i)
+        qf[nr][i >> 1][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * down,
+                                         __uint_as_float(w[i] & 0xffff0000u) * down);
+      lim_g[nr] = len;
+      if (a.causal && valid) lim_g[nr] = max(0, len - a.q_tokens + r / a.group + 1);
+      lim_min = min(lim_min, lim_g[nr]);
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        qs[nr][e2] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e2));
+        lim[nr][e2] = __shfl_sync(0xffffffffu, lim_g[nr], 4 * (2 * t + e2));
       }
-      lim[hf] = len;
-      if (a.causal && valid) lim[hf] = max(0, len - a.q_tokens + tok + 1);
-      lim_min = min(lim_min, lim[hf]);
     }
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
-    float o[S::VN][4];
+    float o[NR][S::MT][4];
+    float m[NR][2], l[NR][2];
 #pragma unroll
-    for (int i = 0; i < S::VN; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float vs_cur = 1.f;   // outputs are o * vs_cur
-    bool first_scale = true;
+    for (int nr = 0; nr < NR; ++nr) {
+      m[nr][0] = m[nr][1] = -INFINITY;
+      l[nr][0] = l[nr][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < S::MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
+    }
+    float vs_cur = 0.f;    // outputs are o * vs_cur; 0 before the first key
 
     for (int i = 0; i < steps; ++i) {
       cp_wait<NST - 2>();
       __syncwarp();
       issue(i + NST - 1);
       fetch_pages(i + NST);
-      const int key0 = key_of(i);
+      const int key0 = key_first + i * S::UNIT;
       if (key0 >= len) continue;
       const uint8_t* kb = ring_ptr + (i % NST) * S::STAGE;
       const uint8_t* vb = kb + S::KS * D;
       const float* scales = ring_sc_ptr + (i % NST) * 4;
 
-      // scores
-      float sc[S::NT][4];
+      // scores of keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
+      float sc[S::GROUPS][NR][4];
 #pragma unroll
-      for (int j = 0; j < S::NT; ++j) {
-        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-        const int row = 8 * j + g;
-        uint32_t w[S::KW];
+      for (int p = 0; p < S::GROUPS; ++p) {
+        uint32_t w[2][S::KW];
 #pragma unroll
-        for (int i4 = 0; i4 < S::KW / 4; ++i4) {
-          const int chunk = t * (S::KW / 4) + i4;
-          const int sw = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-          const uint4 x = *reinterpret_cast<const uint4*>(kb + row * D + 16 * sw);
-          w[4 * i4] = x.x; w[4 * i4 + 1] = x.y; w[4 * i4 + 2] = x.z; w[4 * i4 + 3] = x.w;
+        for (int h = 0; h < 2; ++h) {
+          const int row = 16 * p + 8 * h + g;
+#pragma unroll
+          for (int i4 = 0; i4 < S::KW / 4; ++i4) {
+            const int ch = t * (S::KW / 4) + i4;
+            const int sw = D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
+            const uint4 x = *reinterpret_cast<const uint4*>(kb + row * D + 16 * sw);
+            w[h][4 * i4] = x.x; w[h][4 * i4 + 1] = x.y; w[h][4 * i4 + 2] = x.z; w[h][4 * i4 + 3] = x.w;
+          }
         }
 #pragma unroll
-        for (int q = 0; q < S::KW; ++q)
-          mma_f16(sc[j], qf[q][0], qf[q][1], qf[q][2], qf[q][3], f16x2_of_e4m3x2(w[q]),
-                  f16x2_of_e4m3x2_hi(w[q]));
+        for (int nr = 0; nr < NR; ++nr) sc[p][nr][0] = sc[p][nr][1] = sc[p][nr][2] = sc[p][nr][3] = 0.f;
+#pragma unroll
+        for (int q = 0; q < S::KW; ++q) {
+          const uint32_t a0 = f16x2_of_e4m3x2(w[0][q]), a1 = f16x2_of_e4m3x2(w[1][q]);
+          const uint32_t a2 = f16x2_of_e4m3x2_hi(w[0][q]), a3 = f16x2_of_e4m3x2_hi(w[1][q]);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+            mma_f16(sc[p][nr], a0, a1, a2, a3, qf[nr][q][0], qf[nr][q][1]);
+        }
       }
       const bool edge = key0 + S::KS > lim_min;   // some row does not see some key (warp-uniform)
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < S::NT; ++j) {
-        const float ks = sane_scale(scales[2 * (j >> 1)]);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = sc[j][2 * hf + e] * (qs[hf] * ks);
-            if (edge && key0 + 8 * j + 2 * t + e >= lim[hf]) x = -INFINITY;
-            sc[j][2 * hf + e] = x;
-            top[hf] = fmaxf(top[hf], x);
-          }
-      }
       bool move = false;
+      float top[NR][2];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xffffffffu, top[hf], 1));
-        top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xffffffffu, top[hf], 2));
-        move = move || top[hf] > m[hf] + P_SLACK || (m[hf] == -INFINITY && top[hf] > -INFINITY);
-      }
-      if (__any_sync(0xffffffffu, move)) {
+      for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float mn = fmaxf(m[hf], top[hf]);
-          const float al = mn == -INFINITY ? 1.f : ex2f(m[hf] - mn);
-          m[hf] = mn;
-          l[hf] *= al;
+        for (int p = 0; p < S::GROUPS; ++p) {
+          const float ks = sane_scale(scales[2 * p]);
+          const float f0 = qs[nr][0] * ks, f1 = qs[nr][1] * ks;
+          sc[p][nr][0] *= f0; sc[p][nr][1] *= f1; sc[p][nr][2] *= f0; sc[p][nr][3] *= f1;
+        }
+        if (edge) {
 #pragma unroll
-          for (int d = 0; d < S::VN; ++d) {
-            o[d][2 * hf] *= al;
-            o[d][2 * hf + 1] *= al;
-          }
+          for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 16 * p + 8 * (e >> 1) + g >= lim[nr][e & 1]) sc[p][nr][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(sc[0][nr][e], sc[0][nr][2 + e]);
+#pragma unroll
+          for (int p = 1; p < S::GROUPS; ++p) x = fmaxf(x, fmaxf(sc[p][nr][e], sc[p][nr][2 + e]));
+          top[nr][e] = x;
+          move = move || x > m[nr][e] + P_SLACK || (m[nr][e] == -INFINITY && x > -INFINITY);
         }
       }
-      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - P_SHIFT,
-                            m[1] == -INFINITY ? 0.f : m[1] - P_SHIFT};
+      if (__any_sync(0xffffffffu, move)) {
+        // the maxima over all keys of the step; the reference moves where it has to
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[nr][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m[nr][e], x);
+            const float al = mn == -INFINITY ? 1.f : ex2f(m[nr][e] - mn);
+            m[nr][e] = mn;
+            l[nr][e] *= al;
+#pragma unroll
+            for (int d = 0; d < S::MT; ++d) {
+              o[nr][d][e] *= al;
+              o[nr][d][2 + e] *= al;
+            }
+          }
+      }
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
         const float vs = sane_scale(scales[2 * p + 1]);
-        if (first_scale) {
-          vs_cur = vs;
-          first_scale = false;
-        }
-        float ratio = vs / vs_cur;
-        if (!(ratio >= 0x1p-6f && ratio <= 1.f)) {
-          // larger than the accumulators' unit, or far below it: move them (by 2^80 at most)
-          const float f = vs_cur / vs;
+        float ratio = 1.f;
+        if (vs != vs_cur) {
+          ratio = vs_cur > 0.f ? vs / vs_cur : 2.f;
+          if (!(ratio >= 0x1p-6f && ratio <= 1.f)) {
+            // larger than the accumulators' unit, or far below it: move them (by 2^80 at most)
+            const float f = vs_cur / vs;
 #pragma unroll
-          for (int d = 0; d < S::VN; ++d) {
-            o[d][0] *= f; o[d][1] *= f; o[d][2] *= f; o[d][3] *= f;
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+              for (int d = 0; d < S::MT; ++d) {
+                o[nr][d][0] *= f; o[nr][d][1] *= f; o[nr][d][2] *= f; o[nr][d][3] *= f;
+              }
+            vs_cur = vs;
+            ratio = 1.f;
           }
-          vs_cur = vs;
-          ratio = 1.f;
         }
-        float pr[2][4];   // [tile of the group][c index]
+        uint32_t b[NR][2];
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
+        for (int nr = 0; nr < NR; ++nr) {
+          float pr[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = ex2f(sc[2 * p + jj][e] - ref[e >> 1]);
-            l[e >> 1] += x;
-            pr[jj][e] = x * ratio;
+            const float mr = m[nr][e & 1];
+            pr[e] = ex2f(sc[p][nr][e] - (mr == -INFINITY ? 0.f : mr - P_SHIFT));
+            l[nr][e & 1] += pr[e];
           }
-        const uint32_t a0 = pack_f16(pr[0][0], pr[0][1]), a1 = pack_f16(pr[0][2], pr[0][3]);
-        const uint32_t a2 = pack_f16(pr[1][0], pr[1][1]), a3 = pack_f16(pr[1][2], pr[1][3]);
+          if (ratio != 1.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[e] *= ratio;
+          }
+          b[nr][0] = transposed(pack_f16(pr[0], pr[1]));
+          b[nr][1] = transposed(pack_f16(pr[2], pr[3]));
+        }
         // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group, D/8 values each
         uint32_t w[4][S::VN / 4];
 #pragma unroll
@@ -446,38 +524,43 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
             for (int hb = 0; hb < 2; ++hb) {
               const uint32_t x = __byte_perm(w[0][q], w[1][q], hb ? 0x7362 : 0x5140);
               const uint32_t y = __byte_perm(w[2][q], w[3][q], hb ? 0x7362 : 0x5140);
-              mma_f16(o[4 * q + 2 * hb], a0, a1, a2, a3, f16x2_of_e4m3x2(x), f16x2_of_e4m3x2(y));
-              mma_f16(o[4 * q + 2 * hb + 1], a0, a1, a2, a3, f16x2_of_e4m3x2_hi(x),
-                      f16x2_of_e4m3x2_hi(y));
+              const uint32_t a0 = f16x2_of_e4m3x2(x), a1 = f16x2_of_e4m3x2_hi(x);
+              const uint32_t a2 = f16x2_of_e4m3x2(y), a3 = f16x2_of_e4m3x2_hi(y);
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr)
+                mma_f16(o[nr][2 * q + hb], a0, a1, a2, a3, b[nr][0], b[nr][1]);
             }
         } else {
-          // second product: 1 where a row sees a key, times 1 where V is NaN
-          uint32_t see[4];
+          // second product: 1 where V is NaN, times 1 where a row sees the key
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int hf = k & 1, key = key0 + 16 * p + 8 * (k >> 1) + 2 * t;
-            see[k] = pack_f16(key < lim[hf] ? 1.f : 0.f, key + 1 < lim[hf] ? 1.f : 0.f);
-          }
+          for (int nr = 0; nr < NR; ++nr) {
+            uint32_t see[2];
 #pragma unroll
-          for (int q = 0; q < S::VN / 4; ++q)
-#pragma unroll
-            for (int hb = 0; hb < 4; ++hb) {
-              const uint32_t sel = hb == 0 ? 0x40 : hb == 1 ? 0x51 : hb == 2 ? 0x62 : 0x73;
-              uint32_t b[2], n[2];
-#pragma unroll
-              for (int h2 = 0; h2 < 2; ++h2) {
-                const uint32_t codes = __byte_perm(w[2 * h2][q], w[2 * h2 + 1][q], sel) & 0xffffu;
-                const uint32_t nan = (nan_codes(codes) & 0x8080u) >> 7;   // 1 per NaN code
-                b[h2] = f16x2_of_e4m3x2(codes & ~(nan * 0xffu));
-                n[h2] = ((nan & 1u) ? 0x3c00u : 0u) | ((nan & 0x100u) ? 0x3c000000u : 0u);
-              }
-              float hit[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(o[4 * q + hb], a0, a1, a2, a3, b[0], b[1]);
-              mma_f16(hit, see[0], see[1], see[2], see[3], n[0], n[1]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (hit[e] > 0.f) o[4 * q + hb][e] = __int_as_float(0x7fc00000);
+            for (int h = 0; h < 2; ++h) {
+              const int key = key0 + 16 * p + 8 * h + 2 * t;
+              see[h] = pack_f16(key < lim_g[nr] ? 1.f : 0.f, key + 1 < lim_g[nr] ? 1.f : 0.f);
             }
+#pragma unroll
+            for (int q = 0; q < S::VN / 4; ++q)
+#pragma unroll
+              for (int hb = 0; hb < 2; ++hb) {
+                uint32_t av[4], an[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {     // a0, a1: keys 2t..; a2, a3: keys 2t + 8..
+                  const uint32_t sel = 0x40u + 0x11u * (2 * hb + (k & 1));
+                  const uint32_t codes = __byte_perm(w[2 * (k >> 1)][q], w[2 * (k >> 1) + 1][q], sel) & 0xffffu;
+                  const uint32_t nan = (nan_codes(codes) & 0x8080u) >> 7;   // 1 per NaN code
+                  av[k] = f16x2_of_e4m3x2(codes & ~(nan * 0xffu));
+                  an[k] = ((nan & 1u) ? 0x3c00u : 0u) | ((nan & 0x100u) ? 0x3c000000u : 0u);
+                }
+                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(o[nr][2 * q + hb], av[0], av[1], av[2], av[3], b[nr][0], b[nr][1]);
+                mma_f16(hit, an[0], an[1], an[2], an[3], see[0], see[1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (hit[e] > 0.f) o[nr][2 * q + hb][e] = __int_as_float(0x7fc00000);
+              }
+          }
         }
       }
     }
@@ -485,42 +568,47 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 
     // ---- join the four warps ----
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-      l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-      // from here on m is the exponent's reference; -inf only where no key was seen (scores
-      // that are all NaN leave the maximum at -inf, but a NaN sum)
-      m[hf] = m[hf] != -INFINITY ? m[hf] - P_SHIFT : l[hf] == 0.f ? -INFINITY : 0.f;
-      if (t == 0) {
-        sm_m[warp][g + 8 * hf] = m[hf];
-        sm_l[warp][g + 8 * hf] = l[hf];
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nr][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        // from here on m is the exponent's reference; -inf only where no key was seen (scores
+        // that are all NaN leave the maximum at -inf, but a NaN sum)
+        m[nr][e] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
+        if (g == 0) {
+          sm_m[warp][8 * nr + 2 * t + e] = m[nr][e];
+          sm_l[warp][8 * nr + 2 * t + e] = x;
+        }
       }
-    }
     __syncthreads();   // all warps are done with their rings: they hold the outputs now
     float* sm_o = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float mx = -INFINITY;
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][g + 8 * hf]);
-      const float f = (m[hf] == -INFINITY ? 0.f : ex2f(m[hf] - mx)) * vs_cur;
-      float* to = sm_o + (warp * ROWS + g + 8 * hf) * S::OUT_LD + t * (D / 4);
-      // o[d] columns 2t, 2t + 1 are values (2t) VN + d and (2t + 1) VN + d
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * nr + 2 * t + e;
+        float mx = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][row]);
+        const bool none = m[nr][e] == -INFINITY;
+        const float f = (none ? 0.f : ex2f(m[nr][e] - mx)) * vs_cur;
+        float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * S::VN;
 #pragma unroll
-        for (int d = 0; d < S::VN; d += 4) {
+        for (int d = 0; d < S::MT; d += 2) {   // tile d: columns 2d and 2d + 1 of the lane's
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (m[hf] != -INFINITY)
-            x = make_float4(o[d][2 * hf + e] * f, o[d + 1][2 * hf + e] * f, o[d + 2][2 * hf + e] * f,
-                            o[d + 3][2 * hf + e] * f);
-          *reinterpret_cast<float4*>(to + e * S::VN + d) = x;
+          if (!none)
+            x = make_float4(o[nr][d][e] * f, o[nr][d][2 + e] * f, o[nr][d + 1][e] * f,
+                            o[nr][d + 1][2 + e] * f);
+          *reinterpret_cast<float4*>(to + 2 * d) = x;
         }
-    }
+      }
     __syncthreads();
     {
       constexpr int TPR = THREADS / ROWS;    // threads a row
-      constexpr int CPT = D / TPR;           // columns a thread
+      constexpr int CPT = D / TPR;           // columns a thread (4 or more)
       const int row = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * CPT;
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -543,120 +631,119 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       const int r = r0 + row;
       if (k0 == 0 && k1 == cur.n) {
         if (r < rows) {
-          const int tok = r / a.group, hd = head * a.group + r % a.group;
-          const long long at = ((long long)s * a.q_tokens + tok) * a.q_heads + hd;
+          const long long at = row_at(a, s, head, r);
           const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
-          uint32_t w[CPT / 2];
 #pragma unroll
-          for (int i = 0; i < CPT / 2; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(mx == -INFINITY ? 0.f : acc[2 * i] * inv,
-                                                           mx == -INFINITY ? 0.f : acc[2 * i + 1] * inv);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int i = 0; i < CPT; i += 4) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i + 2] * inv, acc[i + 3] * inv);
+            uint2 x;
+            x.x = *reinterpret_cast<const uint32_t*>(&lo);
+            x.y = *reinterpret_cast<const uint32_t*>(&hi);
+            *reinterpret_cast<uint2*>(a.out + at * D + c0 + i) = x;
           }
-#pragma unroll
-          for (int i = 0; i < CPT / 8; ++i)
-            *reinterpret_cast<uint4*>(a.out + at * D + c0 + 8 * i) =
-                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           if (a.lse && c0 == 0)
             a.lse[at] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
         }
       } else {
         // part 1 begins in this CTA and goes on in the next; part 0 began in an earlier one
-        float* to = part_of<D>(a, blockIdx.x, k0 == 0 ? 1 : 0);
+        float* to = part_of<D, NR>(a, blockIdx.x, k0 == 0 ? 1 : 0);
 #pragma unroll
-        for (int i = 0; i < CPT; i += 2)
-          *reinterpret_cast<float2*>(to + row * D + c0 + i) = make_float2(acc[i], acc[i + 1]);
+        for (int i = 0; i < CPT; i += 4)
+          *reinterpret_cast<float4*>(to + row * D + c0 + i) =
+              make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
         if (c0 == 0) {
           to[ROWS * D + row] = mx;
           to[ROWS * D + ROWS + row] = sum;
         }
+        if (k0 == 0)
+          begun = make_int4(s, item, kv8_worker_of(total, workers, cur.base + (item + 1LL) * cur.n - 1), 1);
       }
     }
     __syncthreads();   // before the rings are filled again
-    u += k1 - k0;
+    u += whole ? 1 : k1 - k0;
   }
+  if (!whole && threadIdx.x == 0) a.split[blockIdx.x] = begun;
 }
 
-// Joins the items that were split: the CTA in whose share such an item begins reads its parts in
-// order. One thread per (row, 4 columns).
-template <int D>
-__global__ void __launch_bounds__(ROWS * D / 4) k_combine(Kv8View c, Args a, int grid_main) {
-  using S = Shape<D>;
-  const long long total = total_units(c, a, S::UNIT, nullptr);
-  const int workers = workers_of(total, grid_main);
+// Joins the items that were split: the parts of an item lie with consecutive CTAs, the first of
+// which notes them. Four columns of one row a thread.
+template <int D, int NR>
+__global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a) {
+  constexpr int ROWS = Shape<D, NR>::ROWS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are there
   const int w0 = blockIdx.x;
-  if (w0 >= workers) return;
-  const long long u_begin = kv8_share(total, workers, w0), u_end = kv8_share(total, workers, w0 + 1);
-  Cursor cur{0, 0, 0, 0};
-  seek(c, a, S::UNIT, u_end - 1, cur);
-  const long long in = u_end - 1 - cur.base;
-  const int item = (int)(in / cur.n);
-  const long long i_begin = cur.base + (long long)item * cur.n, i_end = i_begin + cur.n;
-  if (i_begin < u_begin || i_end <= u_end) return;   // begins earlier, or ends here
-  const int w1 = kv8_worker_of(total, workers, i_end - 1);
-  const int row = threadIdx.x / (D / 4), c0 = (threadIdx.x % (D / 4)) * 4;
-  const int head = item / a.tiles, r = (item % a.tiles) * ROWS + row;
+  const int4 split = a.split[w0];
+  if (!split.w) return;
+  const int row = blockIdx.y * (512 / D) + threadIdx.x / (D / 4), c0 = (threadIdx.x % (D / 4)) * 4;
+  const int s = split.x, head = split.y / a.tiles, r = (split.y % a.tiles) * ROWS + row;
   if (r >= a.q_tokens * a.group) return;
+  const int n = split.z - w0 + 1;
+  // part k: the second of CTA w0, the first of each further one
+  auto part = [&](int k) { return part_of<D, NR>(a, w0 + k, k == 0); };
   float mx = -INFINITY;
-  for (int w = w0; w <= w1; ++w) mx = fmaxf(mx, part_of<D>(a, w, w == w0)[ROWS * D + row]);
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) mx = fmaxf(mx, part(k)[ROWS * D + row]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  if (mx != -INFINITY) {
-    for (int w = w0; w <= w1; ++w) {
-      const float* p = part_of<D>(a, w, w == w0);
-      const float pm = p[ROWS * D + row];
-      if (pm == -INFINITY) continue;
-      const float f = ex2f(pm - mx);
-      const float2 x = *reinterpret_cast<const float2*>(p + row * D + c0);
-      const float2 y = *reinterpret_cast<const float2*>(p + row * D + c0 + 2);
-      sum = fmaf(p[ROWS * D + ROWS + row], f, sum);
-      acc.x = fmaf(x.x, f, acc.x); acc.y = fmaf(x.y, f, acc.y);
-      acc.z = fmaf(y.x, f, acc.z); acc.w = fmaf(y.y, f, acc.w);
-    }
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float* p = part(k);
+    const float pm = p[ROWS * D + row];
+    const float f = pm == -INFINITY ? 0.f : ex2f(pm - mx);   // a part that saw no key holds zeros
+    const float4 x = *reinterpret_cast<const float4*>(p + row * D + c0);
+    sum = fmaf(p[ROWS * D + ROWS + row], f, sum);
+    acc.x = fmaf(x.x, f, acc.x); acc.y = fmaf(x.y, f, acc.y);
+    acc.z = fmaf(x.z, f, acc.z); acc.w = fmaf(x.w, f, acc.w);
   }
-  const int tok = r / a.group, hd = head * a.group + r % a.group;
-  const long long at = ((long long)cur.s * a.q_tokens + tok) * a.q_heads + hd;
+  const long long at = row_at(a, s, head, r);
   const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 o2;
-  o2.x = *reinterpret_cast<const uint32_t*>(&lo);
-  o2.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(a.out + at * D + c0) = o2;
+  uint2 x;
+  x.x = *reinterpret_cast<const uint32_t*>(&lo);
+  x.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(a.out + at * D + c0) = x;
   if (a.lse && c0 == 0)
     a.lse[at] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
 }
 
-int tiles_of(int q_tokens, int group) { return (q_tokens * group + ROWS - 1) / ROWS; }
+// Bytes of the split notes at the head of the workspace.
+size_t notes_bytes(int num_sms) { return (size_t)num_sms * CTAS_PER_SM * sizeof(int4); }
 
-// CTAs of a call: every SM's slots, or the units there can be if they are fewer.
-int grid_of(int tiles, int heads, int batch, long long max_units, int num_sms) {
-  const long long slots = (long long)num_sms * CTAS_PER_SM;
-  const long long most = max_units > slots ? slots : max_units * heads * tiles * batch;
-  return (int)(most < slots ? (most < 1 ? 1 : most) : slots);
-}
-
-template <int D>
-cudaError_t launch(const Kv8View& c, const Args& a, int* err_flag, int num_sms, cudaStream_t s) {
-  using S = Shape<D>;
+template <int D, int NR>
+cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStream_t s) {
+  using S = Shape<D, NR>;
   static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = set_max_dynamic_smem((const void*)k_attention_kv8<D>, S::SMEM, attr_done);
+  cudaError_t e = set_max_dynamic_smem((const void*)k_attention_kv8<D, NR>, S::SMEM, attr_done);
   if (e != cudaSuccess) return e;
+  a.tiles = (a.q_tokens * a.group + S::ROWS - 1) / S::ROWS;
   const long long max_len = (long long)c.max_pages << c.page_log2;
-  const int grid = grid_of(a.tiles, c.heads, c.batch, (max_len + S::UNIT - 1) / S::UNIT, num_sms);
-  k_attention_kv8<D><<<grid, THREADS, S::SMEM, s>>>(c, a, err_flag);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (max_len > S::UNIT) {   // otherwise every item is one unit and none is split
-    k_combine<D><<<grid, ROWS * D / 4, 0, s>>>(c, a, grid);
-    e = cudaGetLastError();
-  }
-  return e;
+  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT, slots = (long long)num_sms * CTAS_PER_SM;
+  const long long items = (long long)c.batch * c.heads * a.tiles;
+  const int whole = max_units <= WHOLE_UNITS;
+  // every SM's slots, or the work there can be if that is less
+  const long long work = whole ? items : max_units > slots ? slots : items * max_units;
+  const int grid = (int)(work < slots ? work : slots);
+  k_attention_kv8<D, NR><<<grid, THREADS, S::SMEM, s>>>(c, a, whole, err_flag);
+  if ((e = cudaGetLastError()) != cudaSuccess || whole) return e;
+  // set up while the first kernel runs; it waits for that kernel's end before it reads
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, S::ROWS * D / 512);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_combine<D, NR>, c, a);
 }
 
 }  // namespace
 
 size_t attention_kv8_workspace(int dim, int num_sms) {
-  return (size_t)num_sms * CTAS_PER_SM * 2 * ROWS * (dim + 2) * sizeof(float);
+  return notes_bytes(num_sms) + (size_t)num_sms * CTAS_PER_SM * 2 * 16 * (dim + 2) * sizeof(float);
 }
 
 cudaError_t attention_kv8(const Kv8View& c, const bf16* q, int q_tokens, int q_heads,
@@ -667,15 +754,19 @@ cudaError_t attention_kv8(const Kv8View& c, const bf16* q, int q_tokens, int q_h
   a.kv_len = kv_len;
   a.out = out;
   a.lse = lse;
-  a.part = (float*)workspace;
+  a.split = (int4*)workspace;
+  a.part = (float*)((uint8_t*)workspace + notes_bytes(num_sms));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.q_tokens = q_tokens;
   a.q_heads = q_heads;
   a.group = q_heads / c.heads;
-  a.tiles = tiles_of(q_tokens, a.group);
+  a.tiles = 0;
   a.causal = causal;
-  if (c.dim == 64) return launch<64>(c, a, err_flag, num_sms, s);
-  if (c.dim == 128) return launch<128>(c, a, err_flag, num_sms, s);
+  const bool narrow = q_tokens * a.group <= 8;
+  if (c.dim == 64)
+    return narrow ? launch<64, 1>(c, a, err_flag, num_sms, s) : launch<64, 2>(c, a, err_flag, num_sms, s);
+  if (c.dim == 128)
+    return narrow ? launch<128, 1>(c, a, err_flag, num_sms, s) : launch<128, 2>(c, a, err_flag, num_sms, s);
   return cudaErrorInvalidValue;
 }
 
