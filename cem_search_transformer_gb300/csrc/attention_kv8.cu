@@ -36,10 +36,11 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int NST = 4;              // cp.async stages of a warp
+constexpr int NST = 3;              // cp.async stages of a warp
 constexpr int CTAS_PER_SM = 3;
 constexpr int MIN_UNITS = 4;        // units a CTA takes at least where items are split
 constexpr int WHOLE_UNITS = 8;      // items up to this many units are not split
+constexpr int ITEM_UNITS = 2;       // what an item costs besides its units: start and joining
 
 // Probabilities are 2^(s - m + P_SHIFT) for the running reference m, which trails the maximum by
 // P_SLACK at most: up to 2^15 as f16, so that the many small weights of a long context keep
@@ -56,9 +57,10 @@ struct Shape {
   static constexpr int VN = D / 8;                 // values of a V row a lane takes
   static constexpr int MT = D / 16;                // output tiles of 16 columns
   static constexpr int STAGE = 2 * KS * D;         // K and V codes
+  static constexpr int OUT_LD = D + 4;             // fp32 row of a warp's output for the joining
   static constexpr int OFF_SCALE = WARPS * NST * STAGE;
-  static constexpr int SMEM = OFF_SCALE + WARPS * NST * 16;
-  static constexpr int OUT_LD = D + 4;             // fp32 row of a partial in shared memory
+  static constexpr int OFF_OUT = OFF_SCALE + WARPS * NST * 16;
+  static constexpr int SMEM = OFF_OUT + WARPS * ROWS * OUT_LD * 4;
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -142,20 +144,22 @@ __device__ __forceinline__ int length_of(const Kv8View& c, const Args& a, int s,
 __device__ __forceinline__ int units_of(int len, int unit) {
   return len > 0 ? (len + unit - 1) / unit : 1;   // an empty sequence has its (zero) rows written
 }
+// Places of an item in the line: ITEM_UNITS for its start and end, then its units.
+__device__ __forceinline__ int places_of(int len, int unit) { return units_of(len, unit) + ITEM_UNITS; }
 
-// The line of units: sequence by sequence, each with heads * tiles items of units_of(len) units.
+// The line: sequence by sequence, each with heads * tiles items of places_of(len) places.
 // Totals by one warp (every warp of the CTA computes the same).
-__device__ __forceinline__ long long total_units(const Kv8View& c, const Args& a, int unit,
+__device__ __forceinline__ long long total_places(const Kv8View& c, const Args& a, int unit,
                                                  int* err_flag) {
   const int lane = threadIdx.x & 31;
   long long n = 0;
-  for (int s = lane; s < c.batch; s += 32) n += units_of(length_of(c, a, s, err_flag), unit);
+  for (int s = lane; s < c.batch; s += 32) n += places_of(length_of(c, a, s, err_flag), unit);
 #pragma unroll
   for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n * c.heads * a.tiles;
 }
 
-// Position in the line: sequence s whose items begin at unit `base`, of `n` units each.
+// Position in the line: sequence s whose items begin at place `base`, of `n` places each.
 struct Cursor {
   int s, n, len;
   long long base;
@@ -168,7 +172,7 @@ __device__ __forceinline__ void seek(const Kv8View& c, const Args& a, int unit, 
   for (int s0 = at.s; s0 < c.batch; s0 += 32) {
     const int s = s0 + lane;
     const int len = s < c.batch ? length_of(c, a, s, nullptr) : 0;
-    const int n = s < c.batch ? units_of(len, unit) : 0;
+    const int n = s < c.batch ? places_of(len, unit) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -189,7 +193,7 @@ __device__ __forceinline__ void seek(const Kv8View& c, const Args& a, int unit, 
   at.s = c.batch;
 }
 
-// CTAs that take part in a split line: each has MIN_UNITS units at least.
+// CTAs that take part in a split line: each has MIN_UNITS places at least.
 __device__ __forceinline__ int workers_of(long long total, int grid) {
   const long long w = (total + MIN_UNITS - 1) / MIN_UNITS;
   return w < grid ? (int)w : grid;
@@ -206,6 +210,48 @@ __device__ __forceinline__ long long row_at(const Args& a, int s, int head, int 
   return ((long long)s * a.q_tokens + tok) * a.q_heads + head * a.group + (r - tok * a.group);
 }
 
+// Units [k0, k1) of n of one item: what a CTA does before it goes on to the next.
+struct Segment {
+  int s, item, len, n, k0, k1;
+  long long next;      // place in the line where the CTA's next segment begins
+  long long last;      // the item's last place
+};
+
+template <int UNIT>
+__device__ __forceinline__ bool plan(const Kv8View& c, const Args& a, int whole, long long u,
+                                     long long u_end, Cursor& cur, Segment& g) {
+  if (whole) {
+    if (u >= u_end) return false;
+    const int per = c.heads * a.tiles;
+    g.s = (int)(u / per);
+    g.item = (int)(u % per);
+    g.len = length_of(c, a, g.s, nullptr);
+    g.n = units_of(g.len, UNIT);
+    g.k0 = 0;
+    g.k1 = g.n;
+    g.next = u + 1;
+    return true;
+  }
+  while (u < u_end) {
+    seek(c, a, UNIT, u, cur);
+    const long long in = u - cur.base;
+    const int item = (int)(in / cur.n), at = (int)(in % cur.n);
+    const int to = (int)min((long long)cur.n, at + (u_end - u));
+    u += to - at;
+    if (to <= ITEM_UNITS) continue;              // nothing but the item's start
+    g.s = cur.s;
+    g.item = item;
+    g.len = cur.len;
+    g.n = cur.n - ITEM_UNITS;
+    g.k0 = max(at - ITEM_UNITS, 0);
+    g.k1 = to - ITEM_UNITS;
+    g.next = u;
+    g.last = cur.base + (item + 1LL) * cur.n - 1;
+    return true;
+  }
+  return false;
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     k_attention_kv8(Kv8View c, Args a, int whole, int* err_flag) {
@@ -220,18 +266,19 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   const uint32_t ring_sc =
       (uint32_t)__cvta_generic_to_shared(smem) + S::OFF_SCALE + warp * (NST * 16);
   const float* ring_sc_ptr = reinterpret_cast<const float*>(smem + S::OFF_SCALE) + warp * NST * 4;
+  float* const sm_o = reinterpret_cast<float*>(smem + S::OFF_OUT);
 
   int* const flag0 = blockIdx.x == 0 ? err_flag : nullptr;
   long long u_begin, u_end, total = 0;
   int workers = 0;
   if (whole) {
-    // items in equal numbers; `units` below then count items of one unit each
+    // items in equal numbers, a place each
     const long long items = (long long)c.batch * c.heads * a.tiles;
     u_begin = kv8_share(items, gridDim.x, blockIdx.x);
     u_end = kv8_share(items, gridDim.x, blockIdx.x + 1);
-    if (flag0 && warp == 0) total_units(c, a, S::UNIT, flag0);   // reports lengths out of range
+    if (flag0 && warp == 0) total_places(c, a, S::UNIT, flag0);   // reports lengths out of range
   } else {
-    total = total_units(c, a, S::UNIT, flag0);
+    total = total_places(c, a, S::UNIT, flag0);
     workers = workers_of(total, gridDim.x);
     if ((int)blockIdx.x >= workers) {
       if (threadIdx.x == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -241,82 +288,74 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     u_end = kv8_share(total, workers, blockIdx.x + 1);
   }
   int4 begun = make_int4(0, 0, 0, 0);
-  Cursor cur{0, 0, 0, 0};
   const int rows = a.q_tokens * a.group;
   const long long v_ahead = c.v - c.k;         // bytes from a key's codes to its value's
 
-  for (long long u = u_begin; u < u_end;) {
-    int item, k0, k1;                          // units [k0, k1) of the item
-    if (whole) {
-      const int per = c.heads * a.tiles;
-      cur.s = (int)(u / per);
-      item = (int)(u % per);
-      cur.len = length_of(c, a, cur.s, nullptr);
-      cur.n = units_of(cur.len, S::UNIT);
-      k0 = 0;
-      k1 = cur.n;
-    } else {
-      seek(c, a, S::UNIT, u, cur);
-      const long long in = u - cur.base;
-      item = (int)(in / cur.n);
-      k0 = (int)(in % cur.n);
-      k1 = (int)min((long long)cur.n, k0 + (u_end - u));
+  // ---- loading: the warp's steps of all segments in one stream, NST - 1 ahead of their use ----
+  constexpr int CPR = D / 16;                  // 16-byte chunks of a row
+  constexpr int RPI = 32 / CPR;                // rows a warp copies in one instruction
+  const int chunk = lane % CPR, sub = lane / CPR;
+  Cursor load_cur{0, 0, 0, 0};
+  Segment ld;
+  int ld_step = 0, ld_stage = 0;
+  bool ld_more = plan<S::UNIT>(c, a, whole, u_begin, u_end, load_cur, ld);
+  int pg_next[S::GROUPS];                      // pages of the step that is issued next
+  auto fetch_pages = [&]() {
+#pragma unroll
+    for (int p = 0; p < S::GROUPS; ++p) {
+      const int key = (ld.k0 + ld_step) * S::UNIT + warp * S::KS + 16 * p;
+      pg_next[p] = ld_more && key < ld.len
+                       ? __ldg(c.table + (long long)ld.s * c.max_pages + (key >> c.page_log2))
+                       : -1;
     }
-    const int head = item / a.tiles, r0 = (item % a.tiles) * ROWS;
-    const int s = cur.s, len = cur.len;
-    const int* const table = c.table + (long long)s * c.max_pages;
-
-    // ---- the warp's share of the keys: steps k0 .. k1 - 1, KS keys each ----
-    const int steps = k1 - k0;
-    const int key_first = k0 * S::UNIT + warp * S::KS;
-    constexpr int CPR = D / 16;                // 16-byte chunks of a row
-    constexpr int RPI = 32 / CPR;              // rows a warp copies in one instruction
-    const int chunk = lane % CPR, sub = lane / CPR;
-    int pg_next[S::GROUPS];                    // pages of the step that is issued next
-    auto fetch_pages = [&](int i) {
+  };
+  auto issue = [&]() {                         // the next step of the stream into the next stage
+    const int key0 = (ld.k0 + ld_step) * S::UNIT + warp * S::KS;
+    if (ld_more && key0 < ld.len) {
+      const uint32_t st = ring + ld_stage * S::STAGE;
+      const int head = ld.item / a.tiles;
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
-        const int key = key_first + i * S::UNIT + 16 * p;
-        pg_next[p] = i < steps && key < len ? __ldg(table + (key >> c.page_log2)) : -1;
-      }
-    };
-    auto issue = [&](int i) {   // step i into stage i % NST
-      const uint32_t st = ring + (i % NST) * S::STAGE;
-      const int key0 = key_first + i * S::UNIT;
-      if (i < steps && key0 < len) {
+        const bool page_ok = pg_next[p] >= 0 && pg_next[p] < c.num_pages;
+        const int pg = page_ok ? pg_next[p] : 0, key_p = key0 + 16 * p;
+        const int keys = page_ok ? min(16, ld.len - key_p) : 0;      // of this group that are there
+        const long long block = (long long)pg * c.heads + head;
+        const uint8_t* from = c.k + (block * c.page + (key_p & (c.page - 1)) + sub) * D + 16 * chunk;
 #pragma unroll
-        for (int p = 0; p < S::GROUPS; ++p) {
-          const bool page_ok = pg_next[p] >= 0 && pg_next[p] < c.num_pages;
-          const int pg = page_ok ? pg_next[p] : 0, key_p = key0 + 16 * p;
-          const int keys = page_ok ? min(16, len - key_p) : 0;      // of this group that are there
-          const long long block = (long long)pg * c.heads + head;
-          const uint8_t* from =
-              c.k + (block * c.page + (key_p & (c.page - 1)) + sub) * D + 16 * chunk;
-#pragma unroll
-          for (int q = 0; q < 16 / RPI; ++q) {
-            const int row = 16 * p + q * RPI + sub;
-            const int sw = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-            const uint32_t to = st + row * D + 16 * sw;
-            const uint32_t bytes = q * RPI + sub < keys ? 16 : 0;
-            cp16(to, from + q * RPI * D, bytes);
-            cp16(to + S::KS * D, from + v_ahead + q * RPI * D, bytes);
-          }
-          if (lane < 2) {
-            if (!page_ok && key_p < len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
-            cp4(ring_sc + (i % NST) * 16 + (2 * p + lane) * 4, (lane ? c.v_scale : c.k_scale) + block,
-                page_ok ? 4 : 0);
-          }
+        for (int q = 0; q < 16 / RPI; ++q) {
+          const int row = 16 * p + q * RPI + sub;
+          const int sw = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+          const uint32_t to = st + row * D + 16 * sw;
+          const uint32_t bytes = q * RPI + sub < keys ? 16 : 0;
+          cp16(to, from + q * RPI * D, bytes);
+          cp16(to + S::KS * D, from + v_ahead + q * RPI * D, bytes);
+        }
+        if (lane < 2) {
+          if (!page_ok && key_p < ld.len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+          cp4(ring_sc + ld_stage * 16 + (2 * p + lane) * 4, (lane ? c.v_scale : c.k_scale) + block,
+              page_ok ? 4 : 0);
         }
       }
-      cp_commit();
-    };
-    fetch_pages(0);
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i) {
-      issue(i);
-      fetch_pages(i + 1);
     }
+    cp_commit();
+    ld_stage = ld_stage + 1 == NST ? 0 : ld_stage + 1;
+    if (ld_more && ++ld_step == ld.k1 - ld.k0) {
+      ld_step = 0;
+      ld_more = plan<S::UNIT>(c, a, whole, ld.next, u_end, load_cur, ld);
+    }
+    fetch_pages();
+  };
+  fetch_pages();
+#pragma unroll 1
+  for (int i = 0; i < NST - 1; ++i) issue();
 
+  int stage = 0;
+  Cursor cur{0, 0, 0, 0};
+  Segment sg;
+  sg.next = u_begin;
+  while (plan<S::UNIT>(c, a, whole, sg.next, u_end, cur, sg)) {
+    const int s = sg.s, len = sg.len, item = sg.item;
+    const int head = item / a.tiles, r0 = (item % a.tiles) * ROWS;
     // ---- queries: row g of each 8-row tile as f16, times 2^-e so that |q| < 2^15 ----
     uint32_t qf[NR][S::KW][2];
     float qs[NR][2];       // of rows 2t, 2t + 1: 2^e * softmax scale * log2(e)
@@ -370,16 +409,16 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     }
     float vs_cur = 0.f;    // outputs are o * vs_cur; 0 before the first key
 
-    for (int i = 0; i < steps; ++i) {
+    for (int k = sg.k0; k < sg.k1; ++k) {
       cp_wait<NST - 2>();
       __syncwarp();
-      issue(i + NST - 1);
-      fetch_pages(i + NST);
-      const int key0 = key_first + i * S::UNIT;
-      if (key0 >= len) continue;
-      const uint8_t* kb = ring_ptr + (i % NST) * S::STAGE;
+      issue();                         // into the stage that the step before this one has read
+      const int key0 = k * S::UNIT + warp * S::KS;
+      const uint8_t* kb = ring_ptr + stage * S::STAGE;
       const uint8_t* vb = kb + S::KS * D;
-      const float* scales = ring_sc_ptr + (i % NST) * 4;
+      const float* scales = ring_sc_ptr + stage * 4;
+      stage = stage + 1 == NST ? 0 : stage + 1;
+      if (key0 >= len) continue;
 
       // scores of keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
       float sc[S::GROUPS][NR][4];
@@ -564,9 +603,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         }
       }
     }
-    cp_wait<0>();
-
     // ---- join the four warps ----
+    __syncthreads();   // the joining before this one has been read
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -575,61 +613,48 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
-        // from here on m is the exponent's reference; -inf only where no key was seen (scores
-        // that are all NaN leave the maximum at -inf, but a NaN sum)
-        m[nr][e] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
-        if (g == 0) {
-          sm_m[warp][8 * nr + 2 * t + e] = m[nr][e];
-          sm_l[warp][8 * nr + 2 * t + e] = x;
-        }
-      }
-    __syncthreads();   // all warps are done with their rings: they hold the outputs now
-    float* sm_o = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
         const int row = 8 * nr + 2 * t + e;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][row]);
-        const bool none = m[nr][e] == -INFINITY;
-        const float f = (none ? 0.f : ex2f(m[nr][e] - mx)) * vs_cur;
+        if (g == 0) {
+          // from here on m is the exponent's reference; -inf only where no key was seen (scores
+          // that are all NaN leave the maximum at -inf, but a NaN sum)
+          sm_m[warp][row] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
+          sm_l[warp][row] = x;
+        }
         float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * S::VN;
 #pragma unroll
-        for (int d = 0; d < S::MT; d += 2) {   // tile d: columns 2d and 2d + 1 of the lane's
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!none)
-            x = make_float4(o[nr][d][e] * f, o[nr][d][2 + e] * f, o[nr][d + 1][e] * f,
-                            o[nr][d + 1][2 + e] * f);
-          *reinterpret_cast<float4*>(to + 2 * d) = x;
-        }
+        for (int d = 0; d < S::MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
+          *reinterpret_cast<float4*>(to + 2 * d) =
+              make_float4(o[nr][d][e] * vs_cur, o[nr][d][2 + e] * vs_cur, o[nr][d + 1][e] * vs_cur,
+                          o[nr][d + 1][2 + e] * vs_cur);
       }
     __syncthreads();
     {
       constexpr int TPR = THREADS / ROWS;    // threads a row
       constexpr int CPT = D / TPR;           // columns a thread (4 or more)
       const int row = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * CPT;
-      float mx = -INFINITY, sum = 0.f;
+      float mx = -INFINITY, sum = 0.f, f[WARPS];
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sm_m[w][row]);
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w)
-        sum += sm_m[w][row] == -INFINITY ? 0.f : sm_l[w][row] * ex2f(sm_m[w][row] - mx);
+      for (int w = 0; w < WARPS; ++w) {
+        f[w] = sm_m[w][row] == -INFINITY ? 0.f : ex2f(sm_m[w][row] - mx);   // its outputs are zeros
+        sum = fmaf(sm_l[w][row], f[w], sum);
+      }
       float acc[CPT];
 #pragma unroll
       for (int i = 0; i < CPT; i += 4) {
-        float4 x = *reinterpret_cast<const float4*>(sm_o + row * S::OUT_LD + c0 + i);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
           const float4 y =
               *reinterpret_cast<const float4*>(sm_o + (w * ROWS + row) * S::OUT_LD + c0 + i);
-          x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+          x.x = fmaf(y.x, f[w], x.x); x.y = fmaf(y.y, f[w], x.y);
+          x.z = fmaf(y.z, f[w], x.z); x.w = fmaf(y.w, f[w], x.w);
         }
         acc[i] = x.x; acc[i + 1] = x.y; acc[i + 2] = x.z; acc[i + 3] = x.w;
       }
       const int r = r0 + row;
-      if (k0 == 0 && k1 == cur.n) {
+      if (sg.k0 == 0 && sg.k1 == sg.n) {
         if (r < rows) {
           const long long at = row_at(a, s, head, r);
           const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
@@ -647,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         }
       } else {
         // part 1 begins in this CTA and goes on in the next; part 0 began in an earlier one
-        float* to = part_of<D, NR>(a, blockIdx.x, k0 == 0 ? 1 : 0);
+        float* to = part_of<D, NR>(a, blockIdx.x, sg.k0 == 0 ? 1 : 0);
 #pragma unroll
         for (int i = 0; i < CPT; i += 4)
           *reinterpret_cast<float4*>(to + row * D + c0 + i) =
@@ -656,46 +681,54 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
           to[ROWS * D + row] = mx;
           to[ROWS * D + ROWS + row] = sum;
         }
-        if (k0 == 0)
-          begun = make_int4(s, item, kv8_worker_of(total, workers, cur.base + (item + 1LL) * cur.n - 1), 1);
+        if (sg.k0 == 0) begun = make_int4(s, item, kv8_worker_of(total, workers, sg.last), 1);
       }
     }
-    __syncthreads();   // before the rings are filled again
-    u += whole ? 1 : k1 - k0;
   }
+  cp_wait<0>();
   if (!whole && threadIdx.x == 0) a.split[blockIdx.x] = begun;
 }
 
 // Joins the items that were split: the parts of an item lie with consecutive CTAs, the first of
-// which notes them. Four columns of one row a thread.
+// which notes them. D / 4 lanes a row; they read all maxima side by side and then the outputs,
+// eight parts in flight: one after the other, 28 parts took 20 us.
 template <int D, int NR>
-__global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a) {
-  constexpr int ROWS = Shape<D, NR>::ROWS;
+__global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a, int max_parts) {
+  constexpr int ROWS = Shape<D, NR>::ROWS, LPR = D / 4, RPB = 128 / LPR;
+  extern __shared__ float factors[];                   // [RPB][max_parts]
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are there
   const int w0 = blockIdx.x;
   const int4 split = a.split[w0];
   if (!split.w) return;
-  const int row = blockIdx.y * (512 / D) + threadIdx.x / (D / 4), c0 = (threadIdx.x % (D / 4)) * 4;
+  const int sub = threadIdx.x / LPR, li = threadIdx.x % LPR, row = blockIdx.y * RPB + sub, c0 = li * 4;
   const int s = split.x, head = split.y / a.tiles, r = (split.y % a.tiles) * ROWS + row;
-  if (r >= a.q_tokens * a.group) return;
-  const int n = split.z - w0 + 1;
+  const int n = split.z - w0 + 1;                      // at most max_parts = CTAs of the call
+  float* const f = factors + sub * max_parts;
   // part k: the second of CTA w0, the first of each further one
   auto part = [&](int k) { return part_of<D, NR>(a, w0 + k, k == 0); };
-  float mx = -INFINITY;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) mx = fmaxf(mx, part(k)[ROWS * D + row]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* p = part(k);
-    const float pm = p[ROWS * D + row];
-    const float f = pm == -INFINITY ? 0.f : ex2f(pm - mx);   // a part that saw no key holds zeros
-    const float4 x = *reinterpret_cast<const float4*>(p + row * D + c0);
-    sum = fmaf(p[ROWS * D + ROWS + row], f, sum);
-    acc.x = fmaf(x.x, f, acc.x); acc.y = fmaf(x.y, f, acc.y);
-    acc.z = fmaf(x.z, f, acc.z); acc.w = fmaf(x.w, f, acc.w);
+  float mx = -INFINITY, sum = 0.f;
+  for (int k = li; k < n; k += LPR) {
+    f[k] = part(k)[ROWS * D + row];
+    mx = fmaxf(mx, f[k]);
   }
+#pragma unroll
+  for (int o = LPR / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int k = li; k < n; k += LPR) {
+    const float x = f[k] == -INFINITY ? 0.f : ex2f(f[k] - mx);   // a part that saw no key holds zeros
+    f[k] = x;
+    sum = fmaf(part(k)[ROWS * D + ROWS + row], x, sum);
+  }
+#pragma unroll
+  for (int o = LPR / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncwarp();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(part(k) + row * D + c0);
+    acc.x = fmaf(x.x, f[k], acc.x); acc.y = fmaf(x.y, f[k], acc.y);
+    acc.z = fmaf(x.z, f[k], acc.z); acc.w = fmaf(x.w, f[k], acc.w);
+  }
+  if (r >= a.q_tokens * a.group) return;
   const long long at = row_at(a, s, head, r);
   const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
@@ -734,10 +767,11 @@ cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, S::ROWS * D / 512);
   cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = (512 / D) * grid * sizeof(float);   // 15 KB at most
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_combine<D, NR>, c, a);
+  return cudaLaunchKernelEx(&cfg, k_combine<D, NR>, c, a, grid);
 }
 
 }  // namespace
