@@ -182,13 +182,49 @@ def _arg(t, name: str, kind: str, numel: int, host_ok: bool = False,
     return t.data_ptr()
 
 
-def _rows(t, name: str):
-    """(address, elements between tokens) of token rows [tokens, heads, head_dim]: a bf16 CUDA
-    tensor whose heads lie back to back (a slice of a wider projection's rows is fine)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+class _Fast:
+    """What the single-token entry points look up on every call, fetched once: a serving step
+    makes a few such calls a layer, and its kernels take microseconds."""
+
+    torch = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.u8 = frozenset(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if d)
+        cls.bf16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+        cls.f32, cls.i32 = frozenset((torch.float32,)), frozenset((torch.int32,))
+        cls.kinds = {"u8": cls.u8, "bf16": cls.bf16, "f32": cls.f32, "i32": cls.i32}
+        # the stream's address without a Stream object around it, where torch has that
+        cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cls.Tensor = torch.Tensor
+        cls.torch = torch
+
+
+def _dev(t, name: str, kind: str, numel: int, device: int) -> int:
+    """Address of the device tensor `t`, checked as in _arg and for its device."""
+    if (isinstance(t, _Fast.Tensor) and t.dtype in _Fast.kinds[kind] and t.get_device() == device
+            and t.is_contiguous() and t.numel() >= numel):
+        return t.data_ptr()
+    at = _arg(t, name, kind, numel)
+    if isinstance(t, _Fast.Tensor):
+        raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{device}")
+    return at
+
+
+def _opt(t, name: str, kind: str, numel: int, device: int) -> Optional[int]:
+    return None if t is None else _dev(t, name, kind, numel, device)
+
+
+def _rows(t, name: str, device: Optional[int] = None):
+    """(address, elements between tokens, tokens, heads, head_dim) of token rows [tokens, heads,
+    head_dim]: a bf16 CUDA tensor whose heads lie back to back (a slice of a wider projection's
+    rows is fine)."""
+    if _Fast.torch is None:
+        _Fast.load()
+    if not isinstance(t, _Fast.Tensor) or t.dim() != 3:
         raise JepaError(1, f"{name}: expected a tensor [tokens, heads, head_dim]")
-    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+    if t.dtype not in _Fast.bf16:
         raise JepaError(1, f"{name}: dtype {t.dtype} where bf16 is required")
     n, heads, dim = t.shape
     st = t.stride()
@@ -196,7 +232,9 @@ def _rows(t, name: str):
         raise JepaError(1, f"{name}: the heads of a token must be contiguous")
     if not t.is_cuda:
         raise JepaError(1, f"{name} must be a CUDA tensor")
-    return t.data_ptr(), (st[0] if n > 1 else heads * dim)
+    if device is not None and t.get_device() != device:
+        raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{device}")
+    return t.data_ptr(), (st[0] if n > 1 else heads * dim), n, heads, dim
 
 
 class KvCache8:
@@ -207,6 +245,8 @@ class KvCache8:
     float32 [num_pages, kv_heads]; page_table: int32 [batch, max_pages]."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
+        if _Fast.torch is None:
+            _Fast.load()
         if getattr(k, "ndim", 0) != 4 or getattr(page_table, "ndim", 0) != 2:
             raise JepaError(1, "KvCache8: k must be [num_pages, kv_heads, page_size, head_dim] and "
                                "page_table [batch, max_pages]")
@@ -231,12 +271,18 @@ class KvCache8:
             _arg(page_table, "page_table", "i32", batch * max_pages), pages, page, heads, dim, batch,
             max_pages)
         self.ref = ctypes.byref(self.struct)
+        self.index = k.get_device()
+
+    def check(self, device: int):
+        """Raises unless the cache lives on this device."""
+        if self.index != device:
+            raise JepaError(1, f"cache is on {self.device}, the planner on cuda:{device}")
 
 
-def _stream(stream, device=None) -> Optional[int]:
+def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -256,6 +302,15 @@ def energy_l1_noalloc(z_pred, goal, B, N, P, E, energy, stream=None):
     st = lib.jepa_energy_l1_noalloc(zp, gp, B, N, P, E, ep, _stream(stream), buf, len(buf))
     if st != JEPA_OK:
         raise JepaError(st, buf.value.decode())
+
+
+def _stream_on(stream, device: int) -> int:
+    """The given stream, or the device's current one."""
+    if stream is None:
+        if _Fast.raw_stream is not None:
+            return _Fast.raw_stream(device)
+        return _Fast.torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 class Planner:
@@ -453,67 +508,65 @@ class Planner:
 
     # ---- 8-bit paged key/value cache and the attention around it (see the C header) ----
 
-    def _on(self, **tensors):
-        """Tensors (or None) that must live on this planner's device."""
-        for name, t in tensors.items():
-            if t is not None and t.device.index != self.device:
-                raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{self.device}")
-
     def rope_table(self, positions, rot, base=10000.0, factor=1.0, table=None, stream=None):
         """cos / sin table [positions, rot] for rope_append_kv8 (allocated when not given)."""
         self._dims(positions=positions, rot=rot)
+        if _Fast.torch is None:
+            _Fast.load()
         if table is None:
-            import torch
-            table = torch.empty(positions, rot, device=f"cuda:{self.device}")
-        self._on(table=table)
-        self._check(self.lib.jepa_rope_table(self.h, positions, rot, base, factor,
-                                             _arg(table, "table", "f32", positions * rot),
-                                             _stream(stream, self.device)), "rope_table")
+            table = _Fast.torch.empty(positions, rot, device=f"cuda:{self.device}")
+        self._check(self.lib.jepa_rope_table(
+            self.h, positions, rot, base, factor,
+            _dev(table, "table", "f32", positions * rot, self.device),
+            _stream_on(stream, self.device)), "rope_table")
         return table
 
     def rope_append_kv8(self, q, k, v, rope_table, cu, start, cache: KvCache8, q_out, q_norm=None,
                         k_norm=None, norm_eps=1e-6, interleaved=False, k_out=None, stream=None):
         """Norm, rotate and append packed tokens: q [tokens, q_heads, head_dim] (or None with
         q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None."""
-        kp, ks = _rows(k, "k")
-        vp, vs = _rows(v, "v")
-        tokens, heads, dim = k.shape
-        if v.shape != k.shape or heads != cache.kv_heads or dim != cache.head_dim:
+        dev = self.device
+        kp, ks, tokens, heads, dim = _rows(k, "k", dev)
+        vp, vs, *v_shape = _rows(v, "v", dev)
+        if v_shape != [tokens, heads, dim] or heads != cache.kv_heads or dim != cache.head_dim:
             raise JepaError(1, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit the cache's "
                                f"{cache.kv_heads} heads of {cache.head_dim}")
         if (q is None) != (q_out is None):
             raise JepaError(1, "q and q_out are given together")
-        qp, qs, q_heads = None, 0, 0
+        qp, qs, q_heads, qo = None, 0, 0, None
         if q is not None:
-            qp, qs = _rows(q, "q")
-            q_heads = q.shape[1]
-            if q.shape[0] != tokens or q.shape[2] != dim:
+            qp, qs, q_tokens, q_heads, q_dim = _rows(q, "q", dev)
+            if q_tokens != tokens or q_dim != dim:
                 raise JepaError(1, f"q {tuple(q.shape)} does not fit k {tuple(k.shape)}")
+            qo = _dev(q_out, "q_out", "bf16", tokens * q_heads * dim, dev)
         positions, rot = (0, 0) if rope_table is None else rope_table.shape
-        self._on(q=q, k=k, v=v, rope_table=rope_table, cu=cu, start=start, cache=cache, q_out=q_out,
-                 q_norm=q_norm, k_norm=k_norm, k_out=k_out)
-        self._dims(tokens=tokens)
-        self._check(self.lib.jepa_rope_append_kv8(
+        cache.check(dev)
+        if tokens < 1:
+            raise JepaError(1, "tokens must be >= 1 (got 0)")
+        st = self.lib.jepa_rope_append_kv8(
             self.h, cache.ref, qp, qs, kp, ks, vp, vs, tokens, q_heads,
-            _arg(q_norm, "q_norm", "f32", dim, optional=True),
-            _arg(k_norm, "k_norm", "f32", dim, optional=True), norm_eps,
-            _arg(rope_table, "rope_table", "f32", positions * rot, optional=True), positions, rot,
-            int(interleaved), _arg(cu, "cu", "i32", cache.batch + 1),
-            _arg(start, "start", "i32", cache.batch),
-            _arg(q_out, "q_out", "bf16", tokens * q_heads * dim, optional=True),
-            _arg(k_out, "k_out", "bf16", tokens * heads * dim, optional=True),
-            _stream(stream, self.device)), "rope_append_kv8")
+            _opt(q_norm, "q_norm", "f32", dim, dev), _opt(k_norm, "k_norm", "f32", dim, dev), norm_eps,
+            _opt(rope_table, "rope_table", "f32", positions * rot, dev), positions, rot,
+            int(interleaved), _dev(cu, "cu", "i32", cache.batch + 1, dev),
+            _dev(start, "start", "i32", cache.batch, dev), qo,
+            _opt(k_out, "k_out", "bf16", tokens * heads * dim, dev), _stream_on(stream, dev))
+        if st:
+            self._check(st, "rope_append_kv8")
 
     def kv8_read(self, cache: KvCache8, cu, first, k_out, v_out, stream=None):
         """Cached tokens as bf16 into k_out, v_out [tokens, kv_heads, head_dim]."""
+        dev = self.device
+        cache.check(dev)
         tokens = k_out.shape[0]
-        self._dims(tokens=tokens)
+        if tokens < 1:
+            raise JepaError(1, "tokens must be >= 1 (got 0)")
         n = tokens * cache.kv_heads * cache.head_dim
-        self._on(cache=cache, cu=cu, first=first, k_out=k_out, v_out=v_out)
-        self._check(self.lib.jepa_kv8_read(
-            self.h, cache.ref, _arg(cu, "cu", "i32", cache.batch + 1),
-            _arg(first, "first", "i32", cache.batch), tokens, _arg(k_out, "k_out", "bf16", n),
-            _arg(v_out, "v_out", "bf16", n), _stream(stream, self.device)), "kv8_read")
+        st = self.lib.jepa_kv8_read(
+            self.h, cache.ref, _dev(cu, "cu", "i32", cache.batch + 1, dev),
+            _dev(first, "first", "i32", cache.batch, dev), tokens, _dev(k_out, "k_out", "bf16", n, dev),
+            _dev(v_out, "v_out", "bf16", n, dev), _stream_on(stream, dev))
+        if st:
+            self._check(st, "kv8_read")
 
     def attention_kv8_workspace(self, cache: KvCache8) -> int:
         """Bytes of workspace that attention_kv8 needs."""
@@ -526,38 +579,41 @@ class Planner:
                       stream=None):
         """Attention of q [batch, q_tokens, q_heads, head_dim] over the cache; workspace: a uint8
         tensor of attention_kv8_workspace bytes, one for each call that may run at a time."""
+        dev = self.device
         if getattr(q, "ndim", 0) != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
             raise JepaError(1, f"q must be [{cache.batch}, q_tokens, q_heads, {cache.head_dim}]")
+        cache.check(dev)
         batch, q_tokens, q_heads, dim = q.shape
         rows = batch * q_tokens * q_heads
-        self._dims(q_tokens=q_tokens, q_heads=q_heads)
-        self._on(q=q, cache=cache, kv_len=kv_len, out=out, workspace=workspace, lse=lse)
-        self._check(self.lib.jepa_attention_kv8(
-            self.h, cache.ref, _arg(q, "q", "bf16", rows * dim), q_tokens, q_heads,
-            _arg(kv_len, "kv_len", "i32", batch), scale, int(causal),
-            _arg(out, "out", "bf16", rows * dim), _arg(lse, "lse", "f32", rows, optional=True),
-            _arg(workspace, "workspace", "u8", 0), workspace.numel(),
-            _stream(stream, self.device)), "attention_kv8")
+        if rows < 1:
+            raise JepaError(1, "q_tokens and q_heads must be >= 1")
+        st = self.lib.jepa_attention_kv8(
+            self.h, cache.ref, _dev(q, "q", "bf16", rows * dim, dev), q_tokens, q_heads,
+            _dev(kv_len, "kv_len", "i32", batch, dev), scale, int(causal),
+            _dev(out, "out", "bf16", rows * dim, dev), _opt(lse, "lse", "f32", rows, dev),
+            _dev(workspace, "workspace", "u8", 0, dev), workspace.numel(), _stream_on(stream, dev))
+        if st:
+            self._check(st, "attention_kv8")
 
     def attention_packed(self, q, k, v, cu_q, cu_k, out, scale, frame=1, lse=None, stream=None):
         """Attention of packed prompts: q [tokens_q, q_heads, head_dim], k and v [tokens_k,
         kv_heads, head_dim]; cu_q, cu_k [batch + 1]."""
-        qp, qs = _rows(q, "q")
-        kp, ks = _rows(k, "k")
-        vp, vs = _rows(v, "v")
-        tokens_q, q_heads, dim = q.shape
-        tokens_k, kv_heads, k_dim = k.shape
-        if v.shape != k.shape or k_dim != dim:
+        dev = self.device
+        qp, qs, tokens_q, q_heads, dim = _rows(q, "q", dev)
+        kp, ks, tokens_k, kv_heads, k_dim = _rows(k, "k", dev)
+        vp, vs, *v_shape = _rows(v, "v", dev)
+        if v_shape != [tokens_k, kv_heads, k_dim] or k_dim != dim:
             raise JepaError(1, f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
         batch = cu_q.numel() - 1
-        self._dims(tokens_q=tokens_q, tokens_k=tokens_k, batch=batch)
-        self._on(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
-        self._check(self.lib.jepa_attention_packed(
+        if min(tokens_q, tokens_k, batch) < 1:
+            raise JepaError(1, "tokens_q, tokens_k and batch must be >= 1")
+        st = self.lib.jepa_attention_packed(
             self.h, qp, qs, kp, ks, vp, vs, tokens_q, tokens_k, batch, q_heads, kv_heads, dim,
-            _arg(cu_q, "cu_q", "i32", batch + 1), _arg(cu_k, "cu_k", "i32", batch + 1), scale, frame,
-            _arg(out, "out", "bf16", tokens_q * q_heads * dim),
-            _arg(lse, "lse", "f32", tokens_q * q_heads, optional=True),
-            _stream(stream, self.device)), "attention_packed")
+            _dev(cu_q, "cu_q", "i32", batch + 1, dev), _dev(cu_k, "cu_k", "i32", batch + 1, dev), scale,
+            frame, _dev(out, "out", "bf16", tokens_q * q_heads * dim, dev),
+            _opt(lse, "lse", "f32", tokens_q * q_heads, dev), _stream_on(stream, dev))
+        if st:
+            self._check(st, "attention_packed")
 
     def set_use_graphs(self, on: bool):
         self._check(self.lib.jepa_set_use_graphs(self.h, int(on)), "set_use_graphs")

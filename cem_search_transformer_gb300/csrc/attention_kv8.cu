@@ -36,8 +36,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int NST = 3;              // cp.async stages of a warp
-constexpr int CTAS_PER_SM = 3;
+constexpr int MAX_CTAS_PER_SM = 3;  // of any shape: sizes the workspace
 constexpr int MIN_UNITS = 4;        // units a CTA takes at least where items are split
 constexpr int WHOLE_UNITS = 8;      // items up to this many units are not split
 constexpr int ITEM_UNITS = 2;       // what an item costs besides its units: start and joining
@@ -50,6 +49,8 @@ constexpr float P_SHIFT = 7.f, P_SLACK = 8.f;
 template <int D, int NR>
 struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
+  static constexpr int NST = 3;      // cp.async stages of a warp
+  static constexpr int CTAS = 3;     // a SM
   static constexpr int KS = 2048 / D;              // keys a warp takes in a step
   static constexpr int GROUPS = KS / 16;           // 16-key groups of P V
   static constexpr int UNIT = WARPS * KS;          // keys of a unit
@@ -253,10 +254,10 @@ __device__ __forceinline__ bool plan(const Kv8View& c, const Args& a, int whole,
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+__global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     k_attention_kv8(Kv8View c, Args a, int whole, int* err_flag) {
   using S = Shape<D, NR>;
-  constexpr int ROWS = S::ROWS;
+  constexpr int ROWS = S::ROWS, NST = S::NST;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a, int max_part
 }
 
 // Bytes of the split notes at the head of the workspace.
-size_t notes_bytes(int num_sms) { return (size_t)num_sms * CTAS_PER_SM * sizeof(int4); }
+size_t notes_bytes(int num_sms) { return (size_t)num_sms * MAX_CTAS_PER_SM * sizeof(int4); }
 
 template <int D, int NR>
 cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStream_t s) {
@@ -752,7 +753,7 @@ cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStr
   if (e != cudaSuccess) return e;
   a.tiles = (a.q_tokens * a.group + S::ROWS - 1) / S::ROWS;
   const long long max_len = (long long)c.max_pages << c.page_log2;
-  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT, slots = (long long)num_sms * CTAS_PER_SM;
+  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT, slots = (long long)num_sms * S::CTAS;
   const long long items = (long long)c.batch * c.heads * a.tiles;
   const int whole = max_units <= WHOLE_UNITS;
   // every SM's slots, or the work there can be if that is less
@@ -777,7 +778,7 @@ cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStr
 }  // namespace
 
 size_t attention_kv8_workspace(int dim, int num_sms) {
-  return notes_bytes(num_sms) + (size_t)num_sms * CTAS_PER_SM * 2 * 16 * (dim + 2) * sizeof(float);
+  return notes_bytes(num_sms) + (size_t)num_sms * MAX_CTAS_PER_SM * 2 * 16 * (dim + 2) * sizeof(float);
 }
 
 cudaError_t attention_kv8(const Kv8View& c, const bf16* q, int q_tokens, int q_heads,

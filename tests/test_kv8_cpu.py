@@ -93,7 +93,6 @@ class _NoLibrary:
     h = None
     device = 0
     _dims = binding.Planner._dims
-    _on = binding.Planner._on
 
     def _check(self, status, what):
         raise AssertionError(f"{what} returned {status} although an argument was invalid")
@@ -137,7 +136,7 @@ def test_packed_attention_refuses_before_the_call():
     with pytest.raises(binding.JepaError, match="CUDA"):
         binding.Planner.attention_packed(_NoLibrary(), q, q, q, cu, cu, q, 0.125)
     with pytest.raises(binding.JepaError, match="q must be"):
-        cache = type("C", (), dict(batch=2, head_dim=64))()
+        cache = type("C", (), dict(batch=2, head_dim=64, check=lambda self, d: None))()
         binding.Planner.attention_kv8(_NoLibrary(), q, cache, cu, q, 0.125, None)
 
 
