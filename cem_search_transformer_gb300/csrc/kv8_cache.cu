@@ -2,9 +2,13 @@
 // queries and keys, quantisation of keys and values to e4m3 with one power-of-two scale per
 // (page, head), and the read-back to bf16.
 //
-// A page and head is quantised by exactly one team (a warp or a CTA): the team of its "owner",
-// the first new token that lies in the page. No atomics: the result depends neither on the
-// launch shape nor on the order of blocks.
+// Bound by bytes on long appends (2 (q_heads + 2 kv_heads) dim read, 2 q_heads dim + 2 kv_heads dim
+// written a token) and by latency on short ones. A page and head is quantised by exactly one team
+// of warps: that of its "owner", the first new token that lies in the page. No atomics: the result
+// depends neither on the launch shape nor on the order of blocks.
+//
+// A head row is held by D / 16 lanes, 16 elements each: both elements of every rotated pair lie in
+// one lane (no exchange), and its 8 angles serve 16 elements.
 #include "kv8.cuh"
 
 #include <cuda_fp16.h>
@@ -33,15 +37,6 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&y)[8], float inv) {
   u.y = (uint32_t)e4m3x2(y[4] * inv, y[5] * inv) | ((uint32_t)e4m3x2(y[6] * inv, y[7] * inv) << 16);
   return u;
 }
-__device__ __forceinline__ void load8(const bf16* p, float (&y)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = __uint_as_float(w[i] << 16);
-    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 __device__ __forceinline__ void store8(bf16* p, const float (&y)[8]) {
   uint4 u;
   uint32_t w[4];
@@ -60,287 +55,395 @@ __device__ __forceinline__ float sane_scale(float s) {
   return s >= KV8_SCALE_MIN ? fminf(s, KV8_SCALE_MAX) : KV8_SCALE_MIN;
 }
 
-// Sequence of packed token t: the largest s with cu[s] <= t (cu ascending), found by the whole
-// warp with one 32-way probe per level; -1 before the first sequence.
-__device__ __forceinline__ int find_sequence(const int* cu, int batch, int t) {
+// Sequence of a packed token and where it lies.
+struct Place {
+  int s, begin, end, first;   // sequence (-1: none), its packed tokens [begin, end), start[s]
+};
+// The largest s with cu[s] <= t (cu ascending), by the whole warp: 32-way probes, the last of
+// which brings the bounds and the start along.
+__device__ __forceinline__ Place locate(const int* __restrict__ cu, const int* __restrict__ start,
+                                        int batch, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = batch;
-  if (__ldg(cu) > t) return -1;
-  while (n > 1) {
-    const int step = (n + 31) >> 5;
-    const int at = lane * step;
+  while (n > 32) {
+    const int step = (n + 31) >> 5, at = lane * step;
     const bool le = at < n && __ldg(cu + lo + at) <= t;
     const int last = 31 - __clz((int)(__ballot_sync(0xffffffffu, le) | 1u));
     lo += last * step;
     n = min(step, n - last * step);
   }
-  return lo;
+  int b = 0x7fffffff, e = 0, f = 0;
+  if (lane < n) {
+    b = __ldg(cu + lo + lane);
+    e = __ldg(cu + lo + lane + 1);
+    f = __ldg(start + lo + lane);
+  }
+  const uint32_t le = __ballot_sync(0xffffffffu, b <= t);
+  const int last = le ? 31 - __clz((int)le) : 0;
+  Place p;
+  p.s = le ? lo + last : -1;
+  p.begin = __shfl_sync(0xffffffffu, b, last);
+  p.end = __shfl_sync(0xffffffffu, e, last);
+  p.first = __shfl_sync(0xffffffffu, f, last);
+  return p;
 }
 
-// cos / sin of the pairs that a lane's 8 elements (8 c .. 8 c + 7) belong to.
-struct Angles {
-  float c[8], s[8];
-};
-
-template <bool INTER>
-__device__ __forceinline__ void load_angles(Angles& a, const float* row, int rot, int e0) {
-  if (e0 >= rot) return;
-  const int half = rot >> 1;
-  if (INTER) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + (e0 >> 1)));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + (e0 >> 1)));
-    a.c[0] = c.x; a.c[1] = c.y; a.c[2] = c.z; a.c[3] = c.w;
-    a.s[0] = s.x; a.s[1] = s.y; a.s[2] = s.z; a.s[3] = s.w;
-  } else {
-    const int at = e0 < half ? e0 : e0 - half;
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + at + i));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + at + i));
-      a.c[i] = c.x; a.c[i + 1] = c.y; a.c[i + 2] = c.z; a.c[i + 3] = c.w;
-      a.s[i] = s.x; a.s[i + 1] = s.y; a.s[i + 2] = s.z; a.s[i + 3] = s.w;
+// The 16 elements of a head row that a lane holds: chunks of 8 at c0 and c1.
+template <int D, bool INTER>
+struct Lane {
+  int c0, c1, p;
+  bool rotates;
+  __device__ __forceinline__ explicit Lane(int rot) {
+    constexpr int L = D / 16;
+    p = (threadIdx.x & 31) % L;
+    rotates = 16 * p < rot;
+    if (INTER || !rotates) {
+      // neighbours; past rot these are the chunks rot / 8 + 2 (p - rot / 16) and the next
+      c0 = 2 * p;
+      c1 = 2 * p + 1;
+    } else {
+      c0 = p;
+      c1 = p + (rot >> 4);
     }
   }
+};
+
+// cos (first 8) and sin of a lane's pairs 8 p .. 8 p + 7 from a row of the table.
+__device__ __forceinline__ void load_angles(float (&an)[16], const float* row, int rot, int p) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(row + h * (rot >> 1) + 8 * p + i));
+      an[8 * h + i] = x.x; an[8 * h + i + 1] = x.y; an[8 * h + i + 2] = x.z; an[8 * h + i + 3] = x.w;
+    }
 }
 
-// Norm and rotation of one head row held by the D / 8 lanes of a group, 8 elements a lane:
 // y = x * w / sqrt(mean(x^2) + eps), then (a, b) -> (a cos - b sin, b cos + a sin) for the pairs
 // (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1), i < rot / 2. All lanes of the warp call it.
 template <int D, bool INTER>
-__device__ __forceinline__ void norm_rotate(float (&y)[8], const float* __restrict__ w, float eps,
-                                            const Angles& a, int rot) {
-  constexpr int L = D / 8;
-  const int lane = threadIdx.x & 31, c = lane % L, e0 = 8 * c;
+__device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>& ln,
+                                            const float* __restrict__ w, float eps,
+                                            const float (&an)[16]) {
+  constexpr int L = D / 16;
   if (w) {
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+    for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = __frsqrt_rn(ss * (1.0f / D) + eps);
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 g = __ldg(reinterpret_cast<const float4*>(w + e0 + i));
+    for (int i = 0; i < 16; i += 4) {
+      const float4 g =
+          __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 8 ? ln.c0 : ln.c1) + (i & 7)));
       y[i] *= r * g.x; y[i + 1] *= r * g.y; y[i + 2] *= r * g.z; y[i + 3] *= r * g.w;
     }
   }
-  if (INTER) {
-    if (e0 < rot) {
+  if (ln.rotates) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = y[2 * i], q = y[2 * i + 1];
-        y[2 * i] = p * a.c[i] - q * a.s[i];
-        y[2 * i + 1] = q * a.c[i] + p * a.s[i];
-      }
-    }
-  } else {
-    // the partner elements sit rot / 16 lanes away (rot is a multiple of 16)
-    const int away = rot >> 4;
-    const bool first = e0 < (rot >> 1), on = e0 < rot;
-    const int src = on ? (lane + (first ? away : -away)) : lane;
-    float other[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, y[i], src);
-    if (on) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        y[i] = first ? y[i] * a.c[i] - other[i] * a.s[i] : y[i] * a.c[i] + other[i] * a.s[i];
+    for (int i = 0; i < 8; ++i) {
+      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : 8 + i;
+      const float p = y[ia], q = y[ib];
+      y[ia] = p * an[i] - q * an[8 + i];
+      y[ib] = q * an[i] + p * an[8 + i];
     }
   }
 }
 
-__device__ __forceinline__ float abs_max(const float (&y)[8], float m) {
+template <class LaneT>
+__device__ __forceinline__ void load16(const bf16* row, const LaneT& ln, uint4 (&u)[2]) {
+  u[0] = *reinterpret_cast<const uint4*>(row + 8 * ln.c0);
+  u[1] = *reinterpret_cast<const uint4*>(row + 8 * ln.c1);
+}
+__device__ __forceinline__ void widen(const uint4 (&u)[2], float (&y)[16]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));   // fmaxf drops NaN
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
+      y[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+template <class LaneT>
+__device__ __forceinline__ void store16(bf16* row, const LaneT& ln, const float (&y)[16]) {
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = y[i];
+    b[i] = y[8 + i];
+  }
+  store8(row + 8 * ln.c0, a);
+  store8(row + 8 * ln.c1, b);
+}
+template <class LaneT>
+__device__ __forceinline__ void store_codes(uint8_t* row, const LaneT& ln, const float (&y)[16], float inv) {
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = y[i];
+    b[i] = y[8 + i];
+  }
+  *reinterpret_cast<uint2*>(row + 8 * ln.c0) = e4m3x8(a, inv);
+  *reinterpret_cast<uint2*>(row + 8 * ln.c1) = e4m3x8(b, inv);
+}
+__device__ __forceinline__ float abs_max(const float (&y)[16], float m) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(y[i]));   // fmaxf drops NaN
   return m;
 }
 
-// Queries: a warp takes one token and up to Q_HEADS_PER_WARP of its heads, so that the angles
-// are read once for them.
-constexpr int Q_HEADS_PER_WARP = 8;
+// Codes of a page's `off` earlier tokens moved to a scale 1 / factor times theirs (exact but for
+// codes that become subnormal), `members` threads together.
+template <int D>
+__device__ __forceinline__ void rescale_codes(uint8_t* base, int off, float factor, int member,
+                                              int members) {
+  for (int i = member; i < off * (D / 8); i += members) {
+    uint2* at = reinterpret_cast<uint2*>(base) + i;
+    const uint2 u = *at;
+    float z[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = e4m3x2_values((uint16_t)((k < 2 ? u.x : u.y) >> (16 * (k & 1))));
+      z[2 * k] = f.x;
+      z[2 * k + 1] = f.y;
+    }
+    *at = e4m3x8(z, factor);
+  }
+}
+
+__device__ __forceinline__ int positions_of(const Kv8View& c, const AppendArgs& a) {
+  return min(a.positions, c.max_pages << c.page_log2);
+}
+
+// Queries: a warp takes one token and up to Q_HEADS of its heads, which share the angles. The
+// loads of the rows and of the token's sequence go out together.
+constexpr int Q_HEADS = 8;
 
 template <int D, bool INTER>
-__device__ __forceinline__ void rotate_queries(const AppendArgs& a, int batch, int positions_max,
+__device__ __forceinline__ void rotate_queries(const Kv8View& c, const AppendArgs& a,
                                                long long unit, int* err_flag) {
-  constexpr int L = D / 8, ROWS = 32 / L, PASSES = Q_HEADS_PER_WARP / ROWS;
-  const int blocks = (a.q_heads + Q_HEADS_PER_WARP - 1) / Q_HEADS_PER_WARP;
+  constexpr int L = D / 16, ROWS = 32 / L, PASSES = Q_HEADS / ROWS;
+  const int blocks = (a.q_heads + Q_HEADS - 1) / Q_HEADS;
   if (unit >= (long long)a.tokens * blocks) return;
-  const int t = (int)(unit / blocks), h0 = (int)(unit % blocks) * Q_HEADS_PER_WARP;
-  const int lane = threadIdx.x & 31, sub = lane / L, e0 = 8 * (lane % L);
-  float y[PASSES][8];
+  const int t = (int)(unit / blocks), h0 = (int)(unit - (long long)t * blocks) * Q_HEADS;
+  const int sub = (threadIdx.x & 31) / L;
+  const Lane<D, INTER> ln(a.rot);
+  uint4 raw[PASSES][2];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int h = h0 + p * ROWS + sub;
-    if (h < a.q_heads) {
-      load8(a.q + t * a.q_stride + (long long)h * D + e0, y[p]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[p][i] = 0.f;
-    }
+    raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    if (h < a.q_heads) load16(a.q + t * a.q_stride + (long long)h * D, ln, raw[p]);
   }
-  const int s = find_sequence(a.cu, batch, t);
-  if (s < 0 || t >= __ldg(a.cu + batch)) return;   // behind the last sequence: left as it is
-  const int first = __ldg(a.start + s);
-  const int pos = (int)((unsigned)first + (unsigned)(t - __ldg(a.cu + s)));
-  if (first < 0 || pos < 0 || pos >= positions_max) {
+  const Place at = locate(a.cu, a.start, c.batch, t);
+  if (at.s < 0 || t >= at.end) return;            // behind the last sequence: left as it is
+  const int pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
+  if (at.first < 0 || pos < 0 || pos >= positions_of(c, a)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+    return;
+  }
+  float an[16];
+  if (ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    float y[16];
+    widen(raw[p], y);
+    norm_rotate<D, INTER>(y, ln, a.q_norm, a.eps, an);
+    const int h = h0 + p * ROWS + sub;
+    if (h < a.q_heads) store16(a.q_out + ((long long)t * a.q_heads + h) * D, ln, y);
+  }
+}
+
+// The part of a sequence's new tokens that lies in one page.
+struct Piece {
+  int t, n, off, pos, page;   // first packed token, tokens, slot in the page, position, page (-1: bad)
+};
+// What begins at packed token t of the sequence `at`; false where t's page belongs to an earlier
+// owner. Advances t behind it.
+__device__ __forceinline__ bool next_piece(const Kv8View& c, const AppendArgs& a, const Place& at,
+                                           int end, int& t, Piece& p) {
+  p.t = t;
+  p.pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
+  p.off = p.pos & (c.page - 1);
+  p.n = min(c.page - p.off, end - t);
+  t += p.n;
+  if (p.t != at.begin && p.off != 0) return false;
+  p.page = at.first >= 0 && p.pos >= 0 && (long long)p.pos + p.n <= positions_of(c, a)
+               ? kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, at.s, p.pos)
+               : -1;
+  return true;
+}
+
+// Short appends (a few tokens a sequence): a warp takes one owner token and, of k or v, as many
+// heads as it has groups of D / 16 lanes. Segments of more than one token are read twice.
+template <int D, bool INTER>
+__device__ __forceinline__ void append_short(const Kv8View& c, const AppendArgs& a, long long unit,
+                                             int* err_flag) {
+  constexpr int L = D / 16, HEADS = 32 / L;
+  const int blocks = (c.heads + HEADS - 1) / HEADS;
+  const bool is_v = unit & 1;
+  const int t0 = (int)((unit >> 1) / blocks), h0 = (int)((unit >> 1) - (long long)t0 * blocks) * HEADS;
+  if (t0 >= a.tokens) return;
+  const int lane = threadIdx.x & 31, head = h0 + lane / L;
+  const bool on = head < c.heads;
+  const Lane<D, INTER> ln(a.rot);
+  const bf16* src = (is_v ? a.v : a.k) + (long long)(on ? head : 0) * D;
+  const long long stride = is_v ? a.v_stride : a.k_stride;
+  uint4 raw[2];
+  load16(src + t0 * stride, ln, raw);
+  const Place at = locate(a.cu, a.start, c.batch, t0);
+  if (at.s < 0 || t0 >= at.end) return;
+  int t = t0;
+  Piece p;
+  if (!next_piece(c, a, at, min(at.end, a.tokens), t, p)) return;
+  if (p.page < 0) {
     if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
   }
-  Angles an;
-  load_angles<INTER>(an, a.rope + (long long)pos * a.rot, a.rot, e0);
+  const long long block = (long long)p.page * c.heads + (on ? head : 0);
+  float* const scale_at = (is_v ? c.v_scale : c.k_scale) + block;
+  const float was = p.off != 0 ? sane_scale(*scale_at) : 0.f;
+  // row r of the segment, normed and rotated (keys); all lanes call it
+  auto row_values = [&](int r, float (&y)[16]) {
+    if (r > 0) load16(src + (p.t + r) * stride, ln, raw);
+    widen(raw, y);
+    if (!is_v) {
+      float an[16];
+      if (ln.rotates) load_angles(an, a.rope + (long long)(p.pos + r) * a.rot, a.rot, ln.p);
+      norm_rotate<D, INTER>(y, ln, a.k_norm, a.eps, an);
+    }
+  };
+  float y[16], m = 0.f;
+  for (int r = p.n - 1; r >= 0; --r) {   // the first row last: it then is at hand
+    if (r == 0 && p.n > 1) load16(src + p.t * stride, ln, raw);
+    row_values(r, y);
+    m = abs_max(y, m);
+  }
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    norm_rotate<D, INTER>(y[p], a.q_norm, a.eps, an, a.rot);
-    const int h = h0 + p * ROWS + sub;
-    if (h < a.q_heads) store8(a.q_out + ((long long)t * a.q_heads + h) * D + e0, y[p]);
+  for (int o = L / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!on) m = 0.f;
+  float scale = pow2(kv8_exponent(__float_as_uint(m)));
+  uint8_t* const base = (is_v ? c.v : c.k) + block * ((long long)c.page * D);
+  __syncwarp();                          // all lanes have read the scale
+  if (p.off != 0 && on) {
+    if (scale > was) rescale_codes<D>(base, p.off, was / scale, lane % L, L);
+    scale = fmaxf(scale, was);           // a page that holds tokens never shrinks its scale
+  }
+  if (on && lane % L == 0) *scale_at = scale;
+  const float inv = 1.0f / scale;
+  for (int r = 0; r < p.n; ++r) {
+    if (r > 0) row_values(r, y);
+    if (on) {
+      store_codes(base + (long long)(p.off + r) * D, ln, y, inv);
+      if (!is_v && a.k_out) store16(a.k_out + ((long long)(p.t + r) * c.heads + head) * D, ln, y);
+    }
   }
 }
 
-// Keys or values of one head for the owners among packed tokens [t0, t1): each owner's segment
-// (its page's new tokens) is read once into registers, its maximum taken, and quantised.
-// TEAM threads (a warp or the CTA) work together, IT rows of 8 elements a thread.
-template <int D, bool INTER, int TEAM, int IT>
-__device__ __forceinline__ void append_owned(const Kv8View& c, const AppendArgs& a, int t0, int t1,
-                                             int head, bool is_v, float* red, int* err_flag) {
-  constexpr int L = D / 8, ROWS = TEAM / L;    // tokens a pass
-  const int lane = threadIdx.x & 31, member = TEAM == 32 ? lane : threadIdx.x;
-  const int row = member / L, e0 = 8 * (member % L);
-  const int limit = min(a.positions, c.max_pages << c.page_log2);
-  const int last = min(__ldg(a.cu + c.batch), a.tokens);
-  const bf16* src = is_v ? a.v : a.k;
+// Short appends: key / value warps, then query warps, in one grid.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(THREADS) k_append_short(Kv8View c, AppendArgs a, long long kv_units,
+                                                          int* err_flag) {
+  const long long unit = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
+  if (unit < kv_units)
+    append_short<D, INTER>(c, a, unit, err_flag);
+  else if (a.q)
+    rotate_queries<D, INTER>(c, a, unit - kv_units, err_flag);
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(THREADS, 4) k_rope_queries(Kv8View c, AppendArgs a, int* err_flag) {
+  rotate_queries<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
+}
+
+// Long appends: a team of T warps takes a chunk of `page` packed tokens of one head, k or v, and
+// quantises the pages that have their owner in it (two at most for a long sequence). Each lane
+// holds IT rows' 16 elements between the maximum and the codes, so that the rows are read once.
+template <int D, bool INTER, int T, int IT>
+__global__ void __launch_bounds__(THREADS, 2) k_append_pages(Kv8View c, AppendArgs a, long long units,
+                                                          int* err_flag) {
+  constexpr int L = D / 16, WARPS = THREADS / 32, ROWS = T * (32 / L);   // tokens a pass
+  __shared__ float red[2][WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / T;
+  const long long unit = (long long)blockIdx.x * (WARPS / T) + team;
+  if (unit >= units) return;
+  const int head = (int)(unit % c.heads);
+  const long long ck = unit / c.heads;
+  const bool is_v = ck & 1;
+  const int t0 = (int)(ck >> 1) << c.page_log2;
+  const int member = (warp % T) * 32 + lane, row = member / L;
+  const Lane<D, INTER> ln(a.rot);
+  const bf16* src = (is_v ? a.v : a.k) + (long long)head * D;
   const long long stride = is_v ? a.v_stride : a.k_stride;
-  uint8_t* codes = is_v ? c.v : c.k;
-  float* scales = is_v ? c.v_scale : c.k_scale;
-  t1 = min(t1, last);
-  if (t0 >= t1) return;
-  int s = find_sequence(a.cu, c.batch, t0);
-  if (s < 0) return;
+  Place at = locate(a.cu, a.start, c.batch, t0);
+  if (at.s < 0) return;
+  const int t1 = min(t0 + c.page, a.tokens);
+  int parity = 0;
   for (int t = t0; t < t1;) {
-    while (s + 1 < c.batch && __ldg(a.cu + s + 1) <= t) ++s;
-    const int begin = __ldg(a.cu + s), end = min(__ldg(a.cu + s + 1), last);
-    const int first = __ldg(a.start + s), pos = (int)((unsigned)first + (unsigned)(t - begin));
-    if (end <= t) return;                      // offsets that do not ascend
-    const int off = pos & (c.page - 1), n = min(c.page - off, end - t);
-    if (t != begin && off != 0) {              // this page belongs to an earlier owner
-      t += n;
-      continue;
+    while (t >= at.end) {                  // the next sequence that has tokens
+      if (++at.s >= c.batch) return;
+      at.begin = at.end;
+      at.end = __ldg(a.cu + at.s + 1);
+      at.first = __ldg(a.start + at.s);
     }
-    const int pg = first >= 0 && pos + n <= limit
-                       ? kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, s, pos)
-                       : -1;
-    if (pg < 0) {
+    Piece p;
+    if (!next_piece(c, a, at, min(at.end, a.tokens), t, p)) continue;
+    if (p.n <= 0) return;                  // offsets that do not ascend
+    if (p.page < 0) {
       if (member == 0) atomicOr(err_flag, DEV_ERR_INDEX);
-      t += n;
       continue;
     }
-    // row r of the segment, normed and rotated (keys); all threads of the team call it
-    auto row_values = [&](int r, float (&z)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = 0.f;
-      if (r < n) load8(src + (long long)(t + r) * stride + (long long)head * D + e0, z);
-      if (!is_v) {
-        Angles an;
-        if (r < n) load_angles<INTER>(an, a.rope + (long long)(pos + r) * a.rot, a.rot, e0);
-        norm_rotate<D, INTER>(z, a.k_norm, a.eps, an, a.rot);
-      }
-    };
-    float y[IT][8];
-    float m = 0.f;
+    const long long block = (long long)p.page * c.heads + head;
+    float* const scale_at = (is_v ? c.v_scale : c.k_scale) + block;
+    const float was = p.off != 0 ? sane_scale(*scale_at) : 0.f;
+    uint4 raw[IT][2];
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      if (it * ROWS >= n) break;               // the same for the whole team
       const int r = it * ROWS + row;
-      row_values(r, y[it]);
-      if (r < n) m = abs_max(y[it], m);
+      raw[it][0] = raw[it][1] = make_uint4(0, 0, 0, 0);
+      if (r < p.n) load16(src + (long long)(p.t + r) * stride, ln, raw[it]);
     }
-    for (int r0 = IT * ROWS; r0 < n; r0 += ROWS) {   // warps with a long segment: read twice
-      float z[8];
-      row_values(r0 + row, z);
-      if (r0 + row < n) m = abs_max(z, m);
+    float y[IT][16], m = 0.f;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int r = it * ROWS + row;
+      widen(raw[it], y[it]);
+      if (!is_v) {
+        float an[16];
+        if (ln.rotates && r < p.n) load_angles(an, a.rope + (long long)(p.pos + r) * a.rot, a.rot, ln.p);
+        norm_rotate<D, INTER>(y[it], ln, a.k_norm, a.eps, an);
+      }
+      if (r < p.n) m = abs_max(y[it], m);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (TEAM > 32) {
-      __syncthreads();
-      if (lane == 0) red[threadIdx.x >> 5] = m;
-      __syncthreads();
+    if (T > 1) {
+      if (lane == 0) red[parity][warp] = m;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(T * 32) : "memory");
 #pragma unroll
-      for (int i = 0; i < TEAM / 32; ++i) m = fmaxf(m, red[i]);
+      for (int i = 0; i < T; ++i) m = fmaxf(m, red[parity][team * T + i]);
+      parity ^= 1;
+    } else {
+      __syncwarp();                        // all lanes have read the scale
     }
-    const long long block = (long long)pg * c.heads + head;
-    uint8_t* base = codes + block * ((long long)c.page * D);
     float scale = pow2(kv8_exponent(__float_as_uint(m)));
-    if (off != 0) {
-      // the page holds `off` earlier tokens: its scale never shrinks, and where it grows their
-      // codes move to it (exact but for codes that become subnormal)
-      const float was = sane_scale(scales[block]);
-      if (TEAM > 32) __syncthreads(); else __syncwarp();   // read by all before it is written
-      if (scale > was) {
-        const float factor = was / scale;
-        for (int i = member; i < off * (D / 8); i += TEAM) {
-          uint2* at = reinterpret_cast<uint2*>(base) + i;
-          const uint2 u = *at;
-          float z[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = e4m3x2_values((uint16_t)((k < 2 ? u.x : u.y) >> (16 * (k & 1))));
-            z[2 * k] = f.x;
-            z[2 * k + 1] = f.y;
-          }
-          *at = e4m3x8(z, factor);
-        }
-      } else {
-        scale = was;
-      }
+    uint8_t* const base = (is_v ? c.v : c.k) + block * ((long long)c.page * D);
+    if (p.off != 0) {
+      if (scale > was) rescale_codes<D>(base, p.off, was / scale, member, T * 32);
+      scale = fmaxf(scale, was);           // a page that holds tokens never shrinks its scale
     }
-    if (member == 0) scales[block] = scale;
+    if (member == 0) *scale_at = scale;
     const float inv = 1.0f / scale;
-    auto put = [&](int r, const float (&z)[8]) {
-      if (r >= n) return;
-      *reinterpret_cast<uint2*>(base + (long long)(off + r) * D + e0) = e4m3x8(z, inv);
-      if (!is_v && a.k_out)
-        store8(a.k_out + ((long long)(t + r) * c.heads + head) * D + e0, z);
-    };
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      if (it * ROWS >= n) break;
-      put(it * ROWS + row, y[it]);
+      const int r = it * ROWS + row;
+      if (r >= p.n) continue;
+      store_codes(base + (long long)(p.off + r) * D, ln, y[it], inv);
+      if (!is_v && a.k_out) store16(a.k_out + ((long long)(p.t + r) * c.heads + head) * D, ln, y[it]);
     }
-    for (int r0 = IT * ROWS; r0 < n; r0 += ROWS) {
-      float z[8];
-      row_values(r0 + row, z);
-      put(r0 + row, z);
-    }
-    t += n;
-  }
-}
-
-// Grid: first the key / value teams, then the query warps.
-//   BY_CTA  a CTA per (chunk of `page` packed tokens, head, k | v), for long appends;
-//   else    a warp per (token, head, k | v), for short ones: most warps of a long append would
-//           find that their token owns nothing.
-template <int D, bool INTER, bool BY_CTA, int IT>
-__global__ void __launch_bounds__(THREADS) k_rope_append(Kv8View c, AppendArgs a, int kv_blocks,
-                                                         int* err_flag) {
-  __shared__ float red[THREADS / 32];
-  if ((int)blockIdx.x < kv_blocks) {
-    if (BY_CTA) {
-      const int unit = blockIdx.x, head = (unit >> 1) % c.heads, chunk = (unit >> 1) / c.heads;
-      const int t0 = chunk << c.page_log2;
-      append_owned<D, INTER, THREADS, IT>(c, a, t0, t0 + c.page, head, unit & 1, red, err_flag);
-    } else {
-      const long long unit = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
-      const long long th = unit >> 1;
-      const int head = (int)(th % c.heads);
-      const long long t = th / c.heads;
-      if (t < a.tokens)
-        append_owned<D, INTER, 32, IT>(c, a, (int)t, (int)t + 1, head, unit & 1, red, err_flag);
-    }
-  } else {
-    const long long unit =
-        (long long)(blockIdx.x - kv_blocks) * (THREADS / 32) + (threadIdx.x >> 5);
-    rotate_queries<D, INTER>(a, c.batch, min(a.positions, c.max_pages << c.page_log2), unit,
-                             err_flag);
   }
 }
 
@@ -354,11 +457,11 @@ __global__ void __launch_bounds__(THREADS) k_kv8_read(Kv8View c, const int* __re
   const int t = (int)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= tokens) return;
-  const int s = find_sequence(cu, c.batch, t);
-  if (s < 0 || t >= __ldg(cu + c.batch)) return;
-  const int f = __ldg(first + s), pos = (int)((unsigned)f + (unsigned)(t - __ldg(cu + s)));
+  const Place p = locate(cu, first, c.batch, t);
+  if (p.s < 0 || t >= p.end) return;
+  const int pos = (int)((unsigned)p.first + (unsigned)(t - p.begin));
   const int pg =
-      f < 0 ? -1 : kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, s, pos);
+      p.first < 0 ? -1 : kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, p.s, pos);
   if (pg < 0) {
     if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
@@ -399,31 +502,49 @@ __global__ void k_rope_table(int positions, int rot, double log2_base, double in
   table[(long long)p * rot + half + j] = (float)sn;
 }
 
+template <int D, bool INTER, int T, int IT>
+cudaError_t launch_pages(const Kv8View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
+  constexpr int TEAMS = THREADS / 32 / T;
+  const long long units = (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads * 2;
+  const long long blocks = (units + TEAMS - 1) / TEAMS;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  k_append_pages<D, INTER, T, IT><<<(unsigned)blocks, THREADS, 0, s>>>(c, a, units, err_flag);
+  return cudaGetLastError();
+}
+
 template <int D, bool INTER>
 cudaError_t launch_append(const Kv8View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
-  constexpr int WARPS = THREADS / 32;
-  const long long q_units =
-      a.q ? (long long)a.tokens * ((a.q_heads + Q_HEADS_PER_WARP - 1) / Q_HEADS_PER_WARP) : 0;
-  const long long q_blocks = (q_units + WARPS - 1) / WARPS;
-  // up to four new tokens a sequence on average: one warp holds a segment in registers
-  const bool by_warp = a.tokens <= 4LL * c.batch;
-  const long long kv_blocks =
-      by_warp ? ((long long)a.tokens * c.heads * 2 + WARPS - 1) / WARPS
-              : (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads * 2;
-  if (kv_blocks + q_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)(kv_blocks + q_blocks);
-  const int per_pass = THREADS / (D / 8);   // tokens a CTA holds in one pass
-  if (by_warp)
-    k_rope_append<D, INTER, false, 1><<<grid, THREADS, 0, s>>>(c, a, (int)kv_blocks, err_flag);
-  else if (c.page <= per_pass)
-    k_rope_append<D, INTER, true, 1><<<grid, THREADS, 0, s>>>(c, a, (int)kv_blocks, err_flag);
-  else if (c.page <= 2 * per_pass)
-    k_rope_append<D, INTER, true, 2><<<grid, THREADS, 0, s>>>(c, a, (int)kv_blocks, err_flag);
-  else if (c.page <= 4 * per_pass)
-    k_rope_append<D, INTER, true, 4><<<grid, THREADS, 0, s>>>(c, a, (int)kv_blocks, err_flag);
-  else
-    k_rope_append<D, INTER, true, 8><<<grid, THREADS, 0, s>>>(c, a, (int)kv_blocks, err_flag);
-  return cudaGetLastError();
+  constexpr int WARPS = THREADS / 32, HEADS = 32 / (D / 16);
+  const long long q_units = a.q ? (long long)a.tokens * ((a.q_heads + Q_HEADS - 1) / Q_HEADS) : 0;
+  // up to four new tokens a sequence on average: latency, one launch
+  if (a.tokens <= 4LL * c.batch) {
+    const long long kv_units = 2LL * a.tokens * ((c.heads + HEADS - 1) / HEADS);
+    const long long blocks = (kv_units + q_units + WARPS - 1) / WARPS;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    k_append_short<D, INTER><<<(unsigned)blocks, THREADS, 0, s>>>(c, a, kv_units, err_flag);
+    return cudaGetLastError();
+  }
+  if (q_units) {
+    const long long blocks = (q_units + WARPS - 1) / WARPS;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    k_rope_queries<D, INTER><<<(unsigned)blocks, THREADS, 0, s>>>(c, a, err_flag);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  // 64 elements a lane
+  if (D == 128)
+    switch (c.page) {
+      case 16: return launch_pages<D, INTER, 1, 4>(c, a, err_flag, s);
+      case 32: return launch_pages<D, INTER, 2, 4>(c, a, err_flag, s);
+      case 64: return launch_pages<D, INTER, 4, 4>(c, a, err_flag, s);
+      default: return launch_pages<D, INTER, 8, 4>(c, a, err_flag, s);
+    }
+  switch (c.page) {
+    case 16: return launch_pages<D, INTER, 1, 2>(c, a, err_flag, s);
+    case 32: return launch_pages<D, INTER, 1, 4>(c, a, err_flag, s);
+    case 64: return launch_pages<D, INTER, 2, 4>(c, a, err_flag, s);
+    default: return launch_pages<D, INTER, 4, 4>(c, a, err_flag, s);
+  }
 }
 
 }  // namespace
