@@ -467,24 +467,39 @@ __global__ void __launch_bounds__(THREADS) k_kv8_read(Kv8View c, const int* __re
     return;
   }
   const int off = pos & (c.page - 1), vecs = c.heads * (D / 16);
-  for (int i = lane; i < 2 * vecs; i += 32) {
-    const bool is_v = i >= vecs;
-    const int j = is_v ? i - vecs : i, head = j / (D / 16), e0 = 16 * (j % (D / 16));
-    const long long block = (long long)pg * c.heads + head;
-    const uint4 u = *reinterpret_cast<const uint4*>((is_v ? c.v : c.k) +
-                                                    (block * c.page + off) * D + e0);
-    const float scale = sane_scale((is_v ? c.v_scale : c.k_scale)[block]);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float z[2][8];
+  constexpr int AHEAD = 4;                 // loads a lane has in flight
+  for (int i0 = lane; i0 < 2 * vecs; i0 += 32 * AHEAD) {
+    uint4 u[AHEAD];
+    float scale[AHEAD];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float2 x = e4m3x2_values((uint16_t)(w[q >> 1] >> (16 * (q & 1))));
-      z[q >> 2][2 * (q & 3)] = x.x * scale;
-      z[q >> 2][2 * (q & 3) + 1] = x.y * scale;
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= 2 * vecs) break;
+      const bool is_v = i >= vecs;
+      const int j = is_v ? i - vecs : i, head = j / (D / 16), e0 = 16 * (j % (D / 16));
+      const long long block = (long long)pg * c.heads + head;
+      u[k] = *reinterpret_cast<const uint4*>((is_v ? c.v : c.k) + (block * c.page + off) * D + e0);
+      scale[k] = (is_v ? c.v_scale : c.k_scale)[block];
     }
-    bf16* to = (is_v ? v_out : k_out) + ((long long)t * c.heads + head) * D + e0;
-    store8(to, z[0]);
-    store8(to + 8, z[1]);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= 2 * vecs) break;
+      const bool is_v = i >= vecs;
+      const int j = is_v ? i - vecs : i;
+      const float f = sane_scale(scale[k]);
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      float z[2][8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float2 x = e4m3x2_values((uint16_t)(w[q >> 1] >> (16 * (q & 1))));
+        z[q >> 2][2 * (q & 3)] = x.x * f;
+        z[q >> 2][2 * (q & 3) + 1] = x.y * f;
+      }
+      bf16* to = (is_v ? v_out : k_out) + (long long)t * c.heads * D + 16 * j;
+      store8(to, z[0]);
+      store8(to + 8, z[1]);
+    }
   }
 }
 
