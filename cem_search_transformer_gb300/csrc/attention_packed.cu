@@ -41,7 +41,6 @@ namespace {
 using namespace tc;
 
 constexpr int TQ = 128;            // rows of a query tile (MMA M)
-constexpr int TK = 64;             // keys of a tile
 constexpr int P_THREADS = 384;     // 8 warps of softmax, then two issuers, producer, cleaning
 constexpr int W_MMA = 8, W_TMA = 10;   // issuers: W_MMA and the next; cleaning: the last
 // Registers a thread after setmaxnreg. The block launches with 168 each; the softmax warpgroups
@@ -50,22 +49,28 @@ constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == P_THREADS * 168, "register split");
 constexpr uint32_t P_TMEM = 512;
 constexpr int BLK = TQ * 128;      // bytes of 128 rows x 64 bf16 (one swizzled block of Q)
-constexpr int KBLK = TK * 128;     // the same of K or V
 
 template <int D>
 struct PShape {
+  // Keys of a tile: as many as two score buffers for each query tile leave TMEM for. A step has
+  // fixed costs (hand-overs, waits, the issue of its MMAs) of about 600 cycles.
+  static constexpr int TK = D == 64 ? 96 : 64;
+  static constexpr int NBUF = 2;                    // score buffers of a query tile
+  static constexpr int TM = TK * NBUF + D;          // its columns of TMEM: scores, then output
   static constexpr int NB = D / 64;                 // 64-column blocks
+  static constexpr int KBLK = TK * 128;             // bytes of one block of K or V
   static constexpr int QTILE = NB * BLK, TILE = NB * KBLK;   // bytes of a Q tile, of K or V
-  static constexpr int STAGES = 8;
+  static constexpr int STAGES = D == 64 ? 5 : 4;    // of the ring: V_j and K_{j + NBUF}
   static constexpr int OFF_RING = 2 * QTILE;
-  static constexpr int OFF_OUT = OFF_RING + STAGES * TILE;   // read-out: 32 rows x 64 B a warp
+  static constexpr int OFF_OUT = OFF_RING + STAGES * 2 * TILE;   // read-out: 32 rows x 64 B a warp
   static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
-  // kv_full[STAGES], kv_empty[STAGES], edge_full[STAGES], q_full[2], q_empty[2], s_full[2][2],
-  // p_full[2][2], pv[2][2], item_full[2], item_empty[2], next, teardown
-  static constexpr int NUM_BARS = 3 * STAGES + 22;
+  // kv_full[STAGES], kv_empty[STAGES], edge_full[STAGES], q_full[2], q_empty[2], s_full[2][NBUF],
+  // p_full[2][NBUF], pv[2][NBUF], item_full[2], item_empty[2], next, teardown
+  static constexpr int NUM_BARS = 3 * STAGES + 10 + 6 * NBUF;
   static constexpr int OFF_TAIL = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM = OFF_TAIL + 160 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static_assert(2 * TM <= (int)P_TMEM && TK % 32 == 0 && KBLK % 1024 == 0, "tiles");
 };
 
 struct PArgs {
@@ -131,6 +136,15 @@ __device__ __forceinline__ bool p_wait(uint32_t bar, uint32_t parity, volatile i
     }
   }
 }
+// 32 lanes x 16 columns TMEM store (thread i -> lane i).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
   float part[4];
 #pragma unroll
@@ -149,9 +163,9 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(yes));
   return yes != 0;
 }
-// MN-major operand of two 64-wide blocks: the leading byte offset is the distance between them.
-__device__ __forceinline__ uint64_t desc_mn_blocks(uint32_t saddr) {
-  return (desc_sw128_mn(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(KBLK >> 4) << 16);
+// MN-major operand of two 64-wide blocks `apart` bytes from each other: the leading byte offset.
+__device__ __forceinline__ uint64_t desc_mn_blocks(uint32_t saddr, uint32_t apart) {
+  return (desc_sw128_mn(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(apart >> 4) << 16);
 }
 
 
@@ -179,6 +193,7 @@ __device__ __forceinline__ int limit_of(const Item& it, int i, int frame) {
 }
 
 // The `index`-th 256-row item; sequences in order, within one the last rows (most keys) first.
+template <int TK>
 __device__ __forceinline__ void find_item(const PArgs& a, long long index, Cursor& cur, Item& it,
                                           int* err_flag) {
   const int lane = threadIdx.x & 31, span = 2 * a.per_tile;
@@ -262,6 +277,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     k_attention_packed(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PArgs a, int* err_flag) {
   using S = PShape<D>;
+  constexpr int TK = S::TK, KBLK = S::KBLK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sb = smem_u32(smem);
@@ -273,12 +289,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   auto q_full = [&](int w) { return rest + 8u * w; };
   auto q_empty = [&](int w) { return rest + 16 + 8u * w; };
   // of query tile w and score buffer b
-  auto s_full = [&](int w, int b) { return rest + 32 + 16u * w + 8u * b; };
-  auto p_full = [&](int w, int b) { return rest + 64 + 16u * w + 8u * b; };
-  auto pv_done = [&](int w, int b) { return rest + 96 + 16u * w + 8u * b; };
-  auto item_full = [&](int b) { return rest + 128 + 8u * b; };
-  auto item_empty = [&](int b) { return rest + 144 + 8u * b; };
-  const uint32_t next_full = rest + 160, teardown = rest + 168;
+  auto s_full = [&](int w, int b) { return rest + 32 + 8u * (S::NBUF * w + b); };
+  auto p_full = [&](int w, int b) { return rest + 32 + 8u * (S::NBUF * (2 + w) + b); };
+  auto pv_done = [&](int w, int b) { return rest + 32 + 8u * (S::NBUF * (4 + w) + b); };
+  const uint32_t rest2 = rest + 32 + 48u * S::NBUF;
+  auto item_full = [&](int b) { return rest2 + 8u * b; };
+  auto item_empty = [&](int b) { return rest2 + 16 + 8u * b; };
+  const uint32_t next_full = rest2 + 32, teardown = rest2 + 40;
   uint8_t* tail = smem + ((S::OFF_TAIL + 15) & ~15);
   Item* items = (Item*)tail;                              // two slots
   const uint32_t next_slot = smem_u32(tail + 2 * sizeof(Item));   // 16 bytes, 16-byte aligned
@@ -291,19 +308,19 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   Cursor cursor{0, 0};
   if (warp == W_TMA) {
     Item it;
-    find_item(a, blockIdx.x, cursor, it, err_flag);
+    find_item<S::TK>(a, blockIdx.x, cursor, it, err_flag);
     if (lane == 0) items[0] = it;
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(kv_full(s), 1);
+      mbar_init(kv_full(s), 2);    // the producer twice, or once it and once the cleaning warp
       mbar_init(kv_empty(s), 2);   // both issuers
       mbar_init(edge_full(s), 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(q_full(w), 1);
       mbar_init(q_empty(w), 1);
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < S::NBUF; ++b) {
         mbar_init(s_full(w, b), 1);
         mbar_init(p_full(w, b), 4);
         mbar_init(pv_done(w, b), 1);
@@ -324,8 +341,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  auto tS = [&](int w, int b) { return tmem + 128u * w + 64u * b; };
-  auto tO = [&](int w) { return tmem + 256u + 128u * w; };
+  auto tS = [&](int w, int b) { return tmem + (uint32_t)(S::TM * w + TK * b); };
+  auto tO = [&](int w) { return tmem + (uint32_t)(S::TM * w + TK * S::NBUF); };
   if (warp >= W_MMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     if (warp == W_TMA) {
@@ -343,7 +360,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           const int index = clc_index(next_slot);
           __syncwarp();
           it.valid = 0;
-          if (index >= 0) find_item(a, index, cursor, it, err_flag);
+          if (index >= 0) find_item<S::TK>(a, index, cursor, it, err_flag);
           if (i >= 2) {
             ok = __all_sync(0xffffffffu, p_wait(item_empty(i & 1), ((i >> 1) - 1) & 1, abort_flag, err_flag));
             if (!ok) break;
@@ -369,25 +386,34 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               tma_load_3d(sb + w * S::QTILE + b * BLK, &tmQ, 64 * b, it.head * a.group,
                           it.q0 + it.t0 + w * span, q_full(w));
           }
-          // K_0, K_1, V_0, K_2, V_1, ...: the order in which the issuer takes them
-          auto load = [&](bool is_v, int j) {
+          // K_0 and K_1 in a stage of their own each, then V_j beside K_{j + 2}: what the issuers
+          // take in one step, behind one barrier
+          auto load = [&](int j_v, int j_k) {
             const int st = n % S::STAGES;
             ok = ok && (n < S::STAGES ||
                         p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag));
             if (!ok) return;
             ++n;
-            const uint32_t dst = sb + S::OFF_RING + st * S::TILE;
-      // V tiles with an edge land at the cleaning warp, which passes them on to the issuers
-            const uint32_t at = is_v && j >= it.first_edge ? edge_full(st) : kv_full(st);
-            mbar_expect_tx(at, S::TILE);
-            for (int b = 0; b < S::NB; ++b)
-              tma_load_3d(dst + b * KBLK, is_v ? &tmV : &tmK, 64 * b, it.head, it.k0 + j * TK, at);
+            const uint32_t dst = sb + S::OFF_RING + st * 2 * S::TILE;
+            // V tiles with an edge land at the cleaning warp, which passes them on to the issuers
+            const bool has_k = j_k < n_tiles, has_v = j_v >= 0, edge = has_v && j_v >= it.first_edge;
+            const uint32_t bytes = (has_k ? S::TILE : 0) + (has_v && !edge ? S::TILE : 0);
+            if (edge) mbar_expect_tx(edge_full(st), S::TILE);
+            if (bytes)
+              mbar_expect_tx(kv_full(st), bytes);
+            else
+              mbar_arrive(kv_full(st));
+            if (!edge) mbar_arrive(kv_full(st));
+            for (int b = 0; b < S::NB; ++b) {
+              if (has_v)
+                tma_load_3d(dst + b * KBLK, &tmV, 64 * b, it.head, it.k0 + j_v * TK,
+                            edge ? edge_full(st) : kv_full(st));
+              if (has_k)
+                tma_load_3d(dst + S::TILE + b * KBLK, &tmK, 64 * b, it.head, it.k0 + j_k * TK, kv_full(st));
+            }
           };
-          for (int j = 0; j < min(2, n_tiles); ++j) load(false, j);
-          for (int j = 0; j < n_tiles && ok; ++j) {
-            load(true, j);
-            if (j + 2 < n_tiles) load(false, j + 2);
-          }
+          for (int j = 0; j < min(S::NBUF, n_tiles); ++j) load(-1, j);
+          for (int j = 0; j < n_tiles && ok; ++j) load(j, j + S::NBUF);
         }
         ok = __all_sync(0xffffffffu, ok);
       }
@@ -408,10 +434,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       };
       const int w = __shfl_sync(0xffffffffu, warp - W_MMA, 0);
       const uint32_t leader = elect_one();
-      const uint64_t q_desc = desc_sw128(sb + w * S::QTILE), ring_k = desc_sw128(sb + S::OFF_RING);
-      const uint64_t ring_v =
-          D == 128 ? desc_mn_blocks(sb + S::OFF_RING) : desc_sw128_mn(sb + S::OFF_RING);
-      constexpr uint64_t STEP = S::TILE >> 4;     // of a tile, in descriptor units
+      const uint64_t q_desc = desc_sw128(sb + w * S::QTILE);
+      const uint64_t ring_k = desc_sw128(sb + S::OFF_RING + S::TILE);
+      const uint64_t ring_v = D == 128 ? desc_mn_blocks(sb + S::OFF_RING, KBLK)
+                                       : desc_sw128_mn(sb + S::OFF_RING);
+      constexpr uint64_t STEP = 2 * S::TILE >> 4;     // of a stage, in descriptor units
       int ks = 0, k_phase = 0;       // ring stage and lap of the next tile
       auto advance = [&]() {
         if (++ks == S::STAGES) {
@@ -419,7 +446,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           k_phase ^= 1;
         }
       };
-      int step = 0;                  // key tiles that the query tile has behind it
+      int buf = 0;                   // score buffer and lap of the next key tile
+      uint32_t lap = 0;
       uint32_t q_phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
@@ -432,9 +460,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (lane == 0) mbar_arrive(item_empty(i & 1));
         __syncwarp();
         if (!valid) break;
-        auto scores = [&](int j) {
+        auto scores = [&](int j, int b) {
           const uint64_t kd = ring_k + ks * STEP;
-          const int b = (step + j) & 1;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             w_mma_ss(tS(w, b), q_desc + (uint64_t)((kk >> 2) * (BLK >> 4) + 2 * (kk & 3)),
@@ -442,8 +469,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           w_commit(s_full(w, b), leader);
           if (j + 1 == nt) w_commit(q_empty(w), leader);
         };
-        // K_0, K_1, then V_j and K_{j+2} in turn
-        for (int j = 0; j < min(2, n_tiles) && ok; ++j) {
+        // the first scores, then P V of tile j and the scores of tile j + NBUF in turn
+        int b0 = buf;
+        for (int j = 0; j < min(S::NBUF, n_tiles) && ok; ++j) {
           ok = wait(kv_full(ks), k_phase);
           if (ok && j == 0 && nt > 0) {
             ok = wait(q_full(w), q_phase);
@@ -451,15 +479,16 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           }
           if (!ok) break;
           tc_fence_after();
-          if (j < nt) scores(j);
+          if (j < nt) scores(j, b0);
+          b0 = b0 + 1 == S::NBUF ? 0 : b0 + 1;
           w_commit(kv_empty(ks), leader);
           advance();
         }
         for (int j = 0; j < n_tiles && ok; ++j) {
+          const int b = buf;
           ok = wait(kv_full(ks), k_phase);
           if (ok && j < nt) {
-            const int at = step + j, b = at & 1;
-            ok = wait(p_full(w, b), (at >> 1) & 1);
+            ok = wait(p_full(w, b), lap);
             if (!ok) break;
             tc_fence_after();
             const uint64_t vd = ring_v + ks * STEP;
@@ -468,19 +497,15 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               w_mma_ts(tO(w), tS(w, b) + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)), idO,
                        (j > 0) || (kk > 0), leader);
             w_commit(pv_done(w, b), leader);
+            if (j + S::NBUF < nt) scores(j + S::NBUF, b);
+            if (++buf == S::NBUF) {
+              buf = 0;
+              lap ^= 1;
+            }
           }
           w_commit(kv_empty(ks), leader);
           advance();
-          if (j + 2 < n_tiles) {
-            ok = ok && wait(kv_full(ks), k_phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (j + 2 < nt) scores(j + 2);
-            w_commit(kv_empty(ks), leader);
-            advance();
-          }
         }
-        step += nt;
       }
       w_commit(teardown, leader);
       const unsigned long long t0 = globaltimer();
@@ -498,15 +523,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (!it.valid) break;
         const int n_tiles = max(it.nt[0], it.nt[1]);
         for (int j = it.first_edge; j < n_tiles && ok; ++j) {
-          // tiles of the item ahead of V_j in the ring
-          const int ahead = min(2, n_tiles) + j + max(0, min(j, n_tiles - 2));
-          const int st = (n0 + ahead) % S::STAGES;
+          const int st = (n0 + min(S::NBUF, n_tiles) + j) % S::STAGES;
           ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
           if (!ok) break;
           phase ^= 1u << st;
 #pragma unroll 1
           for (int row = lane; row < TK; row += 32) {   // thread = key
-            uint8_t* v_row = smem + S::OFF_RING + st * S::TILE + row * 128;
+            uint8_t* v_row = smem + S::OFF_RING + st * 2 * S::TILE + row * 128;
             const bool behind = j * TK + row >= it.nk;
             uint32_t odd = 0;
             if (!behind) {
@@ -541,7 +564,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(kv_full(st));
         }
-        n0 += 2 * n_tiles;
+        n0 += min(S::NBUF, n_tiles) + n_tiles;
         __syncwarp();
         if (lane == 0) mbar_arrive(item_empty(i & 1));
       }
@@ -561,7 +584,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     auto all_wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
     };
-    int sn = 0;            // key tiles so far
+    int buf = 0;           // score buffer and lap of the next key tile
+    uint32_t lap = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
       ok = all_wait(item_full(i & 1), (i >> 1) & 1);
@@ -588,23 +612,34 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           if (c >= left) r[c] = __float_as_uint(-INFINITY);
       };
       float m = -INFINITY, l = 0.f;
-      auto scores_of = [&](int n) { return tS(w, n & 1) + lane_off; };
-      auto ready = [&](int n) {
-        const bool there = all_wait(s_full(w, n & 1), (n >> 1) & 1);
+      auto scores_of = [&](int b) { return tS(w, b) + lane_off; };
+      auto ready = [&](int b, uint32_t phase) {
+        const bool there = all_wait(s_full(w, b), phase);
         tc_fence_after();
         return there;
       };
+      auto step_on = [&](int& b, uint32_t& phase) {
+        if (++b == S::NBUF) {
+          b = 0;
+          phase ^= 1;
+        }
+      };
+      int last_buf = 0;                  // of the tile before
+      uint32_t last_lap = 0;
       auto tile = [&](int j) {
-        const int b = sn & 1;
-        if (!ready(sn)) return false;
-        uint32_t r0[32], r1[32];
-        tmem_ld32_async(scores_of(sn), r0);
-        tmem_ld32_async(scores_of(sn) + 32, r1);
-        tmem_wait(r0);
-        tmem_wait(r1);
-        hide(r0, j * TK);
-        hide(r1, j * TK + 32);
-        const float cmax = fmaxf(max32(r0), max32(r1));
+        const int b = buf;
+        if (!ready(b, lap)) return false;
+        uint32_t r[TK / 32][32];
+#pragma unroll
+        for (int q = 0; q < TK / 32; ++q) tmem_ld32_async(scores_of(b) + 32 * q, r[q]);
+#pragma unroll
+        for (int q = 0; q < TK / 32; ++q) tmem_wait(r[q]);
+        float cmax = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < TK / 32; ++q) {
+          hide(r[q], j * TK + 32 * q);
+          cmax = fmaxf(cmax, max32(r[q]));
+        }
         // the exponent's reference moves only when the maximum grew by more than 2^8: the same
         // reference scales O and the sum, so the result is unchanged
         const bool bump = cmax > m && (m == -INFINITY || (cmax - m) * scale_log2 > 8.0f);
@@ -616,7 +651,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           if (j > 0) {
             // the last product must be complete (those before it are: the issuer began this
             // tile's scores after them)
-            if (!all_wait(pv_done(w, b ^ 1), ((sn - 1) >> 1) & 1)) return false;
+            if (!all_wait(pv_done(w, last_buf), last_lap)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -632,43 +667,48 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const float ms = m == -INFINITY ? 0.f : m * scale_log2;
         const unsigned long long sc2 = f2_pack(scale_log2, scale_log2), nms2 = f2_pack(-ms, -ms);
         unsigned long long sum2[2] = {0, 0};
-        uint32_t pk[32];
-        auto exponentials = [&](const uint32_t (&r)[32], uint32_t* to) {
+        // P over the first columns of the scores, two keys a column
+#pragma unroll
+        for (int q = 0; q < TK / 32; ++q) {
+          uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float2 e = f2_unpack(
-                f2_fma(f2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sc2, nms2));
+            const float2 e = f2_unpack(f2_fma(
+                f2_pack(__uint_as_float(r[q][2 * c]), __uint_as_float(r[q][2 * c + 1])), sc2, nms2));
             const float p0 = p_ex2(e.x), p1 = p_ex2(e.y);
             sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(p0, p1));
             const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-            to[c] = *reinterpret_cast<const uint32_t*>(&h);
+            pk[c] = *reinterpret_cast<const uint32_t*>(&h);
           }
-        };
-        exponentials(r0, pk);
-        exponentials(r1, pk + 16);
-        tmem_st32(scores_of(sn), pk);      // P over the first half of the scores' columns
+          tmem_st16(scores_of(b) + 16 * q, pk);
+        }
         const float2 sm = f2_unpack(f2_add(sum2[0], sum2[1]));
         l += sm.x + sm.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(w, b));
-        ++sn;
+        last_buf = b;
+        last_lap = lap;
+        step_on(buf, lap);
         return true;
       };
       if (active) {
         for (int j = 0; j < ntw && ok; ++j) ok = tile(j);
       } else {
-        for (int j = 0; j < ntw && ok; ++j, ++sn) {   // none of the warp's rows is in use
-          ok = ready(sn);
+        for (int j = 0; j < ntw && ok; ++j) {   // none of the warp's rows is in use
+          ok = ready(buf, lap);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(p_full(w, sn & 1));
+          if (lane == 0 && ok) mbar_arrive(p_full(w, buf));
+          last_buf = buf;
+          last_lap = lap;
+          step_on(buf, lap);
         }
       }
       if (!ok) break;
       if (ntw > 0) {
-        ok = all_wait(pv_done(w, (sn - 1) & 1), ((sn - 1) >> 1) & 1);
+        ok = all_wait(pv_done(w, last_buf), last_lap);
         if (!ok) break;
         tc_fence_after();
       }
@@ -800,10 +840,11 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
   a.per_tile = TQ / a.group;
   a.frame = frame;
   a.scale_log2 = scale * 1.4426950408889634f;
+  const int box_keys = dim == 64 ? PShape<64>::TK : PShape<128>::TK;
   CUtensorMap mq, mk, mv;
   if (!make_map_heads(&mq, q, tokens_q, q_heads, dim, q_stride, a.per_tile, a.group) ||
-      !make_map_heads(&mk, k, tokens_k, kv_heads, dim, k_stride, TK, 1) ||
-      !make_map_heads(&mv, v, tokens_k, kv_heads, dim, v_stride, TK, 1))
+      !make_map_heads(&mk, k, tokens_k, kv_heads, dim, k_stride, box_keys, 1) ||
+      !make_map_heads(&mv, v, tokens_k, kv_heads, dim, v_stride, box_keys, 1))
     return cudaErrorInvalidValue;
   if (dim == 64) return launch_packed<64>(mq, mk, mv, a, err_flag, s);
   if (dim == 128) return launch_packed<128>(mq, mk, mv, a, err_flag, s);
