@@ -52,18 +52,16 @@ constexpr int BLK = TQ * 128;      // bytes of 128 rows x 64 bf16 (one swizzled 
 
 template <int D>
 struct PShape {
-  // Keys of a tile: as many as two score buffers for each query tile leave TMEM for. A step has
-  // fixed costs (hand-overs, waits, the issue of its MMAs) of about 600 cycles.
-  static constexpr int TK = D == 64 ? 96 : 64;
+  static constexpr int TK = 64;                     // keys of a tile
   static constexpr int NBUF = 2;                    // score buffers of a query tile
   static constexpr int TM = TK * NBUF + D;          // its columns of TMEM: scores, then output
   static constexpr int NB = D / 64;                 // 64-column blocks
   static constexpr int KBLK = TK * 128;             // bytes of one block of K or V
   static constexpr int QTILE = NB * BLK, TILE = NB * KBLK;   // bytes of a Q tile, of K or V
-  static constexpr int STAGES = D == 64 ? 5 : 4;    // of the ring: V_j and K_{j + NBUF}
+  static constexpr int STAGES = D == 64 ? 8 : 4;    // of the ring: V_j and K_{j + NBUF}
   static constexpr int OFF_RING = 2 * QTILE;
-  static constexpr int OFF_OUT = OFF_RING + STAGES * 2 * TILE;   // read-out: 32 rows x 64 B a warp
-  static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
+  static constexpr int OFF_OUT = OFF_RING + STAGES * 2 * TILE;   // read-out: 2 x 32 rows x 64 B a warp
+  static constexpr int OFF_BAR = OFF_OUT + 8 * 4096;
   // kv_full[STAGES], kv_empty[STAGES], edge_full[STAGES], q_full[2], q_empty[2], s_full[2][NBUF],
   // p_full[2][NBUF], pv[2][NBUF], item_full[2], item_empty[2], next, teardown
   static constexpr int NUM_BARS = 3 * STAGES + 10 + 6 * NBUF;
@@ -80,6 +78,7 @@ struct PArgs {
   long long v_stride;
   const int *cu_q, *cu_k;
   int tokens_q, tokens_k, batch, q_heads, kv_heads, group, per_tile, frame;
+  unsigned long long frame_inv;   // floor(2^63 / frame) + 1
   float scale_log2;
 };
 
@@ -183,12 +182,14 @@ __device__ __forceinline__ void w_commit(uint32_t bar, uint32_t leader) {
   asm volatile("{\n\t.reg .pred q;\n\t" "setp.ne.b32 q, %1, 0;\n\t"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader) : "memory");
 }
-// Keys that token i of a sequence sees.
-__device__ __forceinline__ int limit_of(const Item& it, int i, int frame) {
+// Keys that token i of a sequence sees. floor(p / frame) for 0 <= p < 2^31 as the high half of
+// 2 p * frame_inv: the product exceeds 2^64 p / frame by less than 2 p <= 2^32, too little to
+// reach the next multiple (a division's latency was a third of an item's start).
+__device__ __forceinline__ int limit_of(const Item& it, int i, const PArgs& a) {
   const int p = i + it.nk - it.nq;
   if (p < 0) return 0;
-  if (frame == 1) return p + 1;
-  const long long lim = ((long long)(p / frame) + 1) * frame;
+  const long long f = (long long)__umul64hi(2ull * (unsigned)p, a.frame_inv);
+  const long long lim = (f + 1) * a.frame;
   return lim < it.nk ? (int)lim : it.nk;
 }
 
@@ -238,9 +239,9 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const int t = it.t0 + w * a.per_tile, last = min(it.nq, t + a.per_tile) - 1;
-        it.nt[w] = t < it.nq ? (limit_of(it, last, a.frame) + TK - 1) / TK : 0;
+        it.nt[w] = t < it.nq ? (limit_of(it, last, a) + TK - 1) / TK : 0;
       }
-      it.first_edge = limit_of(it, it.t0, a.frame) / TK;
+      it.first_edge = limit_of(it, it.t0, a) / TK;
       cur.s0 = s0;
       cur.base = base;
       return;
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const float scale_log2 = a.scale_log2;
     const float inv_group = 1.0f / a.group;
     const int row_tok = row / a.group, row_head = row % a.group;
-    uint8_t* stage = smem + S::OFF_OUT + warp * 2048;
+    uint8_t* const stage = smem + S::OFF_OUT + warp * 4096;
     // a warp goes on, or gives up, as one: what follows a wait are warp-wide instructions
     auto all_wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const Item it = items[i & 1];
         const int tok = it.t0 + w * span + row_tok;             // within the sequence
         mine = row < span * a.group && tok < it.nq;
-        if (mine) lim = limit_of(it, tok, a.frame);
+        if (mine) lim = limit_of(it, tok, a);
       }
       const int lim_min = __reduce_min_sync(0xffffffffu, lim);
       const bool active = __any_sync(0xffffffffu, mine);
@@ -718,9 +719,19 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const bool empty = l == 0.f;
         const float inv = empty ? 0.f : 1.f / l;
         const bool fix = ntw > 0 && slot->dirty != 0;
+        // this lane stores 16 bytes of row 8 g + lane / 4 at a time: an offset each (-1: not a row)
+        long long to[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int R = quarter * 32 + 8 * g + (lane >> 2), rt = (int)((R + 0.5f) * inv_group);   // R / group
+          to[g] = rt < span && rt < left
+                      ? ((long long)(q0 + t0 + rt) * a.q_heads + head * a.group + (R - rt * a.group)) * D
+                      : -1;
+        }
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           const int col = 32 * q;
+          uint8_t* const buffer = stage + (q & 1) * 2048;   // two: one barrier a pass is enough
           uint32_t ov[32];
           if (ntw > 0) {
             tmem_ld32_async(tOw + 32 * q, ov);
@@ -751,21 +762,16 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                                                              __uint_as_float(ov[8 * c + 2 * k + 1]));
               u[k] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (c ^ ((lane >> 1) & 3))) =
+            *reinterpret_cast<uint4*>(buffer + lane * 64 + 16 * (c ^ ((lane >> 1) & 3))) =
                 make_uint4(u[0], u[1], u[2], u[3]);
           }
           __syncwarp();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const int rr = 8 * g + (lane >> 2), chunk = lane & 3;
-            const int R = quarter * 32 + rr, rt = (int)((R + 0.5f) * inv_group);   // R / group
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 64 + 16 * (chunk ^ ((rr >> 1) & 3)));
-            if (rt < span && rt < left) {
-              const long long to = (long long)(q0 + t0 + rt) * a.q_heads + head * a.group + (R - rt * a.group);
-              *reinterpret_cast<uint4*>(a.out + to * D + col + 8 * chunk) = x;
-            }
+            const uint4 x = *reinterpret_cast<const uint4*>(buffer + rr * 64 + 16 * (chunk ^ ((rr >> 1) & 3)));
+            if (to[g] >= 0) *reinterpret_cast<uint4*>(a.out + to[g] + col + 8 * chunk) = x;
           }
-          __syncwarp();
         }
         if (mine && a.lse)
           a.lse[(long long)(q0 + t0 + row_tok) * a.q_heads + head * a.group + row_head] =
@@ -839,8 +845,10 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
   a.group = q_heads / kv_heads;
   a.per_tile = TQ / a.group;
   a.frame = frame;
+  a.frame_inv = (1ull << 63) / (unsigned)frame + 1;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const int box_keys = dim == 64 ? PShape<64>::TK : PShape<128>::TK;
+  constexpr int box_keys = PShape<64>::TK;
+  static_assert(box_keys == PShape<128>::TK, "one box for both");
   CUtensorMap mq, mk, mv;
   if (!make_map_heads(&mq, q, tokens_q, q_heads, dim, q_stride, a.per_tile, a.group) ||
       !make_map_heads(&mk, k, tokens_k, kv_heads, dim, k_stride, box_keys, 1) ||
