@@ -36,7 +36,7 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int MAX_CTAS_PER_SM = 3;  // of any shape: sizes the workspace
+constexpr int MAX_CTAS_PER_SM = 4;  // of any shape: sizes the workspace
 constexpr int MIN_UNITS = 4;        // units a CTA takes at least where items are split
 constexpr int WHOLE_UNITS = 8;      // items up to this many units are not split
 constexpr int ITEM_UNITS = 2;       // what an item costs besides its units: start and joining
@@ -49,8 +49,10 @@ constexpr float P_SHIFT = 7.f, P_SLACK = 8.f;
 template <int D, int NR>
 struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
-  static constexpr int NST = 3;      // cp.async stages of a warp
-  static constexpr int CTAS = 3;     // a SM
+  // cp.async stages of a warp and CTAs a SM. Narrow heads: four CTAs with two stages hide more of
+  // a step's latency than three with three (256 candidates of 776 tokens: 97 against 103 us);
+  // heads of 128 the other way round (two long sequences: 96 against 103).
+  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3, CTAS = D == 64 && NR == 1 ? 4 : 3;
   static constexpr int KS = 2048 / D;              // keys a warp takes in a step
   static constexpr int GROUPS = KS / 16;           // 16-key groups of P V
   static constexpr int UNIT = WARPS * KS;          // keys of a unit
@@ -290,8 +292,6 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   }
   int4 begun = make_int4(0, 0, 0, 0);
   const int rows = a.q_tokens * a.group;
-  const long long v_ahead = c.v - c.k;         // bytes from a key's codes to its value's
-
   // ---- loading: the warp's steps of all segments in one stream, NST - 1 ahead of their use ----
   constexpr int CPR = D / 16;                  // 16-byte chunks of a row
   constexpr int RPI = 32 / CPR;                // rows a warp copies in one instruction
@@ -300,42 +300,65 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   Segment ld;
   int ld_step = 0, ld_stage = 0;
   bool ld_more = plan<S::UNIT>(c, a, whole, u_begin, u_end, load_cur, ld);
+  // a lane's place in a 16-key group of codes, in global and (swizzled) in shared memory
+  const uint32_t lane_from = sub * D + 16 * chunk;
+  uint32_t lane_to[16 / RPI];
+#pragma unroll
+  for (int q = 0; q < 16 / RPI; ++q) {
+    const int row = q * RPI + sub;
+    lane_to[q] = ring + row * D + 16 * (D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3));
+  }
+  const uint32_t block_bytes = (uint32_t)c.page * D, slot_mask = c.page - 1;
   int pg_next[S::GROUPS];                      // pages of the step that is issued next
   auto fetch_pages = [&]() {
+    const int key = (ld.k0 + ld_step) * S::UNIT + warp * S::KS;
+    const int* at = c.table + (long long)ld.s * c.max_pages;
 #pragma unroll
-    for (int p = 0; p < S::GROUPS; ++p) {
-      const int key = (ld.k0 + ld_step) * S::UNIT + warp * S::KS + 16 * p;
-      pg_next[p] = ld_more && key < ld.len
-                       ? __ldg(c.table + (long long)ld.s * c.max_pages + (key >> c.page_log2))
-                       : -1;
-    }
+    for (int p = 0; p < S::GROUPS; ++p)
+      pg_next[p] = ld_more && key + 16 * p < ld.len ? __ldg(at + ((key + 16 * p) >> c.page_log2)) : -1;
   };
   auto issue = [&]() {                         // the next step of the stream into the next stage
     const int key0 = (ld.k0 + ld_step) * S::UNIT + warp * S::KS;
     if (ld_more && key0 < ld.len) {
-      const uint32_t st = ring + ld_stage * S::STAGE;
-      const int head = ld.item / a.tiles;
+      const uint32_t st = ld_stage * S::STAGE;
+      const uint32_t head = ld.item / a.tiles;
+      bool whole_step = key0 + S::KS <= ld.len;
+      uint32_t block[S::GROUPS];               // num_pages * heads is below 2^31
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
-        const bool page_ok = pg_next[p] >= 0 && pg_next[p] < c.num_pages;
-        const int pg = page_ok ? pg_next[p] : 0, key_p = key0 + 16 * p;
-        const int keys = page_ok ? min(16, ld.len - key_p) : 0;      // of this group that are there
-        const long long block = (long long)pg * c.heads + head;
-        const uint8_t* from = c.k + (block * c.page + (key_p & (c.page - 1)) + sub) * D + 16 * chunk;
+        const bool there = (uint32_t)pg_next[p] < (uint32_t)c.num_pages;
+        if (!there && key0 + 16 * p < ld.len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+        whole_step = whole_step && there;
+        block[p] = (there ? (uint32_t)pg_next[p] : 0u) * (uint32_t)c.heads + head;
+      }
 #pragma unroll
-        for (int q = 0; q < 16 / RPI; ++q) {
-          const int row = 16 * p + q * RPI + sub;
-          const int sw = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-          const uint32_t to = st + row * D + 16 * sw;
-          const uint32_t bytes = q * RPI + sub < keys ? 16 : 0;
-          cp16(to, from + q * RPI * D, bytes);
-          cp16(to + S::KS * D, from + v_ahead + q * RPI * D, bytes);
+      for (int p = 0; p < S::GROUPS; ++p) {
+        const uint64_t from = (uint64_t)block[p] * block_bytes +
+                              (((uint32_t)(key0 + 16 * p) & slot_mask) * D + lane_from);
+        const uint8_t *fk = c.k + from, *fv = c.v + from;
+        if (whole_step) {
+#pragma unroll
+          for (int q = 0; q < 16 / RPI; ++q) {
+            cp16(lane_to[q] + st + 16 * p * D, fk + q * RPI * D, 16);
+            cp16(lane_to[q] + st + 16 * p * D + S::KS * D, fv + q * RPI * D, 16);
+          }
+        } else {                               // keys past the end, or without a page, are zeros
+          const int keys = (uint32_t)pg_next[p] < (uint32_t)c.num_pages ? ld.len - (key0 + 16 * p) : 0;
+#pragma unroll
+          for (int q = 0; q < 16 / RPI; ++q) {
+            const uint32_t bytes = q * RPI + sub < keys ? 16 : 0;
+            cp16(lane_to[q] + st + 16 * p * D, fk + q * RPI * D, bytes);
+            cp16(lane_to[q] + st + 16 * p * D + S::KS * D, fv + q * RPI * D, bytes);
+          }
         }
-        if (lane < 2) {
-          if (!page_ok && key_p < ld.len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
-          cp4(ring_sc + ld_stage * 16 + (2 * p + lane) * 4, (lane ? c.v_scale : c.k_scale) + block,
-              page_ok ? 4 : 0);
-        }
+      }
+      if (lane < 2 * S::GROUPS) {              // k, v scale of each group
+        const int p = lane >> 1;
+        const bool there =
+            (uint32_t)(S::GROUPS == 1 || p == 0 ? pg_next[0] : pg_next[S::GROUPS - 1]) < (uint32_t)c.num_pages;
+        cp4(ring_sc + ld_stage * 16 + lane * 4,
+            ((lane & 1) ? c.v_scale : c.k_scale) + (p == 0 ? block[0] : block[S::GROUPS - 1]),
+            there ? 4 : 0);
       }
     }
     cp_commit();
@@ -692,11 +715,11 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
 
 // Joins the items that were split: the parts of an item lie with consecutive CTAs, the first of
 // which notes them. D / 4 lanes a row; they read all maxima side by side and then the outputs,
-// eight parts in flight: one after the other, 28 parts took 20 us.
+// 16 parts in flight: one after the other, 28 parts took 20 us.
 template <int D, int NR>
 __global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a, int max_parts) {
-  constexpr int ROWS = Shape<D, NR>::ROWS, LPR = D / 4, RPB = 128 / LPR;
-  extern __shared__ float factors[];                   // [RPB][max_parts]
+  constexpr int ROWS = Shape<D, NR>::ROWS, LPR = D / 4, RPB = 128 / LPR, AHEAD = 16;
+  extern __shared__ float factors[];                   // [2][RPB][max_parts]: maxima, sums
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are there
   const int w0 = blockIdx.x;
   const int4 split = a.split[w0];
@@ -709,7 +732,9 @@ __global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a, int max_part
   auto part = [&](int k) { return part_of<D, NR>(a, w0 + k, k == 0); };
   float mx = -INFINITY, sum = 0.f;
   for (int k = li; k < n; k += LPR) {
-    f[k] = part(k)[ROWS * D + row];
+    const float* p = part(k) + ROWS * D + row;
+    f[k] = p[0];
+    f[max_parts * RPB + k] = p[ROWS];
     mx = fmaxf(mx, f[k]);
   }
 #pragma unroll
@@ -717,17 +742,24 @@ __global__ void __launch_bounds__(128) k_combine(Kv8View c, Args a, int max_part
   for (int k = li; k < n; k += LPR) {
     const float x = f[k] == -INFINITY ? 0.f : ex2f(f[k] - mx);   // a part that saw no key holds zeros
     f[k] = x;
-    sum = fmaf(part(k)[ROWS * D + ROWS + row], x, sum);
+    sum = fmaf(f[max_parts * RPB + k], x, sum);
   }
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   __syncwarp();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(part(k) + row * D + c0);
-    acc.x = fmaf(x.x, f[k], acc.x); acc.y = fmaf(x.y, f[k], acc.y);
-    acc.z = fmaf(x.z, f[k], acc.z); acc.w = fmaf(x.w, f[k], acc.w);
+  for (int k0 = 0; k0 < n; k0 += AHEAD) {
+    float4 x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k0 + k < n) x[k] = *reinterpret_cast<const float4*>(part(k0 + k) + row * D + c0);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k0 + k < n) {
+        const float y = f[k0 + k];
+        acc.x = fmaf(x[k].x, y, acc.x); acc.y = fmaf(x[k].y, y, acc.y);
+        acc.z = fmaf(x[k].z, y, acc.z); acc.w = fmaf(x[k].w, y, acc.w);
+      }
   }
   if (r >= a.q_tokens * a.group) return;
   const long long at = row_at(a, s, head, r);
@@ -768,7 +800,7 @@ cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, S::ROWS * D / 512);
   cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = (512 / D) * grid * sizeof(float);   // 15 KB at most
+  cfg.dynamicSmemBytes = 2 * (512 / D) * grid * sizeof(float);   // 30 KB at most
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -127,9 +127,10 @@ __device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>
                                             const float (&an)[16]) {
   constexpr int L = D / 16;
   if (w) {
-    float ss = 0.f;
+    float part[4] = {0.f, 0.f, 0.f, 0.f};   // short chains: fewer roundings on the way
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
+    for (int i = 0; i < 16; ++i) part[i & 3] = fmaf(y[i], y[i], part[i & 3]);
+    float ss = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = __frsqrt_rn(ss * (1.0f / D) + eps);

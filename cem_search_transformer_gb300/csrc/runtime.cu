@@ -1281,7 +1281,8 @@ static jepa_status kv8_view(jepa_ctx* ctx, const char* what, const jepa_kv8_cach
     return fail(ctx, JEPA_ERR_SHAPE, "%s: page_size must be 16, 32, 64 or 128", what);
   if (c->num_pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024 || c->batch < 1 ||
       c->batch > 65535 || c->max_pages < 1 ||
-      (long long)c->max_pages * c->page_size > (1LL << 30))
+      (long long)c->max_pages * c->page_size > (1LL << 30) ||
+      (long long)c->num_pages * c->kv_heads > 0x7fffffffLL)
     return fail(ctx, JEPA_ERR_SHAPE, "%s: cache sizes out of range", what);
   *out = Kv8View{c->k, c->v, c->k_scale, c->v_scale, c->page_table, c->num_pages, c->page_size,
                  c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7,

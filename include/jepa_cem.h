@@ -308,7 +308,8 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  * v_scale [num_pages][kv_heads] float32: an element stands for code * scale. page_table
  * [batch][max_pages] int32: token t of sequence b lies in page page_table[b][t / page_size],
  * slot t % page_size; entries past a sequence's length are not read. head_dim 64 or 128,
- * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30; k and v 16-byte aligned. Scales
+ * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30, num_pages * kv_heads < 2^31; k and v 16-byte
+ * aligned. Scales
  * lie in [2^-40, 2^40] (others are read as the nearer end); those written here are powers of
  * two. The codes and scales of fresh pages need no initial values. */
 typedef struct {
