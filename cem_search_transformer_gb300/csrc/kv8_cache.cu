@@ -380,10 +380,15 @@ __global__ void __launch_bounds__(THREADS, 2) k_append_pages(Kv8View c, AppendAr
   const bf16* src = (is_v ? a.v : a.k) + (long long)head * D;
   const long long stride = is_v ? a.v_stride : a.k_stride;
   Place at = locate(a.cu, a.start, c.batch, t0);
-  if (at.s < 0) return;
+  if (at.s < 0) {                          // the chunk begins ahead of the first sequence
+    at.s = 0;
+    at.begin = __ldg(a.cu);
+    at.end = __ldg(a.cu + 1);
+    at.first = __ldg(a.start);
+  }
   const int t1 = min(t0 + c.page, a.tokens);
   int parity = 0;
-  for (int t = t0; t < t1;) {
+  for (int t = max(t0, at.begin); t < t1;) {
     while (t >= at.end) {                  // the next sequence that has tokens
       if (++at.s >= c.batch) return;
       at.begin = at.end;

@@ -547,3 +547,123 @@ def test_graph_replay_reads_lengths_anew_and_streams_run_apart(planner):
     for _ in range(3):
         assert torch.equal(direct([3000, 50]), want[(3000, 50)])
     del calls
+
+
+@pytest.mark.parametrize("by_warp", [True, False])
+def test_tokens_ahead_of_the_first_sequence_are_left(planner, by_warp):
+    """Offsets that begin behind packed token 0: the rows ahead belong to nobody."""
+    n, ahead, heads, dim, page = 70, 37, 2, 64, 32
+    pool = Pool([n], heads, page, dim)
+    pad = n if by_warp else 0
+    x = bf16(np.random.default_rng(3).standard_normal((n + ahead, heads, dim))).cuda()
+    from cem_search_transformer_gb300 import binding
+    t = np.full((1 + pad, pool.table_np.shape[1]), -1)
+    t[0] = pool.table_np[0]
+    cache = binding.KvCache8(pool.k, pool.v, pool.ks, pool.vs, i32(t))
+    cu = i32([ahead] + [ahead + n] * (1 + pad))
+    q_out = torch.full_like(x, 5.0)
+    planner.rope_append_kv8(x, x, x, None, cu, i32([0] * (1 + pad)), cache, q_out)
+    k, v = torch.full_like(x, 5.0), torch.full_like(x, 5.0)
+    planner.kv8_read(cache, cu, i32([0] * (1 + pad)), k, v)
+    planner.sync_check()
+    for got in (q_out, k, v):
+        assert torch.all(got[:ahead] == 5)
+    assert torch.equal(q_out[ahead:], x[ahead:])
+    ref = f64(x)[ahead:]
+    for lo in range(0, n, page):
+        for h in range(heads):
+            codes, scale = paged.append_block(np.zeros((0, dim)), 1.0, ref[lo:lo + page, h])
+            assert np.array_equal(f64(k[ahead:])[lo:lo + page, h], codes * scale)
+            assert np.array_equal(f64(v[ahead:])[lo:lo + page, h], codes * scale)
+
+
+def test_thousands_of_sequences(planner):
+    """More sequences than two levels of the search hold, most of them with one token or none."""
+    rng = np.random.default_rng(8)
+    batch, heads, dim, page = 2500, 1, 64, 16
+    new = rng.integers(0, 3, batch)
+    old = rng.integers(0, 20, batch)
+    n = int(new.sum())
+    most = -(-int((new + old).max()) // page)
+    table = np.arange(batch * most).reshape(batch, most)
+    from cem_search_transformer_gb300 import binding
+    shape = (batch * most, heads, page, dim)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full(shape[:2], 2.0 ** -8, device="cuda") for _ in range(2))
+    cache = binding.KvCache8(k, v, ks, vs, i32(table))
+    x = bf16(rng.standard_normal((n, heads, dim))).cuda()
+    planner.rope_append_kv8(None, x, x, None, cu_of(new), i32(old), cache, None)
+    got, got_v = torch.empty_like(x), torch.empty_like(x)
+    planner.kv8_read(cache, cu_of(new), i32(old), got, got_v)
+    planner.sync_check()
+    err = np.abs(f64(got) - f64(x))
+    top = np.abs(f64(x)).max((1, 2), keepdims=True)
+    # half an e4m3 step; the block's scale is set by at most its two new tokens (and 2^-8 before)
+    assert np.all(err <= np.maximum(np.abs(f64(x)) * 2.0 ** -4, 2 * 4 * top.max() / 448 * 2.0 ** -10))
+    assert torch.equal(got, got_v)
+    q = bf16(rng.standard_normal((batch, 1, 2, dim))).cuda()
+    lens = new + old
+    out = torch.full_like(q, 3.0)
+    ws = torch.empty(planner.attention_kv8_workspace(cache), dtype=torch.uint8, device="cuda")
+    planner.attention_kv8(q, cache, i32(lens), out, 0.125, ws)
+    planner.sync_check()
+    assert torch.all(out[torch.from_numpy(lens == 0).cuda()] == 0)
+    for s in rng.integers(0, batch, 20):
+        m = int(lens[s])
+        if m:
+            pages = [int(p) for p in table[s][:-(-m // page)]]
+            kk, vv = (np.concatenate([(codes_f64(c[p]) * f64(sc[p])[:, None, None]).transpose(1, 0, 2) for p in pages])[:m]
+                      for c, sc in ((k, ks), (v, vs)))
+            want, _, a, s_abs = paged.softmax_rows(f64(q[s]), kk, vv, [m], 0.125)
+            assert np.all(np.abs(f64(out[s]) - want) <= attention_tolerance(want, a, s_abs, m, dim, np.abs(vv).max()))
+
+
+def test_offsets_past_32_bits(planner):
+    """Pages behind the first 4 GiB of a pool: appended, read back and attended to."""
+    from cem_search_transformer_gb300 import binding
+    heads, page, dim = 8, 64, 128
+    pages = (5 << 30) // (heads * page * dim)
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB")
+    k, v = (torch.empty(pages, heads, page, dim, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(pages, heads, device="cuda") for _ in range(2))
+    lens = [150, 90]
+    table = np.array([[pages - 1, 3, pages - 7], [pages - 2, pages - 3, 0]])
+    cache = binding.KvCache8(k, v, ks, vs, i32(table))
+    x = bf16(np.random.default_rng(2).standard_normal((sum(lens), heads, dim))).cuda()
+    y = bf16(np.random.default_rng(3).standard_normal((sum(lens), heads, dim))).cuda()
+    planner.rope_append_kv8(None, x, y, None, cu_of(lens), i32([0, 0]), cache, None)
+    rk, rv = torch.empty_like(x), torch.empty_like(x)
+    planner.kv8_read(cache, cu_of(lens), i32([0, 0]), rk, rv)
+    planner.sync_check()
+    for got, want in ((rk, x), (rv, y)):
+        assert np.all(np.abs(f64(got) - f64(want)) <= np.maximum(np.abs(f64(want)) * 2.0 ** -4, 2 * 6.0 / 448 * 2.0 ** -10))
+    q = bf16(np.random.default_rng(4).standard_normal((2, 1, 16, dim))).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(planner.attention_kv8_workspace(cache), dtype=torch.uint8, device="cuda")
+    planner.attention_kv8(q, cache, i32(lens), out, dim ** -0.5, ws)
+    planner.sync_check()
+    at = 0
+    for s, n in enumerate(lens):
+        kk, vv = f64(rk[at:at + n]), f64(rv[at:at + n])
+        at += n
+        want, _, a, s_abs = paged.softmax_rows(f64(q[s]), kk, vv, [n], dim ** -0.5)
+        assert np.all(np.abs(f64(out[s]) - want) <= attention_tolerance(want, a, s_abs, n, dim, np.abs(vv).max()))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scales_that_are_no_powers_of_two(planner, dim):
+    """A cache written by others: any scale in the range stands for code * scale."""
+    lens = [400, 37]
+    pool = Pool(lens, 2, 32, dim)
+    ref = pool.fill(lens, 3)
+    rng = np.random.default_rng(1)
+    for s in range(2):
+        for i in range(-(-lens[s] // 32)):
+            pg, rows = int(pool.table_np[s, i]), slice(32 * i, min(lens[s], 32 * i + 32))
+            for scales, which in ((pool.ks, 0), (pool.vs, 1)):
+                f = rng.uniform(0.6, 1.7, 2).astype(np.float32)
+                old = f64(scales[pg])
+                scales[pg] = cuda(f) * scales[pg]
+                ref[s][which][rows] *= (f64(scales[pg]) / old)[None, :, None]
+    check_attention(planner, pool, ref, lens, 1, 4, True, seed=1)
