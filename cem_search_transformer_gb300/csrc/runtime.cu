@@ -1424,8 +1424,9 @@ jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_st
       bad_ptr(cu_q) || bad_ptr(cu_k) || bad_ptr(out) || !aligned(out, 16) || !aligned(lse, 4) ||
       !(scale > 0.f) || !std::isfinite(scale) || frame < 1)
     return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_packed: bad argument");
-  if (q_heads / kv_heads > 128 || tokens_q > (1 << 30) || tokens_k > (1 << 30))
-    return fail(ctx, JEPA_ERR_SHAPE, "attention_packed: more than 128 heads a group, or too many tokens");
+  // 2^27 keys are about a second of one CTA's steps: within the limit of a device wait
+  if (q_heads / kv_heads > 128 || tokens_q > (1 << 27) || tokens_k > (1 << 27))
+    return fail(ctx, JEPA_ERR_SHAPE, "attention_packed: more than 128 heads a group, or 2^27 tokens");
   OnDevice on(ctx->device);
   CK(on.status);
   CK(attention_packed((const bf16*)q, q_stride, (const bf16*)k, k_stride, (const bf16*)v, v_stride,

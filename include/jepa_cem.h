@@ -298,7 +298,8 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  * heads * head_dim, a multiple of 8), so q, k and v may be slices of one projection's rows.
  *
  * Packed sequences: `cu` [batch + 1] int32 dev, ascending; sequence b owns packed tokens cu[b] ..
- * cu[b+1] - 1 (none is fine). Output rows behind the last sequence are left as they were.
+ * cu[b+1] - 1 (none is fine). Output rows ahead of the first sequence and behind the last are left
+ * as they were.
  *
  * A page index, position, length or offset on the device that lies outside its buffer is never
  * followed: what depends on it is skipped or read as zero (those outputs are unspecified), and
@@ -308,10 +309,10 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  * v_scale [num_pages][kv_heads] float32: an element stands for code * scale. page_table
  * [batch][max_pages] int32: token t of sequence b lies in page page_table[b][t / page_size],
  * slot t % page_size; entries past a sequence's length are not read. head_dim 64 or 128,
- * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30, num_pages * kv_heads < 2^31; k and v 16-byte
- * aligned. Scales
- * lie in [2^-40, 2^40] (others are read as the nearer end); those written here are powers of
- * two. The codes and scales of fresh pages need no initial values. */
+ * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30, num_pages * kv_heads < 2^31; k and
+ * v 16-byte aligned. Scales lie in [2^-40, 2^40] (others are read as the nearer end, NaN as the
+ * least); those written here are powers of two. The codes and scales of fresh pages need no
+ * initial values. */
 typedef struct {
   uint8_t* k;
   uint8_t* v;
@@ -344,7 +345,7 @@ jepa_status jepa_rope_table(jepa_ctx* ctx, int positions, int rot, double base, 
  *   rope_table [positions][rot]; cu [batch + 1], start [batch] int32 dev.
  *   q_heads a multiple of kv_heads; rot a multiple of 16, 0 <= rot <= head_dim (0: no rotation);
  *   q_out may be q and k_out may be k where those rows are dense; no other overlap.
- * A page that receives tokens belongs to one sequence of the batch (shared pages are full). */
+ * A page that receives tokens belongs to one place of one sequence (shared pages are full). */
 jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
                                  int64_t q_stride, const uint16_t* k, int64_t k_stride,
                                  const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
@@ -388,7 +389,8 @@ jepa_status jepa_attention_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const
  *   aligned, dev; cu_q, cu_k [batch + 1]; out [tokens_q][q_heads][head_dim] dense, 16-byte
  *   aligned; lse [tokens_q][q_heads] float32 or NULL, as in jepa_attention_kv8, whose promises
  *   for unseen keys and empty rows hold here too. head_dim 64 or 128, q_heads a multiple of
- *   kv_heads with at most 128 per key/value head, scale finite and > 0, frame >= 1. */
+ *   kv_heads with at most 128 per key/value head, scale finite and > 0, frame >= 1, tokens_q and
+ *   tokens_k at most 2^27. */
 jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_stride,
                                   const uint16_t* k, int64_t k_stride, const uint16_t* v,
                                   int64_t v_stride, int tokens_q, int tokens_k, int batch,

@@ -72,6 +72,7 @@ def check(planner, nq, nk, q_heads, kv_heads, dim, frame=1, seed=0, behind=0, sc
     ([90], [90], 7, 1, 128, 1),
     ([40, 9], [40, 9], 16, 1, 64, 1),
     ([3], [130], 128, 1, 64, 1),                           # one token a tile
+    ([4], [4], 100, 1, 128, 1),
     ([10, 200], [300, 200], 4, 1, 128, 1),                 # a cached beginning
     ([50, 20], [20, 0], 4, 2, 64, 1),                      # rows that see nothing; no keys at all
     ([300], [40], 1, 1, 128, 1),                           # tiles that see nothing
@@ -139,6 +140,27 @@ def test_bad_offsets_are_skipped_and_reported(planner):
         with pytest.raises(binding.JepaError, match=match):
             planner.attention_packed(**args)
     planner.sync_check()
+
+
+def test_nan_queries_stay_in_their_row(planner):
+    q, k, v, clean = check(planner, [140], [140], 2, 1, 128, seed=4)
+    q = q.contiguous()
+    q[50, 1, 3] = float("nan")
+    q[100, 0, 5] = float("inf")
+    out, lse = call(planner, q, k, v, [140], [140])
+    bad = torch.zeros(140, 2, dtype=torch.bool, device="cuda")
+    bad[50, 1] = bad[100, 0] = True
+    assert torch.all(torch.isnan(out[bad])) and torch.all(torch.isnan(lse[bad]))
+    assert torch.equal(out[~bad], clean[~bad])
+
+
+def test_offsets_that_begin_behind_token_0(planner):
+    x = [bf16(np.random.default_rng(i).standard_normal((200, h, 64))).cuda() for i, h in enumerate((4, 2, 2))]
+    want, _ = call(planner, x[0][30:], x[1][50:], x[2][50:], [100], [150])
+    out = torch.full_like(x[0], 9.0)
+    planner.attention_packed(*x, i32([30, 130]), i32([50, 200]), out, 0.125)
+    planner.sync_check()
+    assert torch.equal(out[30:130], want[:100]) and torch.all(out[:30] == 9) and torch.all(out[130:] == 9)
 
 
 def test_graph_replay(planner):
