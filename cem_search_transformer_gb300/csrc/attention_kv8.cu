@@ -51,8 +51,11 @@ struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
   // cp.async stages of a warp and CTAs a SM. Narrow heads: four CTAs with two stages hide more of
   // a step's latency than three with three (256 candidates of 776 tokens: 97 against 103 us);
-  // heads of 128 the other way round (two long sequences: 96 against 103).
-  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3, CTAS = D == 64 && NR == 1 ? 4 : 3;
+  // heads of 128 the other way round (two long sequences: 96 against 103). Two row tiles of 128
+  // columns need 250 registers a thread and 82 KB, so two CTAs (32 sequences of up to 8000
+  // tokens, 16 rows: 89 us; 110 with three CTAs of two stages, which spill).
+  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;
+  static constexpr int CTAS = D == 64 ? (NR == 1 ? 4 : 3) : (NR == 1 ? 3 : 2);
   static constexpr int KS = 2048 / D;              // keys a warp takes in a step
   static constexpr int GROUPS = KS / 16;           // 16-key groups of P V
   static constexpr int UNIT = WARPS * KS;          // keys of a unit
@@ -64,6 +67,7 @@ struct Shape {
   static constexpr int OFF_SCALE = WARPS * NST * STAGE;
   static constexpr int OFF_OUT = OFF_SCALE + WARPS * NST * 16;
   static constexpr int SMEM = OFF_OUT + WARPS * ROWS * OUT_LD * 4;
+  static_assert(CTAS <= MAX_CTAS_PER_SM && CTAS * (SMEM + 2048) <= 228 * 1024, "CTAs of a SM");
 };
 
 __device__ __forceinline__ float ex2f(float x) {

@@ -348,6 +348,7 @@ __device__ __forceinline__ void append_short(const Kv8View& c, const AppendArgs&
 template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS) k_append_short(Kv8View c, AppendArgs a, long long kv_units,
                                                           int* err_flag) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long unit = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
   if (unit < kv_units)
     append_short<D, INTER>(c, a, unit, err_flag);
@@ -357,15 +358,32 @@ __global__ void __launch_bounds__(THREADS) k_append_short(Kv8View c, AppendArgs 
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 4) k_rope_queries(Kv8View c, AppendArgs a, int* err_flag) {
+  asm volatile("griddepcontrol.launch_dependents;");
   rotate_queries<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
+}
+
+// Launch that, with `early`, begins while the kernel before it in the stream still runs: what may
+// not overlap stands behind a griddepcontrol.wait, which lasts until that kernel's end.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, bool early, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = early;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Long appends: a team of T warps takes a chunk of `page` packed tokens of one head, k or v, and
 // quantises the pages that have their owner in it (two at most for a long sequence). Each lane
 // holds IT rows' 16 elements between the maximum and the codes, so that the rows are read once.
 template <int D, bool INTER, int T, int IT>
-__global__ void __launch_bounds__(THREADS, 2) k_append_pages(Kv8View c, AppendArgs a, long long units,
-                                                          int* err_flag) {
+__device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs& a, long long units,
+                                             int* err_flag) {
   constexpr int L = D / 16, WARPS = THREADS / 32, ROWS = T * (32 / L);   // tokens a pass
   __shared__ float red[2][WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / T;
@@ -453,6 +471,16 @@ __global__ void __launch_bounds__(THREADS, 2) k_append_pages(Kv8View c, AppendAr
   }
 }
 
+// The pages share no data with the queries' kernel ahead of them and run beside its last blocks (24
+// frames of 258 tokens: 35 us with the read-back that follows, 42 one after the other); the wait
+// at the end keeps the order for what comes next.
+template <int D, bool INTER, int T, int IT>
+__global__ void __launch_bounds__(THREADS, 2)
+    k_append_pages(Kv8View c, AppendArgs a, long long units, int* err_flag) {
+  append_pages<D, INTER, T, IT>(c, a, units, err_flag);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Cached tokens back as bf16 (code * power of two has at most four significant bits: exact).
 // A warp per packed token; a lane moves 16 codes at a time.
 template <int D>
@@ -460,6 +488,7 @@ __global__ void __launch_bounds__(THREADS) k_kv8_read(Kv8View c, const int* __re
                                                       const int* __restrict__ first, int tokens,
                                                       bf16* __restrict__ k_out,
                                                       bf16* __restrict__ v_out, int* err_flag) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t = (int)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= tokens) return;
@@ -529,8 +558,7 @@ cudaError_t launch_pages(const Kv8View& c, const AppendArgs& a, int* err_flag, c
   const long long units = (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads * 2;
   const long long blocks = (units + TEAMS - 1) / TEAMS;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  k_append_pages<D, INTER, T, IT><<<(unsigned)blocks, THREADS, 0, s>>>(c, a, units, err_flag);
-  return cudaGetLastError();
+  return launch_early(k_append_pages<D, INTER, T, IT>, (unsigned)blocks, a.q != nullptr, s, c, a, units, err_flag);
 }
 
 template <int D, bool INTER>
@@ -542,8 +570,7 @@ cudaError_t launch_append(const Kv8View& c, const AppendArgs& a, int* err_flag, 
     const long long kv_units = 2LL * a.tokens * ((c.heads + HEADS - 1) / HEADS);
     const long long blocks = (kv_units + q_units + WARPS - 1) / WARPS;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    k_append_short<D, INTER><<<(unsigned)blocks, THREADS, 0, s>>>(c, a, kv_units, err_flag);
-    return cudaGetLastError();
+    return launch_early(k_append_short<D, INTER>, (unsigned)blocks, true, s, c, a, kv_units, err_flag);
   }
   if (q_units) {
     const long long blocks = (q_units + WARPS - 1) / WARPS;
@@ -587,12 +614,10 @@ cudaError_t kv8_read(const Kv8View& c, const int* cu, const int* first, int toke
   if (tokens <= 0) return cudaSuccess;
   const unsigned grid = (unsigned)(((long long)tokens * 32 + THREADS - 1) / THREADS);
   if (c.dim == 64)
-    k_kv8_read<64><<<grid, THREADS, 0, s>>>(c, cu, first, tokens, k_out, v_out, err_flag);
-  else if (c.dim == 128)
-    k_kv8_read<128><<<grid, THREADS, 0, s>>>(c, cu, first, tokens, k_out, v_out, err_flag);
-  else
-    return cudaErrorInvalidValue;
-  return cudaGetLastError();
+    return launch_early(k_kv8_read<64>, grid, true, s, c, cu, first, tokens, k_out, v_out, err_flag);
+  if (c.dim == 128)
+    return launch_early(k_kv8_read<128>, grid, true, s, c, cu, first, tokens, k_out, v_out, err_flag);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t rope_table(int positions, int rot, double base, double factor, float* table,

@@ -667,3 +667,68 @@ def test_scales_that_are_no_powers_of_two(planner, dim):
                 scales[pg] = cuda(f) * scales[pg]
                 ref[s][which][rows] *= (f64(scales[pg]) / old)[None, :, None]
     check_attention(planner, pool, ref, lens, 1, 4, True, seed=1)
+
+
+@pytest.mark.parametrize("n_new", [[1, 1, 1], [70, 3, 129]])
+def test_captured_append_attention_and_read(planner, n_new):
+    """Copies, fills, torch's kernels and a joined stream ahead of the calls of one graph."""
+    page, dim, heads, q_heads = 32, 64, 2, 4
+    old = [40, 0, 95]
+    total, cu = sum(n_new), cu_of(n_new)
+    lens = [a + b for a, b in zip(old, n_new)]
+    start, kv_len = i32(old), i32(lens)
+    rng = np.random.default_rng(21)
+    rounds = [[bf16(rng.standard_normal((total, h, dim))).cuda() for h in (q_heads, heads, heads)] for _ in range(4)]
+    rope = planner.rope_table(256, dim)
+    past = [bf16(rng.standard_normal((sum(old), heads, dim))).cuda() for _ in range(2)]
+
+    def fresh():
+        pool = Pool(lens, heads, page, dim, seed=5)
+        planner.rope_append_kv8(None, *past, rope, cu_of(old), i32([0] * 3), pool.cache, None)
+        return pool
+
+    def steps(pool, x, q_out, k, v, att, ws):
+        planner.rope_append_kv8(*x, rope, cu, start, pool.cache, q_out, stream=torch.cuda.current_stream())
+        planner.attention_kv8(q_out[-3:].unsqueeze(1), pool.cache, kv_len, att, 0.125, ws,
+                              stream=torch.cuda.current_stream())
+        planner.kv8_read(pool.cache, cu, start, k, v, stream=torch.cuda.current_stream())
+
+    def buffers():
+        return [torch.empty(total, h, dim, dtype=torch.bfloat16, device="cuda") for h in (q_heads, heads, heads)] + \
+            [torch.empty(3, 1, q_heads, dim, dtype=torch.bfloat16, device="cuda")]
+
+    pool, x, given = fresh(), [torch.empty_like(t) for t in rounds[0]], [torch.empty_like(t) for t in rounds[0]]
+    ws = torch.empty(planner.attention_kv8_workspace(pool.cache), dtype=torch.uint8, device="cuda")
+    got = buffers()
+    codes = [t.clone() for t in (pool.k, pool.v, pool.ks, pool.vs)]
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for t, s in zip((pool.k, pool.v, pool.ks, pool.vs), codes):
+            t.copy_(s)                                   # every replay begins with the same cache
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            x[0].copy_(given[0])
+        for a, b in zip(x[1:], given[1:]):
+            a.zero_()
+            a.add_(b)
+        torch.cuda.current_stream().wait_stream(other)
+        steps(pool, x, *got, ws)
+        for t in x:
+            t.zero_()                                    # the calls are done with their inputs
+    for values in rounds:
+        for a, b in zip(given, values):
+            a.copy_(b)
+        for t in got:
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+            graph.replay()
+        torch.cuda.synchronize()
+        want, again = buffers(), fresh()
+        steps(again, values, *want, ws)
+        planner.sync_check()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
