@@ -26,6 +26,12 @@
 // are there when the softmax is done with tile j: with one buffer of 128 keys a tile waited about
 // 1200 cycles for its P V and the next scores after 2200 of softmax (D = 128). The price is 64-key
 // scores MMAs, which read Q from shared memory twice as often.
+// What bounds it. D = 128: the tensor cores and the power limit (one prompt of 10007 tokens, 32
+// query heads over 8: 506 us, 1.63 PFLOP/s). D = 64: the chain of a step, scores -> softmax -> P,
+// about 1500 cycles for both tiles where the exponentials alone take 1024 and half of them left
+// out takes 6% off; and an item's 2000 to 3000 cycles between two loops, of which half is hidden
+// (32 prompts of 774 tokens, 16 heads, frames of 258: 125 us, of which 31 for the last six rows of
+// each, a tile of their own; its keys shared out over both tiles took 124, and 2% more elsewhere).
 // What lies behind a sequence's last key in its last tile is another sequence's (or nothing), and
 // a masked probability of 0 times an infinity or NaN there is NaN. So in tiles where some row's
 // limit ends, a warp zeroes V rows past the sequence and any non-finite value before the product
@@ -66,7 +72,8 @@ struct PShape {
   // p_full[2][NBUF], pv[2][NBUF], item_full[2], item_empty[2], next, teardown
   static constexpr int NUM_BARS = 3 * STAGES + 10 + 6 * NBUF;
   static constexpr int OFF_TAIL = OFF_BAR + NUM_BARS * 8;
-  static constexpr int SMEM = OFF_TAIL + 160 + 1024;
+  static constexpr int OFF_ROWS = OFF_TAIL + 176;   // (token, place among its heads) of a tile's rows
+  static constexpr int SMEM = OFF_ROWS + TQ * 8 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   static_assert(2 * TM <= (int)P_TMEM && TK % 32 == 0 && KBLK % 1024 == 0, "tiles");
 };
@@ -102,6 +109,11 @@ struct Cursor {
 __device__ __forceinline__ float p_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float p_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float p_max3(float a, float b, float c) {
@@ -306,6 +318,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int span = a.per_tile;
+  int2* const tile_rows = (int2*)(smem + S::OFF_ROWS);
+  if (threadIdx.x < TQ) {
+    const int t = threadIdx.x / a.group;
+    tile_rows[threadIdx.x] = make_int2(t < span ? t : 0x7fffffff, t * a.q_heads + (threadIdx.x - t * a.group));
+  }
   Cursor cursor{0, 0};
   if (warp == W_TMA) {
     Item it;
@@ -578,7 +595,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tOw = tO(w) + lane_off;
     const float scale_log2 = a.scale_log2;
-    const float inv_group = 1.0f / a.group;
     const int row_tok = row / a.group, row_head = row % a.group;
     uint8_t* const stage = smem + S::OFF_OUT + warp * 4096;
     // a warp goes on, or gives up, as one: what follows a wait are warp-wide instructions
@@ -587,23 +603,30 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     };
     int buf = 0;           // score buffer and lap of the next key tile
     uint32_t lap = 0;
-    bool ok = true;
+    // what the row does next: read ahead, while the last product of the item before it runs (the
+    // producer hands an item over without waiting for the read-out of the one before)
+    struct Ahead {
+      bool valid, mine, active;
+      int ntw, lim, lim_min;
+    } next;
+    auto look = [&](int i) {
+      if (!all_wait(item_full(i & 1), (i >> 1) & 1)) return false;
+      const Item it = items[i & 1];
+      next.valid = it.valid;
+      next.ntw = ((const volatile Item*)items)[i & 1].nt[w];
+      const int tok = it.t0 + w * span + row_tok;               // within the sequence
+      next.mine = row_tok < span && tok < it.nq;
+      next.lim = next.mine ? limit_of(it, tok, a) : 0x7fffffff;
+      next.lim_min = __reduce_min_sync(0xffffffffu, next.lim);
+      next.active = __any_sync(0xffffffffu, next.mine);
+      return true;
+    };
+    bool ok = look(0);
     for (int i = 0; ok; ++i) {
-      ok = all_wait(item_full(i & 1), (i >> 1) & 1);
-      if (!ok) break;
+      if (!next.valid) break;
       const volatile Item* slot = &items[i & 1];
-      if (!slot->valid) break;
-      const int ntw = slot->nt[w];
-      int lim = 0x7fffffff;
-      bool mine;
-      {
-        const Item it = items[i & 1];
-        const int tok = it.t0 + w * span + row_tok;             // within the sequence
-        mine = row < span * a.group && tok < it.nq;
-        if (mine) lim = limit_of(it, tok, a);
-      }
-      const int lim_min = __reduce_min_sync(0xffffffffu, lim);
-      const bool active = __any_sync(0xffffffffu, mine);
+      const int ntw = next.ntw, lim = next.lim, lim_min = next.lim_min;
+      const bool mine = next.mine, active = next.active;
       // scores of 32 keys from key0 on, those past the row's limit to -inf
       auto hide = [&](uint32_t (&r)[32], int key0) {
         if (key0 + 32 <= lim_min) return;                       // seen by all rows of the warp
@@ -707,6 +730,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           step_on(buf, lap);
         }
       }
+      ok = ok && look(i + 1);
       if (!ok) break;
       if (ntw > 0) {
         ok = all_wait(pv_done(w, last_buf), last_lap);
@@ -717,16 +741,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         // the item is read again here: its fields need not live through the loop above
         const int q0 = slot->q0, t0 = slot->t0 + w * span, left = slot->nq - t0, head = slot->head;
         const bool empty = l == 0.f;
-        const float inv = empty ? 0.f : 1.f / l;
+        const float inv = empty ? 0.f : p_rcp(l);                // 1 ulp, ahead of bf16
         const bool fix = ntw > 0 && slot->dirty != 0;
         // this lane stores 16 bytes of row 8 g + lane / 4 at a time: an offset each (-1: not a row)
         long long to[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int R = quarter * 32 + 8 * g + (lane >> 2), rt = (int)((R + 0.5f) * inv_group);   // R / group
-          to[g] = rt < span && rt < left
-                      ? ((long long)(q0 + t0 + rt) * a.q_heads + head * a.group + (R - rt * a.group)) * D
-                      : -1;
+          const int2 at = tile_rows[quarter * 32 + 8 * g + (lane >> 2)];
+          to[g] = at.x < left ? ((long long)(q0 + t0) * a.q_heads + head * a.group + at.y) * D : -1;
         }
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
@@ -828,8 +850,7 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
                              const bf16* v, long long v_stride, int tokens_q, int tokens_k,
                              int batch, int q_heads, int kv_heads, int dim, const int* cu_q,
                              const int* cu_k, float scale, int frame, bf16* out, float* lse,
-                             int* err_flag, int num_sms, cudaStream_t s) {
-  (void)num_sms;
+                             int* err_flag, cudaStream_t s) {
   PArgs a;
   a.out = out;
   a.lse = lse;

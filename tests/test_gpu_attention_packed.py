@@ -125,6 +125,37 @@ def test_unseen_values_do_not_reach_a_query(planner, dim, frame):
     assert torch.equal(out[mine], clean[mine]) and torch.all(torch.isnan(out[150 + first:350]))
 
 
+@pytest.mark.parametrize("nq,nk,q_heads,kv_heads,dim,frame", [
+    ([1], [1000], 2, 1, 64, 1),
+    ([100], [1000], 1, 1, 128, 1),
+    ([5], [193], 16, 1, 128, 1),                           # four tiles of keys, one in the last
+    ([5], [192], 16, 1, 64, 1),
+    ([60, 300, 2, 7], [500, 300, 3, 700], 4, 2, 64, 50),
+    ([1, 17, 130, 40], [900, 640, 450, 321], 2, 2, 128, 1),
+])
+def test_few_queries_over_many_keys(planner, nq, nk, q_heads, kv_heads, dim, frame):
+    check(planner, nq, nk, q_heads, kv_heads, dim, frame, seed=nk[0])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_few_queries_and_values_that_are_not_finite(planner, dim):
+    nq, nk = [6, 3], [500, 400]
+    q, k, v, clean = check(planner, nq, nk, 2, 1, dim, seed=2)
+    k, v = k.contiguous(), v.contiguous()
+    v2, k2 = v.clone(), k.clone()
+    v2[497, 0, 5] = float("inf")                           # the first two queries do not see key 497 ..
+    v2[40, 0, 7] = -float("inf")                           # all of the sequence see key 40
+    k2[498] = float("nan")                                 # nor the first four key 498
+    out, lse = call(planner, q, k2, v2, nq, nk)
+    assert torch.all(out[:6, :, 7][:4] == -float("inf"))
+    rest = torch.ones(dim, dtype=torch.bool, device="cuda")
+    rest[5] = rest[7] = False
+    assert torch.equal(out[:4][..., rest], clean[:4][..., rest])
+    assert torch.equal(out[:3, :, 5], clean[:3, :, 5]) and torch.all(out[3, :, 5] == float("inf"))
+    assert torch.all(torch.isnan(out[4:6])) and torch.all(torch.isnan(lse[4:6]))
+    assert torch.equal(out[6:], clean[6:])
+
+
 def test_bad_offsets_are_skipped_and_reported(planner):
     from cem_search_transformer_gb300 import binding
     x = bf16(np.random.default_rng(0).standard_normal((64, 2, 64))).cuda()
