@@ -3,7 +3,9 @@
 // (page, head), and the read-back to bf16.
 //
 // Bound by bytes on long appends (2 (q_heads + 2 kv_heads) dim read, 2 q_heads dim + 2 kv_heads dim
-// written a token) and by latency on short ones. A page and head is quantised by exactly one team
+// written a token) and by latency on short ones. Nine prompts of 100 to 4500 tokens, 32 query heads
+// over 8 of 128: queries 57 us (5.6 TB/s), keys 30 us (2 TB/s: a page's chain of search, table,
+// loads, angles and maximum with 16 warps a SM), read-back 26 us (4.6 TB/s). A page and head is quantised by exactly one team
 // of warps: that of its "owner", the first new token that lies in the page. No atomics: the result
 // depends neither on the launch shape nor on the order of blocks.
 //
@@ -196,6 +198,20 @@ __device__ __forceinline__ float abs_max(const float (&y)[16], float m) {
   return m;
 }
 
+__device__ __forceinline__ float abs_max(const uint4 (&u)[2], float m) {
+  __nv_bfloat162 x = __float2bfloat162_rn(m);   // exact: m is a bf16 value here
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = w[i] & 0x7fff7fffu;
+      x = __hmax2(x, *reinterpret_cast<const __nv_bfloat162*>(&b));   // drops NaN
+    }
+  }
+  return fmaxf(__low2float(x), __high2float(x));
+}
+
 // Codes of a page's `off` earlier tokens moved to a scale 1 / factor times theirs (exact but for
 // codes that become subnormal), `members` threads together.
 template <int D>
@@ -378,10 +394,10 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, bool early, cuda
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Long appends: a team of T warps takes a chunk of `page` packed tokens of one head, k or v, and
+// Long appends: a team of T warps takes a chunk of `page` packed tokens of one head and
 // quantises the pages that have their owner in it (two at most for a long sequence). Each lane
 // holds IT rows' 16 elements between the maximum and the codes, so that the rows are read once.
-template <int D, bool INTER, int T, int IT>
+template <int D, bool INTER, int T, int IT, bool V>
 __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs& a, long long units,
                                              int* err_flag) {
   constexpr int L = D / 16, WARPS = THREADS / 32, ROWS = T * (32 / L);   // tokens a pass
@@ -390,13 +406,11 @@ __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs&
   const long long unit = (long long)blockIdx.x * (WARPS / T) + team;
   if (unit >= units) return;
   const int head = (int)(unit % c.heads);
-  const long long ck = unit / c.heads;
-  const bool is_v = ck & 1;
-  const int t0 = (int)(ck >> 1) << c.page_log2;
+  const int t0 = (int)(unit / c.heads) << c.page_log2;
   const int member = (warp % T) * 32 + lane, row = member / L;
   const Lane<D, INTER> ln(a.rot);
-  const bf16* src = (is_v ? a.v : a.k) + (long long)head * D;
-  const long long stride = is_v ? a.v_stride : a.k_stride;
+  const bf16* src = (V ? a.v : a.k) + (long long)head * D;
+  const long long stride = V ? a.v_stride : a.k_stride;
   Place at = locate(a.cu, a.start, c.batch, t0);
   if (at.s < 0) {                          // the chunk begins ahead of the first sequence
     at.s = 0;
@@ -421,7 +435,7 @@ __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs&
       continue;
     }
     const long long block = (long long)p.page * c.heads + head;
-    float* const scale_at = (is_v ? c.v_scale : c.k_scale) + block;
+    float* const scale_at = (V ? c.v_scale : c.k_scale) + block;
     const float was = p.off != 0 ? sane_scale(*scale_at) : 0.f;
     uint4 raw[IT][2];
 #pragma unroll
@@ -430,17 +444,19 @@ __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs&
       raw[it][0] = raw[it][1] = make_uint4(0, 0, 0, 0);
       if (r < p.n) load16(src + (long long)(p.t + r) * stride, ln, raw[it]);
     }
-    float y[IT][16], m = 0.f;
+    float y[V ? 1 : IT][16], m = 0.f;   // keys between the maximum and the codes; values stay raw
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
       const int r = it * ROWS + row;
-      widen(raw[it], y[it]);
-      if (!is_v) {
+      if (V) {
+        m = abs_max(raw[it], m);         // rows past the end are zeros
+      } else {
+        widen(raw[it], y[it]);
         float an[16];
         if (ln.rotates && r < p.n) load_angles(an, a.rope + (long long)(p.pos + r) * a.rot, a.rot, ln.p);
         norm_rotate<D, INTER>(y[it], ln, a.k_norm, a.eps, an);
+        if (r < p.n) m = abs_max(y[it], m);
       }
-      if (r < p.n) m = abs_max(y[it], m);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -454,7 +470,7 @@ __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs&
       __syncwarp();                        // all lanes have read the scale
     }
     float scale = pow2(kv8_exponent(__float_as_uint(m)));
-    uint8_t* const base = (is_v ? c.v : c.k) + block * ((long long)c.page * D);
+    uint8_t* const base = (V ? c.v : c.k) + block * ((long long)c.page * D);
     if (p.off != 0) {
       if (scale > was) rescale_codes<D>(base, p.off, was / scale, member, T * 32);
       scale = fmaxf(scale, was);           // a page that holds tokens never shrinks its scale
@@ -465,19 +481,23 @@ __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs&
     for (int it = 0; it < IT; ++it) {
       const int r = it * ROWS + row;
       if (r >= p.n) continue;
-      store_codes(base + (long long)(p.off + r) * D, ln, y[it], inv);
-      if (!is_v && a.k_out) store16(a.k_out + ((long long)(p.t + r) * c.heads + head) * D, ln, y[it]);
+      if (V) widen(raw[it], y[0]);
+      store_codes(base + (long long)(p.off + r) * D, ln, y[V ? 0 : it], inv);
+      if (!V && a.k_out) store16(a.k_out + ((long long)(p.t + r) * c.heads + head) * D, ln, y[V ? 0 : it]);
     }
   }
 }
 
-// The pages share no data with the queries' kernel ahead of them and run beside its last blocks (24
-// frames of 258 tokens: 35 us with the read-back that follows, 42 one after the other); the wait
-// at the end keeps the order for what comes next.
-template <int D, bool INTER, int T, int IT>
-__global__ void __launch_bounds__(THREADS, 2)
+// Values and keys in a kernel each: values need half the registers and no arithmetic but the scale,
+// so twice the warps (nine prompts of 100 to 4500 tokens, 8 heads of 128: 123 us with the queries and
+// the read-back, 127 with both in one kernel; queries in the same grid too: 150). They share no
+// data with the kernel ahead of them in the call and run beside its last blocks (24 frames of 258
+// tokens: 35 us, 42 one after the other); the wait at the end keeps the order for what comes next.
+template <int D, bool INTER, int T, int IT, bool V>
+__global__ void __launch_bounds__(THREADS, V ? 4 : 2)
     k_append_pages(Kv8View c, AppendArgs a, long long units, int* err_flag) {
-  append_pages<D, INTER, T, IT>(c, a, units, err_flag);
+  asm volatile("griddepcontrol.launch_dependents;");
+  append_pages<D, INTER, T, IT, V>(c, a, units, err_flag);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -555,10 +575,13 @@ __global__ void k_rope_table(int positions, int rot, double log2_base, double in
 template <int D, bool INTER, int T, int IT>
 cudaError_t launch_pages(const Kv8View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
   constexpr int TEAMS = THREADS / 32 / T;
-  const long long units = (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads * 2;
+  const long long units = (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads;
   const long long blocks = (units + TEAMS - 1) / TEAMS;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_early(k_append_pages<D, INTER, T, IT>, (unsigned)blocks, a.q != nullptr, s, c, a, units, err_flag);
+  const cudaError_t e = launch_early(k_append_pages<D, INTER, T, IT, true>, (unsigned)blocks, a.q != nullptr, s,
+                                     c, a, units, err_flag);
+  if (e != cudaSuccess) return e;
+  return launch_early(k_append_pages<D, INTER, T, IT, false>, (unsigned)blocks, true, s, c, a, units, err_flag);
 }
 
 template <int D, bool INTER>
