@@ -156,6 +156,16 @@ def test_few_queries_and_values_that_are_not_finite(planner, dim):
     assert torch.equal(out[6:], clean[6:])
 
 
+def test_mostly_empty_batch(planner):
+    """A batch padded with empty sequences, ahead, between and behind those with tokens: far more
+    places than there are items."""
+    n = [0] * 900
+    for at, tokens in ((40, 300), (41, 1), (600, 150), (899, 20)):
+        n[at] = tokens
+    check(planner, n, n, 4, 4, 64, seed=9, behind=700)
+    check(planner, [0] * 50 + [5], [7] * 50 + [5], 2, 1, 128, seed=10, behind=5)
+
+
 def test_bad_offsets_are_skipped_and_reported(planner):
     from cem_search_transformer_gb300 import binding
     x = bf16(np.random.default_rng(0).standard_normal((64, 2, 64))).cuda()
