@@ -155,8 +155,11 @@ __device__ __forceinline__ int length_of(const Kv8View& c, const Args& a, int s,
 __device__ __forceinline__ int units_of(int len, int unit) {
   return len > 0 ? (len + unit - 1) / unit : 1;   // an empty sequence has its (zero) rows written
 }
-// Places of an item in the line: ITEM_UNITS for its start and end, then its units.
-__device__ __forceinline__ int places_of(int len, int unit) { return units_of(len, unit) + ITEM_UNITS; }
+// Places of an item in the line: ITEM_UNITS for its start and end, then its units; none where there
+// is nothing to read.
+__device__ __forceinline__ int places_of(int len, int unit) {
+  return len > 0 ? units_of(len, unit) + ITEM_UNITS : 0;
+}
 
 // The line: sequence by sequence, each with heads * tiles items of places_of(len) places.
 // Totals by one warp (every warp of the CTA computes the same).
@@ -179,6 +182,7 @@ __device__ __forceinline__ void seek(const Kv8View& c, const Args& a, int unit, 
                                      Cursor& at) {
   const int lane = threadIdx.x & 31;
   const long long per = (long long)c.heads * a.tiles;
+  if (u < at.base + at.n * per) return;          // another item of the same sequence
   long long base = at.base;
   for (int s0 = at.s; s0 < c.batch; s0 += 32) {
     const int s = s0 + lane;
@@ -208,6 +212,19 @@ __device__ __forceinline__ void seek(const Kv8View& c, const Args& a, int unit, 
 __device__ __forceinline__ int workers_of(long long total, int grid) {
   const long long w = (total + MIN_UNITS - 1) / MIN_UNITS;
   return w < grid ? (int)w : grid;
+}
+
+// Zeros for the sequences that are not in the line, those with nothing cached.
+template <int D>
+__device__ __forceinline__ void write_empty(const Kv8View& c, const Args& a) {
+  const int rows = a.q_tokens * a.q_heads;
+  for (int s = blockIdx.x; s < c.batch; s += gridDim.x) {
+    if (length_of(c, a, s, nullptr) != 0) continue;
+    for (int i = threadIdx.x; i < rows * (D / 8); i += THREADS)
+      reinterpret_cast<uint4*>(a.out + (long long)s * rows * D)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = threadIdx.x; i < rows; i += THREADS) a.lse[(long long)s * rows + i] = -INFINITY;
+  }
 }
 
 template <int D, int NR>
@@ -246,7 +263,9 @@ __device__ __forceinline__ bool plan(const Kv8View& c, const Args& a, int whole,
   while (u < u_end) {
     seek(c, a, UNIT, u, cur);
     const long long in = u - cur.base;
-    const int item = (int)(in / cur.n), at = (int)(in % cur.n);
+    // a 64-bit division only where it has to be one
+    const int item = in <= 0xffffffffLL ? (int)((uint32_t)in / (uint32_t)cur.n) : (int)(in / cur.n);
+    const int at = (int)(in - (long long)item * cur.n);
     const int to = (int)min((long long)cur.n, at + (u_end - u));
     u += to - at;
     if (to <= ITEM_UNITS) continue;              // nothing but the item's start
@@ -293,6 +312,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     workers = workers_of(total, gridDim.x);
     if ((int)blockIdx.x >= workers) {
       if (threadIdx.x == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+      write_empty<D>(c, a);
       return;
     }
     u_begin = kv8_share(total, workers, blockIdx.x);
@@ -718,7 +738,9 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     }
   }
   cp_wait<0>();
-  if (!whole && threadIdx.x == 0) a.split[blockIdx.x] = begun;
+  if (whole) return;
+  if (threadIdx.x == 0) a.split[blockIdx.x] = begun;
+  write_empty<D>(c, a);
 }
 
 // Joins the items that were split: the parts of an item lie with consecutive CTAs, the first of

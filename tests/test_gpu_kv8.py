@@ -732,3 +732,15 @@ def test_captured_append_attention_and_read(planner, n_new):
         planner.sync_check()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("longest,page", [(2000, 64), (100, 16)])
+def test_attention_of_a_mostly_empty_batch(planner, longest, page):
+    lens = [0] * 300
+    for at, n in ((3, 1), (60, longest), (61, 17), (299, longest // 2)):
+        lens[at] = n
+    pool = Pool(lens, 2, page, 128)
+    ref = pool.fill(lens, 5)
+    check_attention(planner, pool, ref, lens, 1, 4, True, seed=4)
+    check_attention(planner, pool, ref, lens, 2, 16, False, seed=5)
+    check_attention(planner, pool, ref, [0] * 300, 1, 4, True, seed=6)
