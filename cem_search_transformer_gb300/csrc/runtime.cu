@@ -1290,6 +1290,8 @@ static jepa_status kv8_view(jepa_ctx* ctx, const char* what, const jepa_kv8_cach
   return JEPA_OK;
 }
 
+static bool bad_ints(const int32_t* p) { return bad_ptr(p) || !aligned(p, 4); }
+
 static bool bad_rows(const void* p, int64_t stride, int heads, int dim) {
   return bad_ptr(p) || !aligned(p, 16) || stride < (int64_t)heads * dim || stride % 8 ||
          stride > (1LL << 31);
@@ -1318,7 +1320,7 @@ jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, con
   Kv8View c;
   const jepa_status st = kv8_view(ctx, "rope_append_kv8", cache, &c);
   if (st) return st;
-  if (tokens < 1 || bad_ptr(cu) || bad_ptr(start) || bad_rows(k, k_stride, c.heads, c.dim) ||
+  if (tokens < 1 || bad_ints(cu) || bad_ints(start) || bad_rows(k, k_stride, c.heads, c.dim) ||
       bad_rows(v, v_stride, c.heads, c.dim) || (q == nullptr) != (q_out == nullptr) ||
       !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
       (interleaved != 0 && interleaved != 1) || !(norm_eps >= 0.f))
@@ -1364,7 +1366,7 @@ jepa_status jepa_kv8_read(jepa_ctx* ctx, const jepa_kv8_cache* cache, const int3
   Kv8View c;
   const jepa_status st = kv8_view(ctx, "kv8_read", cache, &c);
   if (st) return st;
-  if (tokens < 1 || bad_ptr(cu) || bad_ptr(first) || bad_ptr(k_out) || bad_ptr(v_out) ||
+  if (tokens < 1 || bad_ints(cu) || bad_ints(first) || bad_ptr(k_out) || bad_ptr(v_out) ||
       !aligned(k_out, 16) || !aligned(v_out, 16))
     return fail(ctx, JEPA_ERR_INVALID_ARG, "kv8_read: bad argument");
   OnDevice on(ctx->device);
@@ -1391,8 +1393,8 @@ jepa_status jepa_attention_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const
   Kv8View c;
   const jepa_status st = kv8_view(ctx, "attention_kv8", cache, &c);
   if (st) return st;
-  if (bad_ptr(q) || bad_ptr(out) || bad_ptr(kv_len) || bad_ptr(workspace) || !aligned(q, 16) ||
-      !aligned(out, 16) || !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(kv_len, 4) ||
+  if (bad_ptr(q) || bad_ptr(out) || bad_ints(kv_len) || bad_ptr(workspace) || !aligned(q, 16) ||
+      !aligned(out, 16) || !aligned(workspace, 256) || !aligned(lse, 4) ||
       q_tokens < 1 || q_heads < 1 || q_heads % c.heads || (causal != 0 && causal != 1) ||
       !(scale > 0.f) || !std::isfinite(scale))
     return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv8: bad argument");
@@ -1421,7 +1423,7 @@ jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_st
   if (tokens_q < 1 || tokens_k < 1 || batch < 1 || batch > 65535 || q_heads < 1 || kv_heads < 1 ||
       q_heads % kv_heads || q_heads > 65535 || bad_rows(q, q_stride, q_heads, head_dim) ||
       bad_rows(k, k_stride, kv_heads, head_dim) || bad_rows(v, v_stride, kv_heads, head_dim) ||
-      bad_ptr(cu_q) || bad_ptr(cu_k) || bad_ptr(out) || !aligned(out, 16) || !aligned(lse, 4) ||
+      bad_ints(cu_q) || bad_ints(cu_k) || bad_ptr(out) || !aligned(out, 16) || !aligned(lse, 4) ||
       !(scale > 0.f) || !std::isfinite(scale) || frame < 1)
     return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_packed: bad argument");
   // 2^27 keys are about a second of one CTA's steps: within the limit of a device wait

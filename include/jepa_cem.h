@@ -295,7 +295,8 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  * nothing, and can be captured into a CUDA graph; what they read from the device (offsets,
  * lengths, page tables) is read when the graph runs. Tensors are bf16 bit patterns (uint16).
  * Token rows are [tokens][heads][head_dim] with `*_stride` elements between tokens (at least
- * heads * head_dim, a multiple of 8), so q, k and v may be slices of one projection's rows.
+ * heads * head_dim, a multiple of 8), so q, k and v may be slices of one projection's rows. What a
+ * call writes overlaps nothing that it reads, but where it says so.
  *
  * Packed sequences: `cu` [batch + 1] int32 dev, ascending; sequence b owns packed tokens cu[b] ..
  * cu[b+1] - 1 (none is fine). Output rows ahead of the first sequence and behind the last are left

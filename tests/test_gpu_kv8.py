@@ -744,3 +744,21 @@ def test_attention_of_a_mostly_empty_batch(planner, longest, page):
     check_attention(planner, pool, ref, lens, 1, 4, True, seed=4)
     check_attention(planner, pool, ref, lens, 2, 16, False, seed=5)
     check_attention(planner, pool, ref, [0] * 300, 1, 4, True, seed=6)
+
+
+def test_misaligned_offsets_are_refused(planner):
+    pool, lib, h = Pool([32], 2, 16, 64), planner.lib, planner.h
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    n = torch.zeros(8, dtype=torch.int32, device="cuda")
+    ws = torch.empty(planner.attention_kv8_workspace(pool.cache), dtype=torch.uint8, device="cuda")
+    p, good, odd, ref = x.data_ptr(), n.data_ptr(), n.data_ptr() + 2, pool.cache.ref
+    for a, b in ((odd, good), (good, odd)):
+        assert lib.jepa_kv8_read(h, ref, a, b, 4, y.data_ptr(), z.data_ptr(), None) == 1
+        assert lib.jepa_rope_append_kv8(h, ref, None, 0, p, 128, p, 128, 4, 0, None, None, 0.0, None, 0, 0, 0, a, b,
+                                        None, None, None) == 1
+        assert lib.jepa_attention_packed(h, p, 128, p, 128, p, 128, 4, 4, 1, 2, 2, 64, a, b, 0.1, 1, y.data_ptr(),
+                                         None, None) == 1
+    assert lib.jepa_attention_kv8(h, ref, p, 1, 2, odd, 0.1, 1, y.data_ptr(), None, ws.data_ptr(), ws.numel(),
+                                  None) == 1
+    planner.sync_check()
