@@ -26,10 +26,12 @@
 //     the order of the summed index is free, and so is the naming of output rows. Both are wide
 //     loads without bank conflicts under the XOR swizzle (dim 64: two-way for V), and a lane ends
 //     with D/8 consecutive outputs of two query rows.
-// Measured, inputs behind L2: those two sequences 88 us (5.6 TB/s), 32 sequences of 100 to 8000
-// tokens 61 us (4.5 TB/s), 256 of 776 tokens with 16 heads of 64 and two queries 92 us (4.5 TB/s),
+// Measured, inputs behind L2: those two sequences 86 us (5.7 TB/s), 32 sequences of 100 to 8000
+// tokens 57 us (4.9 TB/s), 256 of 776 tokens with 16 heads of 64 and two queries 87 us (4.7 TB/s),
 // one of 517 tokens 10 us (latency). What is left of the copy rate is the start, the shares' uneven
-// ends and the joining, 15 us of the first; heads of 64 are bound by issue.
+// ends and the joining, 12 us of the first; heads of 64 are bound by issue: the load stream's state
+// (keys left, the table's row, the head) is kept from step to step, a division for the head in
+// each step took 5% there.
 #include "kv8.cuh"
 
 #include <cuda_fp16.h>
@@ -54,10 +56,10 @@ template <int D, int NR>
 struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
   // cp.async stages of a warp and CTAs a SM. Narrow heads: four CTAs with two stages hide more of
-  // a step's latency than three with three (256 candidates of 776 tokens: 97 against 103 us);
-  // heads of 128 the other way round (two long sequences: 96 against 103). Two row tiles of 128
+  // a step's latency than three with three (256 candidates of 776 tokens: 6% less);
+  // heads of 128 the other way round (two long sequences: 7% less). Two row tiles of 128
   // columns need 250 registers a thread and 82 KB, so two CTAs (32 sequences of up to 8000
-  // tokens, 16 rows: 89 us; 110 with three CTAs of two stages, which spill).
+  // tokens, 16 rows: 85 us; a quarter more with three CTAs of two stages, which spill).
   static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;
   static constexpr int CTAS = D == 64 ? (NR == 1 ? 4 : 3) : (NR == 1 ? 3 : 2);
   static constexpr int KS = 2048 / D;              // keys a warp takes in a step
@@ -241,30 +243,37 @@ __device__ __forceinline__ long long row_at(const Args& a, int s, int head, int 
 // Units [k0, k1) of n of one item: what a CTA does before it goes on to the next.
 struct Segment {
   int s, item, len, n, k0, k1;
+  int head, r0;        // of the item: key / value head, first row
   long long next;      // place in the line where the CTA's next segment begins
   long long last;      // the item's last place
 };
 
-template <int UNIT>
+// a / b for a, b >= 0: a 64-bit division (some hundred instructions) only where it has to be one.
+__device__ __forceinline__ long long divided(long long a, int b) {
+  return a <= 0xffffffffLL ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+template <int UNIT, int ROWS>
 __device__ __forceinline__ bool plan(const Kv8View& c, const Args& a, int whole, long long u,
                                      long long u_end, Cursor& cur, Segment& g) {
   if (whole) {
     if (u >= u_end) return false;
     const int per = c.heads * a.tiles;
-    g.s = (int)(u / per);
-    g.item = (int)(u % per);
+    g.s = (int)divided(u, per);
+    g.item = (int)(u - (long long)g.s * per);
     g.len = length_of(c, a, g.s, nullptr);
     g.n = units_of(g.len, UNIT);
     g.k0 = 0;
     g.k1 = g.n;
     g.next = u + 1;
+    g.head = a.tiles == 1 ? g.item : g.item / a.tiles;
+    g.r0 = (g.item - g.head * a.tiles) * ROWS;
     return true;
   }
   while (u < u_end) {
     seek(c, a, UNIT, u, cur);
     const long long in = u - cur.base;
-    // a 64-bit division only where it has to be one
-    const int item = in <= 0xffffffffLL ? (int)((uint32_t)in / (uint32_t)cur.n) : (int)(in / cur.n);
+    const int item = (int)divided(in, cur.n);
     const int at = (int)(in - (long long)item * cur.n);
     const int to = (int)min((long long)cur.n, at + (u_end - u));
     u += to - at;
@@ -277,6 +286,8 @@ __device__ __forceinline__ bool plan(const Kv8View& c, const Args& a, int whole,
     g.k1 = to - ITEM_UNITS;
     g.next = u;
     g.last = cur.base + (item + 1LL) * cur.n - 1;
+    g.head = a.tiles == 1 ? item : item / a.tiles;
+    g.r0 = (item - g.head * a.tiles) * ROWS;
     return true;
   }
   return false;
@@ -326,8 +337,8 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   const int chunk = lane % CPR, sub = lane / CPR;
   Cursor load_cur{0, 0, 0, 0};
   Segment ld;
-  int ld_step = 0, ld_stage = 0;
-  bool ld_more = plan<S::UNIT>(c, a, whole, u_begin, u_end, load_cur, ld);
+  int ld_left = 0, ld_stage = 0;               // steps left of the segment
+  bool ld_more = plan<S::UNIT, ROWS>(c, a, whole, u_begin, u_end, load_cur, ld);
   // a lane's place in a 16-key group of codes, in global and (swizzled) in shared memory
   const uint32_t lane_from = sub * D + 16 * chunk;
   uint32_t lane_to[16 / RPI];
@@ -338,18 +349,25 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   }
   const uint32_t block_bytes = (uint32_t)c.page * D, slot_mask = c.page - 1;
   int pg_next[S::GROUPS];                      // pages of the step that is issued next
+  int ld_key = 0;                              // first key of that step
+  const int* ld_pages = nullptr;               // the sequence's row of the table
+  auto begin_segment = [&]() {
+    ld_key = ld.k0 * S::UNIT + warp * S::KS;
+    ld_pages = c.table + (long long)ld.s * c.max_pages;
+    ld_left = ld.k1 - ld.k0;
+  };
+  if (ld_more) begin_segment();
   auto fetch_pages = [&]() {
-    const int key = (ld.k0 + ld_step) * S::UNIT + warp * S::KS;
-    const int* at = c.table + (long long)ld.s * c.max_pages;
+    const int key = ld_key;
+    const int* at = ld_pages;
 #pragma unroll
     for (int p = 0; p < S::GROUPS; ++p)
       pg_next[p] = ld_more && key + 16 * p < ld.len ? __ldg(at + ((key + 16 * p) >> c.page_log2)) : -1;
   };
   auto issue = [&]() {                         // the next step of the stream into the next stage
-    const int key0 = (ld.k0 + ld_step) * S::UNIT + warp * S::KS;
+    const int key0 = ld_key;
     if (ld_more && key0 < ld.len) {
       const uint32_t st = ld_stage * S::STAGE;
-      const uint32_t head = ld.item / a.tiles;
       bool whole_step = key0 + S::KS <= ld.len;
       uint32_t block[S::GROUPS];               // num_pages * heads is below 2^31
 #pragma unroll
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
         const bool there = (uint32_t)pg_next[p] < (uint32_t)c.num_pages;
         if (!there && key0 + 16 * p < ld.len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
         whole_step = whole_step && there;
-        block[p] = (there ? (uint32_t)pg_next[p] : 0u) * (uint32_t)c.heads + head;
+        block[p] = (there ? (uint32_t)pg_next[p] : 0u) * (uint32_t)c.heads + (uint32_t)ld.head;
       }
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
@@ -391,9 +409,10 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     }
     cp_commit();
     ld_stage = ld_stage + 1 == NST ? 0 : ld_stage + 1;
-    if (ld_more && ++ld_step == ld.k1 - ld.k0) {
-      ld_step = 0;
-      ld_more = plan<S::UNIT>(c, a, whole, ld.next, u_end, load_cur, ld);
+    ld_key += S::UNIT;
+    if (ld_more && --ld_left == 0) {
+      ld_more = plan<S::UNIT, ROWS>(c, a, whole, ld.next, u_end, load_cur, ld);
+      begin_segment();
     }
     fetch_pages();
   };
@@ -405,9 +424,9 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   Cursor cur{0, 0, 0, 0};
   Segment sg;
   sg.next = u_begin;
-  while (plan<S::UNIT>(c, a, whole, sg.next, u_end, cur, sg)) {
+  while (plan<S::UNIT, ROWS>(c, a, whole, sg.next, u_end, cur, sg)) {
     const int s = sg.s, len = sg.len, item = sg.item;
-    const int head = item / a.tiles, r0 = (item % a.tiles) * ROWS;
+    const int head = sg.head, r0 = sg.r0;
     // ---- queries: row g of each 8-row tile as f16, times 2^-e so that |q| < 2^15 ----
     uint32_t qf[NR][S::KW][2];
     float qs[NR][2];       // of rows 2t, 2t + 1: 2^e * softmax scale * log2(e)
