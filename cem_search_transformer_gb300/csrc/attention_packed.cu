@@ -5,7 +5,8 @@
 //   p = i + nk - nq: the query's position among the keys; F = 1 is causal, F = T block-causal over
 //   frames of T tokens (the predictor's mask), F >= nk without a mask.
 //
-// A CTA takes 256 query rows of one sequence and key/value head, two tiles of 128. A row is a
+// A CTA takes 256 query rows of one sequence and key/value head, two tiles of 128 (or the last 128
+// of two heads). A row is a
 // (token, head of the group) pair, token-major, so that a group's heads share the tile of keys
 // and short prompts still fill the rows; groups that do not divide 128 leave a few rows unused.
 // Warps:
@@ -30,8 +31,9 @@
 // query heads over 8: 506 us, 1.63 PFLOP/s). D = 64: the chain of a step, scores -> softmax -> P,
 // about 1500 cycles for both tiles where the exponentials alone take 1024 and half of them left
 // out takes 6% off; and an item's 2000 to 3000 cycles between two loops, of which half is hidden
-// (32 prompts of 774 tokens, 16 heads, frames of 258: 125 us, of which 31 for the last six rows of
-// each, a tile of their own; its keys shared out over both tiles took 124, and 2% more elsewhere).
+// (32 prompts of 774 tokens, 16 heads, frames of 258: 118 us, of which 22 for the last six rows of
+// each, a tile of their own, two heads at a time; 125 a head at a time, and with its keys shared
+// out over both tiles 124, and 2% more elsewhere).
 // What lies behind a sequence's last key in its last tile is another sequence's (or nothing), and
 // a masked probability of 0 times an infinity or NaN there is NaN. So in tiles where some row's
 // limit ends, a warp zeroes V rows past the sequence and any non-finite value before the product
@@ -54,6 +56,11 @@ constexpr int W_MMA = 8, W_TMA = 10;   // issuers: W_MMA and the next; cleaning:
 constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == P_THREADS * 168, "register split");
 constexpr uint32_t P_TMEM = 512;
+// Items for each SM from which on a sequence's last rows, where they fill one query tile at most, are
+// taken for two heads at a time, a tile each with its own keys: the two chains run side by side (512
+// sequences of six tokens 105 against 155 us). With few items the heads are better on SMs of their
+// own (four sequences of 774 tokens, 16 heads: 29 us, 32 in pairs).
+constexpr int PAIRS_FROM = 4;
 constexpr int BLK = TQ * 128;      // bytes of 128 rows x 64 bf16 (one swizzled block of Q)
 
 template <int D>
@@ -75,6 +82,7 @@ struct PShape {
   static constexpr int OFF_ROWS = OFF_TAIL + 176;   // (token, place among its heads) of a tile's rows
   static constexpr int SMEM = OFF_ROWS + TQ * 8 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static_assert(NBUF == 2, "two score buffers in turn");
   static_assert(2 * TM <= (int)P_TMEM && TK % 32 == 0 && KBLK % 1024 == 0, "tiles");
 };
 
@@ -85,6 +93,7 @@ struct PArgs {
   long long v_stride;
   const int *cu_q, *cu_k;
   int tokens_q, tokens_k, batch, q_heads, kv_heads, group, per_tile, frame;
+  int pairs;                      // 1: items of a single query tile take two heads
   unsigned long long frame_inv;   // floor(2^63 / frame) + 1
   float scale_log2;
 };
@@ -98,7 +107,7 @@ struct Item {
   int nt[2];           // key tiles of each query tile (0: no rows, or none that sees a key)
   int first_edge;      // the first key tile in which some row's limit ends
   int dirty;           // a non-finite V was taken out of one of its tiles
-  int pad;
+  int pair;            // both tiles hold the sequence's last rows, of this head and the next
 };
 // Where the search for an item goes on: items come in ascending order as a rule.
 struct Cursor {
@@ -205,7 +214,8 @@ __device__ __forceinline__ int limit_of(const Item& it, int i, const PArgs& a) {
   return lim < it.nk ? (int)lim : it.nk;
 }
 
-// The `index`-th 256-row item; sequences in order, within one the last rows (most keys) first.
+// The `index`-th 256-row item; sequences in order, within one the last rows (most keys) first, of
+// which a pair of heads may be one item.
 template <int TK>
 __device__ __forceinline__ void find_item(const PArgs& a, long long index, Cursor& cur, Item& it,
                                           int* err_flag) {
@@ -230,21 +240,31 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
       }
     }
     const int tiles = (nq + span - 1) / span;
-    long long incl = tiles;
+    const bool lone = a.pairs && tiles > 0 && nq - (tiles - 1) * span <= a.per_tile;
+    const long long mine = (long long)tiles * a.kv_heads - (lone ? a.kv_heads >> 1 : 0);
+    long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const uint32_t beyond = __ballot_sync(0xffffffffu, base + incl * a.kv_heads > index);
+    const uint32_t beyond = __ballot_sync(0xffffffffu, base + incl > index);
     if (beyond) {
       const int src = __ffs((int)beyond) - 1;
       const int n = __shfl_sync(0xffffffffu, tiles, src);
-      const long long first = base + (__shfl_sync(0xffffffffu, incl, src) - n) * a.kv_heads;
-      const long long in = index - first;
+      const bool pairs = __shfl_sync(0xffffffffu, (int)lone, src) != 0;
+      const unsigned in = (unsigned)__shfl_sync(0xffffffffu, (int)(index - base - (incl - mine)), src);
+      const unsigned heads = a.kv_heads, wide = pairs ? (heads + 1) >> 1 : heads;
+      int row = 0;
+      if (in < wide) {
+        it.head = (int)(pairs ? 2 * in : in);
+      } else {
+        row = 1 + (int)((in - wide) / heads);
+        it.head = (int)((in - wide) % heads);
+      }
       it.valid = 1;
-      it.head = (int)(in % a.kv_heads);
-      it.t0 = (n - 1 - (int)(in / a.kv_heads)) * span;
+      it.pair = pairs && row == 0 && it.head + 1 < a.kv_heads;
+      it.t0 = (n - 1 - row) * span;
       it.q0 = __shfl_sync(0xffffffffu, q0, src);
       it.nq = __shfl_sync(0xffffffffu, nq, src);
       it.k0 = __shfl_sync(0xffffffffu, k0, src);
@@ -254,12 +274,13 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
         const int t = it.t0 + w * a.per_tile, last = min(it.nq, t + a.per_tile) - 1;
         it.nt[w] = t < it.nq ? (limit_of(it, last, a) + TK - 1) / TK : 0;
       }
+      if (it.pair) it.nt[1] = it.nt[0];
       it.first_edge = limit_of(it, it.t0, a) / TK;
       cur.s0 = s0;
       cur.base = base;
       return;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31) * a.kv_heads;
+    base += __shfl_sync(0xffffffffu, incl, 31);
   }
   cur.total = base;
 }
@@ -407,7 +428,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (!it.valid) break;
         ask();
         if (lane == 0) {
-          const int n_tiles = max(it.nt[0], it.nt[1]);
+          const int pair = it.pair, n_tiles = max(it.nt[0], it.nt[1]) << pair;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || it.nt[w] == 0) continue;
@@ -416,12 +437,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             ++qn[w];
             mbar_expect_tx(q_full(w), (uint32_t)(S::NB * box));
             for (int b = 0; b < S::NB; ++b)
-              tma_load_3d(sb + w * S::QTILE + b * BLK, &tmQ, 64 * b, it.head * a.group,
-                          it.q0 + it.t0 + w * span, q_full(w));
+              tma_load_3d(sb + w * S::QTILE + b * BLK, &tmQ, 64 * b, (it.head + (pair & w)) * a.group,
+                          it.q0 + it.t0 + (pair ? 0 : w * span), q_full(w));
           }
           // K_0 and K_1 in a stage of their own each, then V_j beside K_{j + 2}: what the issuers
-          // take in one step, behind one barrier
-          auto load = [&](int j_v, int j_k) {
+          // take in one step, behind one barrier. A pair's heads take turns: i is its key tile i / 2
+          auto load = [&](int i_v, int i_k) {
+            const int j_v = i_v >> pair, j_k = i_k >> pair;
+            const int head = it.head + (pair & i_k);              // i_v is i_k - 2 or none
             const int st = n % S::STAGES;
             ok = ok && (n < S::STAGES ||
                         p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag));
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             ++n;
             const uint32_t dst = sb + S::OFF_RING + st * 2 * S::TILE;
             // V tiles with an edge land at the cleaning warp, which passes them on to the issuers
-            const bool has_k = j_k < n_tiles, has_v = j_v >= 0, edge = has_v && j_v >= it.first_edge;
+            const bool has_k = i_k < n_tiles, has_v = i_v >= 0, edge = has_v && j_v >= it.first_edge;
             const uint32_t bytes = (has_k ? S::TILE : 0) + (has_v && !edge ? S::TILE : 0);
             if (edge) mbar_expect_tx(edge_full(st), S::TILE);
             if (bytes)
@@ -439,10 +462,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             if (!edge) mbar_arrive(kv_full(st));
             for (int b = 0; b < S::NB; ++b) {
               if (has_v)
-                tma_load_3d(dst + b * KBLK, &tmV, 64 * b, it.head, it.k0 + j_v * TK,
+                tma_load_3d(dst + b * KBLK, &tmV, 64 * b, head, it.k0 + j_v * TK,
                             edge ? edge_full(st) : kv_full(st));
               if (has_k)
-                tma_load_3d(dst + S::TILE + b * KBLK, &tmK, 64 * b, it.head, it.k0 + j_k * TK, kv_full(st));
+                tma_load_3d(dst + S::TILE + b * KBLK, &tmK, 64 * b, head, it.k0 + j_k * TK, kv_full(st));
             }
           };
           for (int j = 0; j < min(S::NBUF, n_tiles); ++j) load(-1, j);
@@ -489,7 +512,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const volatile Item* slot = &items[i & 1];
         const int valid = __shfl_sync(0xffffffffu, slot->valid, 0);
         const int nt = __shfl_sync(0xffffffffu, slot->nt[w], 0);
-        const int n_tiles = __shfl_sync(0xffffffffu, max(slot->nt[0], slot->nt[1]), 0);
+        const int pair = __shfl_sync(0xffffffffu, slot->pair, 0);
+        const int n_tiles = __shfl_sync(0xffffffffu, max(slot->nt[0], slot->nt[1]), 0) << pair;
         if (lane == 0) mbar_arrive(item_empty(i & 1));
         __syncwarp();
         if (!valid) break;
@@ -502,25 +526,32 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           w_commit(s_full(w, b), leader);
           if (j + 1 == nt) w_commit(q_empty(w), leader);
         };
-        // the first scores, then P V of tile j and the scores of tile j + NBUF in turn
+        // the first scores, then P V of tile j and the scores of tile j + 2 in turn. Of a pair this
+        // tile's are every other one, and its next scores, in the other buffer, come first
         int b0 = buf;
-        for (int j = 0; j < min(S::NBUF, n_tiles) && ok; ++j) {
+        for (int i2 = 0; i2 < min(S::NBUF, n_tiles) && ok; ++i2) {
           ok = wait(kv_full(ks), k_phase);
-          if (ok && j == 0 && nt > 0) {
+          if (ok && i2 == 0 && nt > 0) {
             ok = wait(q_full(w), q_phase);
             q_phase ^= 1;
           }
           if (!ok) break;
           tc_fence_after();
-          if (j < nt) scores(j, b0);
-          b0 = b0 + 1 == S::NBUF ? 0 : b0 + 1;
+          if (pair ? i2 == w : i2 < nt) {
+            scores(i2 >> pair, b0);
+            b0 ^= 1;
+          }
           w_commit(kv_empty(ks), leader);
           advance();
         }
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          const int b = buf;
+        for (int i2 = 0; i2 < n_tiles && ok; ++i2) {
+          const int b = buf, j = i2 >> pair;
           ok = wait(kv_full(ks), k_phase);
-          if (ok && j < nt) {
+          if (ok && (pair ? (i2 & 1) == w : j < nt)) {
+            if (pair && j + 1 < nt) {
+              tc_fence_after();
+              scores(j + 1, b ^ 1);
+            }
             ok = wait(p_full(w, b), lap);
             if (!ok) break;
             tc_fence_after();
@@ -530,7 +561,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               w_mma_ts(tO(w), tS(w, b) + 8u * kk, vd + (uint64_t)(kk * (2048 >> 4)), idO,
                        (j > 0) || (kk > 0), leader);
             w_commit(pv_done(w, b), leader);
-            if (j + S::NBUF < nt) scores(j + S::NBUF, b);
+            if (!pair && j + 2 < nt) scores(j + 2, b);
             if (++buf == S::NBUF) {
               buf = 0;
               lap ^= 1;
@@ -554,9 +585,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (!ok) break;
         const Item it = items[i & 1];
         if (!it.valid) break;
-        const int n_tiles = max(it.nt[0], it.nt[1]);
-        for (int j = it.first_edge; j < n_tiles && ok; ++j) {
-          const int st = (n0 + min(S::NBUF, n_tiles) + j) % S::STAGES;
+        const int n_tiles = max(it.nt[0], it.nt[1]) << it.pair;
+        for (int i2 = it.first_edge << it.pair; i2 < n_tiles && ok; ++i2) {
+          const int j = i2 >> it.pair, st = (n0 + min(S::NBUF, n_tiles) + i2) % S::STAGES;
           ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
           if (!ok) break;
           phase ^= 1u << st;
@@ -629,7 +660,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       const Item it = items[i & 1];
       next.valid = it.valid;
       next.ntw = ((const volatile Item*)items)[i & 1].nt[w];
-      const int tok = it.t0 + w * span + row_tok;               // within the sequence
+      const int tok = it.t0 + (it.pair ? 0 : w * span) + row_tok;   // within the sequence
       next.mine = row_tok < span && tok < it.nq;
       next.lim = next.mine ? limit_of(it, tok, a) : 0x7fffffff;
       next.lim_min = __reduce_min_sync(0xffffffffu, next.lim);
@@ -754,7 +785,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       }
       if (active) {
         // the item is read again here: its fields need not live through the loop above
-        const int q0 = slot->q0, t0 = slot->t0 + w * span, left = slot->nq - t0, head = slot->head;
+        const int pair = slot->pair, q0 = slot->q0, t0 = slot->t0 + (pair ? 0 : w * span);
+        const int left = slot->nq - t0, head = slot->head + (pair & w);
         const bool empty = l == 0.f;
         const float inv = empty ? 0.f : p_rcp(l);                // 1 ulp, ahead of bf16
         const bool fix = ntw > 0 && slot->dirty != 0;
@@ -847,7 +879,7 @@ bool make_map_heads(CUtensorMap* m, const void* ptr, int tokens, int heads, int 
 
 template <int D>
 cudaError_t launch_packed(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                          const PArgs& a, int* err_flag, cudaStream_t s) {
+                          PArgs a, int* err_flag, int num_sms, cudaStream_t s) {
   using S = PShape<D>;
   static std::atomic<unsigned long long> attr_done{0};
   const cudaError_t e = set_max_dynamic_smem((const void*)k_attention_packed<D>, S::SMEM, attr_done);
@@ -855,6 +887,7 @@ cudaError_t launch_packed(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   // lengths are on the device: an upper bound of the items
   const int sequences = a.batch < a.tokens_q ? a.batch : a.tokens_q;   // that are not empty
   const long long items = ((long long)a.tokens_q / (2 * a.per_tile) + sequences) * a.kv_heads;
+  a.pairs = items >= PAIRS_FROM * num_sms;
   if (items > (1LL << 28)) return cudaErrorInvalidValue;   // taking them out may last a second
   k_attention_packed<D><<<(unsigned)items, P_THREADS, S::SMEM, s>>>(mq, mk, mv, a, err_flag);
   return cudaGetLastError();
@@ -866,7 +899,7 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
                              const bf16* v, long long v_stride, int tokens_q, int tokens_k,
                              int batch, int q_heads, int kv_heads, int dim, const int* cu_q,
                              const int* cu_k, float scale, int frame, bf16* out, float* lse,
-                             int* err_flag, cudaStream_t s) {
+                             int* err_flag, int num_sms, cudaStream_t s) {
   PArgs a;
   a.out = out;
   a.lse = lse;
@@ -882,6 +915,7 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
   a.group = q_heads / kv_heads;
   a.per_tile = TQ / a.group;
   a.frame = frame;
+  a.pairs = 0;
   a.frame_inv = (1ull << 63) / (unsigned)frame + 1;
   a.scale_log2 = scale * 1.4426950408889634f;
   constexpr int box_keys = PShape<64>::TK;
@@ -891,8 +925,8 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
       !make_map_heads(&mk, k, tokens_k, kv_heads, dim, k_stride, box_keys, 1) ||
       !make_map_heads(&mv, v, tokens_k, kv_heads, dim, v_stride, box_keys, 1))
     return cudaErrorInvalidValue;
-  if (dim == 64) return launch_packed<64>(mq, mk, mv, a, err_flag, s);
-  if (dim == 128) return launch_packed<128>(mq, mk, mv, a, err_flag, s);
+  if (dim == 64) return launch_packed<64>(mq, mk, mv, a, err_flag, num_sms, s);
+  if (dim == 128) return launch_packed<128>(mq, mk, mv, a, err_flag, num_sms, s);
   return cudaErrorInvalidValue;
 }
 

@@ -57,6 +57,6 @@ cudaError_t attention_packed(const bf16* q, long long q_stride, const bf16* k, l
                              const bf16* v, long long v_stride, int tokens_q, int tokens_k,
                              int batch, int q_heads, int kv_heads, int dim, const int* cu_q,
                              const int* cu_k, float scale, int frame, bf16* out, float* lse,
-                             int* err_flag, cudaStream_t s);
+                             int* err_flag, int num_sms, cudaStream_t s);
 
 }  // namespace jepa

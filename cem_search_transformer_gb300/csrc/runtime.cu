@@ -1433,7 +1433,7 @@ jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_st
   CK(on.status);
   CK(attention_packed((const bf16*)q, q_stride, (const bf16*)k, k_stride, (const bf16*)v, v_stride,
                       tokens_q, tokens_k, batch, q_heads, kv_heads, head_dim, cu_q, cu_k, scale,
-                      frame, (bf16*)out, lse, ctx->dev_err, (cudaStream_t)stream));
+                      frame, (bf16*)out, lse, ctx->dev_err, ctx->num_sms, (cudaStream_t)stream));
   return JEPA_OK;
 }
 

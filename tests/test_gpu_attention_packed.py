@@ -156,6 +156,30 @@ def test_few_queries_and_values_that_are_not_finite(planner, dim):
     assert torch.equal(out[6:], clean[6:])
 
 
+@pytest.mark.parametrize("heads,group,dim,frame,prefix", [(7, 1, 64, 1, 0), (8, 2, 128, 1, 200), (8, 1, 64, 50, 90),
+                                                          (9, 3, 128, 7, 0)])
+def test_many_short_sequences(planner, heads, group, dim, frame, prefix):
+    """Enough items that one query tile's worth of rows is taken for two heads at a time."""
+    rng = np.random.default_rng(heads)
+    nq = [int(n) for n in rng.integers(0, 300 // group, 100)]
+    nk = [n + int(p) for n, p in zip(nq, rng.integers(0, prefix + 1, 100))]
+    q, k, v, clean = check(planner, nq, nk, heads * group, heads, dim, frame, seed=3, behind=2)
+    s = max(range(100), key=lambda i: (0 < nq[i] <= 128 // group) * nk[i])   # one tile of queries
+    q0, k0 = sum(nq[:s]), sum(nk[:s])
+    k, v = k.contiguous(), v.contiguous()
+    last = k0 + nk[s] - 1                                  # seen by its last queries alone, if causal
+    v[last, 1, 3] = float("nan")
+    v[last, 0, 4] = float("inf")
+    out, _ = call(planner, q, k, v, nq, nk, frame)
+    sees = np.array(paged.limits(nq[s], nk[s], frame)) == nk[s]
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    rows = torch.from_numpy(np.flatnonzero(sees)).cuda() + q0
+    for at, column in ((1, 3), (0, 4)):
+        hit[rows, at * group:(at + 1) * group, column] = True
+    assert torch.equal(out[~hit], clean[~hit])
+    assert torch.all(torch.isnan(out[rows, group:2 * group, 3])) and torch.all(out[rows, :group, 4] == float("inf"))
+
+
 def test_mostly_empty_batch(planner):
     """A batch padded with empty sequences, ahead, between and behind those with tokens: far more
     places than there are items."""
