@@ -6,9 +6,9 @@
 //   frames of T tokens (the predictor's mask), F >= nk without a mask.
 //
 // A CTA takes 256 query rows of one sequence and key/value head, two tiles of 128 (or the last 128
-// of two heads). A row is a
-// (token, head of the group) pair, token-major, so that a group's heads share the tile of keys
-// and short prompts still fill the rows; groups that do not divide 128 leave a few rows unused.
+// of two heads). A row is a (token, head of the group) pair, token-major, so that a group's heads
+// share the tile of keys and short prompts still fill the rows; groups that do not divide 128
+// leave a few rows unused.
 // Warps:
 //   0-3, 4-7  softmax of tile 0 and 1, a row a thread: read S from TMEM, running maximum and sum,
 //             P (bf16) over the read scores, rescale O in TMEM when the maximum moved by more than
