@@ -90,6 +90,21 @@ __device__ __forceinline__ Place locate(const int* __restrict__ cu, const int* _
   return p;
 }
 
+// Whether packed token t belongs to the sequence that locate found. Not where it lies ahead of the
+// first sequence or behind the last, nor in one whose offsets leave the rows: that one is skipped.
+__device__ __forceinline__ bool holds(const Place& p, int t, int tokens) {
+  return p.s >= 0 && t < p.end && kv8_span_ok(p.begin, p.end, tokens);
+}
+
+// Reports the sequences that are skipped, empty ones too, each by one thread of the grid. Stands at
+// a kernel's end, where the offsets are in the cache.
+__device__ __forceinline__ void report_offsets(const int* __restrict__ cu, int batch, int tokens,
+                                               int* err_flag) {
+  for (long long s = (long long)blockIdx.x * THREADS + threadIdx.x; s < batch;
+       s += (long long)gridDim.x * THREADS)
+    if (!kv8_span_ok(__ldg(cu + s), __ldg(cu + s + 1), tokens)) atomicOr(err_flag, DEV_ERR_INDEX);
+}
+
 // The 16 elements of a head row that a lane holds: chunks of 8 at c0 and c1.
 template <int D, bool INTER>
 struct Lane {
@@ -256,7 +271,7 @@ __device__ __forceinline__ void rotate_queries(const Kv8View& c, const AppendArg
     if (h < a.q_heads) load16(a.q + t * a.q_stride + (long long)h * D, ln, raw[p]);
   }
   const Place at = locate(a.cu, a.start, c.batch, t);
-  if (at.s < 0 || t >= at.end) return;            // behind the last sequence: left as it is
+  if (!holds(at, t, a.tokens)) return;            // left as it is
   const int pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
   if (at.first < 0 || pos < 0 || pos >= positions_of(c, a)) {
     if ((threadIdx.x & 31) == 0) atomicOr(err_flag, DEV_ERR_INDEX);
@@ -281,11 +296,11 @@ struct Piece {
 // What begins at packed token t of the sequence `at`; false where t's page belongs to an earlier
 // owner. Advances t behind it.
 __device__ __forceinline__ bool next_piece(const Kv8View& c, const AppendArgs& a, const Place& at,
-                                           int end, int& t, Piece& p) {
+                                           int& t, Piece& p) {
   p.t = t;
   p.pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
   p.off = p.pos & (c.page - 1);
-  p.n = min(c.page - p.off, end - t);
+  p.n = min(c.page - p.off, at.end - t);
   t += p.n;
   if (p.t != at.begin && p.off != 0) return false;
   p.page = at.first >= 0 && p.pos >= 0 && (long long)p.pos + p.n <= positions_of(c, a)
@@ -312,10 +327,10 @@ __device__ __forceinline__ void append_short(const Kv8View& c, const AppendArgs&
   uint4 raw[2];
   load16(src + t0 * stride, ln, raw);
   const Place at = locate(a.cu, a.start, c.batch, t0);
-  if (at.s < 0 || t0 >= at.end) return;
+  if (!holds(at, t0, a.tokens)) return;
   int t = t0;
   Piece p;
-  if (!next_piece(c, a, at, min(at.end, a.tokens), t, p)) return;
+  if (!next_piece(c, a, at, t, p)) return;
   if (p.page < 0) {
     if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
@@ -370,6 +385,7 @@ __global__ void __launch_bounds__(THREADS) k_append_short(Kv8View c, AppendArgs 
     append_short<D, INTER>(c, a, unit, err_flag);
   else if (a.q)
     rotate_queries<D, INTER>(c, a, unit - kv_units, err_flag);
+  report_offsets(a.cu, c.batch, a.tokens, err_flag);
 }
 
 template <int D, bool INTER>
@@ -427,9 +443,12 @@ __device__ __forceinline__ void append_pages(const Kv8View& c, const AppendArgs&
       at.end = __ldg(a.cu + at.s + 1);
       at.first = __ldg(a.start + at.s);
     }
+    if (!kv8_span_ok(at.begin, at.end, a.tokens)) {
+      t = at.end;
+      continue;
+    }
     Piece p;
-    if (!next_piece(c, a, at, min(at.end, a.tokens), t, p)) continue;
-    if (p.n <= 0) return;                  // offsets that do not ascend
+    if (!next_piece(c, a, at, t, p)) continue;
     if (p.page < 0) {
       if (member == 0) atomicOr(err_flag, DEV_ERR_INDEX);
       continue;
@@ -498,22 +517,22 @@ __global__ void __launch_bounds__(THREADS, V ? 4 : 2)
     k_append_pages(Kv8View c, AppendArgs a, long long units, int* err_flag) {
   asm volatile("griddepcontrol.launch_dependents;");
   append_pages<D, INTER, T, IT, V>(c, a, units, err_flag);
+  if (V) report_offsets(a.cu, c.batch, a.tokens, err_flag);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Cached tokens back as bf16 (code * power of two has at most four significant bits: exact).
 // A warp per packed token; a lane moves 16 codes at a time.
 template <int D>
-__global__ void __launch_bounds__(THREADS) k_kv8_read(Kv8View c, const int* __restrict__ cu,
-                                                      const int* __restrict__ first, int tokens,
-                                                      bf16* __restrict__ k_out,
-                                                      bf16* __restrict__ v_out, int* err_flag) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void read_token(const Kv8View& c, const int* __restrict__ cu,
+                                           const int* __restrict__ first, int tokens,
+                                           bf16* __restrict__ k_out, bf16* __restrict__ v_out,
+                                           int* err_flag) {
   const int t = (int)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= tokens) return;
   const Place p = locate(cu, first, c.batch, t);
-  if (p.s < 0 || t >= p.end) return;
+  if (!holds(p, t, tokens)) return;
   const int pos = (int)((unsigned)p.first + (unsigned)(t - p.begin));
   const int pg =
       p.first < 0 ? -1 : kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, p.s, pos);
@@ -556,6 +575,16 @@ __global__ void __launch_bounds__(THREADS) k_kv8_read(Kv8View c, const int* __re
       store8(to + 8, z[1]);
     }
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) k_kv8_read(Kv8View c, const int* __restrict__ cu,
+                                                      const int* __restrict__ first, int tokens,
+                                                      bf16* __restrict__ k_out,
+                                                      bf16* __restrict__ v_out, int* err_flag) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  read_token<D>(c, cu, first, tokens, k_out, v_out, err_flag);
+  report_offsets(cu, c.batch, tokens, err_flag);
 }
 
 // cos and sin of position / factor * base^(-2 i / rot), in 64 bits: fp32 angles of far positions

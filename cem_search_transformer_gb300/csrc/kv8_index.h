@@ -12,6 +12,11 @@
 
 namespace jepa {
 
+// Whether a packed sequence's tokens [begin, end) are rows of a buffer of `tokens` (none is fine).
+KV8_HD inline bool kv8_span_ok(int begin, int end, int tokens) {
+  return begin >= 0 && begin <= end && end <= tokens;
+}
+
 // Page holding position `pos` of sequence s, or -1 where the position, the table's entry or the
 // page is out of range.
 KV8_HD inline int kv8_page_at(const int* table, int max_pages, int num_pages,

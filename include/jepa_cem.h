@@ -304,7 +304,8 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  *
  * A page index, position, length or offset on the device that lies outside its buffer is never
  * followed: what depends on it is skipped or read as zero (those outputs are unspecified), and
- * the next jepa_sync_check reports JEPA_ERR_INVALID_ARG. */
+ * the next jepa_sync_check reports JEPA_ERR_INVALID_ARG. A sequence whose two offsets descend or lie
+ * outside [0, tokens] is skipped as a whole. */
 
 /* One layer's cache. k, v [num_pages][kv_heads][page_size][head_dim] e4m3 codes; k_scale,
  * v_scale [num_pages][kv_heads] float32: an element stands for code * scale. page_table
