@@ -232,7 +232,7 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
       q0 = __ldg(a.cu_q + s);
       k0 = __ldg(a.cu_k + s);
       const int q1 = __ldg(a.cu_q + s + 1), k1 = __ldg(a.cu_k + s + 1);
-      if (q0 < 0 || q1 < q0 || q1 > a.tokens_q || k0 < 0 || k1 < k0 || k1 > a.tokens_k) {
+      if (!kv8_span_ok(q0, q1, a.tokens_q) || !kv8_span_ok(k0, k1, a.tokens_k)) {
         atomicOr(err_flag, DEV_ERR_INDEX);   // offsets outside the buffers: sequence skipped
       } else {
         nq = q1 - q0;
@@ -278,6 +278,12 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
       it.first_edge = limit_of(it, it.t0, a) / TK;
       cur.s0 = s0;
       cur.base = base;
+      // who has the grid's last place looks at the sequences behind it: nobody else need get there
+      if (index + 1 == gridDim.x)
+        for (int r = s + 32; r < a.batch; r += 32)
+          if (!kv8_span_ok(__ldg(a.cu_q + r), __ldg(a.cu_q + r + 1), a.tokens_q) ||
+              !kv8_span_ok(__ldg(a.cu_k + r), __ldg(a.cu_k + r + 1), a.tokens_k))
+            atomicOr(err_flag, DEV_ERR_INDEX);
       return;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

@@ -91,3 +91,22 @@ def test_read_skips_and_reports(planner, case):
         got.append([k, v])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("side", ["q", "k"])
+@pytest.mark.parametrize("end", [5, -3])
+def test_attention_of_one_query_reports_a_bad_offset_far_behind_it(planner, side, end):
+    """As many places as there are items: no search goes past the last item's sequence by itself."""
+    from cem_search_transformer_gb300 import binding
+    x = [bf16(np.random.default_rng(i).standard_normal((1, 2, 64))).cuda() for i in range(3)]
+    good = [0] + [1] * 70
+    out = [torch.full_like(x[0], 9.0) for _ in range(2)]
+    planner.attention_packed(*x, i32(good), i32(good), out[0], 0.125)
+    planner.sync_check()
+    cu = dict(q=i32(good), k=i32(good))
+    cu[side] = i32(good[:-1] + [end])
+    planner.attention_packed(*x, cu["q"], cu["k"], out[1], 0.125)
+    with pytest.raises(binding.JepaError, match="outside its buffer"):
+        planner.sync_check()
+    planner.sync_check()
+    assert torch.equal(*out)
