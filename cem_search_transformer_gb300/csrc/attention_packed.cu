@@ -38,9 +38,11 @@
 // a masked probability of 0 times an infinity or NaN there is NaN. So in tiles where some row's
 // limit ends, a warp zeroes V rows past the sequence and any non-finite value before the product
 // reads them; the (rare) latter are added to the rows that see them in the read-out.
-// All waits are bounded.
+// All waits are bounded. Most last a step; those that may last an item (the cleaning warp's for its
+// next edge, a query tile's for its next item; 2^27 keys 1.6 s) give up only where nothing moves.
 #include "kv8.cuh"
 #include "tc_common.cuh"
+#include "wait_clock.h"
 
 namespace jepa {
 
@@ -139,16 +141,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 // Bounded wait as mbar_wait of the other kernels, without a call: the register split of
-// setmaxnreg does not go together with one.
+// setmaxnreg does not go together with one. A wait that may last an ITEM counts its limit from the last
+// time that the CTA loaded a tile; the number of those lies behind the abort flag. All waits that way
+// took 4% of a long prompt: the code for it among the steps' (one of 10007 tokens 531 us, 505).
+template <bool ITEM = false>
 __device__ __forceinline__ bool p_wait(uint32_t bar, uint32_t parity, volatile int* abort_smem,
                                        int* err_flag) {
   if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+  WaitClock clock(globaltimer());
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0) {
       if (*abort_smem) return false;
-      if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+      const unsigned long long now = globaltimer();
+      if (clock.due(now, WAIT_LIMIT_NS) && (!ITEM || clock.stuck(now, (unsigned)abort_smem[1]))) {
         *abort_smem = 1;
         atomicOr(err_flag, DEV_ERR_TIMEOUT);
         return false;
@@ -343,7 +349,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   const uint32_t next_slot = smem_u32(tail + 2 * sizeof(Item));   // 16 bytes, 16-byte aligned
   uint32_t* tmem_slot = (uint32_t*)(tail + 2 * sizeof(Item) + 16);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-  static_assert(2 * sizeof(Item) + 16 + 8 + 15 <= 160 && sizeof(Item) % 16 == 0, "tail");
+  volatile int* tiles_loaded = abort_flag + 1;
+  static_assert(2 * sizeof(Item) + 16 + 12 + 15 <= 160 && sizeof(Item) % 16 == 0, "tail");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int span = a.per_tile;
@@ -378,6 +385,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     mbar_init(next_full, 1);
     mbar_init(teardown, 2);
     *abort_flag = 0;
+    *tiles_loaded = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -456,6 +464,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         p_wait(kv_empty(st), ((n / S::STAGES) - 1) & 1, abort_flag, err_flag));
             if (!ok) return;
             ++n;
+            *tiles_loaded = n;
             const uint32_t dst = sb + S::OFF_RING + st * 2 * S::TILE;
             // V tiles with an edge land at the cleaning warp, which passes them on to the issuers
             const bool has_k = i_k < n_tiles, has_v = i_v >= 0, edge = has_v && j_v >= it.first_edge;
@@ -587,14 +596,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       uint32_t phase = 0;            // a bit for each stage
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        ok = __all_sync(0xffffffffu, p_wait(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
+        ok = __all_sync(0xffffffffu, p_wait<true>(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
         if (!ok) break;
         const Item it = items[i & 1];
         if (!it.valid) break;
         const int n_tiles = max(it.nt[0], it.nt[1]) << it.pair;
         for (int i2 = it.first_edge << it.pair; i2 < n_tiles && ok; ++i2) {
           const int j = i2 >> it.pair, st = (n0 + min(S::NBUF, n_tiles) + i2) % S::STAGES;
-          ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
+          ok = __all_sync(0xffffffffu, p_wait<true>(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
           if (!ok) break;
           phase ^= 1u << st;
 #pragma unroll 1
@@ -662,7 +671,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       int ntw, lim, lim_min;
     } next;
     auto look = [&](int i) {
-      if (!all_wait(item_full(i & 1), (i >> 1) & 1)) return false;
+      if (!__all_sync(0xffffffffu, p_wait<true>(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag)))
+        return false;
       const Item it = items[i & 1];
       next.valid = it.valid;
       next.ntw = ((const volatile Item*)items)[i & 1].nt[w];
