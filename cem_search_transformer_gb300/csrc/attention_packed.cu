@@ -38,8 +38,8 @@
 // a masked probability of 0 times an infinity or NaN there is NaN. So in tiles where some row's
 // limit ends, a warp zeroes V rows past the sequence and any non-finite value before the product
 // reads them; the (rare) latter are added to the rows that see them in the read-out.
-// All waits are bounded. Most last a step; those that may last an item (the cleaning warp's for its
-// next edge, a query tile's for its next item; 2^27 keys 1.6 s) give up only where nothing moves.
+// All waits are bounded, by what moves and not by the clock alone: an item of 2^27 keys lasts 1.6 s
+// (twice that for a pair of heads), and adding non-finite values of as many keys 19 s.
 #include "kv8.cuh"
 #include "tc_common.cuh"
 #include "wait_clock.h"
@@ -107,8 +107,9 @@ struct Item {
   int q0, nq, k0, nk;  // the sequence's first packed row and length
   int t0;              // first token of tile 0 within the sequence
   int nt[2];           // key tiles of each query tile (0: no rows, or none that sees a key)
-  int first_edge;      // the first key tile in which some row's limit ends
-  int dirty;           // a non-finite V was taken out of one of its tiles
+  int first_edge;      // the first key tile in which some row's limit ends; where dirty, the first in
+                       // which V is not finite (the cleaning warp moves it)
+  int dirty;           // 0, or one past the last tile out of which a non-finite V was taken
   int pair;            // both tiles hold the sequence's last rows, of this head and the next
 };
 // Where the search for an item goes on: items come in ascending order as a rule.
@@ -141,10 +142,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 // Bounded wait as mbar_wait of the other kernels, without a call: the register split of
-// setmaxnreg does not go together with one. A wait that may last an ITEM counts its limit from the last
-// time that the CTA loaded a tile; the number of those lies behind the abort flag. All waits that way
-// took 4% of a long prompt: the code for it among the steps' (one of 10007 tokens 531 us, 505).
-template <bool ITEM = false>
+// setmaxnreg does not go together with one. The producer's, the cleaning warp's and those for an item
+// give up where nothing MOVED for one to two limits: no tile was loaded, no key read again in the
+// read-out (counted behind the abort flag), and take all others along. A step's waits, of the issuers
+// and the softmax, have a limit beyond the longest read-out of two tiles instead: with that rule in
+// them too one prompt of 10007 tokens took 531 us (505), in the issuers' alone all cases 0.7% more.
+constexpr unsigned long long STEP_LIMIT_NS = 20 * WAIT_LIMIT_NS;
+template <bool MOVED = true>
 __device__ __forceinline__ bool p_wait(uint32_t bar, uint32_t parity, volatile int* abort_smem,
                                        int* err_flag) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -154,7 +158,8 @@ __device__ __forceinline__ bool p_wait(uint32_t bar, uint32_t parity, volatile i
     if ((i & 255u) == 0) {
       if (*abort_smem) return false;
       const unsigned long long now = globaltimer();
-      if (clock.due(now, WAIT_LIMIT_NS) && (!ITEM || clock.stuck(now, (unsigned)abort_smem[1]))) {
+      if (clock.due(now, MOVED ? WAIT_LIMIT_NS : STEP_LIMIT_NS) &&
+          (!MOVED || clock.stuck(now, (unsigned)(abort_smem[1] + abort_smem[2])))) {
         *abort_smem = 1;
         atomicOr(err_flag, DEV_ERR_TIMEOUT);
         return false;
@@ -350,7 +355,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(tail + 2 * sizeof(Item) + 16);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* tiles_loaded = abort_flag + 1;
-  static_assert(2 * sizeof(Item) + 16 + 12 + 15 <= 160 && sizeof(Item) % 16 == 0, "tail");
+  int* const keys_read = (int*)(tmem_slot + 3);
+  static_assert(2 * sizeof(Item) + 16 + 16 + 15 <= 160 && sizeof(Item) % 16 == 0, "tail");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int span = a.per_tile;
@@ -386,6 +392,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     mbar_init(teardown, 2);
     *abort_flag = 0;
     *tiles_loaded = 0;
+    *keys_read = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -501,7 +508,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       constexpr uint32_t idS = idesc_bf16(TQ, TK, false);
       constexpr uint32_t idO = idesc_bf16(TQ, D, true);
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
+        return __all_sync(0xffffffffu, p_wait<false>(bar, parity, abort_flag, err_flag)) != 0;
       };
       const int w = __shfl_sync(0xffffffffu, warp - W_MMA, 0);
       const uint32_t leader = elect_one();
@@ -596,16 +603,18 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       uint32_t phase = 0;            // a bit for each stage
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        ok = __all_sync(0xffffffffu, p_wait<true>(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
+        ok = __all_sync(0xffffffffu, p_wait(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
         if (!ok) break;
         const Item it = items[i & 1];
         if (!it.valid) break;
         const int n_tiles = max(it.nt[0], it.nt[1]) << it.pair;
+        bool found = false;
         for (int i2 = it.first_edge << it.pair; i2 < n_tiles && ok; ++i2) {
           const int j = i2 >> it.pair, st = (n0 + min(S::NBUF, n_tiles) + i2) % S::STAGES;
-          ok = __all_sync(0xffffffffu, p_wait<true>(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
+          ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
           if (!ok) break;
           phase ^= 1u << st;
+          bool any = false;
 #pragma unroll 1
           for (int row = lane; row < TK; row += 32) {   // thread = key
             uint8_t* v_row = smem + S::OFF_RING + st * 2 * S::TILE + row * 128;
@@ -621,7 +630,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               odd &= 0x80008000u;
             }
             if (behind || odd) {
-              if (odd) *(volatile int*)&items[i & 1].dirty = 1;
+              any = any || odd;
 #pragma unroll 1
               for (int c = 0; c < D / 8; ++c) {
                 uint4* at = reinterpret_cast<uint4*>(v_row + (c >> 3) * KBLK + 16 * ((c & 7) ^ (row & 7)));
@@ -638,6 +647,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 *at = make_uint4(x[0], x[1], x[2], x[3]);
               }
             }
+          }
+          if (__any_sync(0xffffffffu, any)) {
+            volatile Item* slot = &items[i & 1];
+            if (lane == 0) {
+              if (!found) slot->first_edge = j;
+              slot->dirty = j + 1;
+            }
+            found = true;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -660,7 +677,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint8_t* const stage = smem + S::OFF_OUT + warp * 4096;
     // a warp goes on, or gives up, as one: what follows a wait are warp-wide instructions
     auto all_wait = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
+      return __all_sync(0xffffffffu, p_wait<false>(bar, parity, abort_flag, err_flag)) != 0;
     };
     int buf = 0;           // score buffer and lap of the next key tile
     uint32_t lap = 0;
@@ -671,8 +688,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       int ntw, lim, lim_min;
     } next;
     auto look = [&](int i) {
-      if (!__all_sync(0xffffffffu, p_wait<true>(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag)))
-        return false;
+      if (!__all_sync(0xffffffffu, p_wait(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag))) return false;
       const Item it = items[i & 1];
       next.valid = it.valid;
       next.ntw = ((const volatile Item*)items)[i & 1].nt[w];
@@ -825,14 +841,35 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             ov[c] = __float_as_uint(empty ? 0.f : __uint_as_float(ov[c]) * inv);
-          if (fix && mine) {
+          if (fix) {
+            // lane = column: a key's 32 in one load, 16 keys in flight. The keys up to the least limit,
+            // added to the rows that have it, then on to the next limit
+            const int last = mine ? min(lim, slot->dirty * TK) : 0;
+            const bf16* column = a.v + (long long)slot->k0 * a.v_stride + (long long)head * D + col + lane;
+            float odd = 0.f;             // sum of the column's values so far that are not finite
+            for (int key = slot->first_edge * TK;;) {
+              const int next = __reduce_min_sync(0xffffffffu, last > key ? last : 0x7fffffff);
+              if (next == 0x7fffffff) break;
 #pragma unroll 1
-            for (int key = slot->first_edge * TK; key < lim; ++key) {
-              const bf16* vr = a.v + (long long)(slot->k0 + key) * a.v_stride + (long long)head * D + col;
+              for (; key + 16 <= next; key += 16) {
+                float x[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = __bfloat162float(column[(long long)(key + k) * a.v_stride]);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) odd += fabsf(x[k]) < INFINITY ? 0.f : x[k];
+                if ((key & 0x3ff0) == 0 && lane == 0) atomicAdd(keys_read, 1);
+              }
+#pragma unroll 1
+              for (; key < next; ++key) {
+                const float x = __bfloat162float(column[(long long)key * a.v_stride]);
+                odd += fabsf(x) < INFINITY ? 0.f : x;
+              }
+              const uint32_t columns = __ballot_sync(0xffffffffu, odd != 0.f);
+              if (columns == 0) continue;
 #pragma unroll
               for (int c = 0; c < 32; ++c) {
-                const float x = __bfloat162float(vr[c]);
-                if (!(fabsf(x) < INFINITY)) ov[c] = __float_as_uint(__uint_as_float(ov[c]) + x);
+                const float x = __shfl_sync(0xffffffffu, odd, c);
+                if (last == next && (columns >> c & 1)) ov[c] = __float_as_uint(__uint_as_float(ov[c]) + x);
               }
             }
           }
