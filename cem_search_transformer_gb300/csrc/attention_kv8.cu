@@ -43,6 +43,7 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int MAX_CTAS_PER_SM = 4;  // of any shape: sizes the workspace
+constexpr int MAX_SMS = 160;        // of the whole chip; this part has 152 in use
 constexpr int MIN_UNITS = 4;        // units a CTA takes at least where items are split
 constexpr int WHOLE_UNITS = 8;      // items up to this many units are not split
 constexpr int ITEM_UNITS = 2;       // what an item costs besides its units: start and joining
@@ -58,7 +59,7 @@ struct Shape {
   // cp.async stages of a warp and CTAs a SM. Narrow heads: four CTAs with two stages hide more of
   // a step's latency than three with three (256 candidates of 776 tokens: 6% less);
   // heads of 128 the other way round (two long sequences: 7% less). Two row tiles of 128
-  // columns need 250 registers a thread and 82 KB, so two CTAs (32 sequences of up to 8000
+  // columns need 244 registers a thread and 82 KB, so two CTAs (32 sequences of up to 8000
   // tokens, 16 rows: 85 us; a quarter more with three CTAs of two stages, which spill).
   static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;
   static constexpr int CTAS = D == 64 ? (NR == 1 ? 4 : 3) : (NR == 1 ? 3 : 2);
@@ -74,6 +75,9 @@ struct Shape {
   static constexpr int OFF_OUT = OFF_SCALE + WARPS * NST * 16;
   static constexpr int SMEM = OFF_OUT + WARPS * ROWS * OUT_LD * 4;
   static_assert(CTAS <= MAX_CTAS_PER_SM && CTAS * (SMEM + 2048) <= 228 * 1024, "CTAs of a SM");
+  // k_combine: a maximum and a sum of each part for its 512 / D rows (heads of 64: 38 KB on 152 SMs)
+  static constexpr int COMBINE_SMEM = 2 * (512 / D) * (int)sizeof(float);   // bytes a CTA of the call
+  static_assert(COMBINE_SMEM * CTAS * MAX_SMS <= 48 * 1024, "what a launch may have without an attribute");
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -834,7 +838,8 @@ cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStr
   if (e != cudaSuccess) return e;
   a.tiles = (a.q_tokens * a.group + S::ROWS - 1) / S::ROWS;
   const long long max_len = (long long)c.max_pages << c.page_log2;
-  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT, slots = (long long)num_sms * S::CTAS;
+  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT;
+  const long long slots = (long long)(num_sms < MAX_SMS ? num_sms : MAX_SMS) * S::CTAS;
   const long long items = (long long)c.batch * c.heads * a.tiles;
   const int whole = max_units <= WHOLE_UNITS;
   // every SM's slots, or the work there can be if that is less
@@ -849,7 +854,7 @@ cudaError_t launch(const Kv8View& c, Args a, int* err_flag, int num_sms, cudaStr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, S::ROWS * D / 512);
   cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 2 * (512 / D) * grid * sizeof(float);   // 30 KB at most
+  cfg.dynamicSmemBytes = S::COMBINE_SMEM * grid;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
