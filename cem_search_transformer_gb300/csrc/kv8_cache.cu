@@ -601,8 +601,9 @@ __global__ void k_rope_table(int positions, int rot, double log2_base, double in
   table[(long long)p * rot + half + j] = (float)sn;
 }
 
-template <int D, bool INTER, int T, int IT>
+template <int D, bool INTER, int PAGE, int T, int IT>
 cudaError_t launch_pages(const Kv8View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
+  static_assert(T * (512 / D) * IT == PAGE, "a team's lanes hold a page's rows, no less and no more");
   constexpr int TEAMS = THREADS / 32 / T;
   const long long units = (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads;
   const long long blocks = (units + TEAMS - 1) / TEAMS;
@@ -631,19 +632,21 @@ cudaError_t launch_append(const Kv8View& c, const AppendArgs& a, int* err_flag, 
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // 64 elements a lane
-  if (D == 128)
+  // 64 elements a lane (32 where a page of 16 rows gives one warp no more)
+  if constexpr (D == 128) {
     switch (c.page) {
-      case 16: return launch_pages<D, INTER, 1, 4>(c, a, err_flag, s);
-      case 32: return launch_pages<D, INTER, 2, 4>(c, a, err_flag, s);
-      case 64: return launch_pages<D, INTER, 4, 4>(c, a, err_flag, s);
-      default: return launch_pages<D, INTER, 8, 4>(c, a, err_flag, s);
+      case 16: return launch_pages<D, INTER, 16, 1, 4>(c, a, err_flag, s);
+      case 32: return launch_pages<D, INTER, 32, 2, 4>(c, a, err_flag, s);
+      case 64: return launch_pages<D, INTER, 64, 4, 4>(c, a, err_flag, s);
+      default: return launch_pages<D, INTER, 128, 8, 4>(c, a, err_flag, s);
     }
-  switch (c.page) {
-    case 16: return launch_pages<D, INTER, 1, 2>(c, a, err_flag, s);
-    case 32: return launch_pages<D, INTER, 1, 4>(c, a, err_flag, s);
-    case 64: return launch_pages<D, INTER, 2, 4>(c, a, err_flag, s);
-    default: return launch_pages<D, INTER, 4, 4>(c, a, err_flag, s);
+  } else {
+    switch (c.page) {
+      case 16: return launch_pages<D, INTER, 16, 1, 2>(c, a, err_flag, s);
+      case 32: return launch_pages<D, INTER, 32, 1, 4>(c, a, err_flag, s);
+      case 64: return launch_pages<D, INTER, 64, 2, 4>(c, a, err_flag, s);
+      default: return launch_pages<D, INTER, 128, 4, 4>(c, a, err_flag, s);
+    }
   }
 }
 
