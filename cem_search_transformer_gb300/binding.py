@@ -216,6 +216,16 @@ def _opt(t, name: str, kind: str, numel: int, device: int) -> Optional[int]:
     return None if t is None else _dev(t, name, kind, numel, device)
 
 
+def _sized(t, name: str):
+    """`t` itself, once it is a tensor: for arguments whose size the call goes by, where an address
+    says too little."""
+    if _Fast.torch is None:
+        _Fast.load()
+    if not isinstance(t, _Fast.Tensor):
+        raise JepaError(1, f"{name}: expected a torch tensor, got {type(t).__name__}")
+    return t
+
+
 def _rows(t, name: str, device: Optional[int] = None):
     """(address, elements between tokens, tokens, heads, head_dim) of token rows [tokens, heads,
     head_dim]: a bf16 CUDA tensor whose heads lie back to back (a slice of a wider projection's
@@ -245,9 +255,10 @@ class KvCache8:
     float32 [num_pages, kv_heads]; page_table: int32 [batch, max_pages]."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table):
-        if _Fast.torch is None:
-            _Fast.load()
-        if getattr(k, "ndim", 0) != 4 or getattr(page_table, "ndim", 0) != 2:
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale),
+                        ("page_table", page_table)):
+            _sized(t, "KvCache8: " + name)
+        if k.dim() != 4 or page_table.dim() != 2:
             raise JepaError(1, "KvCache8: k must be [num_pages, kv_heads, page_size, head_dim] and "
                                "page_table [batch, max_pages]")
         pages, heads, page, dim = k.shape
@@ -539,7 +550,11 @@ class Planner:
             if q_tokens != tokens or q_dim != dim:
                 raise JepaError(1, f"q {tuple(q.shape)} does not fit k {tuple(k.shape)}")
             qo = _dev(q_out, "q_out", "bf16", tokens * q_heads * dim, dev)
-        positions, rot = (0, 0) if rope_table is None else rope_table.shape
+        positions = rot = 0
+        if rope_table is not None:
+            if _sized(rope_table, "rope_table").dim() != 2:
+                raise JepaError(1, "rope_table must be [positions, rot]")
+            positions, rot = rope_table.shape
         cache.check(dev)
         if tokens < 1:
             raise JepaError(1, "tokens must be >= 1 (got 0)")
@@ -557,7 +572,7 @@ class Planner:
         """Cached tokens as bf16 into k_out, v_out [tokens, kv_heads, head_dim]."""
         dev = self.device
         cache.check(dev)
-        tokens = k_out.shape[0]
+        tokens = k_out.shape[0] if _sized(k_out, "k_out").dim() else 0
         if tokens < 1:
             raise JepaError(1, "tokens must be >= 1 (got 0)")
         n = tokens * cache.kv_heads * cache.head_dim
@@ -591,7 +606,8 @@ class Planner:
             self.h, cache.ref, _dev(q, "q", "bf16", rows * dim, dev), q_tokens, q_heads,
             _dev(kv_len, "kv_len", "i32", batch, dev), scale, int(causal),
             _dev(out, "out", "bf16", rows * dim, dev), _opt(lse, "lse", "f32", rows, dev),
-            _dev(workspace, "workspace", "u8", 0, dev), workspace.numel(), _stream_on(stream, dev))
+            _dev(_sized(workspace, "workspace"), "workspace", "u8", 0, dev), workspace.numel(),
+            _stream_on(stream, dev))
         if st:
             self._check(st, "attention_kv8")
 
@@ -604,7 +620,7 @@ class Planner:
         vp, vs, *v_shape = _rows(v, "v", dev)
         if v_shape != [tokens_k, kv_heads, k_dim] or k_dim != dim:
             raise JepaError(1, f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
-        batch = cu_q.numel() - 1
+        batch = _sized(cu_q, "cu_q").numel() - 1
         if min(tokens_q, tokens_k, batch) < 1:
             raise JepaError(1, "tokens_q, tokens_k and batch must be >= 1")
         st = self.lib.jepa_attention_packed(
