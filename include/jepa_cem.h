@@ -291,7 +291,7 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  * For histories longer than the planner's dense per-candidate caches hold well: sequences of
  * different lengths share one pool of pages, keys and values take a byte an element, and
  * sequences with a common context may name the same pages. Serving only (no gradients). All of
- * these entry points need a bf16 (or fp8) context and no weights, enqueue on `stream`, allocate
+ * these entry points need a bf16 (or fp8) context (jepa_rope_table any) and no weights, enqueue on `stream`, allocate
  * nothing, and can be captured into a CUDA graph; what they read from the device (offsets,
  * lengths, page tables) is read when the graph runs. Tensors are bf16 bit patterns (uint16).
  * Token rows are [tokens][heads][head_dim] with `*_stride` elements between tokens (at least
@@ -311,8 +311,8 @@ jepa_status jepa_attention_bf16(jepa_ctx* ctx, const uint16_t* q, const uint16_t
  * v_scale [num_pages][kv_heads] float32: an element stands for code * scale. page_table
  * [batch][max_pages] int32: token t of sequence b lies in page page_table[b][t / page_size],
  * slot t % page_size; entries past a sequence's length are not read. head_dim 64 or 128,
- * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30, num_pages * kv_heads < 2^31; k and
- * v 16-byte aligned. Scales lie in [2^-40, 2^40] (others are read as the nearer end, NaN as the
+ * page_size 16, 32, 64 or 128, max_pages * page_size <= 2^30, num_pages * kv_heads < 2^31, batch at
+ * most 65535, kv_heads at most 1024; k and v 16-byte aligned. Scales lie in [2^-40, 2^40] (others are read as the nearer end, NaN as the
  * least); those written here are powers of two. The codes and scales of fresh pages need no
  * initial values. */
 typedef struct {
@@ -345,7 +345,7 @@ jepa_status jepa_rope_table(jepa_ctx* ctx, int positions, int rot, double base, 
  *   [tokens][kv_heads][head_dim] dev; k_out (dense, the rotated keys as bf16, as
  *   jepa_attention_packed wants them) dev or NULL; q_norm, k_norm [head_dim] float32 dev or NULL;
  *   rope_table [positions][rot]; cu [batch + 1], start [batch] int32 dev.
- *   q_heads a multiple of kv_heads; rot a multiple of 16, 0 <= rot <= head_dim (0: no rotation);
+ *   q_heads a multiple of kv_heads, at most 65535; rot a multiple of 16, 0 <= rot <= head_dim (0: no rotation);
  *   q_out may be q and k_out may be k where those rows are dense; no other overlap.
  * A page that receives tokens belongs to one place of one sequence (shared pages are full). */
 jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
@@ -376,7 +376,8 @@ jepa_status jepa_attention_kv8_workspace(jepa_ctx* ctx, const jepa_kv8_cache* ca
  * whatever it holds.
  *   q, out [batch][q_tokens][q_heads][head_dim], 16-byte aligned, dev; kv_len [batch] int32
  *   dev; lse [batch][q_tokens][q_heads] float32 dev or NULL; workspace: device memory of the
- *   size above, 256-byte aligned, its contents between calls without meaning. Calls that may
+ *   size above, 256-byte aligned, its contents between calls without meaning. At most 65536 query
+ *   rows a key/value head of a sequence (q_tokens * q_heads / kv_heads) and 2^30 in all. Calls that may
  *   overlap on the device (streams, graphs) need a workspace each. scale finite, > 0. */
 jepa_status jepa_attention_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
                                int q_tokens, int q_heads, const int32_t* kv_len, float scale,
@@ -391,8 +392,12 @@ jepa_status jepa_attention_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const
  *   aligned, dev; cu_q, cu_k [batch + 1]; out [tokens_q][q_heads][head_dim] dense, 16-byte
  *   aligned; lse [tokens_q][q_heads] float32 or NULL, as in jepa_attention_kv8, whose promises
  *   for unseen keys and empty rows hold here too. head_dim 64 or 128, q_heads a multiple of
- *   kv_heads with at most 128 per key/value head, scale finite and > 0, frame >= 1, tokens_q and
- *   tokens_k at most 2^27. */
+ *   kv_heads with at most 128 per key/value head and 65535 in all, scale finite and > 0, frame >= 1,
+ *   batch at most 65535, tokens_q and tokens_k at most 2^27, and
+ *   (tokens_q / (2 * (128 / group)) + min(batch, tokens_q)) * kv_heads at most 2^28 with group =
+ *   q_heads / kv_heads. A value of v that is not finite reaches the queries that see it; where many
+ *   of them lie behind some query's limit in its block of 256 rows, that block costs up to 0.15 us a
+ *   key more. */
 jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_stride,
                                   const uint16_t* k, int64_t k_stride, const uint16_t* v,
                                   int64_t v_stride, int tokens_q, int tokens_k, int batch,
