@@ -96,13 +96,16 @@ __device__ __forceinline__ bool holds(const Place& p, int t, int tokens) {
   return p.s >= 0 && t < p.end && kv8_span_ok(p.begin, p.end, tokens);
 }
 
-// Reports the sequences that are skipped, empty ones too, each by one thread of the grid. Stands at
-// a kernel's end, where the offsets are in the cache.
+// Reports the sequences that are skipped, empty ones too, each by one thread of the grid (which has a
+// thread for each). Stands at a kernel's end, where the offsets are in the cache.
 __device__ __forceinline__ void report_offsets(const int* __restrict__ cu, int batch, int tokens,
                                                int* err_flag) {
-  for (long long s = (long long)blockIdx.x * THREADS + threadIdx.x; s < batch;
-       s += (long long)gridDim.x * THREADS)
-    if (!kv8_span_ok(__ldg(cu + s), __ldg(cu + s + 1), tokens)) atomicOr(err_flag, DEV_ERR_INDEX);
+  const long long s = (long long)blockIdx.x * THREADS + threadIdx.x;
+  if (s < batch && !kv8_span_ok(__ldg(cu + s), __ldg(cu + s + 1), tokens)) atomicOr(err_flag, DEV_ERR_INDEX);
+}
+// Blocks for `threads` of work and at least one thread a sequence.
+long long blocks_for(long long threads, int batch) {
+  return ((threads > batch ? threads : batch) + THREADS - 1) / THREADS;
 }
 
 // The 16 elements of a head row that a lane holds: chunks of 8 at c0 and c1.
@@ -605,9 +608,8 @@ __global__ void k_rope_table(int positions, int rot, double log2_base, double in
 template <int D, bool INTER, int PAGE, int T, int IT>
 cudaError_t launch_pages(const Kv8View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
   static_assert(T * (512 / D) * IT == PAGE, "a team's lanes hold a page's rows, no less and no more");
-  constexpr int TEAMS = THREADS / 32 / T;
   const long long units = (((long long)a.tokens + c.page - 1) >> c.page_log2) * c.heads;
-  const long long blocks = (units + TEAMS - 1) / TEAMS;
+  const long long blocks = blocks_for(units * T * 32, c.batch);   // a team has T warps
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const cudaError_t e = launch_early(k_append_pages<D, INTER, T, IT, true>, (unsigned)blocks, a.q != nullptr, s,
                                      c, a, units, err_flag);
@@ -627,7 +629,7 @@ cudaError_t launch_append(const Kv8View& c, const AppendArgs& a, int* err_flag, 
   // tokens beside 200 single ones 76 us, the page kernels 15.
   if (a.tokens <= 4LL * c.batch) {
     const long long kv_units = 2LL * a.tokens * ((c.heads + HEADS - 1) / HEADS);
-    const long long blocks = (kv_units + q_units + WARPS - 1) / WARPS;
+    const long long blocks = blocks_for(32 * (kv_units + q_units), c.batch);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_early(k_append_short<D, INTER>, (unsigned)blocks, true, s, c, a, kv_units, err_flag);
   }
@@ -673,7 +675,7 @@ cudaError_t rope_append_kv8(const Kv8View& c, const AppendArgs& a, int* err_flag
 cudaError_t kv8_read(const Kv8View& c, const int* cu, const int* first, int tokens, bf16* k_out,
                      bf16* v_out, int* err_flag, cudaStream_t s) {
   if (tokens <= 0) return cudaSuccess;
-  const unsigned grid = (unsigned)(((long long)tokens * 32 + THREADS - 1) / THREADS);
+  const unsigned grid = (unsigned)blocks_for(32LL * tokens, c.batch);
   if (c.dim == 64)
     return launch_early(k_kv8_read<64>, grid, true, s, c, cu, first, tokens, k_out, v_out, err_flag);
   if (c.dim == 128)

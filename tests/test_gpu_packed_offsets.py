@@ -110,3 +110,27 @@ def test_attention_of_one_query_reports_a_bad_offset_far_behind_it(planner, side
         planner.sync_check()
     planner.sync_check()
     assert torch.equal(*out)
+
+
+@pytest.mark.parametrize("end", [2, 0])
+def test_the_last_of_65535_sequences(planner, end):
+    """As many sequences as a call may have and one token: every pair of offsets is looked at."""
+    from cem_search_transformer_gb300 import binding
+    batch, heads, dim, page = 65535, 1, 64, 16
+    pool = Pool([16], heads, page, dim, seed=1)
+    table = torch.full((batch, 1), -1, dtype=torch.int32, device="cuda")
+    table[0] = int(pool.table_np[0, 0])
+    cache = binding.KvCache8(pool.k, pool.v, pool.ks, pool.vs, table)
+    x = bf16(np.random.default_rng(1).standard_normal((1, heads, dim))).cuda()
+    start, k, v = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.zeros_like(x), torch.zeros_like(x)
+    for last in (1, end):
+        cu = torch.ones(batch + 1, dtype=torch.int32, device="cuda")
+        cu[0], cu[batch] = 0, last
+        for call in (lambda: planner.rope_append_kv8(None, x, x, None, cu, start, cache, None),
+                     lambda: planner.kv8_read(cache, cu, start, k, v)):
+            call()
+            if last != 1:
+                with pytest.raises(binding.JepaError, match="outside its buffer"):
+                    planner.sync_check()
+            planner.sync_check()
+    assert torch.equal(k, v) and torch.max(torch.abs(k.float() - x.float())) <= 2.0 ** -4 * torch.max(torch.abs(x.float()))
