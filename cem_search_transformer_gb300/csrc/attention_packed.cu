@@ -248,7 +248,7 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
       q0 = __ldg(a.cu_q + s);
       k0 = __ldg(a.cu_k + s);
       const int q1 = __ldg(a.cu_q + s + 1), k1 = __ldg(a.cu_k + s + 1);
-      if (!kv8_span_ok(q0, q1, a.tokens_q) || !kv8_span_ok(k0, k1, a.tokens_k)) {
+      if (!(kv8_span_ok(q0, q1, a.tokens_q) & kv8_span_ok(k0, k1, a.tokens_k))) {
         atomicOr(err_flag, DEV_ERR_INDEX);   // offsets outside the buffers: sequence skipped
       } else {
         nq = q1 - q0;
@@ -294,17 +294,29 @@ __device__ __forceinline__ void find_item(const PArgs& a, long long index, Curso
       it.first_edge = limit_of(it, it.t0, a) / TK;
       cur.s0 = s0;
       cur.base = base;
-      // who has the grid's last place looks at the sequences behind it: nobody else need get there
-      if (index + 1 == gridDim.x)
-        for (int r = s + 32; r < a.batch; r += 32)
-          if (!kv8_span_ok(__ldg(a.cu_q + r), __ldg(a.cu_q + r + 1), a.tokens_q) ||
-              !kv8_span_ok(__ldg(a.cu_k + r), __ldg(a.cu_k + r + 1), a.tokens_k))
-            atomicOr(err_flag, DEV_ERR_INDEX);
       return;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
   cur.total = base;
+}
+
+// Reports bad offsets among the sequences of a place of the grid, 256 at a time, by THREADS threads.
+// Searches look at all sequences as long as one of them runs to the end, which may be none where
+// there are more sequences than queries: every place then has an item. (One query among 65535
+// sequences 31 us, 10 unchecked; among 1024 the same 10.)
+template <int THREADS>
+__device__ __forceinline__ void report_offsets(const PArgs& a, int place, int thread, int* err_flag) {
+  bool ok = true;
+#pragma unroll 4
+  for (long long s0 = place * 256LL; s0 < a.batch; s0 += gridDim.x * 256LL)
+#pragma unroll
+    for (int k = thread; k < 256; k += THREADS) {
+      const int s = (int)min(s0 + k, a.batch - 1LL);
+      ok &= kv8_span_ok(__ldg(a.cu_q + s), __ldg(a.cu_q + s + 1), a.tokens_q) &
+            kv8_span_ok(__ldg(a.cu_k + s), __ldg(a.cu_k + s + 1), a.tokens_k);
+    }
+  if (!ok) atomicOr(err_flag, DEV_ERR_INDEX);
 }
 
 // Asks for the next CTA of the grid that has not begun to run to be given to this one instead (16
@@ -375,6 +387,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     Item it;
     find_item<S::TK>(a, blockIdx.x, cursor, it, err_flag);
     if (lane == 0) items[0] = it;
+  } else if (warp < W_MMA && a.tokens_q < a.batch) {
+    report_offsets<256>(a, blockIdx.x, threadIdx.x, err_flag);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
@@ -441,6 +455,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           const int index = clc_index(next_slot);
           __syncwarp();
           if (index < 0) break;
+          if (a.tokens_q < a.batch) report_offsets<32>(a, index, lane, err_flag);
           find_item<S::TK>(a, index, cursor, it, err_flag);
         }
         if (!ok) break;

@@ -14,7 +14,8 @@ namespace jepa {
 
 // Whether a packed sequence's tokens [begin, end) are rows of a buffer of `tokens` (none is fine).
 KV8_HD inline bool kv8_span_ok(int begin, int end, int tokens) {
-  return begin >= 0 && begin <= end && end <= tokens;
+  // as unsigned a negative offset lies behind every other
+  return ((uint32_t)begin <= (uint32_t)end) & ((uint32_t)end <= (uint32_t)tokens);
 }
 
 // Page holding position `pos` of sequence s, or -1 where the position, the table's entry or the
