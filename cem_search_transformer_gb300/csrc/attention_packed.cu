@@ -147,13 +147,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 // Bounded wait as mbar_wait of the other kernels, without a call: the register split of
-// setmaxnreg does not go together with one. The producer's, the cleaning warp's and those for an item
-// give up where nothing MOVED for one to two limits: no tile was loaded, no key read again in the
-// read-out (counted behind the abort flag), and take all others along. A step's waits, of the issuers
-// and the softmax, have a limit beyond the longest read-out of two tiles instead: with that rule in
-// them too one prompt of 10007 tokens took 531 us (505), in the issuers' alone all cases 0.7% more.
+// setmaxnreg does not go together with one. The cleaning warp waits as long as there are items, and so
+// stands watch: its waits give up where nothing MOVED for one to two limits (no tile was loaded, no key
+// read again in the read-out: counted behind the abort flag), and take all others along. The others'
+// limit lies beyond the longest item or read-out of two tiles: the rule's code in the softmax too took
+// 5% (one prompt of 10007 tokens 531 us, 505), in all but softmax and issuers 1% of the frames' case.
 constexpr unsigned long long STEP_LIMIT_NS = 20 * WAIT_LIMIT_NS;
-template <bool MOVED = true>
+template <bool MOVED = false>
 __device__ __forceinline__ bool p_wait(uint32_t bar, uint32_t parity, volatile int* abort_smem,
                                        int* err_flag) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       constexpr uint32_t idS = idesc_bf16(TQ, TK, false);
       constexpr uint32_t idO = idesc_bf16(TQ, D, true);
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, p_wait<false>(bar, parity, abort_flag, err_flag)) != 0;
+        return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
       };
       const int w = __shfl_sync(0xffffffffu, warp - W_MMA, 0);
       const uint32_t leader = elect_one();
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       uint32_t phase = 0;            // a bit for each stage
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        ok = __all_sync(0xffffffffu, p_wait(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
+        ok = __all_sync(0xffffffffu, p_wait<true>(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag));
         if (!ok) break;
         const Item it = items[i & 1];
         if (!it.valid) break;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         bool found = false;
         for (int i2 = it.first_edge << it.pair; i2 < n_tiles && ok; ++i2) {
           const int j = i2 >> it.pair, st = (n0 + min(S::NBUF, n_tiles) + i2) % S::STAGES;
-          ok = __all_sync(0xffffffffu, p_wait(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
+          ok = __all_sync(0xffffffffu, p_wait<true>(edge_full(st), (phase >> st) & 1, abort_flag, err_flag));
           if (!ok) break;
           phase ^= 1u << st;
           bool any = false;
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint8_t* const stage = smem + S::OFF_OUT + warp * 4096;
     // a warp goes on, or gives up, as one: what follows a wait are warp-wide instructions
     auto all_wait = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, p_wait<false>(bar, parity, abort_flag, err_flag)) != 0;
+      return __all_sync(0xffffffffu, p_wait(bar, parity, abort_flag, err_flag)) != 0;
     };
     int buf = 0;           // score buffer and lap of the next key tile
     uint32_t lap = 0;
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       int ntw, lim, lim_min;
     } next;
     auto look = [&](int i) {
-      if (!__all_sync(0xffffffffu, p_wait(item_full(i & 1), (i >> 1) & 1, abort_flag, err_flag))) return false;
+      if (!all_wait(item_full(i & 1), (i >> 1) & 1)) return false;
       const Item it = items[i & 1];
       next.valid = it.valid;
       next.ntw = ((const volatile Item*)items)[i & 1].nt[w];
