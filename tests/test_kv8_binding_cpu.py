@@ -6,8 +6,6 @@ import torch
 from cem_search_transformer_gb300 import binding
 from test_kv8_cpu import _cache_tensors, _NoLibrary
 
-CUDA = "CUDA"
-
 
 class _Cache:
     batch, kv_heads, head_dim = 2, 2, 64
