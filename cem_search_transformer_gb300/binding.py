@@ -30,7 +30,9 @@ EXPORTS = ("jepa_create", "jepa_destroy", "jepa_last_error", "jepa_status_string
            "jepa_cem_closed_loop", "jepa_linear_fp8", "jepa_quantize_rows_fp8",
            "jepa_set_use_graphs", "jepa_selftest_bounded_wait", "jepa_linear_resid_bf16",
            "jepa_linear_qkv_bf16", "jepa_rope_table", "jepa_rope_append_kv8", "jepa_kv8_read",
-           "jepa_attention_kv8_workspace", "jepa_attention_kv8", "jepa_attention_packed")
+           "jepa_attention_kv8_workspace", "jepa_attention_kv8", "jepa_attention_packed",
+           "jepa_rope_append_kv4", "jepa_kv4_read", "jepa_attention_kv4_workspace", "jepa_attention_kv4",
+           "jepa_kv4_evict_workspace", "jepa_kv4_evict", "jepa_add_rmsnorm_fp8")
 
 
 class JepaError(RuntimeError):
@@ -65,6 +67,15 @@ class Kv8Struct(ctypes.Structure):
                 ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
+class Kv4Struct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_unit", ctypes.c_void_p), ("v_unit", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 def load(path: str = _LIB_PATH):
     """Load the library (once) and declare its signatures."""
     global _lib
@@ -75,6 +86,7 @@ def load(path: str = _LIB_PATH):
     lib = ctypes.CDLL(path)
     P, I, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_float
     I64, D, Z, CACHE = ctypes.c_int64, ctypes.c_double, ctypes.c_size_t, ctypes.POINTER(Kv8Struct)
+    CACHE4 = ctypes.POINTER(Kv4Struct)
     sig = {
         "jepa_create": ([ctypes.POINTER(Config), I, ctypes.POINTER(P)], I),
         "jepa_destroy": ([P], None),
@@ -110,6 +122,14 @@ def load(path: str = _LIB_PATH):
         "jepa_attention_kv8": ([P, CACHE, P, I, I, P, F, I, P, P, P, Z, P], I),
         "jepa_attention_packed": ([P, P, I64, P, I64, P, I64, I, I, I, I, I, I, P, P, F, I, P, P, P],
                                   I),
+        "jepa_rope_append_kv4": ([P, CACHE4, P, I64, P, I64, P, I64, I, I, P, P, F, P, I, I, I, P, P,
+                                  P, P, P], I),
+        "jepa_kv4_read": ([P, CACHE4, P, P, I, P, P, P], I),
+        "jepa_attention_kv4_workspace": ([P, CACHE4, ctypes.POINTER(Z)], I),
+        "jepa_attention_kv4": ([P, CACHE4, P, I, I, P, F, I, P, P, P, P, F, P, Z, P], I),
+        "jepa_kv4_evict_workspace": ([P, CACHE4, I, ctypes.POINTER(Z)], I),
+        "jepa_kv4_evict": ([P, CACHE4, P, P, I, I, CACHE4, P, P, P, Z, P], I),
+        "jepa_add_rmsnorm_fp8": ([P, P, I, I64, P, I, I64, P, F, I, I, P, I64, P, P, P, P], I),
         "jepa_set_use_graphs": ([P, I], I),
         "jepa_selftest_bounded_wait": ([P, P], I),
     }
@@ -290,6 +310,72 @@ class KvCache8:
             raise JepaError(1, f"cache is on {self.device}, the planner on cuda:{device}")
 
 
+class KvCache4:
+    """One layer's 4-bit paged key/value cache (jepa_kv4_cache of the C header) over tensors that
+    the caller owns; the handle keeps them alive and checks them once.
+
+    k, v: uint8 [num_pages, kv_heads, page_size, head_dim / 2]; k_scale, v_scale: uint8 or
+    float8_e4m3fn [num_pages, kv_heads, page_size, head_dim / 16]; page_table: int32 [batch,
+    max_pages]; k_unit, v_unit: float32 [kv_heads], powers of two, or None (1)."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, k_unit=None, v_unit=None):
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale),
+                        ("page_table", page_table)):
+            _sized(t, "KvCache4: " + name)
+        if k.dim() != 4 or page_table.dim() != 2:
+            raise JepaError(1, "KvCache4: k must be [num_pages, kv_heads, page_size, head_dim / 2] and "
+                               "page_table [batch, max_pages]")
+        pages, heads, page, half = k.shape
+        dim = 2 * half
+        if dim not in (64, 128) or page not in (16, 32, 64, 128):
+            raise JepaError(2, "KvCache4: head_dim must be 64 or 128, page_size 16, 32, 64 or 128")
+        if tuple(v.shape) != tuple(k.shape):
+            raise JepaError(1, f"KvCache4: v has shape {tuple(v.shape)}, k {tuple(k.shape)}")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if tuple(s.shape) != (pages, heads, page, dim // 16):
+                raise JepaError(1, f"KvCache4: {name} must be [{pages}, {heads}, {page}, {dim // 16}]")
+        for name, u in (("k_unit", k_unit), ("v_unit", v_unit)):
+            if u is not None and tuple(_sized(u, "KvCache4: " + name).shape) != (heads,):
+                raise JepaError(1, f"KvCache4: {name} must be [{heads}]")
+        self.tensors = tuple(t for t in (k, v, k_scale, v_scale, page_table, k_unit, v_unit) if t is not None)
+        if len({t.device for t in self.tensors}) != 1:
+            raise JepaError(1, "KvCache4: all tensors must be on one device")
+        n = pages * heads * page
+        batch, max_pages = page_table.shape
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.batch, self.max_pages, self.device = batch, max_pages, k.device
+        self.struct = Kv4Struct(
+            _arg(k, "k", "u8", n * half), _arg(v, "v", "u8", n * half),
+            _arg(k_scale, "k_scale", "u8", n * dim // 16), _arg(v_scale, "v_scale", "u8", n * dim // 16),
+            _arg(k_unit, "k_unit", "f32", heads, optional=True),
+            _arg(v_unit, "v_unit", "f32", heads, optional=True),
+            _arg(page_table, "page_table", "i32", batch * max_pages), pages, page, heads, dim, batch,
+            max_pages)
+        self.ref = ctypes.byref(self.struct)
+        self.index = k.get_device()
+
+    def check(self, device: int):
+        """Raises unless the cache lives on this device."""
+        if self.index != device:
+            raise JepaError(1, f"cache is on {self.device}, the planner on cuda:{device}")
+
+
+def _matrix(t, name: str, device: int):
+    """(address, 1 where bf16, elements between rows, rows, cols) of a float32 or bf16 CUDA tensor
+    [rows, cols] whose rows are contiguous (columns of a wider tensor are fine)."""
+    if not isinstance(t, _Fast.Tensor) or t.dim() != 2:
+        raise JepaError(1, f"{name}: expected a tensor [rows, cols]")
+    half = t.dtype is _Fast.torch.bfloat16
+    if not half and t.dtype is not _Fast.torch.float32:
+        raise JepaError(1, f"{name}: dtype {t.dtype} where float32 or bfloat16 is required")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise JepaError(1, f"{name}: the elements of a row must be contiguous")
+    if t.get_device() != device:
+        raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{device}")
+    return t.data_ptr(), int(half), (t.stride(0) if rows > 1 else cols), rows, cols
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
@@ -322,6 +408,75 @@ def _stream_on(stream, device: int) -> int:
             return _Fast.raw_stream(device)
         return _Fast.torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _append_method(name: str):
+    """Planner's append to one of the paged caches (jepa_<name> of the C header)."""
+    call = "jepa_" + name
+
+    def append(self, q, k, v, rope_table, cu, start, cache, q_out, q_norm=None, k_norm=None,
+               norm_eps=1e-6, interleaved=False, k_out=None, stream=None):
+        """Norm, rotate and append packed tokens: q [tokens, q_heads, head_dim] (or None with
+        q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None."""
+        dev = self.device
+        kp, ks, tokens, heads, dim = _rows(k, "k", dev)
+        vp, vs, *v_shape = _rows(v, "v", dev)
+        if v_shape != [tokens, heads, dim] or heads != cache.kv_heads or dim != cache.head_dim:
+            raise JepaError(1, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit the cache's "
+                               f"{cache.kv_heads} heads of {cache.head_dim}")
+        if (q is None) != (q_out is None):
+            raise JepaError(1, "q and q_out are given together")
+        qp, qs, q_heads, qo = None, 0, 0, None
+        if q is not None:
+            qp, qs, q_tokens, q_heads, q_dim = _rows(q, "q", dev)
+            if q_tokens != tokens or q_dim != dim:
+                raise JepaError(1, f"q {tuple(q.shape)} does not fit k {tuple(k.shape)}")
+            qo = _dev(q_out, "q_out", "bf16", tokens * q_heads * dim, dev)
+        positions = rot = 0
+        if rope_table is not None:
+            if _sized(rope_table, "rope_table").dim() != 2:
+                raise JepaError(1, "rope_table must be [positions, rot]")
+            positions, rot = rope_table.shape
+        cache.check(dev)
+        if tokens < 1:
+            raise JepaError(1, "tokens must be >= 1 (got 0)")
+        st = getattr(self.lib, call)(
+            self.h, cache.ref, qp, qs, kp, ks, vp, vs, tokens, q_heads,
+            _opt(q_norm, "q_norm", "f32", dim, dev), _opt(k_norm, "k_norm", "f32", dim, dev), norm_eps,
+            _opt(rope_table, "rope_table", "f32", positions * rot, dev), positions, rot,
+            int(interleaved), _dev(cu, "cu", "i32", cache.batch + 1, dev),
+            _dev(start, "start", "i32", cache.batch, dev), qo,
+            _opt(k_out, "k_out", "bf16", tokens * heads * dim, dev), _stream_on(stream, dev))
+        if st:
+            self._check(st, name)
+
+    append.__name__ = name
+    append.__qualname__ = "Planner." + name
+    return append
+
+
+def _read_method(name: str):
+    """Planner's read-back of one of the paged caches."""
+    call = "jepa_" + name
+
+    def read(self, cache, cu, first, k_out, v_out, stream=None):
+        """Cached tokens as bf16 into k_out, v_out [tokens, kv_heads, head_dim]."""
+        dev = self.device
+        cache.check(dev)
+        tokens = k_out.shape[0] if _sized(k_out, "k_out").dim() else 0
+        if tokens < 1:
+            raise JepaError(1, "tokens must be >= 1 (got 0)")
+        n = tokens * cache.kv_heads * cache.head_dim
+        st = getattr(self.lib, call)(
+            self.h, cache.ref, _dev(cu, "cu", "i32", cache.batch + 1, dev),
+            _dev(first, "first", "i32", cache.batch, dev), tokens, _dev(k_out, "k_out", "bf16", n, dev),
+            _dev(v_out, "v_out", "bf16", n, dev), _stream_on(stream, dev))
+        if st:
+            self._check(st, name)
+
+    read.__name__ = name
+    read.__qualname__ = "Planner." + name
+    return read
 
 
 class Planner:
@@ -532,56 +687,8 @@ class Planner:
             _stream_on(stream, self.device)), "rope_table")
         return table
 
-    def rope_append_kv8(self, q, k, v, rope_table, cu, start, cache: KvCache8, q_out, q_norm=None,
-                        k_norm=None, norm_eps=1e-6, interleaved=False, k_out=None, stream=None):
-        """Norm, rotate and append packed tokens: q [tokens, q_heads, head_dim] (or None with
-        q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None."""
-        dev = self.device
-        kp, ks, tokens, heads, dim = _rows(k, "k", dev)
-        vp, vs, *v_shape = _rows(v, "v", dev)
-        if v_shape != [tokens, heads, dim] or heads != cache.kv_heads or dim != cache.head_dim:
-            raise JepaError(1, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit the cache's "
-                               f"{cache.kv_heads} heads of {cache.head_dim}")
-        if (q is None) != (q_out is None):
-            raise JepaError(1, "q and q_out are given together")
-        qp, qs, q_heads, qo = None, 0, 0, None
-        if q is not None:
-            qp, qs, q_tokens, q_heads, q_dim = _rows(q, "q", dev)
-            if q_tokens != tokens or q_dim != dim:
-                raise JepaError(1, f"q {tuple(q.shape)} does not fit k {tuple(k.shape)}")
-            qo = _dev(q_out, "q_out", "bf16", tokens * q_heads * dim, dev)
-        positions = rot = 0
-        if rope_table is not None:
-            if _sized(rope_table, "rope_table").dim() != 2:
-                raise JepaError(1, "rope_table must be [positions, rot]")
-            positions, rot = rope_table.shape
-        cache.check(dev)
-        if tokens < 1:
-            raise JepaError(1, "tokens must be >= 1 (got 0)")
-        st = self.lib.jepa_rope_append_kv8(
-            self.h, cache.ref, qp, qs, kp, ks, vp, vs, tokens, q_heads,
-            _opt(q_norm, "q_norm", "f32", dim, dev), _opt(k_norm, "k_norm", "f32", dim, dev), norm_eps,
-            _opt(rope_table, "rope_table", "f32", positions * rot, dev), positions, rot,
-            int(interleaved), _dev(cu, "cu", "i32", cache.batch + 1, dev),
-            _dev(start, "start", "i32", cache.batch, dev), qo,
-            _opt(k_out, "k_out", "bf16", tokens * heads * dim, dev), _stream_on(stream, dev))
-        if st:
-            self._check(st, "rope_append_kv8")
-
-    def kv8_read(self, cache: KvCache8, cu, first, k_out, v_out, stream=None):
-        """Cached tokens as bf16 into k_out, v_out [tokens, kv_heads, head_dim]."""
-        dev = self.device
-        cache.check(dev)
-        tokens = k_out.shape[0] if _sized(k_out, "k_out").dim() else 0
-        if tokens < 1:
-            raise JepaError(1, "tokens must be >= 1 (got 0)")
-        n = tokens * cache.kv_heads * cache.head_dim
-        st = self.lib.jepa_kv8_read(
-            self.h, cache.ref, _dev(cu, "cu", "i32", cache.batch + 1, dev),
-            _dev(first, "first", "i32", cache.batch, dev), tokens, _dev(k_out, "k_out", "bf16", n, dev),
-            _dev(v_out, "v_out", "bf16", n, dev), _stream_on(stream, dev))
-        if st:
-            self._check(st, "kv8_read")
+    rope_append_kv8 = _append_method("rope_append_kv8")
+    kv8_read = _read_method("kv8_read")
 
     def attention_kv8_workspace(self, cache: KvCache8) -> int:
         """Bytes of workspace that attention_kv8 needs."""
@@ -630,6 +737,97 @@ class Planner:
             _opt(lse, "lse", "f32", tokens_q * q_heads, dev), _stream_on(stream, dev))
         if st:
             self._check(st, "attention_packed")
+
+    # ---- 4-bit paged key/value cache, eviction, and the norm ahead of 8-bit products ----
+
+    rope_append_kv4 = _append_method("rope_append_kv4")
+    kv4_read = _read_method("kv4_read")
+
+    def attention_kv4_workspace(self, cache: KvCache4) -> int:
+        """Bytes of workspace that attention_kv4 needs."""
+        n = ctypes.c_size_t()
+        self._check(self.lib.jepa_attention_kv4_workspace(self.h, cache.ref, ctypes.byref(n)),
+                    "attention_kv4_workspace")
+        return n.value
+
+    def attention_kv4(self, q, cache: KvCache4, kv_len, out, scale, workspace, causal=True, lse=None,
+                      mass=None, mass_out=None, decay=1.0, stream=None):
+        """Attention of q [batch, q_tokens, q_heads, head_dim] over the cache; workspace: a uint8
+        tensor of attention_kv4_workspace bytes, one for each call that may run at a time. With
+        mass_out [batch, kv_heads, max_pages * page_size] (and lse), also decay * mass + the weights
+        that the cached tokens received (mass None: zeros; the same tensor: in place)."""
+        dev = self.device
+        if getattr(q, "ndim", 0) != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
+            raise JepaError(1, f"q must be [{cache.batch}, q_tokens, q_heads, {cache.head_dim}]")
+        cache.check(dev)
+        batch, q_tokens, q_heads, dim = q.shape
+        rows = batch * q_tokens * q_heads
+        if rows < 1:
+            raise JepaError(1, "q_tokens and q_heads must be >= 1")
+        held = batch * cache.kv_heads * cache.max_pages * cache.page_size
+        st = self.lib.jepa_attention_kv4(
+            self.h, cache.ref, _dev(q, "q", "bf16", rows * dim, dev), q_tokens, q_heads,
+            _dev(kv_len, "kv_len", "i32", batch, dev), scale, int(causal),
+            _dev(out, "out", "bf16", rows * dim, dev), _opt(lse, "lse", "f32", rows, dev),
+            _opt(mass, "mass", "f32", held, dev), _opt(mass_out, "mass_out", "f32", held, dev), decay,
+            _dev(_sized(workspace, "workspace"), "workspace", "u8", 0, dev), workspace.numel(),
+            _stream_on(stream, dev))
+        if st:
+            self._check(st, "attention_kv4")
+
+    def kv4_evict_workspace(self, cache: KvCache4, keep: int) -> int:
+        """Bytes of workspace that kv4_evict needs."""
+        n = ctypes.c_size_t()
+        self._check(self.lib.jepa_kv4_evict_workspace(self.h, cache.ref, keep, ctypes.byref(n)),
+                    "kv4_evict_workspace")
+        return n.value
+
+    def kv4_evict(self, cache: KvCache4, kv_len, mass, keep, recent, to: KvCache4, len_out, mass_out,
+                  workspace, stream=None):
+        """Keep the last `recent` tokens of each sequence and head and those with the largest mass,
+        `keep` in all, as the tokens of `to`'s pages; len_out [batch], mass_out (or None) [batch,
+        kv_heads, to.max_pages * to.page_size]; workspace: kv4_evict_workspace bytes."""
+        dev = self.device
+        cache.check(dev)
+        to.check(dev)
+        heads = cache.batch * cache.kv_heads
+        st = self.lib.jepa_kv4_evict(
+            self.h, cache.ref, _dev(_sized(kv_len, "kv_len"), "kv_len", "i32", cache.batch, dev),
+            _dev(mass, "mass", "f32", heads * cache.max_pages * cache.page_size, dev), keep, recent,
+            to.ref, _dev(len_out, "len_out", "i32", cache.batch, dev),
+            _opt(mass_out, "mass_out", "f32", heads * to.max_pages * to.page_size, dev),
+            _dev(_sized(workspace, "workspace"), "workspace", "u8", 0, dev), workspace.numel(),
+            _stream_on(stream, dev))
+        if st:
+            self._check(st, "kv4_evict")
+
+    def add_rmsnorm_fp8(self, x, delta, weight, x_out, codes, scales, eps=1e-6, y=None, stream=None):
+        """s = x + delta to x_out (None: not wanted; x: in place), its RMS norm times weight as e4m3
+        codes [rows, cols] with scales [rows] (or both None), and as bf16 to y [rows, cols] (or None).
+        x and x_out float32 or bf16 [rows, cols], delta either or None."""
+        if _Fast.torch is None:
+            _Fast.load()
+        dev = self.device
+        xp, xh, xs, rows, cols = _matrix(x, "x", dev)
+        dp, dh, ds = None, 0, 0
+        if delta is not None:
+            dp, dh, ds, *d_shape = _matrix(delta, "delta", dev)
+            if d_shape != [rows, cols]:
+                raise JepaError(1, f"delta {tuple(delta.shape)} does not fit x {tuple(x.shape)}")
+        op, os_ = None, 0
+        if x_out is not None:
+            op, oh, os_, *o_shape = _matrix(x_out, "x_out", dev)
+            if o_shape != [rows, cols] or oh != xh:
+                raise JepaError(1, "x_out must have x's shape and type")
+        if rows < 1 or cols < 1:
+            raise JepaError(1, "rows and cols must be >= 1")
+        n = rows * cols
+        st = self.lib.jepa_add_rmsnorm_fp8(
+            self.h, xp, xh, xs, dp, dh, ds, _dev(weight, "weight", "f32", cols, dev), eps, rows, cols, op,
+            os_, _opt(codes, "codes", "u8", n, dev), _opt(scales, "scales", "f32", rows, dev),
+            _opt(y, "y", "bf16", n, dev), _stream_on(stream, dev))
+        if st:
+            self._check(st, "add_rmsnorm_fp8")
 
     def set_use_graphs(self, on: bool):
         self._check(self.lib.jepa_set_use_graphs(self.h, int(on)), "set_use_graphs")

@@ -1,0 +1,599 @@
+// Attention of a few new tokens per sequence over the 4-bit paged cache, and the weights that the
+// cached tokens receive.
+//
+//   o[r] = sum_j w[r][j] V[j],  w[r][j] = softmax_j(scale q[r] . K[j]),  K, V = code * scale * unit
+//   mass_out[j] = decay * mass[j] + sum_r w[r][j]
+//
+// for the rows r = (new token, head of the group) that share a key/value head. Bound by the HBM
+// bytes of codes and scales (9/8 kv_heads * dim a cached token). Line of work, joining, transposed
+// products and the softmax are those of the attention over the 8-bit cache (attention_kv8.cu). What
+// four bits change:
+//   * Codes to fragments: e2m1 -> f16 two codes an instruction, then one packed product with the
+//     block's e4m3 scale as f16: six significant bits, so exact. Four registers of a fragment of K are four
+//     conversions and four products.
+//   * A lane (g = lane / 4, t = lane % 4) takes elements [t D/4, (t+1) D/4) of keys g and g + 8 for K Q^T:
+//     two blocks (dim 128) or one. For V^T P^T it takes elements [g D/8, (g+1) D/8), one block or half of one, of
+//     keys 2t, 2t+1, 2t+8, 2t+9; the halves of their bytes are put together first (two keys of one
+//     element in a byte), so that a conversion gives a register of the fragment.
+//   * No scale varies within what a warp accumulates, as pages' scales do in 8 bits: the units
+//     of a head multiply the scores and the outputs once.
+#include "decode_line.cuh"
+
+#include "kv4.cuh"
+
+namespace jepa {
+
+namespace {
+
+template <int D, int NR>
+struct Shape {
+  static constexpr int ROWS = 8 * NR;              // query rows of an item
+  static constexpr int NST = 3;                    // cp.async stages of a warp
+  static constexpr int CTAS = (D == 64 ? 4 : 3) - (NR == 2);
+  static constexpr int KS = 32;                    // keys a warp takes in a step
+  static constexpr int GROUPS = KS / 16;           // 16-key groups
+  static constexpr int UNIT = WARPS * KS;          // keys of a unit
+  static constexpr int KB = D / 2, SB = D / 16;    // bytes of a key's codes, and of its scales
+  static constexpr int KW = D / 32;                // 32-bit words of a key a lane takes
+  static constexpr int VW = D / 64;                // 32-bit words of a V row a lane takes
+  static constexpr int MT = D / 16;                // output tiles of 16 columns
+  static constexpr int OFF_V = KS * KB, OFF_SC = 2 * KS * KB;   // of a stage: K, V codes, K, V scales
+  static constexpr int STAGE = OFF_SC + 2 * KS * SB;
+  static constexpr int OUT_LD = OUT_ROW<D>;
+  static constexpr int OFF_OUT = WARPS * NST * STAGE;
+  static constexpr int SMEM = OFF_OUT + WARPS * ROWS * OUT_LD * 4;
+  static_assert(CTAS <= MAX_CTAS_PER_SM && CTAS * (SMEM + 2048) <= 228 * 1024, "CTAs of a SM");
+  static_assert(COMBINE_SMEM<D> * CTAS * MAX_SMS <= 48 * 1024, "what a launch may have without an attribute");
+};
+
+// Byte of 16-byte chunk `chunk` of key `row` among a stage's codes. Lines of 128 bytes hold 2 keys (dim
+// 128) or 4; the XOR spreads the rows 2t, t = 0..3, that a load of V takes over the banks.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(int row, int chunk) {
+  if (D == 128) return (row >> 1) * 128 + 16 * (((row & 1) * 4 + chunk) ^ (((row >> 1) & 3) << 1));
+  return (row >> 2) * 128 + 16 * (((row & 3) * 2 + chunk) ^ (((row >> 2) & 1) << 1));
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// Fragments of a 16-key group of K (keys g and g + 8 of this lane): words w[h][i] with the scales
+// sc[h][b], both halves alike.
+template <int D, int NR>
+__device__ __forceinline__ void scores_of(const uint32_t (&w)[2][D / 32], const uint32_t (&sc)[2][D / 64],
+                                          const uint32_t (&qf)[NR][D / 16][2], float (&s)[NR][4]) {
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr) s[nr][0] = s[nr][1] = s[nr][2] = s[nr][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t s0 = sc[0][i / 2], s1 = sc[1][i / 2];
+    const uint32_t a0 = mul2(f16x2_of_e2m1x2<0>(w[0][i]), s0), a1 = mul2(f16x2_of_e2m1x2<0>(w[1][i]), s1);
+    const uint32_t a2 = mul2(f16x2_of_e2m1x2<1>(w[0][i]), s0), a3 = mul2(f16x2_of_e2m1x2<1>(w[1][i]), s1);
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) mma_f16(s[nr], a0, a1, a2, a3, qf[nr][2 * i][0], qf[nr][2 * i][1]);
+    const uint32_t b0 = mul2(f16x2_of_e2m1x2<2>(w[0][i]), s0), b1 = mul2(f16x2_of_e2m1x2<2>(w[1][i]), s1);
+    const uint32_t b2 = mul2(f16x2_of_e2m1x2<3>(w[0][i]), s0), b3 = mul2(f16x2_of_e2m1x2<3>(w[1][i]), s1);
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+      mma_f16(s[nr], b0, b1, b2, b3, qf[nr][2 * i + 1][0], qf[nr][2 * i + 1][1]);
+  }
+}
+
+// A lane's D / 64 scales of one key, each in both halves of a register, from their bytes.
+template <int D>
+__device__ __forceinline__ void key_scales(uint32_t bytes, uint32_t (&sc)[D / 64]) {
+  const uint32_t x = f16x2_of_e4m3_pair(bytes);
+  sc[0] = __byte_perm(x, x, 0x1010);
+  if (D == 128) sc[D / 64 - 1] = __byte_perm(x, x, 0x3232);
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
+    k_attention_kv4(Kv4View c, Args a, int whole, int* err_flag) {
+  using S = Shape<D, NR>;
+  constexpr int ROWS = S::ROWS, NST = S::NST;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");   // k_combine may be set up meanwhile
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (NST * S::STAGE);
+  const uint8_t* ring_ptr = smem + warp * (NST * S::STAGE);
+  float* const sm_o = reinterpret_cast<float*>(smem + S::OFF_OUT);
+
+  int* const flag0 = blockIdx.x == 0 ? err_flag : nullptr;
+  long long u_begin, u_end, total = 0;
+  int workers = 0;
+  if (whole) {
+    // items in equal numbers, a place each
+    const long long items = (long long)c.batch * c.heads * a.tiles;
+    u_begin = kv8_share(items, gridDim.x, blockIdx.x);
+    u_end = kv8_share(items, gridDim.x, blockIdx.x + 1);
+    if (flag0 && warp == 0) total_places(c, a, S::UNIT, flag0);   // reports lengths out of range
+  } else {
+    total = total_places(c, a, S::UNIT, flag0);
+    workers = workers_of(total, gridDim.x);
+    if ((int)blockIdx.x >= workers) {
+      if (threadIdx.x == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+      write_empty<D>(c, a);
+      return;
+    }
+    u_begin = kv8_share(total, workers, blockIdx.x);
+    u_end = kv8_share(total, workers, blockIdx.x + 1);
+  }
+  int4 begun = make_int4(0, 0, 0, 0);
+  const int rows = a.q_tokens * a.group;
+  // ---- loading: the warp's steps of all segments in one stream, NST - 1 ahead of their use ----
+  constexpr int CPR = S::KB / 16;              // 16-byte chunks of a key's codes
+  constexpr int RPI = 32 / CPR;                // keys a warp copies in one instruction
+  constexpr int SPG = D / 16;                  // 16-byte chunks of a group's scales (16 keys)
+  constexpr int KPC = 16 / S::SB;              // keys of such a chunk
+  const int chunk = lane % CPR, sub = lane / CPR;
+  Cursor load_cur{0, 0, 0, 0};
+  Segment ld;
+  int ld_left = 0, ld_stage = 0;               // steps left of the segment
+  bool ld_more = plan<S::UNIT, ROWS>(c, a, whole, u_begin, u_end, load_cur, ld);
+  uint32_t lane_to[16 / RPI];                  // of a lane's chunks of a 16-key group
+#pragma unroll
+  for (int q = 0; q < 16 / RPI; ++q) lane_to[q] = ring + code_at<D>(q * RPI + sub, chunk);
+  const uint32_t lane_from = sub * S::KB + 16 * chunk;
+  // scales of a step: lane -> (K or V, group, chunk of the group)
+  const int sc_chunk = lane % SPG, sc_group = lane / SPG % S::GROUPS, sc_v = lane / SPG / S::GROUPS;
+  const uint32_t sc_to = ring + S::OFF_SC + lane * 16;
+  const uint32_t slot_mask = c.page - 1;
+  int pg_next[S::GROUPS];                      // pages of the step that is issued next
+  int ld_key = 0;                              // first key of that step
+  const int* ld_pages = nullptr;               // the sequence's row of the table
+  auto begin_segment = [&]() {
+    ld_key = ld.k0 * S::UNIT + warp * S::KS;
+    ld_pages = c.table + (long long)ld.s * c.max_pages;
+    ld_left = ld.k1 - ld.k0;
+  };
+  if (ld_more) begin_segment();
+  auto fetch_pages = [&]() {
+    const int key = ld_key;
+    const int* at = ld_pages;
+#pragma unroll
+    for (int p = 0; p < S::GROUPS; ++p)
+      pg_next[p] = ld_more && key + 16 * p < ld.len ? __ldg(at + ((key + 16 * p) >> c.page_log2)) : -1;
+  };
+  auto issue = [&]() {                         // the next step of the stream into the next stage
+    const int key0 = ld_key;
+    if (ld_more && key0 < ld.len) {
+      const uint32_t st = ld_stage * S::STAGE;
+      uint64_t row[S::GROUPS];                 // of the group's first key among all blocks' keys
+      int keys[S::GROUPS];                     // keys there; others are zeros
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) {
+        const bool there = (uint32_t)pg_next[p] < (uint32_t)c.num_pages;
+        const int left = ld.len - (key0 + 16 * p);
+        if (!there && left > 0 && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+        keys[p] = there ? max(0, min(16, left)) : 0;
+        const uint32_t block = (there ? (uint32_t)pg_next[p] : 0u) * (uint32_t)c.heads + (uint32_t)ld.head;
+        row[p] = ((uint64_t)block << c.page_log2) + ((uint32_t)(key0 + 16 * p) & slot_mask);
+      }
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) {
+        const uint64_t from = row[p] * S::KB + lane_from;
+        const uint8_t *fk = c.k + from, *fv = c.v + from;
+#pragma unroll
+        for (int q = 0; q < 16 / RPI; ++q) {
+          const uint32_t bytes = q * RPI + sub < keys[p] ? 16 : 0;
+          cp16(lane_to[q] + st + 16 * p * S::KB, fk + q * RPI * S::KB, bytes);
+          cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, bytes);
+        }
+      }
+      if (lane < 2 * S::GROUPS * SPG) {
+        const bool second = sc_group != 0;
+        const uint64_t first = second ? row[S::GROUPS - 1] : row[0];
+        const int n = (second ? keys[S::GROUPS - 1] : keys[0]) - sc_chunk * KPC;
+        cp16(sc_to + st, (sc_v ? c.v_scale : c.k_scale) + first * S::SB + 16 * sc_chunk,
+             max(0, min(KPC, n)) * S::SB);
+      }
+    }
+    cp_commit();
+    ld_stage = ld_stage + 1 == NST ? 0 : ld_stage + 1;
+    ld_key += S::UNIT;
+    if (ld_more && --ld_left == 0) {
+      ld_more = plan<S::UNIT, ROWS>(c, a, whole, ld.next, u_end, load_cur, ld);
+      begin_segment();
+    }
+    fetch_pages();
+  };
+  fetch_pages();
+#pragma unroll 1
+  for (int i = 0; i < NST - 1; ++i) issue();
+
+  int stage = 0;
+  Cursor cur{0, 0, 0, 0};
+  Segment sg;
+  sg.next = u_begin;
+  while (plan<S::UNIT, ROWS>(c, a, whole, sg.next, u_end, cur, sg)) {
+    const int s = sg.s, len = sg.len;
+    const int head = sg.head, r0 = sg.r0;
+    Queries<D, NR> qr;
+    qr.load(a, s, head, r0, rows, len);
+    {
+      const float unit = kv4_unit(c.k_unit, head);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        qr.qs[nr][0] *= unit;
+        qr.qs[nr][1] *= unit;
+      }
+    }
+    float o[NR][S::MT][4];
+    float m[NR][2], l[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      m[nr][0] = m[nr][1] = -INFINITY;
+      l[nr][0] = l[nr][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < S::MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
+    }
+
+    for (int k = sg.k0; k < sg.k1; ++k) {
+      cp_wait<NST - 2>();
+      __syncwarp();
+      issue();                         // into the stage that the step before this one has read
+      const int key0 = k * S::UNIT + warp * S::KS;
+      const uint8_t* kb = ring_ptr + stage * S::STAGE;
+      const uint8_t* vb = kb + S::OFF_V;
+      const uint8_t* kscale = kb + S::OFF_SC;
+      const uint8_t* vscale = kscale + S::KS * S::SB;
+      stage = stage + 1 == NST ? 0 : stage + 1;
+      if (key0 >= len) continue;
+
+      // scores of keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
+      float sc[S::GROUPS][NR][4];
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) {
+        uint32_t w[2][S::KW], f[2][S::VW];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = 16 * p + 8 * h + g;
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kb + code_at<D>(row, t));
+            w[h][0] = x.x; w[h][1] = x.y; w[h][S::KW - 2] = x.z; w[h][S::KW - 1] = x.w;
+            key_scales<D>(*reinterpret_cast<const uint16_t*>(kscale + row * S::SB + 2 * t), f[h]);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(kb + code_at<D>(row, t >> 1) + 8 * (t & 1));
+            w[h][0] = x.x; w[h][1] = x.y;
+            key_scales<D>(kscale[row * S::SB + t], f[h]);
+          }
+        }
+        scores_of<D, NR>(w, f, qr.qf, sc[p]);
+      }
+      const bool edge = key0 + S::KS > qr.lim_min;   // some row does not see some key (warp-uniform)
+      bool move = false;
+      float top[NR][2];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+        for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[p][nr][e] *= qr.qs[nr][e & 1];
+        if (edge) {
+#pragma unroll
+          for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 16 * p + 8 * (e >> 1) + g >= qr.lim[nr][e & 1]) sc[p][nr][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(sc[0][nr][e], sc[0][nr][2 + e]);
+#pragma unroll
+          for (int p = 1; p < S::GROUPS; ++p) x = fmaxf(x, fmaxf(sc[p][nr][e], sc[p][nr][2 + e]));
+          top[nr][e] = x;
+          move = move || x > m[nr][e] + P_SLACK || (m[nr][e] == -INFINITY && x > -INFINITY);
+        }
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        // the maxima over all keys of the step; the reference moves where it has to
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[nr][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m[nr][e], x);
+            const float al = mn == -INFINITY ? 1.f : ex2f(m[nr][e] - mn);
+            m[nr][e] = mn;
+            l[nr][e] *= al;
+#pragma unroll
+            for (int d = 0; d < S::MT; ++d) {
+              o[nr][d][e] *= al;
+              o[nr][d][2 + e] *= al;
+            }
+          }
+      }
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) {
+        uint32_t b[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          float pr[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float mr = m[nr][e & 1];
+            pr[e] = ex2f(sc[p][nr][e] - (mr == -INFINITY ? 0.f : mr - P_SHIFT));
+            l[nr][e & 1] += pr[e];
+          }
+          b[nr][0] = transposed(pack_f16(pr[0], pr[1]));
+          b[nr][1] = transposed(pack_f16(pr[2], pr[3]));
+        }
+        // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group, D/8 values each, and their scales
+        uint32_t w[4][S::VW], vs[4];
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int row = 16 * p + 2 * t + (k4 & 1) + 8 * (k4 >> 1);
+          if (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vb + code_at<D>(row, g >> 1) + 8 * (g & 1));
+            w[k4][0] = x.x; w[k4][S::VW - 1] = x.y;
+            vs[k4] = vscale[row * S::SB + g];
+          } else {
+            w[k4][0] = *reinterpret_cast<const uint32_t*>(vb + code_at<D>(row, g >> 2) + 4 * (g & 3));
+            vs[k4] = vscale[row * S::SB + (g >> 1)];
+          }
+        }
+        // A block that reads as NaN reaches only rows that see its key: a product with a masked
+        // probability of 0 would spread it. Rows can differ in what they see only at the causal edge.
+        uint32_t nan = 0;                      // bit k4: this lane's block of key k4 is NaN
+        if (edge) {
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+            if ((vs[k4] & 0x7fu) == 0x7fu) {
+              nan |= 1u << k4;
+              vs[k4] = 0;
+            }
+        }
+        const uint32_t sa = f16x2_of_e4m3_pair(vs[0] | (vs[1] << 8)), sb = f16x2_of_e4m3_pair(vs[2] | (vs[3] << 8));
+#pragma unroll
+        for (int q = 0; q < S::VW; ++q) {
+          // bytes (even element of the first key, of the second), and the odd elements
+          const uint32_t x0 = (w[0][q] & 0x0f0f0f0fu) | ((w[1][q] << 4) & 0xf0f0f0f0u);
+          const uint32_t x1 = ((w[0][q] >> 4) & 0x0f0f0f0fu) | (w[1][q] & 0xf0f0f0f0u);
+          const uint32_t y0 = (w[2][q] & 0x0f0f0f0fu) | ((w[3][q] << 4) & 0xf0f0f0f0u);
+          const uint32_t y1 = ((w[2][q] >> 4) & 0x0f0f0f0fu) | (w[3][q] & 0xf0f0f0f0u);
+          auto tile = [&](int d, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+            const uint32_t a0 = mul2(c0, sa), a1 = mul2(c1, sa), a2 = mul2(c2, sb), a3 = mul2(c3, sb);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][d], a0, a1, a2, a3, b[nr][0], b[nr][1]);
+          };
+          tile(4 * q, f16x2_of_e2m1x2<0>(x0), f16x2_of_e2m1x2<0>(x1), f16x2_of_e2m1x2<0>(y0), f16x2_of_e2m1x2<0>(y1));
+          tile(4 * q + 1, f16x2_of_e2m1x2<1>(x0), f16x2_of_e2m1x2<1>(x1), f16x2_of_e2m1x2<1>(y0), f16x2_of_e2m1x2<1>(y1));
+          tile(4 * q + 2, f16x2_of_e2m1x2<2>(x0), f16x2_of_e2m1x2<2>(x1), f16x2_of_e2m1x2<2>(y0), f16x2_of_e2m1x2<2>(y1));
+          tile(4 * q + 3, f16x2_of_e2m1x2<3>(x0), f16x2_of_e2m1x2<3>(x1), f16x2_of_e2m1x2<3>(y0), f16x2_of_e2m1x2<3>(y1));
+        }
+        if (edge && __any_sync(0xffffffffu, nan != 0)) {
+          // how many NaN blocks of a lane's elements each row sees
+          const uint32_t n0 = ((nan & 1u) ? 0x3c00u : 0u) | ((nan & 2u) ? 0x3c000000u : 0u);
+          const uint32_t n1 = ((nan & 4u) ? 0x3c00u : 0u) | ((nan & 8u) ? 0x3c000000u : 0u);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            uint32_t see[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = key0 + 16 * p + 8 * h + 2 * t;
+              see[h] = pack_f16(key < qr.lim_g[nr] ? 1.f : 0.f, key + 1 < qr.lim_g[nr] ? 1.f : 0.f);
+            }
+            float hit[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(hit, n0, n0, n1, n1, see[0], see[1]);
+#pragma unroll
+            for (int d = 0; d < S::MT; ++d)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (hit[e] > 0.f) o[nr][d][e] = __int_as_float(0x7fc00000);
+          }
+        }
+      }
+    }
+    // ---- join the four warps ----
+    __syncthreads();   // the joining before this one has been read
+    const float unit = kv4_unit(c.v_unit, head);
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nr][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int row = 8 * nr + 2 * t + e;
+        if (g == 0) {
+          // from here on m is the exponent's reference; -inf only where no key was seen (scores
+          // that are all NaN leave the maximum at -inf, but a NaN sum)
+          sm_m[warp][row] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
+          sm_l[warp][row] = x;
+        }
+        float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * (D / 8);
+#pragma unroll
+        for (int d = 0; d < S::MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
+          *reinterpret_cast<float4*>(to + 2 * d) =
+              make_float4(o[nr][d][e] * unit, o[nr][d][2 + e] * unit, o[nr][d + 1][e] * unit,
+                          o[nr][d + 1][2 + e] * unit);
+      }
+    __syncthreads();
+    join_warps<D, NR>(a, sg, rows, total, workers, sm_o, sm_m, sm_l, begun);
+  }
+  cp_wait<0>();
+  if (whole) return;
+  if (threadIdx.x == 0) a.split[blockIdx.x] = begun;
+  write_empty<D>(c, a);
+}
+
+// ---- weights ----
+
+template <int D, int NR>
+struct MassShape {
+  static constexpr int ROWS = 8 * NR;
+  static constexpr int KS = 32;                // keys a warp takes in a step
+  static constexpr int GROUPS = KS / 16;
+  static constexpr int UNIT = WARPS * KS;
+};
+
+// The weights' second pass over the keys, once lse is known. Items are (sequence, head); every key of
+// an item belongs to one lane, which sums over all query rows: no atomics, so the order is fixed.
+template <int D, int NR>
+__global__ void __launch_bounds__(THREADS, 4) k_mass_kv4(Kv4View c, Args a, MassArgs w, int* err_flag) {
+  using S = MassShape<D, NR>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rows = a.q_tokens * a.group, tiles = (rows + S::ROWS - 1) / S::ROWS;
+  const long long total = total_places(c, a, S::UNIT, nullptr);
+  const int workers = workers_of(total, gridDim.x);
+  if ((int)blockIdx.x >= workers) return;
+  const long long u_end = kv8_share(total, workers, blockIdx.x + 1);
+  const long long reach = (long long)c.max_pages << c.page_log2;
+  Cursor cur{0, 0, 0, 0};
+  Segment sg;
+  sg.next = kv8_share(total, workers, blockIdx.x);
+  while (plan<S::UNIT, S::ROWS>(c, a, 0, sg.next, u_end, cur, sg)) {
+    const int len = sg.len, head = sg.head;
+    const float unit = kv4_unit(c.k_unit, head);
+    const int* pages = c.table + (long long)sg.s * c.max_pages;
+    const long long at = ((long long)sg.s * c.heads + head) * reach;
+    Queries<D, NR> qr;
+    float norm[NR][2];                         // lse in base 2 of rows 2t, 2t + 1
+    auto load_rows = [&](int r0) {
+      qr.load(a, sg.s, head, r0, rows, len);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * nr + 2 * t + e;
+          qr.qs[nr][e] *= unit;
+          norm[nr][e] = r < rows ? a.lse[row_at(a, sg.s, head, r)] * 1.4426950408889634f : 0.f;
+          if (r >= rows) qr.lim[nr][e] = 0;    // no weight
+        }
+    };
+    if (tiles == 1) load_rows(0);
+    for (int k = sg.k0; k < sg.k1; ++k) {
+      const int key0 = k * S::UNIT + warp * S::KS;
+      if (key0 >= len) continue;
+      uint32_t kw[S::GROUPS][2][D / 32], sc[S::GROUPS][2][D / 64];
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) {
+        const int key = key0 + 16 * p;
+        const int pg = key < len ? __ldg(pages + (key >> c.page_log2)) : -1;
+        const bool there = (uint32_t)pg < (uint32_t)c.num_pages;
+        if (!there && key < len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+        const uint64_t row = (((uint64_t)((there ? (uint32_t)pg : 0u) * (uint32_t)c.heads + (uint32_t)head)) << c.page_log2) +
+                             ((uint32_t)key & (uint32_t)(c.page - 1));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool on = there && key + 8 * h + g < len;
+          const uint64_t r = row + 8 * h + g;
+          uint32_t bytes = 0;
+          if (D == 128) {
+            const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(c.k + r * 64) + t) : make_uint4(0, 0, 0, 0);
+            kw[p][h][0] = x.x; kw[p][h][1] = x.y; kw[p][h][D / 32 - 2] = x.z; kw[p][h][D / 32 - 1] = x.w;
+            if (on) bytes = __ldg(reinterpret_cast<const uint16_t*>(c.k_scale + r * 8) + t);
+          } else {
+            const uint2 x = on ? __ldg(reinterpret_cast<const uint2*>(c.k + r * 32) + t) : make_uint2(0, 0);
+            kw[p][h][0] = x.x; kw[p][h][1] = x.y;
+            if (on) bytes = __ldg(c.k_scale + r * 4 + t);
+          }
+          key_scales<D>(bytes, sc[p][h]);
+        }
+      }
+      float sum[S::GROUPS][2];
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) sum[p][0] = sum[p][1] = 0.f;
+      for (int tile = 0; tile < tiles; ++tile) {
+        if (tiles > 1) load_rows(tile * S::ROWS);
+#pragma unroll
+        for (int p = 0; p < S::GROUPS; ++p) {
+          float s[NR][4];
+          scores_of<D, NR>(kw[p], sc[p], qr.qf, s);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = ex2f(fmaf(s[nr][e], qr.qs[nr][e & 1], -norm[nr][e & 1]));
+              if (key0 + 16 * p + 8 * (e >> 1) + g < qr.lim[nr][e & 1]) sum[p][e >> 1] += x;
+            }
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = sum[p][h];
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          const int key = key0 + 16 * p + 8 * h + g;
+          if (t == 0 && key < len) w.out[at + key] = w.mass ? fmaf(w.decay, w.mass[at + key], x) : x;
+        }
+    }
+  }
+}
+
+template <int D, int NR>
+cudaError_t launch_mass(const Kv4View& c, Args a, const MassArgs& w, int* err_flag, int num_sms,
+                        cudaStream_t s) {
+  using S = MassShape<D, NR>;
+  a.tiles = 1;                                 // an item holds all rows of its head
+  const long long max_len = (long long)c.max_pages << c.page_log2;
+  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT;
+  const long long slots = (long long)num_sms * 4, items = (long long)c.batch * c.heads;
+  const long long work = max_units > slots ? slots : items * max_units;
+  k_mass_kv4<D, NR><<<(unsigned)(work < slots ? work : slots), THREADS, 0, s>>>(c, a, w, err_flag);
+  return cudaGetLastError();
+}
+
+template <int D, int NR>
+cudaError_t launch(const Kv4View& c, Args a, const MassArgs* w, int* err_flag, int num_sms, cudaStream_t s) {
+  using S = Shape<D, NR>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = set_max_dynamic_smem((const void*)k_attention_kv4<D, NR>, S::SMEM, attr_done);
+  if (e != cudaSuccess) return e;
+  a.tiles = (a.q_tokens * a.group + S::ROWS - 1) / S::ROWS;
+  const long long max_len = (long long)c.max_pages << c.page_log2;
+  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT;
+  const long long slots = (long long)(num_sms < MAX_SMS ? num_sms : MAX_SMS) * S::CTAS;
+  const long long items = (long long)c.batch * c.heads * a.tiles;
+  const int whole = max_units <= WHOLE_UNITS;
+  // every SM's slots, or the work there can be if that is less
+  const long long work = whole ? items : max_units > slots ? slots : items * max_units;
+  const int grid = (int)(work < slots ? work : slots);
+  k_attention_kv4<D, NR><<<grid, THREADS, S::SMEM, s>>>(c, a, whole, err_flag);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (!whole && (e = launch_combine<D, NR>(a, grid, s)) != cudaSuccess) return e;
+  return w ? launch_mass<D, NR>(c, a, *w, err_flag, num_sms, s) : cudaSuccess;
+}
+
+}  // namespace
+
+size_t attention_kv4_workspace(int dim, int num_sms) {
+  return notes_bytes(num_sms) + (size_t)num_sms * MAX_CTAS_PER_SM * 2 * 16 * (dim + 2) * sizeof(float);
+}
+
+cudaError_t attention_kv4(const Kv4View& c, const bf16* q, int q_tokens, int q_heads,
+                          const int* kv_len, float scale, int causal, bf16* out, float* lse,
+                          const MassArgs* mass, void* workspace, int* err_flag, int num_sms,
+                          cudaStream_t s) {
+  Args a;
+  a.q = q;
+  a.kv_len = kv_len;
+  a.out = out;
+  a.lse = lse;
+  a.split = (int4*)workspace;
+  a.part = (float*)((uint8_t*)workspace + notes_bytes(num_sms));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q_tokens = q_tokens;
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  a.tiles = 0;
+  a.causal = causal;
+  const bool narrow = q_tokens * a.group <= 8;
+  if (c.dim == 64)
+    return narrow ? launch<64, 1>(c, a, mass, err_flag, num_sms, s) : launch<64, 2>(c, a, mass, err_flag, num_sms, s);
+  if (c.dim == 128)
+    return narrow ? launch<128, 1>(c, a, mass, err_flag, num_sms, s) : launch<128, 2>(c, a, mass, err_flag, num_sms, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace jepa

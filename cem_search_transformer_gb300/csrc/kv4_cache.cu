@@ -1,0 +1,332 @@
+// Filling and reading the 4-bit paged key/value cache: per-head RMS norm and rotary position of
+// queries and keys, keys and values to e2m1 codes with an e4m3 scale for every 16 elements, and
+// the read-back to bf16.
+//
+// Bound by bytes on long appends (2 (q_heads + 2 kv_heads) dim read, 2 q_heads dim + 9/8 kv_heads dim
+// written a token) and by latency on short ones. No token's codes depend on another token, so one
+// kernel serves all lengths: a warp takes a token and up to eight heads of its queries, keys or
+// values, which share the angles.
+//
+// A code is the nearest e2m1 value to x / (scale * unit), and neighbours are a third apart, so what
+// decides between them is computed as the definition has it: the norm's factor is correctly rounded (sum of
+// squares in two floats), the products of the rotation are rounded one by one, and quotients are correctly rounded.
+#include "rope_rows.cuh"
+
+#include "kv4.cuh"
+
+namespace jepa {
+
+namespace {
+
+constexpr int HEADS = 8;   // heads of a token that a warp takes
+
+__device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
+  const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+  hi = s;
+}
+
+// 1 / sqrt(sum / D + eps), correctly rounded but for ties of 2^-40: the sum of squares, which are
+// exact in fp32, over the lanes of a head in two floats, and one Newton step whose remainder is exact.
+template <int D>
+__device__ __forceinline__ float norm_factor(const float (&y)[16], float eps) {
+  constexpr int L = D / 16;
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) two_sum(hi, lo, __fmul_rn(y[i], y[i]));
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+    // both lanes add the larger to the smaller in the same order
+    float a = fmaxf(hi, h), b = __fadd_rn(lo, l);
+    two_sum(a, b, fminf(hi, h));
+    hi = a;
+    lo = b;
+  }
+  hi *= 1.0f / D;
+  lo *= 1.0f / D;
+  two_sum(hi, lo, eps);
+  const float m = __fadd_rn(hi, lo), rest = __fsub_rn(lo, __fsub_rn(m, hi));
+  const float r = __frsqrt_rn(m);
+  if (!(m > 0.f && m < INFINITY)) return r;
+  const float t = __fmul_rn(m, r), tl = __fmaf_rn(m, r, -t);    // m r = t + tl
+  float e = __fmaf_rn(-t, r, 1.f);                              // 1 - (m + rest) r^2
+  e = __fmaf_rn(-tl, r, e);
+  e = __fmaf_rn(-rest, __fmul_rn(r, r), e);
+  return __fmaf_rn(0.5f * r, e, r);
+}
+
+// y = x * (r * w), then (a, b) -> (a cos - b sin, b cos + a sin), each product and sum rounded.
+template <int D, bool INTER>
+__device__ __forceinline__ void norm_rotate_exact(float (&y)[16], const Lane<D, INTER>& ln,
+                                                  const float* __restrict__ w, float eps,
+                                                  const float (&an)[16]) {
+  if (w) {
+    const float r = norm_factor<D>(y, eps);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 g =
+          __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 8 ? ln.c0 : ln.c1) + (i & 7)));
+      y[i] *= r * g.x; y[i + 1] *= r * g.y; y[i + 2] *= r * g.z; y[i + 3] *= r * g.w;
+    }
+  }
+  if (ln.rotates) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : 8 + i;
+      const float p = y[ia], q = y[ib];
+      y[ia] = __fsub_rn(__fmul_rn(p, an[i]), __fmul_rn(q, an[8 + i]));
+      y[ib] = __fadd_rn(__fmul_rn(q, an[i]), __fmul_rn(p, an[8 + i]));
+    }
+  }
+}
+
+// Largest magnitude of 8 elements as bits: above those of infinity where there is a NaN.
+__device__ __forceinline__ uint32_t top_bits(const float (&y)[16], int from) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[from + i]) & 0x7fffffffu);
+  return m;
+}
+
+// The largest magnitudes of the two blocks of 16 that a lane's chunks of 8 lie in. All lanes of the
+// warp call it.
+template <int D, bool INTER>
+__device__ __forceinline__ void block_tops(const float (&y)[16], const Lane<D, INTER>& ln, int rot,
+                                           uint32_t (&top)[2]) {
+  const uint32_t a = top_bits(y, 0), b = top_bits(y, 8);
+  top[0] = top[1] = max(a, b);              // neighbours: one block
+  if (INTER) return;
+  constexpr int L = D / 16;
+  const int first = (threadIdx.x & 31) / L * L, lanes = rot >> 4;   // lanes of a head that rotate
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int other = (h ? ln.c1 : ln.c0) ^ 1;                      // the block's other chunk
+    const int src = first + (ln.rotates ? (other < lanes ? other : other - lanes) : ln.p);
+    const uint32_t x = __shfl_sync(0xffffffffu, a, src), z = __shfl_sync(0xffffffffu, b, src);
+    if (ln.rotates) top[h] = max(h ? b : a, other < lanes ? x : z);
+  }
+}
+
+// Code of a block's scale for its largest magnitude: e4m3(top / 6 / unit), nearest even, at least
+// 2^-9; NaN where the block is not finite.
+__device__ __forceinline__ uint32_t scale_code(uint32_t top, float inv_unit) {
+  if (top >= 0x7f800000u) return 0x7f;
+  const float s = fmaxf(__fmul_rn(__fdiv_rn(__uint_as_float(top), 6.f), inv_unit), KV4_SCALE_MIN);
+  uint16_t p;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(0.f), "f"(s));
+  return p & 0xffu;
+}
+
+// Codes of 8 elements, the first in the lowest bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[16], int from, float scale) {
+  const float inv = __fdiv_rn(1.f, scale);
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = y[from + i], z = __fmul_rn(x, inv);
+    q[i] = __fmaf_rn(__fmaf_rn(-z, scale, x), inv, z);          // the quotient, correctly rounded
+  }
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return w;
+}
+
+// A lane's 16 elements into the cache: `at` counts tokens of all (page, head) blocks.
+template <int D, bool INTER>
+__device__ __forceinline__ void quantise_store(uint8_t* codes, uint8_t* scales, long long at, bool on,
+                                               const float (&y)[16], const Lane<D, INTER>& ln,
+                                               int rot, float unit) {
+  uint32_t top[2];
+  block_tops<D, INTER>(y, ln, rot, top);
+  if (!on) return;
+  const float inv_unit = kv4_inverse(unit);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int chunk = h ? ln.c1 : ln.c0;
+    const uint32_t sc = scale_code(top[h], inv_unit);
+    const uint32_t f = f16x2_of_e4m3_pair(sc);
+    const float scale = __half2float(__ushort_as_half((unsigned short)(f & 0xffffu))) * unit;
+    *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + 4 * chunk) =
+        sc == 0x7f ? 0u : e2m1x8(y, 8 * h, scale);
+    if (!(chunk & 1)) scales[at * (D / 16) + (chunk >> 1)] = (uint8_t)sc;
+  }
+}
+
+// Unit `unit` of the call: token t, a group of HEADS of its query heads, then of keys, then of values.
+template <int D, bool INTER>
+__device__ __forceinline__ void append_unit(const Kv4View& c, const AppendArgs& a, long long unit,
+                                            int q_blocks, int kv_blocks, int* err_flag) {
+  constexpr int L = D / 16, ROWS = 32 / L, PASSES = HEADS / ROWS;
+  const int per = q_blocks + 2 * kv_blocks;
+  const long long token = unit / per;
+  if (token >= a.tokens) return;
+  const int t = (int)token;
+  int block = (int)(unit - token * per);
+  // 0 queries, 1 keys, 2 values
+  const int kind = block < q_blocks ? 0 : block < q_blocks + kv_blocks ? 1 : 2;
+  block -= kind == 0 ? 0 : kind == 1 ? q_blocks : q_blocks + kv_blocks;
+  const int h0 = block * HEADS, heads = kind == 0 ? a.q_heads : c.heads;
+  const int lane = threadIdx.x & 31, sub = lane / L;
+  const Lane<D, INTER> ln(a.rot);
+  const bf16* src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
+  uint4 raw[PASSES][2];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int h = h0 + p * ROWS + sub;
+    raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    if (h < heads) load16(src + (long long)h * D, ln, raw[p]);
+  }
+  const Place at = locate(a.cu, a.start, c.batch, t);
+  if (!holds(at, t, a.tokens)) return;            // left as it is
+  const int pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
+  bool there = at.first >= 0 && pos >= 0 && pos < positions_of(c, a);
+  int page = 0;
+  if (kind && there) {
+    page = kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, at.s, pos);
+    there = page >= 0;
+  }
+  if (!there) {
+    if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+    return;
+  }
+  float an[16];
+  if (kind < 2 && ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int h = h0 + p * ROWS + sub;
+    const bool on = h < heads;
+    float y[16];
+    widen(raw[p], y);
+    if (kind < 2) norm_rotate_exact<D, INTER>(y, ln, kind ? a.k_norm : a.q_norm, a.eps, an);
+    if (kind == 0) {
+      if (on) store16(a.q_out + ((long long)t * heads + h) * D, ln, y);
+      continue;
+    }
+    const long long row = (((long long)page * heads + (on ? h : 0)) << c.page_log2) + (pos & (c.page - 1));
+    const float unit_of = kv4_unit(kind == 1 ? c.k_unit : c.v_unit, on ? h : 0);
+    quantise_store<D, INTER>(kind == 1 ? c.k : c.v, kind == 1 ? c.k_scale : c.v_scale, row, on, y, ln, a.rot, unit_of);
+    if (kind == 1 && a.k_out && on) store16(a.k_out + ((long long)t * heads + h) * D, ln, y);
+  }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(THREADS, 3) k_append_kv4(Kv4View c, AppendArgs a, int q_blocks,
+                                                           int kv_blocks, int* err_flag) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  append_unit<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), q_blocks,
+                        kv_blocks, err_flag);
+  report_offsets(a.cu, c.batch, a.tokens, err_flag);
+}
+
+// Cached tokens back as bf16 (code * scale has at most six significant bits: exact). A warp per
+// packed token; a lane moves a block of 16 elements at a time.
+template <int D>
+__device__ __forceinline__ void read_token(const Kv4View& c, const int* __restrict__ cu,
+                                           const int* __restrict__ first, int tokens,
+                                           bf16* __restrict__ k_out, bf16* __restrict__ v_out,
+                                           int* err_flag) {
+  const long long t = ((long long)blockIdx.x * THREADS + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (t >= tokens) return;
+  const Place p = locate(cu, first, c.batch, (int)t);
+  if (!holds(p, (int)t, tokens)) return;
+  const int pos = (int)((unsigned)p.first + (unsigned)((int)t - p.begin));
+  const int pg =
+      p.first < 0 ? -1 : kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, p.s, pos);
+  if (pg < 0) {
+    if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+    return;
+  }
+  const int off = pos & (c.page - 1), blocks = c.heads * (D / 16);
+  constexpr int AHEAD = 4;                 // loads a lane has in flight
+  for (int i0 = lane; i0 < 2 * blocks; i0 += 32 * AHEAD) {
+    uint2 u[AHEAD];
+    uint32_t scale[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= 2 * blocks) break;
+      const bool is_v = i >= blocks;
+      const int j = is_v ? i - blocks : i, head = j / (D / 16), b = j % (D / 16);
+      const long long row = (((long long)pg * c.heads + head) << c.page_log2) + off;
+      u[k] = *reinterpret_cast<const uint2*>((is_v ? c.v : c.k) + row * (D / 2) + 8 * b);
+      scale[k] = (is_v ? c.v_scale : c.k_scale)[row * (D / 16) + b];
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= 2 * blocks) break;
+      const bool is_v = i >= blocks;
+      const int j = is_v ? i - blocks : i;
+      const float unit = kv4_unit(is_v ? c.v_unit : c.k_unit, j / (D / 16));
+      const uint32_t sc = f16x2_of_e4m3_pair(scale[k] * 0x101u);
+      float z[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = h ? u[k].y : u[k].x;
+        const uint32_t x[4] = {f16x2_of_e2m1x2<0>(w), f16x2_of_e2m1x2<1>(w), f16x2_of_e2m1x2<2>(w),
+                               f16x2_of_e2m1x2<3>(w)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[q]), *reinterpret_cast<const __half2*>(&sc));
+          const float2 f = __half22float2(y);
+          z[h][2 * q] = f.x * unit;
+          z[h][2 * q + 1] = f.y * unit;
+        }
+      }
+      bf16* to = (is_v ? v_out : k_out) + (t * c.heads * (D / 16) + j) * 16;
+      store8(to, z[0]);
+      store8(to + 8, z[1]);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 5)
+    k_kv4_read(Kv4View c, const int* __restrict__ cu, const int* __restrict__ first, int tokens,
+               bf16* __restrict__ k_out, bf16* __restrict__ v_out, int* err_flag) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  read_token<D>(c, cu, first, tokens, k_out, v_out, err_flag);
+  report_offsets(cu, c.batch, tokens, err_flag);
+}
+
+template <int D, bool INTER>
+cudaError_t launch_append(const Kv4View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
+  const int q_blocks = a.q ? (a.q_heads + HEADS - 1) / HEADS : 0, kv_blocks = (c.heads + HEADS - 1) / HEADS;
+  const long long blocks = blocks_for(32LL * a.tokens * (q_blocks + 2 * kv_blocks), c.batch);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_early(k_append_kv4<D, INTER>, (unsigned)blocks, true, s, c, a, q_blocks, kv_blocks, err_flag);
+}
+
+}  // namespace
+
+cudaError_t rope_append_kv4(const Kv4View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
+  if (a.tokens <= 0) return cudaSuccess;
+  if (c.dim == 64)
+    return a.interleaved ? launch_append<64, true>(c, a, err_flag, s)
+                         : launch_append<64, false>(c, a, err_flag, s);
+  if (c.dim == 128)
+    return a.interleaved ? launch_append<128, true>(c, a, err_flag, s)
+                         : launch_append<128, false>(c, a, err_flag, s);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t kv4_read(const Kv4View& c, const int* cu, const int* first, int tokens, bf16* k_out,
+                     bf16* v_out, int* err_flag, cudaStream_t s) {
+  if (tokens <= 0) return cudaSuccess;
+  const long long blocks = blocks_for(32LL * tokens, c.batch);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (c.dim == 64)
+    return launch_early(k_kv4_read<64>, (unsigned)blocks, true, s, c, cu, first, tokens, k_out, v_out, err_flag);
+  if (c.dim == 128)
+    return launch_early(k_kv4_read<128>, (unsigned)blocks, true, s, c, cu, first, tokens, k_out, v_out, err_flag);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace jepa

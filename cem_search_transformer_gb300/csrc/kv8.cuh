@@ -18,11 +18,16 @@ constexpr int DEV_ERR_INDEX = 2;     // a page, position or offset outside its b
 constexpr float KV8_SCALE_MIN = 0x1p-40f;
 constexpr float KV8_SCALE_MAX = 0x1p+40f;
 
-struct Kv8View {
-  uint8_t *k, *v;
-  float *k_scale, *v_scale;
+// The pages of a cache of either width: table [batch][max_pages] into num_pages blocks of `page`
+// tokens a head.
+struct PageView {
   const int* table;
   int num_pages, page, page_log2, heads, dim, batch, max_pages;
+};
+
+struct Kv8View : PageView {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
 };
 
 // ---- launchers (each returns the launch's error) ----

@@ -8,10 +8,7 @@
 // loads, angles and maximum with 16 warps a SM), read-back 26 us (4.6 TB/s). A page and head is quantised by exactly one team
 // of warps: that of its "owner", the first new token that lies in the page. No atomics: the result
 // depends neither on the launch shape nor on the order of blocks.
-//
-// A head row is held by D / 16 lanes, 16 elements each: both elements of every rotated pair lie in
-// one lane (no exchange), and its 8 angles serve 16 elements.
-#include "kv8.cuh"
+#include "rope_rows.cuh"
 
 #include <cuda_fp16.h>
 
@@ -20,8 +17,6 @@
 namespace jepa {
 
 namespace {
-
-constexpr int THREADS = 256;
 
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
   uint16_t p;
@@ -39,104 +34,9 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&y)[8], float inv) {
   u.y = (uint32_t)e4m3x2(y[4] * inv, y[5] * inv) | ((uint32_t)e4m3x2(y[6] * inv, y[7] * inv) << 16);
   return u;
 }
-__device__ __forceinline__ void store8(bf16* p, const float (&y)[8]) {
-  uint4 u;
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  u.x = w[0]; u.y = w[1]; u.z = w[2]; u.w = w[3];
-  *reinterpret_cast<uint4*>(p) = u;
-}
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
 // A scale as the cache's contract has it: positive and within [2^-40, 2^40].
 __device__ __forceinline__ float sane_scale(float s) {
   return s >= KV8_SCALE_MIN ? fminf(s, KV8_SCALE_MAX) : KV8_SCALE_MIN;
-}
-
-// Sequence of a packed token and where it lies.
-struct Place {
-  int s, begin, end, first;   // sequence (-1: none), its packed tokens [begin, end), start[s]
-};
-// The largest s with cu[s] <= t (cu ascending), by the whole warp: 32-way probes, the last of
-// which brings the bounds and the start along.
-__device__ __forceinline__ Place locate(const int* __restrict__ cu, const int* __restrict__ start,
-                                        int batch, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = batch;
-  while (n > 32) {
-    const int step = (n + 31) >> 5, at = lane * step;
-    const bool le = at < n && __ldg(cu + lo + at) <= t;
-    const int last = 31 - __clz((int)(__ballot_sync(0xffffffffu, le) | 1u));
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  int b = 0x7fffffff, e = 0, f = 0;
-  if (lane < n) {
-    b = __ldg(cu + lo + lane);
-    e = __ldg(cu + lo + lane + 1);
-    f = __ldg(start + lo + lane);
-  }
-  const uint32_t le = __ballot_sync(0xffffffffu, b <= t);
-  const int last = le ? 31 - __clz((int)le) : 0;
-  Place p;
-  p.s = le ? lo + last : -1;
-  p.begin = __shfl_sync(0xffffffffu, b, last);
-  p.end = __shfl_sync(0xffffffffu, e, last);
-  p.first = __shfl_sync(0xffffffffu, f, last);
-  return p;
-}
-
-// Whether packed token t belongs to the sequence that locate found. Not where it lies ahead of the
-// first sequence or behind the last, nor in one whose offsets leave the rows: that one is skipped.
-__device__ __forceinline__ bool holds(const Place& p, int t, int tokens) {
-  return p.s >= 0 && t < p.end && kv8_span_ok(p.begin, p.end, tokens);
-}
-
-// Reports the sequences that are skipped, empty ones too, each by one thread of the grid (which has a
-// thread for each). Stands at a kernel's end, where the offsets are in the cache.
-__device__ __forceinline__ void report_offsets(const int* __restrict__ cu, int batch, int tokens,
-                                               int* err_flag) {
-  const long long s = (long long)blockIdx.x * THREADS + threadIdx.x;
-  if (s < batch && !kv8_span_ok(__ldg(cu + s), __ldg(cu + s + 1), tokens)) atomicOr(err_flag, DEV_ERR_INDEX);
-}
-// Blocks for `threads` of work and at least one thread a sequence.
-long long blocks_for(long long threads, int batch) {
-  return ((threads > batch ? threads : batch) + THREADS - 1) / THREADS;
-}
-
-// The 16 elements of a head row that a lane holds: chunks of 8 at c0 and c1.
-template <int D, bool INTER>
-struct Lane {
-  int c0, c1, p;
-  bool rotates;
-  __device__ __forceinline__ explicit Lane(int rot) {
-    constexpr int L = D / 16;
-    p = (threadIdx.x & 31) % L;
-    rotates = 16 * p < rot;
-    if (INTER || !rotates) {
-      // neighbours; past rot these are the chunks rot / 8 + 2 (p - rot / 16) and the next
-      c0 = 2 * p;
-      c1 = 2 * p + 1;
-    } else {
-      c0 = p;
-      c1 = p + (rot >> 4);
-    }
-  }
-};
-
-// cos (first 8) and sin of a lane's pairs 8 p .. 8 p + 7 from a row of the table.
-__device__ __forceinline__ void load_angles(float (&an)[16], const float* row, int rot, int p) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(row + h * (rot >> 1) + 8 * p + i));
-      an[8 * h + i] = x.x; an[8 * h + i + 1] = x.y; an[8 * h + i + 2] = x.z; an[8 * h + i + 3] = x.w;
-    }
 }
 
 // y = x * w / sqrt(mean(x^2) + eps), then (a, b) -> (a cos - b sin, b cos + a sin) for the pairs
@@ -172,33 +72,6 @@ __device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>
   }
 }
 
-template <class LaneT>
-__device__ __forceinline__ void load16(const bf16* row, const LaneT& ln, uint4 (&u)[2]) {
-  u[0] = *reinterpret_cast<const uint4*>(row + 8 * ln.c0);
-  u[1] = *reinterpret_cast<const uint4*>(row + 8 * ln.c1);
-}
-__device__ __forceinline__ void widen(const uint4 (&u)[2], float (&y)[16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
-      y[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-template <class LaneT>
-__device__ __forceinline__ void store16(bf16* row, const LaneT& ln, const float (&y)[16]) {
-  float a[8], b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a[i] = y[i];
-    b[i] = y[8 + i];
-  }
-  store8(row + 8 * ln.c0, a);
-  store8(row + 8 * ln.c1, b);
-}
 template <class LaneT>
 __device__ __forceinline__ void store_codes(uint8_t* row, const LaneT& ln, const float (&y)[16], float inv) {
   float a[8], b[8];
@@ -247,10 +120,6 @@ __device__ __forceinline__ void rescale_codes(uint8_t* base, int off, float fact
     }
     *at = e4m3x8(z, factor);
   }
-}
-
-__device__ __forceinline__ int positions_of(const Kv8View& c, const AppendArgs& a) {
-  return min(a.positions, c.max_pages << c.page_log2);
 }
 
 // Queries: a warp takes one token and up to Q_HEADS of its heads, which share the angles. The
@@ -396,22 +265,6 @@ template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 4) k_rope_queries(Kv8View c, AppendArgs a, int* err_flag) {
   asm volatile("griddepcontrol.launch_dependents;");
   rotate_queries<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
-}
-
-// Launch that, with `early`, begins while the kernel before it in the stream still runs: what may
-// not overlap stands behind a griddepcontrol.wait, which lasts until that kernel's end.
-template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, bool early, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = early;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(THREADS);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Long appends: a team of T warps takes a chunk of `page` packed tokens of one head and

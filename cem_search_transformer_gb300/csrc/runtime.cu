@@ -7,7 +7,9 @@
 // mu/sigma kept in device memory, so the host is not involved between rounds (the pages
 // point out that rounds which must run one after another bound the latency from below).
 #include "jepa_cem.h"
+#include "add_rmsnorm.cuh"
 #include "common.cuh"
+#include "kv4.cuh"
 #include "kv8.cuh"
 
 #include <cmath>
@@ -1267,6 +1269,8 @@ struct OnDevice {
 
 static bool aligned(const void* p, size_t n) { return (((uintptr_t)p) & (n - 1)) == 0; }
 
+static int page_log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
 static jepa_status kv8_view(jepa_ctx* ctx, const char* what, const jepa_kv8_cache* c, Kv8View* out) {
   if (!bf16_mode(ctx)) return fail(ctx, JEPA_ERR_UNSUPPORTED, "%s needs a bf16 context", what);
   if (!c || bad_ptr(c->k) || bad_ptr(c->v) || bad_ptr(c->k_scale) || bad_ptr(c->v_scale) ||
@@ -1284,9 +1288,9 @@ static jepa_status kv8_view(jepa_ctx* ctx, const char* what, const jepa_kv8_cach
       (long long)c->max_pages * c->page_size > (1LL << 30) ||
       (long long)c->num_pages * c->kv_heads > 0x7fffffffLL)
     return fail(ctx, JEPA_ERR_SHAPE, "%s: cache sizes out of range", what);
-  *out = Kv8View{c->k, c->v, c->k_scale, c->v_scale, c->page_table, c->num_pages, c->page_size,
-                 c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7,
-                 c->kv_heads, c->head_dim, c->batch, c->max_pages};
+  *out = Kv8View{{c->page_table, c->num_pages, c->page_size, page_log2_of(c->page_size), c->kv_heads,
+                  c->head_dim, c->batch, c->max_pages},
+                 c->k, c->v, c->k_scale, c->v_scale};
   return JEPA_OK;
 }
 
@@ -1309,32 +1313,26 @@ jepa_status jepa_rope_table(jepa_ctx* ctx, int positions, int rot, double base, 
   return JEPA_OK;
 }
 
-jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
-                                 int64_t q_stride, const uint16_t* k, int64_t k_stride,
-                                 const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
-                                 const float* q_norm, const float* k_norm, float norm_eps,
-                                 const float* rope_table, int positions, int rot, int interleaved,
-                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
-                                 uint16_t* k_out, void* stream) {
-  if (!ctx) return JEPA_ERR_INVALID_ARG;
-  Kv8View c;
-  const jepa_status st = kv8_view(ctx, "rope_append_kv8", cache, &c);
-  if (st) return st;
+// Checks and gathers what the appends to the caches take beside the cache.
+static jepa_status append_args(jepa_ctx* ctx, const char* what, const PageView& c, const uint16_t* q,
+                               int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                               int64_t v_stride, int tokens, int q_heads, const float* q_norm,
+                               const float* k_norm, float norm_eps, const float* rope_table, int positions,
+                               int rot, int interleaved, const int32_t* cu, const int32_t* start,
+                               uint16_t* q_out, uint16_t* k_out, AppendArgs* out) {
   if (tokens < 1 || bad_ints(cu) || bad_ints(start) || bad_rows(k, k_stride, c.heads, c.dim) ||
       bad_rows(v, v_stride, c.heads, c.dim) || (q == nullptr) != (q_out == nullptr) ||
       !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
       (interleaved != 0 && interleaved != 1) || !(norm_eps >= 0.f))
-    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: bad argument");
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: bad argument", what);
   if (q && (q_heads < 1 || q_heads % c.heads || q_heads > 65535 || bad_rows(q, q_stride, q_heads, c.dim)))
-    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: bad queries");
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: bad queries", what);
   if (rot < 0 || rot % 16 || rot > c.dim || (rot > 0 && (bad_ptr(rope_table) || !aligned(rope_table, 16) || positions < 1)))
-    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: bad rotary table");
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: bad rotary table", what);
   // in place only where the rows are dense: a thread then writes the row that it read
   if ((q && q == q_out && q_stride != (int64_t)q_heads * c.dim) ||
       (k == k_out && k_stride != (int64_t)c.heads * c.dim))
-    return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv8: in place needs dense rows");
-  OnDevice on(ctx->device);
-  CK(on.status);
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: in place needs dense rows", what);
   AppendArgs a;
   a.q = (const bf16*)q;
   a.k = (const bf16*)k;
@@ -1355,6 +1353,28 @@ jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, con
   a.start = start;
   a.q_out = (bf16*)q_out;
   a.k_out = (bf16*)k_out;
+  *out = a;
+  return JEPA_OK;
+}
+
+jepa_status jepa_rope_append_kv8(jepa_ctx* ctx, const jepa_kv8_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                 const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
+                                 const float* q_norm, const float* k_norm, float norm_eps,
+                                 const float* rope_table, int positions, int rot, int interleaved,
+                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
+                                 uint16_t* k_out, void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv8View c;
+  const jepa_status st = kv8_view(ctx, "rope_append_kv8", cache, &c);
+  if (st) return st;
+  AppendArgs a;
+  const jepa_status bad = append_args(ctx, "rope_append_kv8", c, q, q_stride, k, k_stride, v, v_stride, tokens,
+                                      q_heads, q_norm, k_norm, norm_eps, rope_table, positions, rot,
+                                      interleaved, cu, start, q_out, k_out, &a);
+  if (bad) return bad;
+  OnDevice on(ctx->device);
+  CK(on.status);
   CK(rope_append_kv8(c, a, ctx->dev_err, (cudaStream_t)stream));
   return JEPA_OK;
 }
@@ -1434,6 +1454,174 @@ jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_st
   CK(attention_packed((const bf16*)q, q_stride, (const bf16*)k, k_stride, (const bf16*)v, v_stride,
                       tokens_q, tokens_k, batch, q_heads, kv_heads, head_dim, cu_q, cu_k, scale,
                       frame, (bf16*)out, lse, ctx->dev_err, ctx->num_sms, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+// ---- 4-bit paged cache ----
+
+static jepa_status kv4_view(jepa_ctx* ctx, const char* what, const jepa_kv4_cache* c, Kv4View* out) {
+  if (!bf16_mode(ctx)) return fail(ctx, JEPA_ERR_UNSUPPORTED, "%s needs a bf16 context", what);
+  if (!c || bad_ptr(c->k) || bad_ptr(c->v) || bad_ptr(c->k_scale) || bad_ptr(c->v_scale) ||
+      bad_ptr(c->page_table))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: null cache or pointer in it", what);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) ||
+      !aligned(c->v_scale, 16) || !aligned(c->page_table, 4) || !aligned(c->k_unit, 4) ||
+      !aligned(c->v_unit, 4))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "%s: misaligned cache buffer", what);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(ctx, JEPA_ERR_SHAPE, "%s: head_dim must be 64 or 128", what);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(ctx, JEPA_ERR_SHAPE, "%s: page_size must be 16, 32, 64 or 128", what);
+  if (c->num_pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024 || c->batch < 1 ||
+      c->batch > 65535 || c->max_pages < 1 ||
+      (long long)c->max_pages * c->page_size > (1LL << 30) ||
+      (long long)c->num_pages * c->kv_heads > 0x7fffffffLL)
+    return fail(ctx, JEPA_ERR_SHAPE, "%s: cache sizes out of range", what);
+  *out = Kv4View{{c->page_table, c->num_pages, c->page_size, page_log2_of(c->page_size), c->kv_heads,
+                  c->head_dim, c->batch, c->max_pages},
+                 c->k, c->v, c->k_scale, c->v_scale, c->k_unit, c->v_unit};
+  return JEPA_OK;
+}
+
+jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                 const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
+                                 const float* q_norm, const float* k_norm, float norm_eps,
+                                 const float* rope_table, int positions, int rot, int interleaved,
+                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
+                                 uint16_t* k_out, void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv4View c;
+  const jepa_status st = kv4_view(ctx, "rope_append_kv4", cache, &c);
+  if (st) return st;
+  AppendArgs a;
+  const jepa_status bad = append_args(ctx, "rope_append_kv4", c, q, q_stride, k, k_stride, v, v_stride, tokens,
+                                      q_heads, q_norm, k_norm, norm_eps, rope_table, positions, rot,
+                                      interleaved, cu, start, q_out, k_out, &a);
+  if (bad) return bad;
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(rope_append_kv4(c, a, ctx->dev_err, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_kv4_read(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int32_t* cu,
+                          const int32_t* first, int tokens, uint16_t* k_out, uint16_t* v_out,
+                          void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv4View c;
+  const jepa_status st = kv4_view(ctx, "kv4_read", cache, &c);
+  if (st) return st;
+  if (tokens < 1 || bad_ints(cu) || bad_ints(first) || bad_ptr(k_out) || bad_ptr(v_out) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_read: bad argument");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(kv4_read(c, cu, first, tokens, (bf16*)k_out, (bf16*)v_out, ctx->dev_err, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_attention_kv4_workspace(jepa_ctx* ctx, const jepa_kv4_cache* cache, size_t* bytes) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv4View c;
+  const jepa_status st = kv4_view(ctx, "attention_kv4_workspace", cache, &c);
+  if (st) return st;
+  if (bad_ptr(bytes)) return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv4_workspace: null bytes");
+  *bytes = attention_kv4_workspace(c.dim, ctx->num_sms);
+  return JEPA_OK;
+}
+
+jepa_status jepa_attention_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
+                               int q_tokens, int q_heads, const int32_t* kv_len, float scale,
+                               int causal, uint16_t* out, float* lse, const float* mass,
+                               float* mass_out, float decay, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv4View c;
+  const jepa_status st = kv4_view(ctx, "attention_kv4", cache, &c);
+  if (st) return st;
+  if (bad_ptr(q) || bad_ptr(out) || bad_ints(kv_len) || bad_ptr(workspace) || !aligned(q, 16) ||
+      !aligned(out, 16) || !aligned(workspace, 256) || !aligned(lse, 4) || !aligned(mass, 4) ||
+      !aligned(mass_out, 4) || q_tokens < 1 || q_heads < 1 || q_heads % c.heads ||
+      (causal != 0 && causal != 1) || !(scale > 0.f) || !std::isfinite(scale))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv4: bad argument");
+  if ((mass && !mass_out) || (mass_out && (!lse || !std::isfinite(decay))))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv4: weights need mass_out, lse and a finite decay");
+  if ((long long)q_tokens * (q_heads / c.heads) > 65536 ||
+      (long long)c.batch * q_tokens * q_heads > (1LL << 30))
+    return fail(ctx, JEPA_ERR_SHAPE, "attention_kv4: too many query rows");
+  if (workspace_bytes < attention_kv4_workspace(c.dim, ctx->num_sms))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv4: the workspace is too small");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  const MassArgs w{mass, mass_out, decay};
+  CK(attention_kv4(c, (const bf16*)q, q_tokens, q_heads, kv_len, scale, causal, (bf16*)out, lse,
+                   mass_out ? &w : nullptr, workspace, ctx->dev_err, ctx->num_sms, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+jepa_status jepa_kv4_evict_workspace(jepa_ctx* ctx, const jepa_kv4_cache* cache, int keep, size_t* bytes) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv4View c;
+  const jepa_status st = kv4_view(ctx, "kv4_evict_workspace", cache, &c);
+  if (st) return st;
+  if (bad_ptr(bytes) || keep < 1 || keep > (1 << 30))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_evict_workspace: null bytes, or keep out of range");
+  *bytes = kv4_evict_workspace(c, keep);
+  return JEPA_OK;
+}
+
+jepa_status jepa_kv4_evict(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int32_t* kv_len,
+                           const float* mass, int keep, int recent, const jepa_kv4_cache* to,
+                           int32_t* len_out, float* mass_out, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  Kv4View c, t;
+  jepa_status st = kv4_view(ctx, "kv4_evict", cache, &c);
+  if (st || (st = kv4_view(ctx, "kv4_evict (to)", to, &t))) return st;
+  if (bad_ints(kv_len) || bad_ptr(mass) || !aligned(mass, 4) || bad_ints(len_out) || !aligned(mass_out, 4) ||
+      mass == mass_out || kv_len == len_out || bad_ptr(workspace) || !aligned(workspace, 256) || keep < 1 ||
+      keep > (1 << 30) || recent < 0 || recent > keep)
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_evict: bad argument");
+  if (t.batch != c.batch || t.heads != c.heads || t.dim != c.dim)
+    return fail(ctx, JEPA_ERR_SHAPE, "kv4_evict: the caches differ in batch, heads or head_dim");
+  if (t.k_unit != c.k_unit || t.v_unit != c.v_unit)
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_evict: the caches must have the same units");
+  if ((long long)t.max_pages * t.page < keep)
+    return fail(ctx, JEPA_ERR_SHAPE, "kv4_evict: the target's table names fewer than keep tokens");
+  if (workspace_bytes < kv4_evict_workspace(c, keep))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_evict: the workspace is too small");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(kv4_evict(c, kv_len, mass, keep, recent, t, len_out, mass_out, workspace, ctx->dev_err,
+               ctx->num_sms, (cudaStream_t)stream));
+  return JEPA_OK;
+}
+
+static bool bad_matrix(const void* p, int64_t stride, int cols) {
+  return !aligned(p, 16) || stride < cols || stride % 8 || stride > (1LL << 31);
+}
+
+jepa_status jepa_add_rmsnorm_fp8(jepa_ctx* ctx, const void* x, int x_bf16, int64_t x_stride,
+                                 const void* delta, int delta_bf16, int64_t delta_stride,
+                                 const float* weight, float eps, int rows, int cols, void* x_out,
+                                 int64_t x_out_stride, uint8_t* codes, float* scales, uint16_t* y,
+                                 void* stream) {
+  if (!ctx) return JEPA_ERR_INVALID_ARG;
+  if (rows < 1 || cols < 16 || cols % 16 || bad_ptr(x) || bad_ptr(weight) || !aligned(weight, 16) ||
+      (x_bf16 != 0 && x_bf16 != 1) || (delta_bf16 != 0 && delta_bf16 != 1) || bad_matrix(x, x_stride, cols) ||
+      (delta && bad_matrix(delta, delta_stride, cols)) || (x_out && bad_matrix(x_out, x_out_stride, cols)) ||
+      (codes == nullptr) != (scales == nullptr) || (!codes && !y) || !aligned(codes, 16) || !aligned(scales, 4) ||
+      !aligned(y, 16) || !(eps >= 0.f))
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "add_rmsnorm_fp8: bad argument");
+  if (cols > ADD_RMSNORM_MAX_COLS)
+    return fail(ctx, JEPA_ERR_SHAPE, "add_rmsnorm_fp8: more than %d columns", ADD_RMSNORM_MAX_COLS);
+  if (x_out == x && x_out_stride != x_stride)
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "add_rmsnorm_fp8: in place needs equal strides");
+  OnDevice on(ctx->device);
+  CK(on.status);
+  CK(add_rmsnorm(x, x_bf16, x_stride, delta, delta_bf16, delta_stride, weight, eps, rows, cols, x_out,
+                 x_out_stride, codes, scales, (bf16*)y, (cudaStream_t)stream));
   return JEPA_OK;
 }
 

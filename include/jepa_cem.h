@@ -405,6 +405,104 @@ jepa_status jepa_attention_packed(jepa_ctx* ctx, const uint16_t* q, int64_t q_st
                                   const int32_t* cu_k, float scale, int frame, uint16_t* out,
                                   float* lse, void* stream);
 
+/* ---- 4-bit paged key/value cache, eviction from it, and the norm ahead of 8-bit products ----
+ *
+ * Everything said above of the 8-bit cache's entry points (contexts, streams, capture, packed
+ * sequences, strides, indices on the device) holds here as well. */
+
+/* One layer's cache in 4 bits. k, v [num_pages][kv_heads][page_size][head_dim / 2]: e2m1 codes (sign,
+ * two bits of exponent, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), element 2i in the
+ * low half of byte i; k_scale, v_scale [num_pages][kv_heads][page_size][head_dim / 16]: e4m3 scales of
+ * 16 elements each; k_unit, v_unit [kv_heads] float32 or NULL (1): a power of two for each head, within
+ * [2^-40, 2^40] (others are read as the power of two at or below, or the nearer end; NaN as the
+ * least). An element stands for code * scale * unit. page_table, sizes and limits as in
+ * jepa_kv8_cache; k, v, k_scale and v_scale 16-byte aligned. A unit near a sixth of the head's usual
+ * magnitude (0.1 to 1000 times that) keeps the scales among e4m3's normal numbers. No token's codes depend on
+ * another's: fresh pages need no initial values, and appends change nothing that is there. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const float* k_unit;
+  const float* v_unit;
+  const int32_t* page_table;
+  int32_t num_pages, page_size, kv_heads, head_dim, batch, max_pages;
+} jepa_kv4_cache;
+
+/* Append new tokens to the cache: arguments, norm, rotation and q_out, k_out as in
+ * jepa_rope_append_kv8. Each 16 elements of a rotated key or of a value are quantised from fp32: scale =
+ * e4m3(max|x| / 6 / unit), nearest even, at least 2^-9 and at most 448; codes = e2m1(x / (scale * unit)),
+ * nearest even, saturating. A block that holds a NaN or an infinity gets a NaN scale and reads as NaN. The
+ * norm's factor 1 / sqrt(mean(x^2) + norm_eps) is rounded once to fp32 and multiplied by the weight
+ * first; each product and sum of the rotation is rounded to fp32. */
+jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
+                                 int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                 const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
+                                 const float* q_norm, const float* k_norm, float norm_eps,
+                                 const float* rope_table, int positions, int rot, int interleaved,
+                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
+                                 uint16_t* k_out, void* stream);
+
+/* Read cached tokens back as bf16 (exact), as jepa_kv8_read. */
+jepa_status jepa_kv4_read(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int32_t* cu,
+                          const int32_t* first, int tokens, uint16_t* k_out, uint16_t* v_out,
+                          void* stream);
+
+/* Bytes of jepa_attention_kv4's workspace for this cache's head_dim (the same for every batch,
+ * length and head count). */
+jepa_status jepa_attention_kv4_workspace(jepa_ctx* ctx, const jepa_kv4_cache* cache, size_t* bytes);
+
+/* Attention of the newest q_tokens tokens of each sequence over its cached tokens: arguments,
+ * promises and limits as in jepa_attention_kv8. Where mass_out is given (lse then has to be), also the
+ * weight that each cached token received, summed over the new tokens and the query heads that share its
+ * key/value head:
+ *   mass_out[b, h, j] = decay * mass[b, h, j] + sum_{t, g} exp(scale * q[b, t, g] . K_j - lse[b, t, g])
+ * for j < kv_len[b]; what lies behind is left as it was. mass, mass_out [batch][kv_heads][max_pages *
+ * page_size] float32 dev; mass NULL: zeros; mass_out may be mass. A token that is appended starts
+ * with what mass holds at its place, so fill it with zeros at first (jepa_kv4_evict does so behind what it
+ * keeps). decay finite. The sums' order is fixed. */
+jepa_status jepa_attention_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
+                               int q_tokens, int q_heads, const int32_t* kv_len, float scale,
+                               int causal, uint16_t* out, float* lse, const float* mass,
+                               float* mass_out, float decay, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Bytes of jepa_kv4_evict's workspace: 4 * batch * kv_heads * keep. */
+jepa_status jepa_kv4_evict_workspace(jepa_ctx* ctx, const jepa_kv4_cache* cache, int keep, size_t* bytes);
+
+/* Evict cached tokens by accumulated weight. Of the n = kv_len[b] tokens of a sequence each key/value
+ * head keeps its last `recent` and, of those before, the ones with the largest mass (as float32; ties go
+ * to the lower place, NaN counts as the least), `keep` in all; all n where n <= keep. In their order they become
+ * tokens 0, 1, .. of the pages that to->page_table names, codes and scales unchanged (keys keep the
+ * rotation of their old positions); len_out[b] = min(n, keep), and mass_out [batch][kv_heads][to->max_pages *
+ * to->page_size] (or NULL) their masses, zeros behind. Different heads of a sequence may keep different tokens.
+ *   `to` may have the same buffers as `cache` with another table, the same units (pointers), batch, heads and
+ *   head_dim; its pages page_size and number may differ. The pages that receive tokens belong to one place of
+ *   one sequence and hold no token that `cache` names (shared pages are thus never written), but for
+ *   sequences with n <= keep, which may name the same pages in both tables where the page sizes are equal.
+ *   kv_len, len_out [batch] int32 dev; mass [batch][kv_heads][max_pages * page_size] float32 dev;
+ *   0 <= recent <= keep, 1 <= keep <= to->max_pages * to->page_size; workspace as above, 256-byte
+ *   aligned. Calls that may overlap on the device need a workspace each. */
+jepa_status jepa_kv4_evict(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int32_t* kv_len,
+                           const float* mass, int keep, int recent, const jepa_kv4_cache* to,
+                           int32_t* len_out, float* mass_out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Residual addition, RMS norm and 8-bit codes of a row, ready for jepa_linear_fp8:
+ *   s = x + delta (fp32), x_out = s in x's type, y = s * weight / sqrt(mean(s^2) + eps),
+ *   codes, scales = y as jepa_quantize_rows_fp8 has it (from fp32), y also as bf16.
+ * The norm is that of the unrounded s. x, x_out [rows][cols] float32 (x_bf16 0) or bf16 (1), delta float32
+ * or bf16 (delta_bf16), each with `*_stride` elements between rows (at least cols, a multiple of 8);
+ * delta NULL: none; x_out NULL: not wanted, or x: in place (equal strides; no other overlap). weight
+ * [cols] float32; codes [rows][cols] with scales [rows] float32, or both NULL; y [rows][cols] bf16 or NULL (not
+ * both left out). All dev, 16-byte aligned but scales. cols a multiple of 16, at most 32768. Any context. */
+jepa_status jepa_add_rmsnorm_fp8(jepa_ctx* ctx, const void* x, int x_bf16, int64_t x_stride,
+                                 const void* delta, int delta_bf16, int64_t delta_stride,
+                                 const float* weight, float eps, int rows, int cols, void* x_out,
+                                 int64_t x_out_stride, uint8_t* codes, float* scales, uint16_t* y,
+                                 void* stream);
+
 /* enable = 0: jepa_cem_plan launches the kernels of its captured graph one by one on the
  * stream instead of replaying the graph (same kernels, same results; for measuring what the
  * graph saves). enable != 0 (the default): graph replay. */
