@@ -28,9 +28,9 @@ namespace {
 template <int D, int NR>
 struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
-  static constexpr int NST = 3;                    // cp.async stages of a warp
+  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;   // cp.async stages of a warp
   static constexpr int CTAS = (D == 64 ? 4 : 3) - (NR == 2);
-  static constexpr int KS = 32;                    // keys a warp takes in a step
+  static constexpr int KS = D == 64 && NR == 1 ? 64 : 32;   // keys a warp takes in a step
   static constexpr int GROUPS = KS / 16;           // 16-key groups
   static constexpr int UNIT = WARPS * KS;          // keys of a unit
   static constexpr int KB = D / 2, SB = D / 16;    // bytes of a key's codes, and of its scales
@@ -42,6 +42,7 @@ struct Shape {
   static constexpr int OUT_LD = OUT_ROW<D>;
   static constexpr int OFF_OUT = WARPS * NST * STAGE;
   static constexpr int SMEM = OFF_OUT + WARPS * ROWS * OUT_LD * 4;
+  static_assert(2 * KS * SB / 16 <= 32, "a step's scales are a chunk a lane at most");
   static_assert(CTAS <= MAX_CTAS_PER_SM && CTAS * (SMEM + 2048) <= 228 * 1024, "CTAs of a SM");
   static_assert(COMBINE_SMEM<D> * CTAS * MAX_SMS <= 48 * 1024, "what a launch may have without an attribute");
 };
@@ -52,6 +53,16 @@ template <int D>
 __device__ __forceinline__ uint32_t code_at(int row, int chunk) {
   if (D == 128) return (row >> 1) * 128 + 16 * (((row & 1) * 4 + chunk) ^ (((row >> 1) & 3) << 1));
   return (row >> 2) * 128 + 16 * (((row & 3) * 2 + chunk) ^ (((row >> 2) & 1) << 1));
+}
+
+// x[i] of an array in registers.
+template <class T, int N>
+__device__ __forceinline__ T pick(const T (&x)[N], int i) {
+  T y = x[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k)
+    if (i == k) y = x[k];
+  return y;
 }
 
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
@@ -85,8 +96,18 @@ __device__ __forceinline__ void scores_of(const uint32_t (&w)[2][D / 32], const 
 template <int D>
 __device__ __forceinline__ void key_scales(uint32_t bytes, uint32_t (&sc)[D / 64]) {
   const uint32_t x = f16x2_of_e4m3_pair(bytes);
-  sc[0] = __byte_perm(x, x, 0x1010);
-  if (D == 128) sc[D / 64 - 1] = __byte_perm(x, x, 0x3232);
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tmov.b32 %0, {lo, lo};\n\t}" : "=r"(sc[0]) : "r"(x));
+  if (D == 128)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tmov.b32 %0, {hi, hi};\n\t}" : "=r"(sc[D / 64 - 1]) : "r"(x));
+}
+
+// Scores are raw products times qs, and masked ones -inf before that: qs stays positive and finite.
+template <int D, int NR>
+__device__ __forceinline__ void scale_queries(Queries<D, NR>& qr, float unit) {
+#pragma unroll
+  for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) qr.qs[nr][e] = fminf(fmaxf(qr.qs[nr][e] * unit, 0x1p-126f), 0x1.fffffep127f);
 }
 
 template <int D, int NR>
@@ -163,33 +184,49 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     if (ld_more && key0 < ld.len) {
       const uint32_t st = ld_stage * S::STAGE;
       uint64_t row[S::GROUPS];                 // of the group's first key among all blocks' keys
-      int keys[S::GROUPS];                     // keys there; others are zeros
+      bool inside = key0 + S::KS <= ld.len;
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
         const bool there = (uint32_t)pg_next[p] < (uint32_t)c.num_pages;
-        const int left = ld.len - (key0 + 16 * p);
-        if (!there && left > 0 && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
-        keys[p] = there ? max(0, min(16, left)) : 0;
+        inside = inside && there;
         const uint32_t block = (there ? (uint32_t)pg_next[p] : 0u) * (uint32_t)c.heads + (uint32_t)ld.head;
         row[p] = ((uint64_t)block << c.page_log2) + ((uint32_t)(key0 + 16 * p) & slot_mask);
       }
+      const uint8_t* const scales = (sc_v ? c.v_scale : c.k_scale) + 16 * sc_chunk;
+      if (inside) {
 #pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) {
-        const uint64_t from = row[p] * S::KB + lane_from;
-        const uint8_t *fk = c.k + from, *fv = c.v + from;
+        for (int p = 0; p < S::GROUPS; ++p) {
+          const uint64_t from = row[p] * S::KB + lane_from;
+          const uint8_t *fk = c.k + from, *fv = c.v + from;
 #pragma unroll
-        for (int q = 0; q < 16 / RPI; ++q) {
-          const uint32_t bytes = q * RPI + sub < keys[p] ? 16 : 0;
-          cp16(lane_to[q] + st + 16 * p * S::KB, fk + q * RPI * S::KB, bytes);
-          cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, bytes);
+          for (int q = 0; q < 16 / RPI; ++q) {
+            cp16(lane_to[q] + st + 16 * p * S::KB, fk + q * RPI * S::KB, 16);
+            cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, 16);
+          }
         }
-      }
-      if (lane < 2 * S::GROUPS * SPG) {
-        const bool second = sc_group != 0;
-        const uint64_t first = second ? row[S::GROUPS - 1] : row[0];
-        const int n = (second ? keys[S::GROUPS - 1] : keys[0]) - sc_chunk * KPC;
-        cp16(sc_to + st, (sc_v ? c.v_scale : c.k_scale) + first * S::SB + 16 * sc_chunk,
-             max(0, min(KPC, n)) * S::SB);
+        if (lane < 2 * S::GROUPS * SPG)
+          cp16(sc_to + st, scales + pick(row, sc_group) * S::SB, 16);
+      } else {                                 // keys past the end, or without a page, are zeros
+        int keys[S::GROUPS];
+#pragma unroll
+        for (int p = 0; p < S::GROUPS; ++p) {
+          const bool there = (uint32_t)pg_next[p] < (uint32_t)c.num_pages;
+          const int left = ld.len - (key0 + 16 * p);
+          if (!there && left > 0 && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+          keys[p] = there ? max(0, min(16, left)) : 0;
+          const uint64_t from = row[p] * S::KB + lane_from;
+          const uint8_t *fk = c.k + from, *fv = c.v + from;
+#pragma unroll
+          for (int q = 0; q < 16 / RPI; ++q) {
+            const uint32_t bytes = q * RPI + sub < keys[p] ? 16 : 0;
+            cp16(lane_to[q] + st + 16 * p * S::KB, fk + q * RPI * S::KB, bytes);
+            cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, bytes);
+          }
+        }
+        if (lane < 2 * S::GROUPS * SPG) {
+          const int n = pick(keys, sc_group) - sc_chunk * KPC;
+          cp16(sc_to + st, scales + pick(row, sc_group) * S::SB, max(0, min(KPC, n)) * S::SB);
+        }
       }
     }
     cp_commit();
@@ -205,6 +242,13 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
 #pragma unroll 1
   for (int i = 0; i < NST - 1; ++i) issue();
 
+  // where a lane reads in a stage: key g; V row 2t (row 2t + 1 lies in the same line); their scales. Eight
+  // keys further on is a fixed distance on.
+  const uint32_t at_k = D == 128 ? code_at<D>(g, t) : code_at<D>(g, t >> 1) + 8 * (t & 1);
+  const uint32_t at_v = S::OFF_V + (D == 128 ? code_at<D>(2 * t, g >> 1) + 8 * (g & 1) : code_at<D>(2 * t, g >> 2) + 4 * (g & 3));
+  const uint32_t at_v1 = S::OFF_V + (D == 128 ? code_at<D>(2 * t + 1, g >> 1) + 8 * (g & 1) : code_at<D>(2 * t + 1, g >> 2) + 4 * (g & 3));
+  const uint32_t at_ks = S::OFF_SC + g * S::SB + (D == 128 ? 2 * t : t);
+  const uint32_t at_vs = S::OFF_SC + S::KS * S::SB + 2 * t * S::SB + (D == 128 ? g : g >> 1);
   int stage = 0;
   Cursor cur{0, 0, 0, 0};
   Segment sg;
@@ -214,19 +258,13 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     const int head = sg.head, r0 = sg.r0;
     Queries<D, NR> qr;
     qr.load(a, s, head, r0, rows, len);
-    {
-      const float unit = kv4_unit(c.k_unit, head);
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        qr.qs[nr][0] *= unit;
-        qr.qs[nr][1] *= unit;
-      }
-    }
+    scale_queries(qr, kv4_unit(c.k_unit, head));
     float o[NR][S::MT][4];
-    float m[NR][2], l[NR][2];
+    float m[NR][2], ref[NR][2], l[NR][2];        // ref: m - P_SHIFT, 0 before the first key
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       m[nr][0] = m[nr][1] = -INFINITY;
+      ref[nr][0] = ref[nr][1] = 0.f;
       l[nr][0] = l[nr][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < S::MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
@@ -238,9 +276,6 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
       issue();                         // into the stage that the step before this one has read
       const int key0 = k * S::UNIT + warp * S::KS;
       const uint8_t* kb = ring_ptr + stage * S::STAGE;
-      const uint8_t* vb = kb + S::OFF_V;
-      const uint8_t* kscale = kb + S::OFF_SC;
-      const uint8_t* vscale = kscale + S::KS * S::SB;
       stage = stage + 1 == NST ? 0 : stage + 1;
       if (key0 >= len) continue;
 
@@ -251,15 +286,15 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
         uint32_t w[2][S::KW], f[2][S::VW];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int row = 16 * p + 8 * h + g;
+          const int row = 16 * p + 8 * h;
           if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kb + code_at<D>(row, t));
+            const uint4 x = *reinterpret_cast<const uint4*>(kb + at_k + row * S::KB);
             w[h][0] = x.x; w[h][1] = x.y; w[h][S::KW - 2] = x.z; w[h][S::KW - 1] = x.w;
-            key_scales<D>(*reinterpret_cast<const uint16_t*>(kscale + row * S::SB + 2 * t), f[h]);
+            key_scales<D>(*reinterpret_cast<const uint16_t*>(kb + at_ks + row * S::SB), f[h]);
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(kb + code_at<D>(row, t >> 1) + 8 * (t & 1));
+            const uint2 x = *reinterpret_cast<const uint2*>(kb + at_k + row * S::KB);
             w[h][0] = x.x; w[h][1] = x.y;
-            key_scales<D>(kscale[row * S::SB + t], f[h]);
+            key_scales<D>(kb[at_ks + row * S::SB], f[h]);
           }
         }
         scores_of<D, NR>(w, f, qr.qf, sc[p]);
@@ -269,10 +304,6 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
       float top[NR][2];
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-        for (int p = 0; p < S::GROUPS; ++p)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[p][nr][e] *= qr.qs[nr][e & 1];
         if (edge) {
 #pragma unroll
           for (int p = 0; p < S::GROUPS; ++p)
@@ -285,8 +316,8 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
           float x = fmaxf(sc[0][nr][e], sc[0][nr][2 + e]);
 #pragma unroll
           for (int p = 1; p < S::GROUPS; ++p) x = fmaxf(x, fmaxf(sc[p][nr][e], sc[p][nr][2 + e]));
-          top[nr][e] = x;
-          move = move || x > m[nr][e] + P_SLACK || (m[nr][e] == -INFINITY && x > -INFINITY);
+          top[nr][e] = x * qr.qs[nr][e];
+          move = move || top[nr][e] > m[nr][e] + P_SLACK;   // a first score is larger than -inf
         }
       }
       if (__any_sync(0xffffffffu, move)) {
@@ -302,6 +333,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
             const float mn = fmaxf(m[nr][e], x);
             const float al = mn == -INFINITY ? 1.f : ex2f(m[nr][e] - mn);
             m[nr][e] = mn;
+            ref[nr][e] = mn == -INFINITY ? 0.f : mn - P_SHIFT;
             l[nr][e] *= al;
 #pragma unroll
             for (int d = 0; d < S::MT; ++d) {
@@ -318,8 +350,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
           float pr[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float mr = m[nr][e & 1];
-            pr[e] = ex2f(sc[p][nr][e] - (mr == -INFINITY ? 0.f : mr - P_SHIFT));
+            pr[e] = ex2f(fmaf(sc[p][nr][e], qr.qs[nr][e & 1], -ref[nr][e & 1]));
             l[nr][e & 1] += pr[e];
           }
           b[nr][0] = transposed(pack_f16(pr[0], pr[1]));
@@ -329,15 +360,15 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
         uint32_t w[4][S::VW], vs[4];
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
-          const int row = 16 * p + 2 * t + (k4 & 1) + 8 * (k4 >> 1);
+          const int row = 16 * p + 8 * (k4 >> 1);
+          const uint8_t* from = kb + ((k4 & 1) ? at_v1 : at_v) + row * S::KB;
           if (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(vb + code_at<D>(row, g >> 1) + 8 * (g & 1));
+            const uint2 x = *reinterpret_cast<const uint2*>(from);
             w[k4][0] = x.x; w[k4][S::VW - 1] = x.y;
-            vs[k4] = vscale[row * S::SB + g];
           } else {
-            w[k4][0] = *reinterpret_cast<const uint32_t*>(vb + code_at<D>(row, g >> 2) + 4 * (g & 3));
-            vs[k4] = vscale[row * S::SB + (g >> 1)];
+            w[k4][0] = *reinterpret_cast<const uint32_t*>(from);
           }
+          vs[k4] = kb[at_vs + (row + (k4 & 1)) * S::SB];
         }
         // A block that reads as NaN reaches only rows that see its key: a product with a masked
         // probability of 0 would spread it. Rows can differ in what they see only at the causal edge.
@@ -433,12 +464,13 @@ struct MassShape {
   static constexpr int KS = 32;                // keys a warp takes in a step
   static constexpr int GROUPS = KS / 16;
   static constexpr int UNIT = WARPS * KS;
+  static constexpr int CTAS = D == 64 ? 4 : NR == 1 ? 3 : 2;   // of a SM, by their registers
 };
 
 // The weights' second pass over the keys, once lse is known. Items are (sequence, head); every key of
 // an item belongs to one lane, which sums over all query rows: no atomics, so the order is fixed.
 template <int D, int NR>
-__global__ void __launch_bounds__(THREADS, 4) k_mass_kv4(Kv4View c, Args a, MassArgs w, int* err_flag) {
+__global__ void __launch_bounds__(THREADS, (MassShape<D, NR>::CTAS)) k_mass_kv4(Kv4View c, Args a, MassArgs w, int* err_flag) {
   using S = MassShape<D, NR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rows = a.q_tokens * a.group, tiles = (rows + S::ROWS - 1) / S::ROWS;
@@ -457,53 +489,82 @@ __global__ void __launch_bounds__(THREADS, 4) k_mass_kv4(Kv4View c, Args a, Mass
     const long long at = ((long long)sg.s * c.heads + head) * reach;
     Queries<D, NR> qr;
     float norm[NR][2];                         // lse in base 2 of rows 2t, 2t + 1
+    bool full = false;                         // no row of the tile lies behind the last
     auto load_rows = [&](int r0) {
       qr.load(a, sg.s, head, r0, rows, len);
+      scale_queries(qr, unit);
+      full = r0 + S::ROWS <= rows;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = r0 + 8 * nr + 2 * t + e;
-          qr.qs[nr][e] *= unit;
           norm[nr][e] = r < rows ? a.lse[row_at(a, sg.s, head, r)] * 1.4426950408889634f : 0.f;
           if (r >= rows) qr.lim[nr][e] = 0;    // no weight
         }
     };
     if (tiles == 1) load_rows(0);
-    for (int k = sg.k0; k < sg.k1; ++k) {
-      const int key0 = k * S::UNIT + warp * S::KS;
-      if (key0 >= len) continue;
-      uint32_t kw[S::GROUPS][2][D / 32], sc[S::GROUPS][2][D / 64];
+    // codes and scales of the step ahead, pages of the one behind it
+    uint32_t kn[S::GROUPS][2][D / 32], sn[S::GROUPS][2];
+    int pg[S::GROUPS];
+    auto fetch_pages = [&](int k) {
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
-        const int key = key0 + 16 * p;
-        const int pg = key < len ? __ldg(pages + (key >> c.page_log2)) : -1;
-        const bool there = (uint32_t)pg < (uint32_t)c.num_pages;
-        if (!there && key < len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
-        const uint64_t row = (((uint64_t)((there ? (uint32_t)pg : 0u) * (uint32_t)c.heads + (uint32_t)head)) << c.page_log2) +
-                             ((uint32_t)key & (uint32_t)(c.page - 1));
+        const int key = k * S::UNIT + warp * S::KS + 16 * p;
+        pg[p] = k < sg.k1 && key < len ? __ldg(pages + (key >> c.page_log2)) : -1;
+      }
+    };
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p) {
+        const int key = k * S::UNIT + warp * S::KS + 16 * p;
+        const bool there = (uint32_t)pg[p] < (uint32_t)c.num_pages;
+        if (!there && k < sg.k1 && key < len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+        const uint64_t row = (((uint64_t)((there ? (uint32_t)pg[p] : 0u) * (uint32_t)c.heads + (uint32_t)head)) << c.page_log2) +
+                             ((uint32_t)key & (uint32_t)(c.page - 1)) + g;
+        const uint8_t *codes = c.k + row * (D / 2) + t * (D / 8), *scales = c.k_scale + row * (D / 16) + t * (D / 64);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const bool on = there && key + 8 * h + g < len;
-          const uint64_t r = row + 8 * h + g;
-          uint32_t bytes = 0;
+          sn[p][h] = 0;
           if (D == 128) {
-            const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(c.k + r * 64) + t) : make_uint4(0, 0, 0, 0);
-            kw[p][h][0] = x.x; kw[p][h][1] = x.y; kw[p][h][D / 32 - 2] = x.z; kw[p][h][D / 32 - 1] = x.w;
-            if (on) bytes = __ldg(reinterpret_cast<const uint16_t*>(c.k_scale + r * 8) + t);
+            const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(codes + 8 * h * (D / 2))) : make_uint4(0, 0, 0, 0);
+            kn[p][h][0] = x.x; kn[p][h][1] = x.y; kn[p][h][D / 32 - 2] = x.z; kn[p][h][D / 32 - 1] = x.w;
+            if (on) sn[p][h] = __ldg(reinterpret_cast<const uint16_t*>(scales + 8 * h * (D / 16)));
           } else {
-            const uint2 x = on ? __ldg(reinterpret_cast<const uint2*>(c.k + r * 32) + t) : make_uint2(0, 0);
-            kw[p][h][0] = x.x; kw[p][h][1] = x.y;
-            if (on) bytes = __ldg(c.k_scale + r * 4 + t);
+            const uint2 x = on ? __ldg(reinterpret_cast<const uint2*>(codes + 8 * h * (D / 2))) : make_uint2(0, 0);
+            kn[p][h][0] = x.x; kn[p][h][1] = x.y;
+            if (on) sn[p][h] = __ldg(scales + 8 * h * (D / 16));
           }
-          key_scales<D>(bytes, sc[p][h]);
         }
       }
+    };
+    fetch_pages(sg.k0);
+    fetch(sg.k0);
+    fetch_pages(sg.k0 + 1);
+    for (int k = sg.k0; k < sg.k1; ++k) {
+      const int key0 = k * S::UNIT + warp * S::KS;
+      if (key0 >= len) break;                  // the sequence's last unit
+      uint32_t kw[S::GROUPS][2][D / 32], sc[S::GROUPS][2][D / 64];
+      float old[S::GROUPS][2];
+#pragma unroll
+      for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) kw[p][h][i] = kn[p][h][i];
+          key_scales<D>(sn[p][h], sc[p][h]);
+          const int key = key0 + 16 * p + 8 * h + g;
+          old[p][h] = w.mass && t == 0 && key < len ? w.mass[at + key] : 0.f;
+        }
+      fetch(k + 1);
+      fetch_pages(k + 2);
       float sum[S::GROUPS][2];
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) sum[p][0] = sum[p][1] = 0.f;
       for (int tile = 0; tile < tiles; ++tile) {
         if (tiles > 1) load_rows(tile * S::ROWS);
+        const bool inside = full && key0 + S::KS <= qr.lim_min;   // every row sees every key (warp-uniform)
 #pragma unroll
         for (int p = 0; p < S::GROUPS; ++p) {
           float s[NR][4];
@@ -513,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_mass_kv4(Kv4View c, Args a, Mass
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = ex2f(fmaf(s[nr][e], qr.qs[nr][e & 1], -norm[nr][e & 1]));
-              if (key0 + 16 * p + 8 * (e >> 1) + g < qr.lim[nr][e & 1]) sum[p][e >> 1] += x;
+              if (inside || key0 + 16 * p + 8 * (e >> 1) + g < qr.lim[nr][e & 1]) sum[p][e >> 1] += x;
             }
         }
       }
@@ -525,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_mass_kv4(Kv4View c, Args a, Mass
           x += __shfl_xor_sync(0xffffffffu, x, 1);
           x += __shfl_xor_sync(0xffffffffu, x, 2);
           const int key = key0 + 16 * p + 8 * h + g;
-          if (t == 0 && key < len) w.out[at + key] = w.mass ? fmaf(w.decay, w.mass[at + key], x) : x;
+          if (t == 0 && key < len) w.out[at + key] = w.mass ? fmaf(w.decay, old[p][h], x) : x;
         }
     }
   }
@@ -538,7 +599,7 @@ cudaError_t launch_mass(const Kv4View& c, Args a, const MassArgs& w, int* err_fl
   a.tiles = 1;                                 // an item holds all rows of its head
   const long long max_len = (long long)c.max_pages << c.page_log2;
   const long long max_units = (max_len + S::UNIT - 1) / S::UNIT;
-  const long long slots = (long long)num_sms * 4, items = (long long)c.batch * c.heads;
+  const long long slots = (long long)num_sms * S::CTAS, items = (long long)c.batch * c.heads;
   const long long work = max_units > slots ? slots : items * max_units;
   k_mass_kv4<D, NR><<<(unsigned)(work < slots ? work : slots), THREADS, 0, s>>>(c, a, w, err_flag);
   return cudaGetLastError();

@@ -3,9 +3,8 @@
 // the read-back to bf16.
 //
 // Bound by bytes on long appends (2 (q_heads + 2 kv_heads) dim read, 2 q_heads dim + 9/8 kv_heads dim
-// written a token) and by latency on short ones. No token's codes depend on another token, so one
-// kernel serves all lengths: a warp takes a token and up to eight heads of its queries, keys or
-// values, which share the angles.
+// written a token) and by latency on short ones. No token's codes depend on another token: a warp
+// takes a token and up to eight heads of its queries, keys or values, which share the angles.
 //
 // A code is the nearest e2m1 value to x / (scale * unit), and neighbours are a third apart, so what
 // decides between them is computed as the definition has it: the norm's factor is correctly rounded (sum of
@@ -18,7 +17,13 @@ namespace jepa {
 
 namespace {
 
-constexpr int HEADS = 8;   // heads of a token that a warp takes
+constexpr int HEADS = 8;           // heads of a token that a warp takes
+constexpr int ONE_LAUNCH = 7296;   // warps: twice what 152 SMs hold at once
+
+typedef unsigned long long pair;   // two fp32 numbers (the packed operations of common.cuh)
+
+__device__ __forceinline__ pair f2_sub(pair a, pair b) { return f2_fma(b, f2_pack(-1.f, -1.f), a); }
+__device__ __forceinline__ pair f2_both(float x) { return f2_pack(x, x); }
 
 __device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
   const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
@@ -28,12 +33,20 @@ __device__ __forceinline__ void two_sum(float& hi, float& lo, float x) {
 
 // 1 / sqrt(sum / D + eps), correctly rounded but for ties of 2^-40: the sum of squares, which are
 // exact in fp32, over the lanes of a head in two floats, and one Newton step whose remainder is exact.
+// y: a lane's elements in pairs.
 template <int D>
-__device__ __forceinline__ float norm_factor(const float (&y)[16], float eps) {
+__device__ __forceinline__ float norm_factor(const pair (&y)[8], float eps) {
   constexpr int L = D / 16;
-  float hi = 0.f, lo = 0.f;
+  pair hi2 = f2_mul(y[0], y[0]), lo2 = f2_both(0.f);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) two_sum(hi, lo, __fmul_rn(y[i], y[i]));
+  for (int i = 1; i < 8; ++i) {
+    const pair x = f2_mul(y[i], y[i]), s = f2_add(hi2, x), b = f2_sub(s, hi2);
+    lo2 = f2_add(lo2, f2_add(f2_sub(hi2, f2_sub(s, b)), f2_sub(x, b)));
+    hi2 = s;
+  }
+  const float2 h2 = f2_unpack(hi2), l2 = f2_unpack(lo2);
+  float hi = h2.x, lo = __fadd_rn(l2.x, l2.y);
+  two_sum(hi, lo, h2.y);
 #pragma unroll
   for (int o = L / 2; o; o >>= 1) {
     const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
@@ -56,45 +69,58 @@ __device__ __forceinline__ float norm_factor(const float (&y)[16], float eps) {
   return __fmaf_rn(0.5f * r, e, r);
 }
 
-// y = x * (r * w), then (a, b) -> (a cos - b sin, b cos + a sin), each product and sum rounded.
+// y = x * (r * w), then (a, b) -> (a cos - b sin, b cos + a sin), each product and sum rounded. A lane's
+// elements in pairs (2 i, 2 i + 1) of its two chunks.
 template <int D, bool INTER>
-__device__ __forceinline__ void norm_rotate_exact(float (&y)[16], const Lane<D, INTER>& ln,
+__device__ __forceinline__ void norm_rotate_exact(pair (&y)[8], const Lane<D, INTER>& ln,
                                                   const float* __restrict__ w, float eps,
                                                   const float (&an)[16]) {
   if (w) {
-    const float r = norm_factor<D>(y, eps);
+    const pair r = f2_both(norm_factor<D>(y, eps));
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 g =
-          __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 8 ? ln.c0 : ln.c1) + (i & 7)));
-      y[i] *= r * g.x; y[i + 1] *= r * g.y; y[i + 2] *= r * g.z; y[i + 3] *= r * g.w;
+    for (int i = 0; i < 8; i += 2) {
+      const float4 g = __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 4 ? ln.c0 : ln.c1) + 2 * (i & 3)));
+      y[i] = f2_mul(y[i], f2_mul(r, f2_pack(g.x, g.y)));
+      y[i + 1] = f2_mul(y[i + 1], f2_mul(r, f2_pack(g.z, g.w)));
     }
   }
   if (ln.rotates) {
+    if (INTER) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : 8 + i;
-      const float p = y[ia], q = y[ib];
-      y[ia] = __fsub_rn(__fmul_rn(p, an[i]), __fmul_rn(q, an[8 + i]));
-      y[ib] = __fadd_rn(__fmul_rn(q, an[i]), __fmul_rn(p, an[8 + i]));
+      for (int i = 0; i < 8; ++i) {
+        const float2 p = f2_unpack(y[i]);
+        y[i] = f2_pack(__fsub_rn(__fmul_rn(p.x, an[i]), __fmul_rn(p.y, an[8 + i])),
+                       __fadd_rn(__fmul_rn(p.y, an[i]), __fmul_rn(p.x, an[8 + i])));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const pair c = f2_pack(an[2 * i], an[2 * i + 1]), sn = f2_pack(an[8 + 2 * i], an[9 + 2 * i]);
+        const pair p = y[i], q = y[4 + i];
+        y[i] = f2_sub(f2_mul(p, c), f2_mul(q, sn));
+        y[4 + i] = f2_add(f2_mul(q, c), f2_mul(p, sn));
+      }
     }
   }
 }
 
 // Largest magnitude of 8 elements as bits: above those of infinity where there is a NaN.
-__device__ __forceinline__ uint32_t top_bits(const float (&y)[16], int from) {
+__device__ __forceinline__ uint32_t top_bits(const pair (&y)[8], int from) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[from + i]) & 0x7fffffffu);
+  for (int i = 0; i < 4; ++i) {
+    const pair x = y[from + i];
+    m = max(m, max((uint32_t)x & 0x7fffffffu, (uint32_t)(x >> 32) & 0x7fffffffu));
+  }
   return m;
 }
 
 // The largest magnitudes of the two blocks of 16 that a lane's chunks of 8 lie in. All lanes of the
 // warp call it.
 template <int D, bool INTER>
-__device__ __forceinline__ void block_tops(const float (&y)[16], const Lane<D, INTER>& ln, int rot,
+__device__ __forceinline__ void block_tops(const pair (&y)[8], const Lane<D, INTER>& ln, int rot,
                                            uint32_t (&top)[2]) {
-  const uint32_t a = top_bits(y, 0), b = top_bits(y, 8);
+  const uint32_t a = top_bits(y, 0), b = top_bits(y, 4);
   top[0] = top[1] = max(a, b);              // neighbours: one block
   if (INTER) return;
   constexpr int L = D / 16;
@@ -119,13 +145,16 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t top, float inv_unit) {
 }
 
 // Codes of 8 elements, the first in the lowest bits.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[16], int from, float scale) {
-  const float inv = __fdiv_rn(1.f, scale);
+__device__ __forceinline__ uint32_t e2m1x8(const pair (&y)[8], int from, float scale) {
+  const float inv1 = __fdiv_rn(1.f, scale);
+  const pair inv = f2_both(inv1), neg = f2_both(-scale);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = y[from + i], z = __fmul_rn(x, inv);
-    q[i] = __fmaf_rn(__fmaf_rn(-z, scale, x), inv, z);          // the quotient, correctly rounded
+  for (int i = 0; i < 4; ++i) {
+    const pair x = y[from + i], z = f2_mul(x, inv);
+    const float2 f = f2_unpack(f2_fma(f2_fma(z, neg, x), inv, z));   // the quotients, correctly rounded
+    q[2 * i] = f.x;
+    q[2 * i + 1] = f.y;
   }
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -140,7 +169,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&y)[16], int from, float
 // A lane's 16 elements into the cache: `at` counts tokens of all (page, head) blocks.
 template <int D, bool INTER>
 __device__ __forceinline__ void quantise_store(uint8_t* codes, uint8_t* scales, long long at, bool on,
-                                               const float (&y)[16], const Lane<D, INTER>& ln,
+                                               const pair (&y)[8], const Lane<D, INTER>& ln,
                                                int rot, float unit) {
   uint32_t top[2];
   block_tops<D, INTER>(y, ln, rot, top);
@@ -153,79 +182,95 @@ __device__ __forceinline__ void quantise_store(uint8_t* codes, uint8_t* scales, 
     const uint32_t f = f16x2_of_e4m3_pair(sc);
     const float scale = __half2float(__ushort_as_half((unsigned short)(f & 0xffffu))) * unit;
     *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + 4 * chunk) =
-        sc == 0x7f ? 0u : e2m1x8(y, 8 * h, scale);
+        sc == 0x7f ? 0u : e2m1x8(y, 4 * h, scale);
     if (!(chunk & 1)) scales[at * (D / 16) + (chunk >> 1)] = (uint8_t)sc;
   }
 }
 
-// Unit `unit` of the call: token t, a group of HEADS of its query heads, then of keys, then of values.
+// A warp takes one token and up to HEADS heads of its keys or of its values.
 template <int D, bool INTER>
-__device__ __forceinline__ void append_unit(const Kv4View& c, const AppendArgs& a, long long unit,
-                                            int q_blocks, int kv_blocks, int* err_flag) {
+__device__ __forceinline__ void append_heads(const Kv4View& c, const AppendArgs& a, long long unit, int* err_flag) {
   constexpr int L = D / 16, ROWS = 32 / L, PASSES = HEADS / ROWS;
-  const int per = q_blocks + 2 * kv_blocks;
-  const long long token = unit / per;
+  const int blocks = (c.heads + HEADS - 1) / HEADS;
+  const long long token = unit / (2 * blocks);
   if (token >= a.tokens) return;
-  const int t = (int)token;
-  int block = (int)(unit - token * per);
-  // 0 queries, 1 keys, 2 values
-  const int kind = block < q_blocks ? 0 : block < q_blocks + kv_blocks ? 1 : 2;
-  block -= kind == 0 ? 0 : kind == 1 ? q_blocks : q_blocks + kv_blocks;
-  const int h0 = block * HEADS, heads = kind == 0 ? a.q_heads : c.heads;
+  const int t = (int)token, block = (int)(unit - token * (2 * blocks));
+  const bool is_v = block >= blocks;
+  const int h0 = (is_v ? block - blocks : block) * HEADS;
   const int lane = threadIdx.x & 31, sub = lane / L;
   const Lane<D, INTER> ln(a.rot);
-  const bf16* src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
+  const bf16* src = is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride;
   uint4 raw[PASSES][2];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int h = h0 + p * ROWS + sub;
     raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
-    if (h < heads) load16(src + (long long)h * D, ln, raw[p]);
+    if (h < c.heads) load16(src + (long long)h * D, ln, raw[p]);
   }
   const Place at = locate(a.cu, a.start, c.batch, t);
   if (!holds(at, t, a.tokens)) return;            // left as it is
   const int pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
-  bool there = at.first >= 0 && pos >= 0 && pos < positions_of(c, a);
-  int page = 0;
-  if (kind && there) {
-    page = kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, at.s, pos);
-    there = page >= 0;
-  }
-  if (!there) {
+  const int page = at.first >= 0 && pos >= 0 && pos < positions_of(c, a)
+                       ? kv8_page_at(c.table, c.max_pages, c.num_pages, c.page_log2, at.s, pos)
+                       : -1;
+  if (page < 0) {
     if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
   }
   float an[16];
-  if (kind < 2 && ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
+  if (!is_v && ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int h = h0 + p * ROWS + sub;
-    const bool on = h < heads;
-    float y[16];
-    widen(raw[p], y);
-    if (kind < 2) norm_rotate_exact<D, INTER>(y, ln, kind ? a.k_norm : a.q_norm, a.eps, an);
-    if (kind == 0) {
-      if (on) store16(a.q_out + ((long long)t * heads + h) * D, ln, y);
-      continue;
+    const bool on = h < c.heads;
+    pair y[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t w[4] = {raw[p][q].x, raw[p][q].y, raw[p][q].z, raw[p][q].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[4 * q + i] = (pair)(w[i] << 16) | ((pair)(w[i] & 0xffff0000u) << 32);
     }
-    const long long row = (((long long)page * heads + (on ? h : 0)) << c.page_log2) + (pos & (c.page - 1));
-    const float unit_of = kv4_unit(kind == 1 ? c.k_unit : c.v_unit, on ? h : 0);
-    quantise_store<D, INTER>(kind == 1 ? c.k : c.v, kind == 1 ? c.k_scale : c.v_scale, row, on, y, ln, a.rot, unit_of);
-    if (kind == 1 && a.k_out && on) store16(a.k_out + ((long long)t * heads + h) * D, ln, y);
+    if (!is_v) norm_rotate_exact<D, INTER>(y, ln, a.k_norm, a.eps, an);
+    const long long row = (((long long)page * c.heads + (on ? h : 0)) << c.page_log2) + (pos & (c.page - 1));
+    const float unit_of = kv4_unit(is_v ? c.v_unit : c.k_unit, on ? h : 0);
+    quantise_store<D, INTER>(is_v ? c.v : c.k, is_v ? c.v_scale : c.k_scale, row, on, y, ln, a.rot, unit_of);
+    if (!is_v && a.k_out && on) {
+      float z[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = f2_unpack(y[i]);
+        z[2 * i] = f.x;
+        z[2 * i + 1] = f.y;
+      }
+      store16(a.k_out + ((long long)t * c.heads + h) * D, ln, z);
+    }
   }
 }
 
+// Few tokens: key / value warps, then query warps, in one grid.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(THREADS, 3) k_append_kv4(Kv4View c, AppendArgs a, int q_blocks,
-                                                           int kv_blocks, int* err_flag) {
+__global__ void __launch_bounds__(THREADS, 3) k_append_kv4(Kv4View c, AppendArgs a, long long kv_units, int* err_flag) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  append_unit<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), q_blocks,
-                        kv_blocks, err_flag);
+  const long long unit = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
+  if (unit < kv_units)
+    append_heads<D, INTER>(c, a, unit, err_flag);
+  else if (a.q)
+    rotate_queries<D, INTER>(c, a, unit - kv_units, err_flag);
   report_offsets(a.cu, c.batch, a.tokens, err_flag);
 }
 
+// Keys and values beside the last blocks of the queries' kernel, with which they share no data; the
+// wait at the end keeps the order for what comes next.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(THREADS, 3) k_append_heads(Kv4View c, AppendArgs a, int* err_flag) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  append_heads<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
+  report_offsets(a.cu, c.batch, a.tokens, err_flag);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Cached tokens back as bf16 (code * scale has at most six significant bits: exact). A warp per
-// packed token; a lane moves a block of 16 elements at a time.
+// packed token; a lane moves 8 elements at a time, so that a warp's stores are whole lines.
 template <int D>
 __device__ __forceinline__ void read_token(const Kv4View& c, const int* __restrict__ cu,
                                            const int* __restrict__ first, int tokens,
@@ -243,46 +288,39 @@ __device__ __forceinline__ void read_token(const Kv4View& c, const int* __restri
     if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
   }
-  const int off = pos & (c.page - 1), blocks = c.heads * (D / 16);
-  constexpr int AHEAD = 4;                 // loads a lane has in flight
-  for (int i0 = lane; i0 < 2 * blocks; i0 += 32 * AHEAD) {
-    uint2 u[AHEAD];
-    uint32_t scale[AHEAD];
+  const int off = pos & (c.page - 1), chunks = c.heads * (D / 8);
+  constexpr int AHEAD = 8;                 // loads a lane has in flight
+  for (int i0 = lane; i0 < 2 * chunks; i0 += 32 * AHEAD) {
+    uint32_t u[AHEAD], scale[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const int i = i0 + 32 * k;
-      if (i >= 2 * blocks) break;
-      const bool is_v = i >= blocks;
-      const int j = is_v ? i - blocks : i, head = j / (D / 16), b = j % (D / 16);
+      if (i >= 2 * chunks) break;
+      const bool is_v = i >= chunks;
+      const int j = is_v ? i - chunks : i, head = j / (D / 8), b = j % (D / 8);
       const long long row = (((long long)pg * c.heads + head) << c.page_log2) + off;
-      u[k] = *reinterpret_cast<const uint2*>((is_v ? c.v : c.k) + row * (D / 2) + 8 * b);
-      scale[k] = (is_v ? c.v_scale : c.k_scale)[row * (D / 16) + b];
+      u[k] = *reinterpret_cast<const uint32_t*>((is_v ? c.v : c.k) + row * (D / 2) + 4 * b);
+      scale[k] = (is_v ? c.v_scale : c.k_scale)[row * (D / 16) + (b >> 1)];
     }
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const int i = i0 + 32 * k;
-      if (i >= 2 * blocks) break;
-      const bool is_v = i >= blocks;
-      const int j = is_v ? i - blocks : i;
-      const float unit = kv4_unit(is_v ? c.v_unit : c.k_unit, j / (D / 16));
+      if (i >= 2 * chunks) break;
+      const bool is_v = i >= chunks;
+      const int j = is_v ? i - chunks : i;
+      const float unit = kv4_unit(is_v ? c.v_unit : c.k_unit, j / (D / 8));
       const uint32_t sc = f16x2_of_e4m3_pair(scale[k] * 0x101u);
-      float z[2][8];
+      const uint32_t x[4] = {f16x2_of_e2m1x2<0>(u[k]), f16x2_of_e2m1x2<1>(u[k]), f16x2_of_e2m1x2<2>(u[k]),
+                             f16x2_of_e2m1x2<3>(u[k])};
+      float z[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w = h ? u[k].y : u[k].x;
-        const uint32_t x[4] = {f16x2_of_e2m1x2<0>(w), f16x2_of_e2m1x2<1>(w), f16x2_of_e2m1x2<2>(w),
-                               f16x2_of_e2m1x2<3>(w)};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[q]), *reinterpret_cast<const __half2*>(&sc));
-          const float2 f = __half22float2(y);
-          z[h][2 * q] = f.x * unit;
-          z[h][2 * q + 1] = f.y * unit;
-        }
+      for (int q = 0; q < 4; ++q) {
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[q]), *reinterpret_cast<const __half2*>(&sc));
+        const float2 f = __half22float2(y);
+        z[2 * q] = f.x * unit;
+        z[2 * q + 1] = f.y * unit;
       }
-      bf16* to = (is_v ? v_out : k_out) + (t * c.heads * (D / 16) + j) * 16;
-      store8(to, z[0]);
-      store8(to + 8, z[1]);
+      store8((is_v ? v_out : k_out) + (t * chunks + j) * 8, z);
     }
   }
 }
@@ -298,10 +336,19 @@ __global__ void __launch_bounds__(THREADS, 5)
 
 template <int D, bool INTER>
 cudaError_t launch_append(const Kv4View& c, const AppendArgs& a, int* err_flag, cudaStream_t s) {
-  const int q_blocks = a.q ? (a.q_heads + HEADS - 1) / HEADS : 0, kv_blocks = (c.heads + HEADS - 1) / HEADS;
-  const long long blocks = blocks_for(32LL * a.tokens * (q_blocks + 2 * kv_blocks), c.batch);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_early(k_append_kv4<D, INTER>, (unsigned)blocks, true, s, c, a, q_blocks, kv_blocks, err_flag);
+  const long long q_units = a.q ? (long long)a.tokens * ((a.q_heads + Q_HEADS - 1) / Q_HEADS) : 0;
+  const long long kv_units = 2LL * a.tokens * ((c.heads + HEADS - 1) / HEADS);
+  // one launch where it holds all the warps at once; above that the queries' kernel, which needs fewer
+  // registers, goes by itself
+  const bool one = kv_units + q_units <= ONE_LAUNCH || !q_units;
+  const long long blocks = blocks_for(32 * (kv_units + (one ? q_units : 0)), c.batch);
+  const long long q_blocks = (q_units + THREADS / 32 - 1) / (THREADS / 32);
+  if (blocks > 0x7fffffffLL || q_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (one) return launch_early(k_append_kv4<D, INTER>, (unsigned)blocks, true, s, c, a, kv_units, err_flag);
+  k_rope_queries<D, INTER><<<(unsigned)q_blocks, THREADS, 0, s>>>(c, a, err_flag);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_early(k_append_heads<D, INTER>, (unsigned)blocks, true, s, c, a, err_flag);
 }
 
 }  // namespace

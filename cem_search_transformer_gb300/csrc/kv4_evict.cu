@@ -24,6 +24,7 @@ namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 256;
+constexpr int MAX_CLUSTER = 8;           // the portable size
 
 // Weights as integers in the same order: NaN the least, -0 as 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -50,36 +51,23 @@ __device__ __forceinline__ int cached_length(const PageView& c, const int* kv_le
   return n;
 }
 
-// Sum over the CTA of two counts packed in 64 bits, and what lies ahead of this thread.
-__device__ __forceinline__ unsigned long long scan(unsigned long long x, unsigned long long* sm,
-                                                   unsigned long long& before) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned long long incl = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();                       // the last scan's sums have been read
-  if (lane == 31) sm[warp] = incl;
-  __syncthreads();
-  unsigned long long ahead = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) ahead += sm[w];
-    total += sm[w];
-  }
-  before = ahead + incl - x;
-  return total;
+__device__ __forceinline__ float unordered(uint32_t u) {
+  if (u == 0) return __int_as_float(0x7fc00000);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 
+constexpr int HELD = 11008;              // weights of a CTA's piece that stay in shared memory (43 KB)
+
 __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a, int out_reach, int* err_flag) {
+  __shared__ uint32_t held[HELD];
   __shared__ int hist[2][BINS];
   __shared__ int counts_all[BINS];       // of the whole cluster
-  __shared__ unsigned long long sums[WARPS], piece_counts;
+  __shared__ uint2 warp_counts[WARPS], piece_counts;   // above the border, equal to it
   __shared__ int found[2];               // bin, tokens above it
+  asm volatile("griddepcontrol.launch_dependents;");   // k_evict_move may be set up meanwhile
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x / size, s = item / c.heads, head = item - s * c.heads;
   const int n = cached_length(c, a.kv_len, s, head == 0 && rank == 0 && threadIdx.x == 0 ? err_flag : nullptr);
   const int kept = min(n, a.keep);
@@ -103,30 +91,61 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     if (mass_out) mass_out[want + i] = mass[old + i];
   }
   if (want == 0) return;
-  const int each = (old + size - 1) / size;
-  const int begin = min(old, rank * each), end = min(old, begin + each);
+  // a warp's piece of the tokens: its lanes take every 32nd, as integers in the order of the weights
+  const int pieces = size * WARPS, each = ((old + pieces - 1) / pieces + 31) & ~31;
+  const int begin = min((long long)old, (long long)(rank * WARPS + warp) * each), end = min(old, begin + each);
+  const int first = warp * each;         // of its piece among the CTA's
+  auto key = [&](int i) {
+    const int at = first + i - begin;
+    return at < HELD ? held[at] : ordered(__ldg(mass + i));
+  };
+  for (int b = threadIdx.x; b < BINS; b += THREADS) hist[0][b] = 0;
+  __syncthreads();
   // ---- the smallest weight kept: digit by digit from the top ----
-  uint32_t prefix = 0;                   // its digits so far
+  constexpr int AHEAD = 4;
+  for (int i0 = begin; i0 < end; i0 += 32 * AHEAD) {
+    float x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + 32 * k + lane;
+      x[k] = i < end ? __ldg(mass + i) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + 32 * k + lane, at = first + i - begin;
+      const uint32_t u = ordered(x[k]);
+      if (i < end && at < HELD) held[at] = u;
+      // weights share few exponents: one addition for the lanes that have the same
+      const uint32_t bin = i < end ? u >> 24 : BINS;
+      const uint32_t same = __match_any_sync(0xffffffffu, bin);
+      if (bin < BINS && lane == __ffs((int)same) - 1) atomicAdd(&hist[0][bin], __popc(same));
+    }
+  }
+  uint32_t prefix = 0;                   // the border's digits so far
   int need = want;                       // tokens still to be taken from those with this prefix
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     int* const mine = hist[pass & 1];    // the other one may still be read
-    for (int b = threadIdx.x; b < BINS; b += THREADS) mine[b] = 0;
-    __syncthreads();
-    for (int i = begin + threadIdx.x; i < end; i += THREADS) {
-      const uint32_t u = ordered(__ldg(mass + i));
-      if (pass == 0 || (u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(mine + ((u >> shift) & 255), 1);
+    if (pass > 0) {
+      for (int b = threadIdx.x; b < BINS; b += THREADS) mine[b] = 0;
+      __syncthreads();
+      for (int i = begin + lane; i < end; i += 32) {
+        const uint32_t u = key(i);
+        if ((u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(mine + ((u >> shift) & 255), 1);
+      }
     }
     cluster.sync();
     if (threadIdx.x < BINS) {
       int all = 0;
-      for (int r = 0; r < size; ++r) all += cluster.map_shared_rank(mine, r)[threadIdx.x];
+#pragma unroll
+      for (int r = 0; r < MAX_CLUSTER; ++r)          // side by side: a microsecond each
+        if (r < size) all += cluster.map_shared_rank(mine, r)[threadIdx.x];
       counts_all[threadIdx.x] = all;
     }
     __syncthreads();
-    if (threadIdx.x < 32) {              // eight bins a lane, from the top
-      const int lane = threadIdx.x, top = BINS - 1 - 8 * lane;
+    if (warp == 0) {                     // eight bins a lane, from the top
+      const int top = BINS - 1 - 8 * lane;
       int own = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) own += counts_all[top - k];
@@ -153,36 +172,53 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     prefix |= (uint32_t)found[0] << shift;
     need -= found[1];
   }
-  // ---- where the kept ones go: all above the prefix, and the first `need` equal to it ----
-  unsigned long long counts = 0, before;
-  for (int i = begin + threadIdx.x; i < end; i += THREADS) {
-    const uint32_t u = ordered(__ldg(mass + i));
-    counts += u > prefix ? 1ull << 32 : u == prefix ? 1ull : 0ull;
+  // ---- where the kept ones go: all above the border, and the first `need` equal to it ----
+  uint32_t above = 0, equal = 0;
+  for (int i = begin + lane; i < end; i += 32) {
+    const uint32_t u = key(i);
+    above += u > prefix;
+    equal += u == prefix;
   }
-  counts = scan(counts, sums, before);
-  if (threadIdx.x == 0) piece_counts = counts;
-  cluster.sync();
-  unsigned int above = 0, equal = 0;     // of the pieces ahead
-  for (int r = 0; r < rank; ++r) {
-    const unsigned long long x = *cluster.map_shared_rank(&piece_counts, r);
-    above += (unsigned int)(x >> 32);
-    equal += (unsigned int)x;
-  }
-  cluster.sync();                        // every CTA's counts have been read before it ends
-  for (int i0 = begin; i0 < end; i0 += THREADS) {
-    const int i = i0 + threadIdx.x;
-    const float x = i < end ? __ldg(mass + i) : 0.f;
-    const uint32_t u = ordered(x);
-    const bool gt = i < end && u > prefix, eq = i < end && u == prefix;
-    const unsigned long long all = scan(gt ? 1ull << 32 : eq ? 1ull : 0ull, sums, before);
-    const unsigned int g = above + (unsigned int)(before >> 32), e = equal + (unsigned int)before;
-    if (gt || (eq && e < (unsigned int)need)) {
-      const unsigned int to = g + min(e, (unsigned int)need);
-      places[to] = i;
-      if (mass_out) mass_out[to] = x;
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) warp_counts[warp] = make_uint2(above, equal);
+  __syncthreads();
+  above = equal = 0;                     // of the warps ahead
+  uint2 total = make_uint2(0, 0);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const uint2 x = warp_counts[w];
+    if (w < warp) {
+      above += x.x;
+      equal += x.y;
     }
-    above += (unsigned int)(all >> 32);
-    equal += (unsigned int)all;
+    total.x += x.x;
+    total.y += x.y;
+  }
+  if (threadIdx.x == 0) piece_counts = total;
+  cluster.sync();
+#pragma unroll
+  for (int r = 0; r < MAX_CLUSTER; ++r)
+    if (r < rank) {
+      const uint2 x = *cluster.map_shared_rank(&piece_counts, r);
+      above += x.x;
+      equal += x.y;
+    }
+  cluster.sync();                        // every CTA's counts have been read before it ends
+  const uint32_t below = (1u << lane) - 1, last = (uint32_t)need;
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t u = i < end ? key(i) : 0u;
+    const bool gt = i < end && u > prefix, eq = i < end && u == prefix;
+    const uint32_t gts = __ballot_sync(0xffffffffu, gt), eqs = __ballot_sync(0xffffffffu, eq);
+    const uint32_t e = equal + __popc(eqs & below);
+    if (gt || (eq && e < last)) {
+      const uint32_t to = above + __popc(gts & below) + min(e, last);
+      places[to] = i;
+      if (mass_out) mass_out[to] = unordered(u);
+    }
+    above += __popc(gts);
+    equal += __popc(eqs);
   }
 }
 
@@ -192,6 +228,7 @@ __global__ void __launch_bounds__(256) k_evict_move(Kv4View c, Kv4View to, const
                                                     const int* places, int* err_flag) {
   constexpr int LPT = D / 16, RPW = 32 / LPT, AHEAD = 4;   // lanes a token, half of them K's, half V's
   constexpr int KB = D / 2, SB = D / 16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the places are there
   const int s = blockIdx.z, head = blockIdx.y, lane = threadIdx.x & 31;
   const int n = min(cached_length(c, kv_len, s, nullptr), keep);
   const int first = (blockIdx.x * (256 / 32) + (threadIdx.x >> 5)) * (RPW * AHEAD) + lane / LPT;
@@ -254,27 +291,27 @@ cudaError_t kv4_evict(const Kv4View& c, const int* kv_len, const float* mass, in
   // CTAs a (sequence, head): pieces of a few thousand tokens, up to the portable cluster size
   const long long reach = (long long)c.max_pages << c.page_log2;
   int size = 1;
-  while (size < 8 && reach > 2048LL * size && items * size < 2LL * num_sms) size *= 2;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = size;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  while (size < MAX_CLUSTER && reach > 2048LL * size && items * size < 2LL * num_sms) size *= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * size));
   cfg.blockDim = dim3(THREADS);
   cfg.stream = s;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, k_evict_select, c, a, to.max_pages << to.page_log2, err_flag);
   if (e != cudaSuccess) return e;
   const int most = (int)(reach < keep ? reach : keep);
   const int per = 8 * (32 / (c.dim / 16)) * 4;             // tokens a CTA moves
-  const dim3 grid((most + per - 1) / per, c.heads, c.batch);
-  if (c.dim == 64)
-    k_evict_move<64><<<grid, 256, 0, s>>>(c, to, kv_len, keep, a.places, err_flag);
-  else
-    k_evict_move<128><<<grid, 256, 0, s>>>(c, to, kv_len, keep, a.places, err_flag);
-  return cudaGetLastError();
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((most + per - 1) / per, c.heads, c.batch);
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, c.dim == 64 ? k_evict_move<64> : k_evict_move<128>, c, to, kv_len, keep,
+                            (const int*)a.places, err_flag);
 }
 
 }  // namespace jepa

@@ -155,6 +155,84 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, bool early, cuda
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// y = x * w / sqrt(mean(x^2) + eps), then (a, b) -> (a cos - b sin, b cos + a sin) for the pairs
+// (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1), i < rot / 2. All lanes of the warp call it.
+template <int D, bool INTER>
+__device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>& ln,
+                                            const float* __restrict__ w, float eps,
+                                            const float (&an)[16]) {
+  constexpr int L = D / 16;
+  if (w) {
+    float part[4] = {0.f, 0.f, 0.f, 0.f};   // short chains: fewer roundings on the way
+#pragma unroll
+    for (int i = 0; i < 16; ++i) part[i & 3] = fmaf(y[i], y[i], part[i & 3]);
+    float ss = (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = __frsqrt_rn(ss * (1.0f / D) + eps);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 g =
+          __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 8 ? ln.c0 : ln.c1) + (i & 7)));
+      y[i] *= r * g.x; y[i + 1] *= r * g.y; y[i + 2] *= r * g.z; y[i + 3] *= r * g.w;
+    }
+  }
+  if (ln.rotates) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : 8 + i;
+      const float p = y[ia], q = y[ib];
+      y[ia] = p * an[i] - q * an[8 + i];
+      y[ib] = q * an[i] + p * an[8 + i];
+    }
+  }
+}
+
+// Queries: a warp takes one token and up to Q_HEADS of its heads, which share the angles. The
+// loads of the rows and of the token's sequence go out together.
+constexpr int Q_HEADS = 8;
+
+template <int D, bool INTER>
+__device__ __forceinline__ void rotate_queries(const PageView& c, const AppendArgs& a,
+                                               long long unit, int* err_flag) {
+  constexpr int L = D / 16, ROWS = 32 / L, PASSES = Q_HEADS / ROWS;
+  const int blocks = (a.q_heads + Q_HEADS - 1) / Q_HEADS;
+  if (unit >= (long long)a.tokens * blocks) return;
+  const int t = (int)(unit / blocks), h0 = (int)(unit - (long long)t * blocks) * Q_HEADS;
+  const int sub = (threadIdx.x & 31) / L;
+  const Lane<D, INTER> ln(a.rot);
+  uint4 raw[PASSES][2];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int h = h0 + p * ROWS + sub;
+    raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    if (h < a.q_heads) load16(a.q + t * a.q_stride + (long long)h * D, ln, raw[p]);
+  }
+  const Place at = locate(a.cu, a.start, c.batch, t);
+  if (!holds(at, t, a.tokens)) return;            // left as it is
+  const int pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
+  if (at.first < 0 || pos < 0 || pos >= positions_of(c, a)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(err_flag, DEV_ERR_INDEX);
+    return;
+  }
+  float an[16];
+  if (ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    float y[16];
+    widen(raw[p], y);
+    norm_rotate<D, INTER>(y, ln, a.q_norm, a.eps, an);
+    const int h = h0 + p * ROWS + sub;
+    if (h < a.q_heads) store16(a.q_out + ((long long)t * a.q_heads + h) * D, ln, y);
+  }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(THREADS, 4) k_rope_queries(PageView c, AppendArgs a, int* err_flag) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  rotate_queries<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
+}
+
 }  // namespace
 
 }  // namespace jepa

@@ -433,9 +433,9 @@ typedef struct {
 /* Append new tokens to the cache: arguments, norm, rotation and q_out, k_out as in
  * jepa_rope_append_kv8. Each 16 elements of a rotated key or of a value are quantised from fp32: scale =
  * e4m3(max|x| / 6 / unit), nearest even, at least 2^-9 and at most 448; codes = e2m1(x / (scale * unit)),
- * nearest even, saturating. A block that holds a NaN or an infinity gets a NaN scale and reads as NaN. The
- * norm's factor 1 / sqrt(mean(x^2) + norm_eps) is rounded once to fp32 and multiplied by the weight
- * first; each product and sum of the rotation is rounded to fp32. */
+ * nearest even, saturating. A block that holds a NaN or an infinity gets a NaN scale and reads as NaN. For
+ * keys the norm's factor 1 / sqrt(mean(x^2) + norm_eps) is rounded once to fp32 and multiplied by the
+ * weight first, and each product and sum of the rotation is rounded to fp32. */
 jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
                                  int64_t q_stride, const uint16_t* k, int64_t k_stride,
                                  const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
