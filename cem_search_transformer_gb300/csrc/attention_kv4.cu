@@ -25,23 +25,29 @@ namespace jepa {
 
 namespace {
 
-template <int D, int NR>
+// What a kernel does: attention with an item's keys shared by the four warps of a CTA, attention with an
+// item a warp, or the weights (a place of the line a warp).
+enum Kind { BY_CTA, BY_WARP, WEIGHTS };
+
+template <int D, int NR, int KIND>
 struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
-  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;   // cp.async stages of a warp
-  static constexpr int CTAS = (D == 64 ? 4 : 3) - (NR == 2);
   static constexpr int KS = D == 64 && NR == 1 ? 64 : 32;   // keys a warp takes in a step
+  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;    // cp.async stages of a warp
+  static constexpr int CTAS = (D == 64 ? 4 : 3) - (NR == 2);
   static constexpr int GROUPS = KS / 16;           // 16-key groups
-  static constexpr int UNIT = WARPS * KS;          // keys of a unit
+  static constexpr int SHARERS = KIND == BY_CTA ? WARPS : 1;   // warps that share an item's keys
+  static constexpr int UNIT = SHARERS * KS;        // keys of a unit
   static constexpr int KB = D / 2, SB = D / 16;    // bytes of a key's codes, and of its scales
   static constexpr int KW = D / 32;                // 32-bit words of a key a lane takes
-  static constexpr int VW = D / 64;                // 32-bit words of a V row a lane takes
-  static constexpr int MT = D / 16;                // output tiles of 16 columns
-  static constexpr int OFF_V = KS * KB, OFF_SC = 2 * KS * KB;   // of a stage: K, V codes, K, V scales
-  static constexpr int STAGE = OFF_SC + 2 * KS * SB;
-  static constexpr int OUT_LD = OUT_ROW<D>;
+  [[maybe_unused]] static constexpr int VW = D / 64;   // 32-bit words of a V row a lane takes
+  [[maybe_unused]] static constexpr int MT = D / 16;   // output tiles of 16 columns
+  static constexpr int KINDS = KIND == WEIGHTS ? 1 : 2;        // K, or K and V
+  static constexpr int OFF_V = KS * KB, OFF_SC = KINDS * KS * KB;   // of a stage: K, V codes, K, V scales
+  static constexpr int STAGE = OFF_SC + KINDS * KS * SB;
+  [[maybe_unused]] static constexpr int OUT_LD = OUT_ROW<D>;
   static constexpr int OFF_OUT = WARPS * NST * STAGE;
-  static constexpr int SMEM = OFF_OUT + WARPS * ROWS * OUT_LD * 4;
+  static constexpr int SMEM = OFF_OUT + (KIND == BY_CTA ? WARPS * ROWS * OUT_LD * 4 : 0);
   static_assert(2 * KS * SB / 16 <= 32, "a step's scales are a chunk a lane at most");
   static_assert(CTAS <= MAX_CTAS_PER_SM && CTAS * (SMEM + 2048) <= 228 * 1024, "CTAs of a SM");
   static_assert(COMBINE_SMEM<D> * CTAS * MAX_SMS <= 48 * 1024, "what a launch may have without an attribute");
@@ -110,40 +116,45 @@ __device__ __forceinline__ void scale_queries(Queries<D, NR>& qr, float unit) {
     for (int e = 0; e < 2; ++e) qr.qs[nr][e] = fminf(fmaxf(qr.qs[nr][e] * unit, 0x1p-126f), 0x1.fffffep127f);
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
-    k_attention_kv4(Kv4View c, Args a, int whole, int* err_flag) {
-  using S = Shape<D, NR>;
+template <int D, int NR, int KIND>
+__global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
+    k_attention_kv4(Kv4View c, Args a, MassArgs ma, int whole, int* err_flag) {
+  using S = Shape<D, NR, KIND>;
   constexpr int ROWS = S::ROWS, NST = S::NST;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;");   // k_combine may be set up meanwhile
+  // worker of the line: the CTA, or the warp
+  const int worker = KIND == BY_CTA ? blockIdx.x : blockIdx.x * WARPS + warp;
+  const int first_key = KIND == BY_CTA ? warp * S::KS : 0;      // of this warp in a unit
+  asm volatile("griddepcontrol.launch_dependents;");   // what comes next may be set up meanwhile
+  if (KIND == WEIGHTS) asm volatile("griddepcontrol.wait;" ::: "memory");   // lse is there
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (NST * S::STAGE);
   const uint8_t* ring_ptr = smem + warp * (NST * S::STAGE);
-  float* const sm_o = reinterpret_cast<float*>(smem + S::OFF_OUT);
 
-  int* const flag0 = blockIdx.x == 0 ? err_flag : nullptr;
+  int* const flag0 = KIND != WEIGHTS && blockIdx.x == 0 ? err_flag : nullptr;
+  const int most = KIND == BY_CTA ? gridDim.x : gridDim.x * WARPS;
   long long u_begin, u_end, total = 0;
-  int workers = 0;
+  int workers = most;
   if (whole) {
     // items in equal numbers, a place each
     const long long items = (long long)c.batch * c.heads * a.tiles;
-    u_begin = kv8_share(items, gridDim.x, blockIdx.x);
-    u_end = kv8_share(items, gridDim.x, blockIdx.x + 1);
+    u_begin = kv8_share(items, most, worker);
+    u_end = kv8_share(items, most, worker + 1);
     if (flag0 && warp == 0) total_places(c, a, S::UNIT, flag0);   // reports lengths out of range
   } else {
     total = total_places(c, a, S::UNIT, flag0);
-    workers = workers_of(total, gridDim.x);
-    if ((int)blockIdx.x >= workers) {
-      if (threadIdx.x == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-      write_empty<D>(c, a);
+    workers = workers_of(total, most);
+    if (worker >= workers) {
+      if (KIND == BY_CTA) {
+        if (threadIdx.x == 0) a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+        write_empty<D>(c, a);
+      }
       return;
     }
-    u_begin = kv8_share(total, workers, blockIdx.x);
-    u_end = kv8_share(total, workers, blockIdx.x + 1);
+    u_begin = kv8_share(total, workers, worker);
+    u_end = kv8_share(total, workers, worker + 1);
   }
-  int4 begun = make_int4(0, 0, 0, 0);
+  [[maybe_unused]] int4 begun = make_int4(0, 0, 0, 0);
   const int rows = a.q_tokens * a.group;
   // ---- loading: the warp's steps of all segments in one stream, NST - 1 ahead of their use ----
   constexpr int CPR = S::KB / 16;              // 16-byte chunks of a key's codes
@@ -167,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   int ld_key = 0;                              // first key of that step
   const int* ld_pages = nullptr;               // the sequence's row of the table
   auto begin_segment = [&]() {
-    ld_key = ld.k0 * S::UNIT + warp * S::KS;
+    ld_key = ld.k0 * S::UNIT + first_key;
     ld_pages = c.table + (long long)ld.s * c.max_pages;
     ld_left = ld.k1 - ld.k0;
   };
@@ -201,10 +212,10 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
 #pragma unroll
           for (int q = 0; q < 16 / RPI; ++q) {
             cp16(lane_to[q] + st + 16 * p * S::KB, fk + q * RPI * S::KB, 16);
-            cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, 16);
+            if (S::KINDS == 2) cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, 16);
           }
         }
-        if (lane < 2 * S::GROUPS * SPG)
+        if (lane < S::KINDS * S::GROUPS * SPG)
           cp16(sc_to + st, scales + pick(row, sc_group) * S::SB, 16);
       } else {                                 // keys past the end, or without a page, are zeros
         int keys[S::GROUPS];
@@ -220,10 +231,10 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
           for (int q = 0; q < 16 / RPI; ++q) {
             const uint32_t bytes = q * RPI + sub < keys[p] ? 16 : 0;
             cp16(lane_to[q] + st + 16 * p * S::KB, fk + q * RPI * S::KB, bytes);
-            cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, bytes);
+            if (S::KINDS == 2) cp16(lane_to[q] + st + 16 * p * S::KB + S::OFF_V, fv + q * RPI * S::KB, bytes);
           }
         }
-        if (lane < 2 * S::GROUPS * SPG) {
+        if (lane < S::KINDS * S::GROUPS * SPG) {
           const int n = pick(keys, sc_group) - sc_chunk * KPC;
           cp16(sc_to + st, scales + pick(row, sc_group) * S::SB, max(0, min(KPC, n)) * S::SB);
         }
@@ -249,6 +260,25 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
   const uint32_t at_v1 = S::OFF_V + (D == 128 ? code_at<D>(2 * t + 1, g >> 1) + 8 * (g & 1) : code_at<D>(2 * t + 1, g >> 2) + 4 * (g & 3));
   const uint32_t at_ks = S::OFF_SC + g * S::SB + (D == 128 ? 2 * t : t);
   const uint32_t at_vs = S::OFF_SC + S::KS * S::SB + 2 * t * S::SB + (D == 128 ? g : g >> 1);
+  const int tiles = KIND == WEIGHTS ? (rows + ROWS - 1) / ROWS : 1;   // row tiles of an item of the weights
+  // scores of a stage's 16-key group p: keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
+  auto scores = [&](const uint8_t* kb, int p, const Queries<D, NR>& qr, float (&x)[NR][4]) {
+            uint32_t w[2][S::KW], f[2][S::VW];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = 16 * p + 8 * h;
+              if (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(kb + at_k + row * S::KB);
+                w[h][0] = x.x; w[h][1] = x.y; w[h][S::KW - 2] = x.z; w[h][S::KW - 1] = x.w;
+                key_scales<D>(*reinterpret_cast<const uint16_t*>(kb + at_ks + row * S::SB), f[h]);
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(kb + at_k + row * S::KB);
+                w[h][0] = x.x; w[h][1] = x.y;
+                key_scales<D>(kb[at_ks + row * S::SB], f[h]);
+              }
+            }
+    scores_of<D, NR>(w, f, qr.qf, x);
+  };
   int stage = 0;
   Cursor cur{0, 0, 0, 0};
   Segment sg;
@@ -257,8 +287,74 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
     const int s = sg.s, len = sg.len;
     const int head = sg.head, r0 = sg.r0;
     Queries<D, NR> qr;
+    const float k_unit = kv4_unit(c.k_unit, head);
+    if constexpr (KIND == WEIGHTS) {
+      const long long at = ((long long)s * c.heads + head) * ((long long)c.max_pages << c.page_log2);
+      float norm[NR][2];                       // lse in base 2 of rows 2t, 2t + 1
+      bool full = false;                       // no row of the tile lies behind the last
+      auto load_rows = [&](int first) {
+        qr.load(a, s, head, first, rows, len);
+        scale_queries(qr, k_unit);
+        full = first + ROWS <= rows;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = first + 8 * nr + 2 * t + e;
+            norm[nr][e] = r < rows ? a.lse[row_at(a, s, head, r)] * 1.4426950408889634f : 0.f;
+            if (r >= rows) qr.lim[nr][e] = 0;  // no weight
+          }
+      };
+      if (tiles == 1) load_rows(0);
+      for (int k = sg.k0; k < sg.k1; ++k) {
+        const int key0 = k * S::UNIT;
+        // what the keys had, a step ahead of its use
+        float old[S::GROUPS][2];
+#pragma unroll
+        for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = key0 + 16 * p + 8 * h + g;
+            old[p][h] = ma.mass && t == 0 && key < len ? ma.mass[at + key] : 0.f;
+          }
+        cp_wait<NST - 2>();
+        __syncwarp();
+        issue();
+        const uint8_t* kb = ring_ptr + stage * S::STAGE;
+        stage = stage + 1 == NST ? 0 : stage + 1;
+        float sum[S::GROUPS][2];
+#pragma unroll
+        for (int p = 0; p < S::GROUPS; ++p) sum[p][0] = sum[p][1] = 0.f;
+        for (int tile = 0; tile < tiles; ++tile) {
+          if (tiles > 1) load_rows(tile * ROWS);
+          const bool inside = full && key0 + S::KS <= qr.lim_min;   // every row sees every key (warp-uniform)
+#pragma unroll
+          for (int p = 0; p < S::GROUPS; ++p) {
+            float x[NR][4];
+            scores(kb, p, qr, x);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y = ex2f(fmaf(x[nr][e], qr.qs[nr][e & 1], -norm[nr][e & 1]));
+                if (inside || key0 + 16 * p + 8 * (e >> 1) + g < qr.lim[nr][e & 1]) sum[p][e >> 1] += y;
+              }
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = sum[p][h];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            const int key = key0 + 16 * p + 8 * h + g;
+            if (t == 0 && key < len) ma.out[at + key] = ma.mass ? fmaf(ma.decay, old[p][h], x) : x;
+          }
+      }
+    } else {
     qr.load(a, s, head, r0, rows, len);
-    scale_queries(qr, kv4_unit(c.k_unit, head));
+    scale_queries(qr, k_unit);
     float o[NR][S::MT][4];
     float m[NR][2], ref[NR][2], l[NR][2];        // ref: m - P_SHIFT, 0 before the first key
 #pragma unroll
@@ -274,30 +370,15 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
       cp_wait<NST - 2>();
       __syncwarp();
       issue();                         // into the stage that the step before this one has read
-      const int key0 = k * S::UNIT + warp * S::KS;
+      const int key0 = k * S::UNIT + first_key;
       const uint8_t* kb = ring_ptr + stage * S::STAGE;
       stage = stage + 1 == NST ? 0 : stage + 1;
       if (key0 >= len) continue;
 
-      // scores of keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
       float sc[S::GROUPS][NR][4];
 #pragma unroll
       for (int p = 0; p < S::GROUPS; ++p) {
-        uint32_t w[2][S::KW], f[2][S::VW];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 16 * p + 8 * h;
-          if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kb + at_k + row * S::KB);
-            w[h][0] = x.x; w[h][1] = x.y; w[h][S::KW - 2] = x.z; w[h][S::KW - 1] = x.w;
-            key_scales<D>(*reinterpret_cast<const uint16_t*>(kb + at_ks + row * S::SB), f[h]);
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(kb + at_k + row * S::KB);
-            w[h][0] = x.x; w[h][1] = x.y;
-            key_scales<D>(kb[at_ks + row * S::SB], f[h]);
-          }
-        }
-        scores_of<D, NR>(w, f, qr.qf, sc[p]);
+        scores(kb, p, qr, sc[p]);
       }
       const bool edge = key0 + S::KS > qr.lim_min;   // some row does not see some key (warp-uniform)
       bool move = false;
@@ -422,208 +503,124 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR>::CTAS))
         }
       }
     }
-    // ---- join the four warps ----
-    __syncthreads();   // the joining before this one has been read
     const float unit = kv4_unit(c.v_unit, head);
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[nr][e];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        const int row = 8 * nr + 2 * t + e;
-        if (g == 0) {
-          // from here on m is the exponent's reference; -inf only where no key was seen (scores
-          // that are all NaN leave the maximum at -inf, but a NaN sum)
-          sm_m[warp][row] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
-          sm_l[warp][row] = x;
-        }
-        float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * (D / 8);
-#pragma unroll
-        for (int d = 0; d < S::MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
-          *reinterpret_cast<float4*>(to + 2 * d) =
-              make_float4(o[nr][d][e] * unit, o[nr][d][2 + e] * unit, o[nr][d + 1][e] * unit,
-                          o[nr][d + 1][2 + e] * unit);
-      }
-    __syncthreads();
-    join_warps<D, NR>(a, sg, rows, total, workers, sm_o, sm_m, sm_l, begun);
-  }
-  cp_wait<0>();
-  if (whole) return;
-  if (threadIdx.x == 0) a.split[blockIdx.x] = begun;
-  write_empty<D>(c, a);
-}
-
-// ---- weights ----
-
-template <int D, int NR>
-struct MassShape {
-  static constexpr int ROWS = 8 * NR;
-  static constexpr int KS = 32;                // keys a warp takes in a step
-  static constexpr int GROUPS = KS / 16;
-  static constexpr int UNIT = WARPS * KS;
-  static constexpr int CTAS = D == 64 ? 4 : NR == 1 ? 3 : 2;   // of a SM, by their registers
-};
-
-// The weights' second pass over the keys, once lse is known. Items are (sequence, head); every key of
-// an item belongs to one lane, which sums over all query rows: no atomics, so the order is fixed.
-template <int D, int NR>
-__global__ void __launch_bounds__(THREADS, (MassShape<D, NR>::CTAS)) k_mass_kv4(Kv4View c, Args a, MassArgs w, int* err_flag) {
-  using S = MassShape<D, NR>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rows = a.q_tokens * a.group, tiles = (rows + S::ROWS - 1) / S::ROWS;
-  const long long total = total_places(c, a, S::UNIT, nullptr);
-  const int workers = workers_of(total, gridDim.x);
-  if ((int)blockIdx.x >= workers) return;
-  const long long u_end = kv8_share(total, workers, blockIdx.x + 1);
-  const long long reach = (long long)c.max_pages << c.page_log2;
-  Cursor cur{0, 0, 0, 0};
-  Segment sg;
-  sg.next = kv8_share(total, workers, blockIdx.x);
-  while (plan<S::UNIT, S::ROWS>(c, a, 0, sg.next, u_end, cur, sg)) {
-    const int len = sg.len, head = sg.head;
-    const float unit = kv4_unit(c.k_unit, head);
-    const int* pages = c.table + (long long)sg.s * c.max_pages;
-    const long long at = ((long long)sg.s * c.heads + head) * reach;
-    Queries<D, NR> qr;
-    float norm[NR][2];                         // lse in base 2 of rows 2t, 2t + 1
-    bool full = false;                         // no row of the tile lies behind the last
-    auto load_rows = [&](int r0) {
-      qr.load(a, sg.s, head, r0, rows, len);
-      scale_queries(qr, unit);
-      full = r0 + S::ROWS <= rows;
+    if constexpr (KIND == BY_WARP) {
+      // ---- the warp has all of the item ----
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          float x = l[nr][e];
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
           const int r = r0 + 8 * nr + 2 * t + e;
-          norm[nr][e] = r < rows ? a.lse[row_at(a, sg.s, head, r)] * 1.4426950408889634f : 0.f;
-          if (r >= rows) qr.lim[nr][e] = 0;    // no weight
-        }
-    };
-    if (tiles == 1) load_rows(0);
-    // codes and scales of the step ahead, pages of the one behind it
-    uint32_t kn[S::GROUPS][2][D / 32], sn[S::GROUPS][2];
-    int pg[S::GROUPS];
-    auto fetch_pages = [&](int k) {
+          if (r >= rows) continue;
+          const bool none = m[nr][e] == -INFINITY && x == 0.f;   // no key was seen (scores of NaN: a NaN sum)
+          const float f = none ? 0.f : unit / x;
+          const long long at = row_at(a, s, head, r);
+          uint32_t w[S::MT];
 #pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) {
-        const int key = k * S::UNIT + warp * S::KS + 16 * p;
-        pg[p] = k < sg.k1 && key < len ? __ldg(pages + (key >> c.page_log2)) : -1;
-      }
-    };
-    auto fetch = [&](int k) {
-#pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) {
-        const int key = k * S::UNIT + warp * S::KS + 16 * p;
-        const bool there = (uint32_t)pg[p] < (uint32_t)c.num_pages;
-        if (!there && k < sg.k1 && key < len && lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
-        const uint64_t row = (((uint64_t)((there ? (uint32_t)pg[p] : 0u) * (uint32_t)c.heads + (uint32_t)head)) << c.page_log2) +
-                             ((uint32_t)key & (uint32_t)(c.page - 1)) + g;
-        const uint8_t *codes = c.k + row * (D / 2) + t * (D / 8), *scales = c.k_scale + row * (D / 16) + t * (D / 64);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool on = there && key + 8 * h + g < len;
-          sn[p][h] = 0;
-          if (D == 128) {
-            const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(codes + 8 * h * (D / 2))) : make_uint4(0, 0, 0, 0);
-            kn[p][h][0] = x.x; kn[p][h][1] = x.y; kn[p][h][D / 32 - 2] = x.z; kn[p][h][D / 32 - 1] = x.w;
-            if (on) sn[p][h] = __ldg(reinterpret_cast<const uint16_t*>(scales + 8 * h * (D / 16)));
-          } else {
-            const uint2 x = on ? __ldg(reinterpret_cast<const uint2*>(codes + 8 * h * (D / 2))) : make_uint2(0, 0);
-            kn[p][h][0] = x.x; kn[p][h][1] = x.y;
-            if (on) sn[p][h] = __ldg(scales + 8 * h * (D / 16));
+          for (int d = 0; d < S::MT; ++d) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o[nr][d][e] * f, o[nr][d][2 + e] * f);
+            w[d] = *reinterpret_cast<const uint32_t*>(&y);
           }
+          uint4* to = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
+#pragma unroll
+          for (int d = 0; d < S::MT; d += 4) to[d / 4] = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
+          if (a.lse && g == 0) a.lse[at] = none ? -INFINITY : (ref[nr][e] + log2f(x)) * 0.69314718055994531f;
         }
-      }
-    };
-    fetch_pages(sg.k0);
-    fetch(sg.k0);
-    fetch_pages(sg.k0 + 1);
-    for (int k = sg.k0; k < sg.k1; ++k) {
-      const int key0 = k * S::UNIT + warp * S::KS;
-      if (key0 >= len) break;                  // the sequence's last unit
-      uint32_t kw[S::GROUPS][2][D / 32], sc[S::GROUPS][2][D / 64];
-      float old[S::GROUPS][2];
+    } else {
+      // ---- join the four warps ----
+      __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
+      float* const sm_o = reinterpret_cast<float*>(smem + S::OFF_OUT);
+      __syncthreads();   // the joining before this one has been read
 #pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p)
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int e = 0; e < 2; ++e) {
+          float x = l[nr][e];
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          const int row = 8 * nr + 2 * t + e;
+          if (g == 0) {
+            // from here on m is the exponent's reference; -inf only where no key was seen (scores
+            // that are all NaN leave the maximum at -inf, but a NaN sum)
+            sm_m[warp][row] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
+            sm_l[warp][row] = x;
+          }
+          float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * (D / 8);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) kw[p][h][i] = kn[p][h][i];
-          key_scales<D>(sn[p][h], sc[p][h]);
-          const int key = key0 + 16 * p + 8 * h + g;
-          old[p][h] = w.mass && t == 0 && key < len ? w.mass[at + key] : 0.f;
+          for (int d = 0; d < S::MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
+            *reinterpret_cast<float4*>(to + 2 * d) =
+                make_float4(o[nr][d][e] * unit, o[nr][d][2 + e] * unit, o[nr][d + 1][e] * unit,
+                            o[nr][d + 1][2 + e] * unit);
         }
-      fetch(k + 1);
-      fetch_pages(k + 2);
-      float sum[S::GROUPS][2];
-#pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) sum[p][0] = sum[p][1] = 0.f;
-      for (int tile = 0; tile < tiles; ++tile) {
-        if (tiles > 1) load_rows(tile * S::ROWS);
-        const bool inside = full && key0 + S::KS <= qr.lim_min;   // every row sees every key (warp-uniform)
-#pragma unroll
-        for (int p = 0; p < S::GROUPS; ++p) {
-          float s[NR][4];
-          scores_of<D, NR>(kw[p], sc[p], qr.qf, s);
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = ex2f(fmaf(s[nr][e], qr.qs[nr][e & 1], -norm[nr][e & 1]));
-              if (inside || key0 + 16 * p + 8 * (e >> 1) + g < qr.lim[nr][e & 1]) sum[p][e >> 1] += x;
-            }
-        }
-      }
-#pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x = sum[p][h];
-          x += __shfl_xor_sync(0xffffffffu, x, 1);
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          const int key = key0 + 16 * p + 8 * h + g;
-          if (t == 0 && key < len) w.out[at + key] = w.mass ? fmaf(w.decay, old[p][h], x) : x;
-        }
+      __syncthreads();
+      join_warps<D, NR>(a, sg, rows, total, workers, sm_o, sm_m, sm_l, begun);
     }
+    }
+  }
+  cp_wait<0>();
+  if (KIND == BY_CTA && !whole) {
+    if (threadIdx.x == 0) a.split[blockIdx.x] = begun;
+    write_empty<D>(c, a);
   }
 }
 
-template <int D, int NR>
-cudaError_t launch_mass(const Kv4View& c, Args a, const MassArgs& w, int* err_flag, int num_sms,
-                        cudaStream_t s) {
-  using S = MassShape<D, NR>;
-  a.tiles = 1;                                 // an item holds all rows of its head
-  const long long max_len = (long long)c.max_pages << c.page_log2;
-  const long long max_units = (max_len + S::UNIT - 1) / S::UNIT;
-  const long long slots = (long long)num_sms * S::CTAS, items = (long long)c.batch * c.heads;
-  const long long work = max_units > slots ? slots : items * max_units;
-  k_mass_kv4<D, NR><<<(unsigned)(work < slots ? work : slots), THREADS, 0, s>>>(c, a, w, err_flag);
-  return cudaGetLastError();
+template <int D, int NR, int KIND>
+cudaError_t start(const Kv4View& c, const Args& a, const MassArgs& w, int grid, int whole, bool early,
+                  int* err_flag, cudaStream_t s) {
+  using S = Shape<D, NR, KIND>;
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = set_max_dynamic_smem((const void*)k_attention_kv4<D, NR, KIND>, S::SMEM, attr_done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = early;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attention_kv4<D, NR, KIND>, c, a, w, whole, err_flag);
+}
+
+// CTAs of a launch whose workers are `sharers` a CTA: every SM's slots, or the work there can be if that is less.
+int grid_of(long long work, long long slots, int sharers) {
+  const long long need = (work + sharers - 1) / sharers;
+  return (int)(need < slots ? need : slots);
 }
 
 template <int D, int NR>
 cudaError_t launch(const Kv4View& c, Args a, const MassArgs* w, int* err_flag, int num_sms, cudaStream_t s) {
-  using S = Shape<D, NR>;
-  static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = set_max_dynamic_smem((const void*)k_attention_kv4<D, NR>, S::SMEM, attr_done);
-  if (e != cudaSuccess) return e;
+  using S = Shape<D, NR, BY_CTA>;
   a.tiles = (a.q_tokens * a.group + S::ROWS - 1) / S::ROWS;
   const long long max_len = (long long)c.max_pages << c.page_log2;
   const long long max_units = (max_len + S::UNIT - 1) / S::UNIT;
   const long long slots = (long long)(num_sms < MAX_SMS ? num_sms : MAX_SMS) * S::CTAS;
   const long long items = (long long)c.batch * c.heads * a.tiles;
   const int whole = max_units <= WHOLE_UNITS;
-  // every SM's slots, or the work there can be if that is less
-  const long long work = whole ? items : max_units > slots ? slots : items * max_units;
-  const int grid = (int)(work < slots ? work : slots);
-  k_attention_kv4<D, NR><<<grid, THREADS, S::SMEM, s>>>(c, a, whole, err_flag);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (!whole && (e = launch_combine<D, NR>(a, grid, s)) != cudaSuccess) return e;
-  return w ? launch_mass<D, NR>(c, a, *w, err_flag, num_sms, s) : cudaSuccess;
+  // Short items a warp each, without barriers and joining, where their rounds fill the warps to four fifths.
+  const long long warps = slots * WARPS, rounds = (items + warps - 1) / warps;
+  cudaError_t e;
+  if (whole && 5 * items >= 4 * rounds * warps) {
+    e = start<D, NR, BY_WARP>(c, a, MassArgs{}, grid_of(items, slots, WARPS), 1, false, err_flag, s);
+  } else {
+    const int grid = whole ? grid_of(items, slots, 1) : grid_of(max_units > slots ? slots : items * max_units, slots, 1);
+    e = start<D, NR, BY_CTA>(c, a, MassArgs{}, grid, whole, false, err_flag, s);
+    if (e == cudaSuccess && !whole) e = launch_combine<D, NR>(a, grid, s);
+  }
+  if (e != cudaSuccess || !w) return e;
+  // The second pass over the keys: items are (sequence, head), each key belongs to one lane, which sums over all
+  // query rows. No atomics: the order is fixed.
+  a.tiles = 1;
+  const long long steps = (max_len + S::KS - 1) / S::KS, all = (long long)c.batch * c.heads;
+  const long long work = steps > slots * WARPS ? slots * WARPS : all * steps;
+  return start<D, NR, WEIGHTS>(c, a, *w, grid_of(work, slots, WARPS), 0, true, err_flag, s);
 }
 
 }  // namespace
