@@ -214,6 +214,7 @@ class _Fast:
         cls.u8 = frozenset(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if d)
         cls.bf16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
         cls.f32, cls.i32 = frozenset((torch.float32,)), frozenset((torch.int32,))
+        cls.matrices = {torch.float32: 0, torch.bfloat16: 1}
         cls.kinds = {"u8": cls.u8, "bf16": cls.bf16, "f32": cls.f32, "i32": cls.i32}
         # the stream's address without a Stream object around it, where torch has that
         cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -360,20 +361,26 @@ class KvCache4:
             raise JepaError(1, f"cache is on {self.device}, the planner on cuda:{device}")
 
 
-def _matrix(t, name: str, device: int):
-    """(address, 1 where bf16, elements between rows, rows, cols) of a float32 or bf16 CUDA tensor
-    [rows, cols] whose rows are contiguous (columns of a wider tensor are fine)."""
+def _matrix(t, name: str, device: int, shape=None):
+    """(address, 1 where bf16, elements between rows) of a float32 or bf16 CUDA tensor [rows, cols]
+    (of this shape, where one is given) whose rows are contiguous (columns of a wider tensor are fine)."""
     if not isinstance(t, _Fast.Tensor) or t.dim() != 2:
         raise JepaError(1, f"{name}: expected a tensor [rows, cols]")
-    half = t.dtype is _Fast.torch.bfloat16
-    if not half and t.dtype is not _Fast.torch.float32:
+    if shape is not None and t.shape != shape:
+        raise JepaError(1, f"{name} {tuple(t.shape)} does not fit x {tuple(shape)}")
+    half = _Fast.matrices.get(t.dtype)
+    if half is None:
         raise JepaError(1, f"{name}: dtype {t.dtype} where float32 or bfloat16 is required")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise JepaError(1, f"{name}: the elements of a row must be contiguous")
+    if t.is_contiguous():
+        stride = t.shape[1] if shape is None else shape[1]
+    else:
+        rows, cols = t.shape
+        if cols > 1 and t.stride(1) != 1:
+            raise JepaError(1, f"{name}: the elements of a row must be contiguous")
+        stride = t.stride(0) if rows > 1 else cols
     if t.get_device() != device:
         raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{device}")
-    return t.data_ptr(), int(half), (t.stride(0) if rows > 1 else cols), rows, cols
+    return t.data_ptr(), half, stride
 
 
 def _stream(stream) -> Optional[int]:
@@ -808,17 +815,13 @@ class Planner:
         if _Fast.torch is None:
             _Fast.load()
         dev = self.device
-        xp, xh, xs, rows, cols = _matrix(x, "x", dev)
-        dp, dh, ds = None, 0, 0
-        if delta is not None:
-            dp, dh, ds, *d_shape = _matrix(delta, "delta", dev)
-            if d_shape != [rows, cols]:
-                raise JepaError(1, f"delta {tuple(delta.shape)} does not fit x {tuple(x.shape)}")
-        op, os_ = None, 0
-        if x_out is not None:
-            op, oh, os_, *o_shape = _matrix(x_out, "x_out", dev)
-            if o_shape != [rows, cols] or oh != xh:
-                raise JepaError(1, "x_out must have x's shape and type")
+        xp, xh, xs = _matrix(x, "x", dev)
+        shape = x.shape
+        rows, cols = shape
+        dp, dh, ds = (None, 0, 0) if delta is None else _matrix(delta, "delta", dev, shape)
+        op, oh, os_ = (None, xh, 0) if x_out is None else _matrix(x_out, "x_out", dev, shape)
+        if oh != xh:
+            raise JepaError(1, "x_out must have x's type")
         if rows < 1 or cols < 1:
             raise JepaError(1, "rows and cols must be >= 1")
         n = rows * cols

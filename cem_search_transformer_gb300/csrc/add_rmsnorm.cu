@@ -64,7 +64,7 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float f) {
   return make_uint2((uint32_t)p[0] | ((uint32_t)p[1] << 16), (uint32_t)p[2] | ((uint32_t)p[3] << 16));
 }
 
-// Sum of `v` and maximum of `m` over the T threads of a row. `sm`: two floats a warp.
+// Sum of `v` and maximum of `m` over the T threads of a row. `sm`: two floats a warp of the row.
 template <int T>
 __device__ __forceinline__ void over_row(float& v, float& m, float2* sm) {
 #pragma unroll
@@ -73,7 +73,7 @@ __device__ __forceinline__ void over_row(float& v, float& m, float2* sm) {
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
   if (T == 32) return;
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float2(v, m);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x % T >> 5] = make_float2(v, m);
   __syncthreads();
   v = m = 0.f;
 #pragma unroll
@@ -90,27 +90,30 @@ constexpr float MOST = 0x1p126f;         // the largest factor of the codes
 template <int T, int V, int R, bool XH, bool DH>
 __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
   __shared__ float2 sm[T * R / 32];
+  static_assert(T == 32 || T * R <= 1024, "rows of several warps meet at the CTA's barrier");
   const long long row = (long long)blockIdx.x * R + threadIdx.x / T;
   const int tid = threadIdx.x % T, vecs = a.cols >> 3;
-  if (R > 1 && row >= a.rows) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernel before writes is there
+  if (T == 32 && row >= a.rows) return;
+  const bool on = row < a.rows;            // rows of several warps meet at the barrier all the same
   float s[V][8];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int i = tid + k * T;
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[k][j] = 0.f;
-    if (i < vecs) load8<XH>(a.x, row * a.x_stride + 8 * i, s[k]);
+    if (on && i < vecs) load8<XH>(a.x, row * a.x_stride + 8 * i, s[k]);
   }
   if (a.delta) {
     float d[V][8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int i = tid + k * T;
-      if (i < vecs) load8<DH>(a.delta, row * a.delta_stride + 8 * i, d[k]);
+      if (on && i < vecs) load8<DH>(a.delta, row * a.delta_stride + 8 * i, d[k]);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k)
-      if (tid + k * T < vecs)
+      if (on && tid + k * T < vecs)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[k][j] += d[k][j];
   }
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int i = tid + k * T;
-    if (a.x_out && i < vecs) store8<XH>(a.x_out, row * a.out_stride + 8 * i, s[k]);
+    if (on && a.x_out && i < vecs) store8<XH>(a.x_out, row * a.out_stride + 8 * i, s[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[j & 3] = fmaf(s[k][j], s[k][j], part[j & 3]);
   }
@@ -137,7 +140,8 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
     }
   }
   float sum = (part[0] + part[1]) + (part[2] + part[3]);
-  over_row<T>(sum, m, sm);
+  over_row<T>(sum, m, sm + threadIdx.x / T * (T / 32));
+  if (!on) return;
   const float r = 1.f / sqrtf(sum / (float)a.cols + a.eps);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
@@ -164,14 +168,18 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
 
 template <int T, int V, int R>
 cudaError_t launch(const Args& a, int x_bf16, int delta_bf16, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.rows + R - 1) / R);
-  if (x_bf16)
-    delta_bf16 ? k_add_rmsnorm<T, V, R, true, true><<<grid, T * R, 0, s>>>(a)
-               : k_add_rmsnorm<T, V, R, true, false><<<grid, T * R, 0, s>>>(a);
-  else
-    delta_bf16 ? k_add_rmsnorm<T, V, R, false, true><<<grid, T * R, 0, s>>>(a)
-               : k_add_rmsnorm<T, V, R, false, false><<<grid, T * R, 0, s>>>(a);
-  return cudaGetLastError();
+  auto* kernel = x_bf16 ? (delta_bf16 ? k_add_rmsnorm<T, V, R, true, true> : k_add_rmsnorm<T, V, R, true, false>)
+                        : (delta_bf16 ? k_add_rmsnorm<T, V, R, false, true> : k_add_rmsnorm<T, V, R, false, false>);
+  cudaLaunchAttribute attr;                // begins while the kernel before it ends
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.rows + R - 1) / R));
+  cfg.blockDim = dim3(T * R);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -181,10 +189,17 @@ cudaError_t add_rmsnorm(const void* x, int x_bf16, long long x_stride, const voi
                         int cols, void* x_out, long long out_stride, uint8_t* codes, float* scales,
                         bf16* y, cudaStream_t s) {
   const Args a{x, delta, x_stride, delta_stride, out_stride, w, eps, rows, cols, x_out, codes, scales, y};
-  if (cols <= 1024) return launch<32, 4, 8>(a, x_bf16, delta_bf16, s);
-  if (cols <= 4096) return launch<128, 4, 1>(a, x_bf16, delta_bf16, s);
+  // One vector a thread while that leaves few warps a row: more of a SM's rows in flight, and a short
+  // chain for a single one. Wider rows take more, as their barriers cost more than the registers. Measured, us:
+  // 6192 x 1024 fp32: 128 threads 16.4, 64 with two vectors 18.1, a warp with four 18.5; 1000 x 4096
+  // bf16: 256 with two 10.2, 128 with four 11.0; 4099 x 8192 bf16: 256 with four 55, 512 with two 58, 1024 68;
+  // 1000 x 16384: 1024 with two 37, 512 with four 41.
+  if (cols <= 256) return launch<32, 1, 8>(a, x_bf16, delta_bf16, s);
+  if (cols <= 512) return launch<64, 1, 2>(a, x_bf16, delta_bf16, s);
+  if (cols <= 1024) return launch<128, 1, 1>(a, x_bf16, delta_bf16, s);
+  if (cols <= 4096) return launch<256, 2, 1>(a, x_bf16, delta_bf16, s);
   if (cols <= 8192) return launch<256, 4, 1>(a, x_bf16, delta_bf16, s);
-  if (cols <= 16384) return launch<512, 4, 1>(a, x_bf16, delta_bf16, s);
+  if (cols <= 16384) return launch<1024, 2, 1>(a, x_bf16, delta_bf16, s);
   if (cols <= ADD_RMSNORM_MAX_COLS) return launch<1024, 4, 1>(a, x_bf16, delta_bf16, s);
   return cudaErrorInvalidValue;
 }

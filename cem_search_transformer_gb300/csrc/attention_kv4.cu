@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
   const int worker = KIND == BY_CTA ? blockIdx.x : blockIdx.x * WARPS + warp;
   const int first_key = KIND == BY_CTA ? warp * S::KS : 0;      // of this warp in a unit
   asm volatile("griddepcontrol.launch_dependents;");   // what comes next may be set up meanwhile
-  if (KIND == WEIGHTS) asm volatile("griddepcontrol.wait;" ::: "memory");   // lse is there
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what the call before writes is there
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (NST * S::STAGE);
   const uint8_t* ring_ptr = smem + warp * (NST * S::STAGE);
 
@@ -308,15 +308,15 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
       if (tiles == 1) load_rows(0);
       for (int k = sg.k0; k < sg.k1; ++k) {
         const int key0 = k * S::UNIT;
-        // what the keys had, a step ahead of its use
-        float old[S::GROUPS][2];
+        // This lane writes keys (16 p + 8 h + g) of its share of the pairs (p, h): with four groups p = t, with
+        // two p = t / 2 and h = t % 2. What they had is loaded ahead of its use.
+        constexpr int OWN = S::GROUPS / 2;
+        float old[OWN];
 #pragma unroll
-        for (int p = 0; p < S::GROUPS; ++p)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key0 + 16 * p + 8 * h + g;
-            old[p][h] = ma.mass && t == 0 && key < len ? ma.mass[at + key] : 0.f;
-          }
+        for (int j = 0; j < OWN; ++j) {
+          const int key = key0 + (OWN == 2 ? 16 * t + 8 * j : 8 * t) + g;
+          old[j] = ma.mass && key < len ? ma.mass[at + key] : 0.f;
+        }
         cp_wait<NST - 2>();
         __syncwarp();
         issue();
@@ -341,16 +341,21 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
               }
           }
         }
+        // sums over the four lanes t of a key, each of which ends with its share: half of the values go
+        // to the lane 2 away and half of what is left to the neighbour
+        float half[S::GROUPS];                 // pairs (p, h) in order, those of this lane's half
 #pragma unroll
-        for (int p = 0; p < S::GROUPS; ++p)
+        for (int i = 0; i < S::GROUPS; ++i) {
+          const float lo = sum[i / 2][i & 1], hi = sum[(S::GROUPS + i) / 2][i & 1];
+          half[i] = ((t & 2) ? hi : lo) + __shfl_xor_sync(0xffffffffu, (t & 2) ? lo : hi, 2);
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = sum[p][h];
-            x += __shfl_xor_sync(0xffffffffu, x, 1);
-            x += __shfl_xor_sync(0xffffffffu, x, 2);
-            const int key = key0 + 16 * p + 8 * h + g;
-            if (t == 0 && key < len) ma.out[at + key] = ma.mass ? fmaf(ma.decay, old[p][h], x) : x;
-          }
+        for (int j = 0; j < OWN; ++j) {
+          const float lo = half[j], hi = half[OWN + j];
+          const float x = ((t & 1) ? hi : lo) + __shfl_xor_sync(0xffffffffu, (t & 1) ? lo : hi, 1);
+          const int key = key0 + (OWN == 2 ? 16 * t + 8 * j : 8 * t) + g;
+          if (key < len) ma.out[at + key] = ma.mass ? fmaf(ma.decay, old[j], x) : x;
+        }
       }
     } else {
     qr.load(a, s, head, r0, rows, len);
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
 }
 
 template <int D, int NR, int KIND>
-cudaError_t start(const Kv4View& c, const Args& a, const MassArgs& w, int grid, int whole, bool early,
+cudaError_t start(const Kv4View& c, const Args& a, const MassArgs& w, int grid, int whole,
                   int* err_flag, cudaStream_t s) {
   using S = Shape<D, NR, KIND>;
   static std::atomic<unsigned long long> attr_done{0};
@@ -578,7 +583,7 @@ cudaError_t start(const Kv4View& c, const Args& a, const MassArgs& w, int grid, 
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = early;
+  attr.val.programmaticStreamSerializationAllowed = 1;   // every path waits for the kernel before
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
@@ -608,10 +613,10 @@ cudaError_t launch(const Kv4View& c, Args a, const MassArgs* w, int* err_flag, i
   const long long warps = slots * WARPS, rounds = (items + warps - 1) / warps;
   cudaError_t e;
   if (whole && 5 * items >= 4 * rounds * warps) {
-    e = start<D, NR, BY_WARP>(c, a, MassArgs{}, grid_of(items, slots, WARPS), 1, false, err_flag, s);
+    e = start<D, NR, BY_WARP>(c, a, MassArgs{}, grid_of(items, slots, WARPS), 1, err_flag, s);
   } else {
     const int grid = whole ? grid_of(items, slots, 1) : grid_of(max_units > slots ? slots : items * max_units, slots, 1);
-    e = start<D, NR, BY_CTA>(c, a, MassArgs{}, grid, whole, false, err_flag, s);
+    e = start<D, NR, BY_CTA>(c, a, MassArgs{}, grid, whole, err_flag, s);
     if (e == cudaSuccess && !whole) e = launch_combine<D, NR>(a, grid, s);
   }
   if (e != cudaSuccess || !w) return e;
@@ -620,7 +625,7 @@ cudaError_t launch(const Kv4View& c, Args a, const MassArgs* w, int* err_flag, i
   a.tiles = 1;
   const long long steps = (max_len + S::KS - 1) / S::KS, all = (long long)c.batch * c.heads;
   const long long work = steps > slots * WARPS ? slots * WARPS : all * steps;
-  return start<D, NR, WEIGHTS>(c, a, *w, grid_of(work, slots, WARPS), 0, true, err_flag, s);
+  return start<D, NR, WEIGHTS>(c, a, *w, grid_of(work, slots, WARPS), 0, err_flag, s);
 }
 
 }  // namespace

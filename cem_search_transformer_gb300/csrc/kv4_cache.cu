@@ -104,13 +104,19 @@ __device__ __forceinline__ void norm_rotate_exact(pair (&y)[8], const Lane<D, IN
   }
 }
 
-// Largest magnitude of 8 elements as bits: above those of infinity where there is a NaN.
-__device__ __forceinline__ uint32_t top_bits(const pair (&y)[8], int from) {
-  uint32_t m = 0;
+// Largest of three, NaN where there is one.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Largest magnitude of 8 elements; NaN where there is one.
+__device__ __forceinline__ float top_of(const pair (&y)[8], int from) {
+  float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const pair x = y[from + i];
-    m = max(m, max((uint32_t)x & 0x7fffffffu, (uint32_t)(x >> 32) & 0x7fffffffu));
+    const float2 x = f2_unpack(y[from + i]);
+    m = max3(m, fabsf(x.x), fabsf(x.y));
   }
   return m;
 }
@@ -119,9 +125,9 @@ __device__ __forceinline__ uint32_t top_bits(const pair (&y)[8], int from) {
 // warp call it.
 template <int D, bool INTER>
 __device__ __forceinline__ void block_tops(const pair (&y)[8], const Lane<D, INTER>& ln, int rot,
-                                           uint32_t (&top)[2]) {
-  const uint32_t a = top_bits(y, 0), b = top_bits(y, 4);
-  top[0] = top[1] = max(a, b);              // neighbours: one block
+                                           float (&top)[2]) {
+  const float a = top_of(y, 0), b = top_of(y, 4);
+  top[0] = top[1] = max3(a, b, 0.f);        // neighbours: one block
   if (INTER) return;
   constexpr int L = D / 16;
   const int first = (threadIdx.x & 31) / L * L, lanes = rot >> 4;   // lanes of a head that rotate
@@ -129,16 +135,22 @@ __device__ __forceinline__ void block_tops(const pair (&y)[8], const Lane<D, INT
   for (int h = 0; h < 2; ++h) {
     const int other = (h ? ln.c1 : ln.c0) ^ 1;                      // the block's other chunk
     const int src = first + (ln.rotates ? (other < lanes ? other : other - lanes) : ln.p);
-    const uint32_t x = __shfl_sync(0xffffffffu, a, src), z = __shfl_sync(0xffffffffu, b, src);
-    if (ln.rotates) top[h] = max(h ? b : a, other < lanes ? x : z);
+    const float x = __shfl_sync(0xffffffffu, a, src), z = __shfl_sync(0xffffffffu, b, src);
+    if (ln.rotates) top[h] = max3(h ? b : a, other < lanes ? x : z, 0.f);
   }
+}
+
+// x / d, correctly rounded: `inv` is 1 / d to a step or two, and the remainder of its quotient is exact.
+__device__ __forceinline__ float quotient(float x, float d, float inv) {
+  const float z = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-z, d, x), inv, z);
 }
 
 // Code of a block's scale for its largest magnitude: e4m3(top / 6 / unit), nearest even, at least
 // 2^-9; NaN where the block is not finite.
-__device__ __forceinline__ uint32_t scale_code(uint32_t top, float inv_unit) {
-  if (top >= 0x7f800000u) return 0x7f;
-  const float s = fmaxf(__fmul_rn(__fdiv_rn(__uint_as_float(top), 6.f), inv_unit), KV4_SCALE_MIN);
+__device__ __forceinline__ uint32_t scale_code(float top, float inv_unit) {
+  if (!(top < INFINITY)) return 0x7f;
+  const float s = fmaxf(__fmul_rn(quotient(top, 6.f, 1.f / 6.f), inv_unit), KV4_SCALE_MIN);
   uint16_t p;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(0.f), "f"(s));
   return p & 0xffu;
@@ -146,7 +158,8 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t top, float inv_unit) {
 
 // Codes of 8 elements, the first in the lowest bits.
 __device__ __forceinline__ uint32_t e2m1x8(const pair (&y)[8], int from, float scale) {
-  const float inv1 = __fdiv_rn(1.f, scale);
+  float inv1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv1) : "f"(scale));
   const pair inv = f2_both(inv1), neg = f2_both(-scale);
   float q[8];
 #pragma unroll
@@ -171,7 +184,7 @@ template <int D, bool INTER>
 __device__ __forceinline__ void quantise_store(uint8_t* codes, uint8_t* scales, long long at, bool on,
                                                const pair (&y)[8], const Lane<D, INTER>& ln,
                                                int rot, float unit) {
-  uint32_t top[2];
+  float top[2];
   block_tops<D, INTER>(y, ln, rot, top);
   if (!on) return;
   const float inv_unit = kv4_inverse(unit);
@@ -187,19 +200,14 @@ __device__ __forceinline__ void quantise_store(uint8_t* codes, uint8_t* scales, 
   }
 }
 
-// A warp takes one token and up to HEADS heads of its keys or of its values.
-template <int D, bool INTER>
-__device__ __forceinline__ void append_heads(const Kv4View& c, const AppendArgs& a, long long unit, int* err_flag) {
+// A warp takes one token and up to HEADS heads of its keys or of its values. Values are not rotated,
+// so that a lane's elements are neighbours.
+template <int D, bool INTER, bool V>
+__device__ __forceinline__ void append_heads(const Kv4View& c, const AppendArgs& a, int t, int h0, int* err_flag) {
   constexpr int L = D / 16, ROWS = 32 / L, PASSES = HEADS / ROWS;
-  const int blocks = (c.heads + HEADS - 1) / HEADS;
-  const long long token = unit / (2 * blocks);
-  if (token >= a.tokens) return;
-  const int t = (int)token, block = (int)(unit - token * (2 * blocks));
-  const bool is_v = block >= blocks;
-  const int h0 = (is_v ? block - blocks : block) * HEADS;
   const int lane = threadIdx.x & 31, sub = lane / L;
   const Lane<D, INTER> ln(a.rot);
-  const bf16* src = is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride;
+  const bf16* src = V ? a.v + t * a.v_stride : a.k + t * a.k_stride;
   uint4 raw[PASSES][2];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
@@ -218,7 +226,7 @@ __device__ __forceinline__ void append_heads(const Kv4View& c, const AppendArgs&
     return;
   }
   float an[16];
-  if (!is_v && ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
+  if (!V && ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int h = h0 + p * ROWS + sub;
@@ -230,11 +238,11 @@ __device__ __forceinline__ void append_heads(const Kv4View& c, const AppendArgs&
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[4 * q + i] = (pair)(w[i] << 16) | ((pair)(w[i] & 0xffff0000u) << 32);
     }
-    if (!is_v) norm_rotate_exact<D, INTER>(y, ln, a.k_norm, a.eps, an);
+    if (!V) norm_rotate_exact<D, INTER>(y, ln, a.k_norm, a.eps, an);
     const long long row = (((long long)page * c.heads + (on ? h : 0)) << c.page_log2) + (pos & (c.page - 1));
-    const float unit_of = kv4_unit(is_v ? c.v_unit : c.k_unit, on ? h : 0);
-    quantise_store<D, INTER>(is_v ? c.v : c.k, is_v ? c.v_scale : c.k_scale, row, on, y, ln, a.rot, unit_of);
-    if (!is_v && a.k_out && on) {
+    const float unit = kv4_unit(V ? c.v_unit : c.k_unit, on ? h : 0);
+    quantise_store<D, INTER>(V ? c.v : c.k, V ? c.v_scale : c.k_scale, row, on, y, ln, a.rot, unit);
+    if (!V && a.k_out && on) {
       float z[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -247,13 +255,27 @@ __device__ __forceinline__ void append_heads(const Kv4View& c, const AppendArgs&
   }
 }
 
+// Unit of keys and values: a token's blocks of heads, keys first.
+template <int D, bool INTER>
+__device__ __forceinline__ void append_unit(const Kv4View& c, const AppendArgs& a, long long unit, int* err_flag) {
+  const int blocks = (c.heads + HEADS - 1) / HEADS;
+  const long long token = unit / (2 * blocks);
+  if (token >= a.tokens) return;
+  const int block = (int)(unit - token * (2 * blocks));
+  if (block < blocks)
+    append_heads<D, INTER, false>(c, a, (int)token, block * HEADS, err_flag);
+  else
+    append_heads<D, true, true>(c, a, (int)token, (block - blocks) * HEADS, err_flag);
+}
+
 // Few tokens: key / value warps, then query warps, in one grid.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 3) k_append_kv4(Kv4View c, AppendArgs a, long long kv_units, int* err_flag) {
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long unit = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
   if (unit < kv_units)
-    append_heads<D, INTER>(c, a, unit, err_flag);
+    append_unit<D, INTER>(c, a, unit, err_flag);
   else if (a.q)
     rotate_queries<D, INTER>(c, a, unit - kv_units, err_flag);
   report_offsets(a.cu, c.batch, a.tokens, err_flag);
@@ -264,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_append_kv4(Kv4View c, AppendArgs
 template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 3) k_append_heads(Kv4View c, AppendArgs a, int* err_flag) {
   asm volatile("griddepcontrol.launch_dependents;");
-  append_heads<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
+  append_unit<D, INTER>(c, a, (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), err_flag);
   report_offsets(a.cu, c.batch, a.tokens, err_flag);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
   __shared__ uint2 warp_counts[WARPS], piece_counts;   // above the border, equal to it
   __shared__ int found[2];               // bin, tokens above it
   asm volatile("griddepcontrol.launch_dependents;");   // k_evict_move may be set up meanwhile
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what the kernel before writes is there
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), size = (int)cluster.num_blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
   for (int b = threadIdx.x; b < BINS; b += THREADS) hist[0][b] = 0;
   __syncthreads();
   // ---- the smallest weight kept: digit by digit from the top ----
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 8;
   for (int i0 = begin; i0 < end; i0 += 32 * AHEAD) {
     float x[AHEAD];
 #pragma unroll
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     if (pass > 0) {
       for (int b = threadIdx.x; b < BINS; b += THREADS) mine[b] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = begin + lane; i < end; i += 32) {
         const uint32_t u = key(i);
         if ((u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(mine + ((u >> shift) & 255), 1);
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
   }
   // ---- where the kept ones go: all above the border, and the first `need` equal to it ----
   uint32_t above = 0, equal = 0;
+#pragma unroll 4
   for (int i = begin + lane; i < end; i += 32) {
     const uint32_t u = key(i);
     above += u > prefix;
@@ -292,22 +295,24 @@ cudaError_t kv4_evict(const Kv4View& c, const int* kv_len, const float* mass, in
   const long long reach = (long long)c.max_pages << c.page_log2;
   int size = 1;
   while (size < MAX_CLUSTER && reach > 2048LL * size && items * size < 2LL * num_sms) size *= 2;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = size;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * size));
   cfg.blockDim = dim3(THREADS);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, k_evict_select, c, a, to.max_pages << to.page_log2, err_flag);
   if (e != cudaSuccess) return e;
   const int most = (int)(reach < keep ? reach : keep);
   const int per = 8 * (32 / (c.dim / 16)) * 4;             // tokens a CTA moves
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr + 1;                  // no clusters
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3((most + per - 1) / per, c.heads, c.batch);
   cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, c.dim == 64 ? k_evict_move<64> : k_evict_move<128>, c, to, kv_len, keep,
