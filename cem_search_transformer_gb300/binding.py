@@ -417,14 +417,21 @@ def _stream_on(stream, device: int) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _refuse(cache, other, what: str):
+    """Refuses a cache of the other width, whose handle the library would not take."""
+    if type(cache) is other:
+        raise JepaError(1, f"{what}: got a {other.__name__}")
+
+
 def _append_method(name: str):
     """Planner's append to one of the paged caches (jepa_<name> of the C header)."""
-    call = "jepa_" + name
+    call, other = "jepa_" + name, KvCache4 if name.endswith("8") else KvCache8
 
     def append(self, q, k, v, rope_table, cu, start, cache, q_out, q_norm=None, k_norm=None,
                norm_eps=1e-6, interleaved=False, k_out=None, stream=None):
         """Norm, rotate and append packed tokens: q [tokens, q_heads, head_dim] (or None with
         q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None."""
+        _refuse(cache, other, name)
         dev = self.device
         kp, ks, tokens, heads, dim = _rows(k, "k", dev)
         vp, vs, *v_shape = _rows(v, "v", dev)
@@ -464,10 +471,11 @@ def _append_method(name: str):
 
 def _read_method(name: str):
     """Planner's read-back of one of the paged caches."""
-    call = "jepa_" + name
+    call, other = "jepa_" + name, KvCache4 if name.startswith("kv8") else KvCache8
 
     def read(self, cache, cu, first, k_out, v_out, stream=None):
         """Cached tokens as bf16 into k_out, v_out [tokens, kv_heads, head_dim]."""
+        _refuse(cache, other, name)
         dev = self.device
         cache.check(dev)
         tokens = k_out.shape[0] if _sized(k_out, "k_out").dim() else 0
@@ -763,6 +771,7 @@ class Planner:
         tensor of attention_kv4_workspace bytes, one for each call that may run at a time. With
         mass_out [batch, kv_heads, max_pages * page_size] (and lse), also decay * mass + the weights
         that the cached tokens received (mass None: zeros; the same tensor: in place)."""
+        _refuse(cache, KvCache8, "attention_kv4")
         dev = self.device
         if getattr(q, "ndim", 0) != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
             raise JepaError(1, f"q must be [{cache.batch}, q_tokens, q_heads, {cache.head_dim}]")
@@ -794,6 +803,8 @@ class Planner:
         """Keep the last `recent` tokens of each sequence and head and those with the largest mass,
         `keep` in all, as the tokens of `to`'s pages; len_out [batch], mass_out (or None) [batch,
         kv_heads, to.max_pages * to.page_size]; workspace: kv4_evict_workspace bytes."""
+        _refuse(cache, KvCache8, "kv4_evict")
+        _refuse(to, KvCache8, "kv4_evict")
         dev = self.device
         cache.check(dev)
         to.check(dev)

@@ -514,3 +514,115 @@ def test_refusals(planner):
         fp32.attention_kv4(**ok)
     fp32.close()
     planner.sync_check()
+
+
+@pytest.mark.parametrize("dim,q_tokens,group,heads", [(128, 1, 4, 8), (64, 2, 1, 16), (128, 2, 8, 4), (64, 3, 5, 6)])
+def test_short_sequences_a_warp_each(planner, dim, q_tokens, group, heads):
+    """As many (sequence, head) items of at most a few hundred tokens as the machine has warps: 3 or 4 CTAs a SM with four
+    warps, one fewer where a head has more than 8 query rows."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    slots = sms * 4 * ((4 if dim == 64 else 3) - (q_tokens * group > 8))
+    tiles = -(-q_tokens * group // (16 if q_tokens * group > 8 else 8))
+    batch = slots // (heads * tiles)
+    rng = np.random.default_rng(dim)
+    lens = [int(n) for n in rng.integers(0, 40, batch)]
+    lens[0], lens[1], lens[2] = 300, 0, 257
+    pool = Pool4(lens, heads, 16, dim)
+    ref = pool.fill(lens, 3)
+    check_attention(planner, pool, ref, lens, q_tokens, heads * group, q_tokens != 2, seed=1)
+
+
+def test_thousands_of_sequences_most_of_them_empty(planner):
+    lens = [0] * 3000
+    for s, n in ((0, 3), (17, 2500), (1031, 70), (2999, 129)):
+        lens[s] = n
+    pool = Pool4(lens, 2, 64, 64)
+    ref = pool.fill(lens, 6)
+    check_attention(planner, pool, ref, lens, 1, 8, True, seed=3)
+
+
+def test_offsets_past_32_bits(planner):
+    """Pools of more than 2^32 bytes of codes: the same tokens at the first and at the last pages."""
+    from cem_search_transformer_gb300 import binding
+    heads, page, dim, n = 8, 128, 128, 300
+    pages = 2 ** 32 // (heads * page * dim // 2) + 9
+    u8 = lambda k: torch.empty(pages, heads, page, k, dtype=torch.uint8, device="cuda")  # noqa: E731
+    pools = u8(dim // 2), u8(dim // 2), u8(dim // 16), u8(dim // 16)
+    rows = bf16(np.random.default_rng(2).standard_normal((n, heads, dim))).cuda()
+    q = bf16(np.random.default_rng(3).standard_normal((1, 1, 16, dim))).cuda()
+    got = []
+    for first in (0, pages - 3):
+        table = i32([[first, first + 1, first + 2]])
+        cache = binding.KvCache4(*pools, table)
+        planner.rope_append_kv4(None, rows, rows, None, cu_of([n]), i32([0]), cache, None)
+        k, v = torch.empty_like(rows), torch.empty_like(rows)
+        planner.kv4_read(cache, cu_of([n]), i32([0]), k, v)
+        out, lse, mass = torch.empty_like(q), torch.empty(1, 1, 16, device="cuda"), torch.zeros(1, heads, 3 * page, device="cuda")
+        ws = torch.empty(planner.attention_kv4_workspace(cache), dtype=torch.uint8, device="cuda")
+        planner.attention_kv4(q, cache, i32([n]), out, 0.1, ws, lse=lse, mass_out=mass)
+        to = binding.KvCache4(*pools, i32([[pages - 5 if first else 4]]))
+        keep, new_len = torch.empty(1, heads, page, device="cuda"), i32([0])
+        work = torch.empty(planner.kv4_evict_workspace(cache, 100), dtype=torch.uint8, device="cuda")
+        planner.kv4_evict(cache, i32([n]), mass, 100, 10, to, new_len, keep, work)
+        kept = torch.empty(100, heads, dim, dtype=torch.bfloat16, device="cuda")
+        planner.kv4_read(to, cu_of([100]), i32([0]), kept, torch.empty_like(kept))
+        planner.sync_check()
+        got.append((k, v, out, lse, mass, keep, kept))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n_new", [[1, 1, 1], [700, 3, 1500]])
+def test_captured_append_attention_and_read(planner, n_new):
+    """One graph with torch's kernels, copies and the calls, replayed with other inputs and lengths; both shapes of the append."""
+    page, dim, heads, q_heads = 32, 64, 8, 16
+    old = [40, 0, 95]
+    total, cu = sum(n_new), cu_of(n_new)
+    lens = [a + b for a, b in zip(old, n_new)]
+    rng = np.random.default_rng(21)
+    rope = planner.rope_table(2048, dim)
+    past = [bf16(rng.standard_normal((sum(old), heads, dim))).cuda() for _ in range(2)]
+    pool = Pool4(lens, heads, page, dim, seed=5)
+    planner.rope_append_kv4(None, *past, rope, cu_of(old), i32([0] * 3), pool.cache, None)
+    reach = pool.table.shape[1] * page
+    given = [torch.empty(total, h, dim, dtype=torch.bfloat16, device="cuda") for h in (q_heads, heads, heads)]
+    start, kv_len = i32(old), i32(lens)
+
+    def buffers():
+        return [torch.empty(total, h, dim, dtype=torch.bfloat16, device="cuda") for h in (q_heads, heads, heads)] + \
+            [torch.empty(3, 1, q_heads, dim, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 1, q_heads, device="cuda"),
+             torch.zeros(3, heads, reach, device="cuda")]
+
+    def steps(x, q_out, k, v, att, lse, mass, ws, stream=None):
+        planner.rope_append_kv4(*x, rope, cu, start, pool.cache, q_out, stream=stream)
+        planner.attention_kv4(q_out[-3:].unsqueeze(1), pool.cache, kv_len, att, 0.125, ws, lse=lse, mass=mass, mass_out=mass,
+                              decay=0.5, stream=stream)
+        planner.kv4_read(pool.cache, cu, start, k, v, stream=stream)
+    ws = torch.empty(planner.attention_kv4_workspace(pool.cache), dtype=torch.uint8, device="cuda")
+    x, got = [torch.empty_like(t) for t in given], buffers()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for a, b in zip(x, given):
+            a.zero_()
+            a.add_(b)
+        got[-1].zero_()
+        steps(x, *got, ws, stream=torch.cuda.current_stream())
+        steps(x, *got, ws, stream=torch.cuda.current_stream())        # the same tokens again: only the weights move on
+        for t in x:
+            t.zero_()                                                 # the calls are done with their inputs
+    for seed in range(3):
+        values = [bf16(np.random.default_rng(seed).standard_normal(t.shape)).cuda() for t in given]
+        for a, b in zip(given, values):
+            a.copy_(b)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        want = buffers()
+        steps(values, *want, ws)
+        steps(values, *want, ws)
+        planner.sync_check()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -66,6 +66,8 @@ def masses(rng, batch, heads, reach, kind):
     ([20000], 1, 128, 64, 64, 5000, 100, "ties"),               # a cluster of eight
     ([20000, 19000], 2, 64, 128, 64, 1, 0, "plain"),            # one token
     ([70] * 200, 2, 64, 16, 16, 33, 4, "plain"),
+    ([100000], 1, 64, 128, 128, 3000, 50, "ties"),              # pieces beyond what shared memory holds
+    ([100000], 1, 64, 128, 128, 50000, 0, "odd"),
 ])
 def test_matches_oracle(planner, lens, heads, dim, page, to_page, keep, recent, kind):
     rng = np.random.default_rng(keep)

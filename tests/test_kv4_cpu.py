@@ -117,6 +117,19 @@ def test_calls_refuse_before_the_library(monkeypatch):
         binding.Planner.kv4_evict(_NoLibrary(), _Cache(), n, q, 4, 1, _Cache(), n, None, None)
 
 
+def test_caches_of_the_other_width_are_refused():
+    eight, four = binding.KvCache8.__new__(binding.KvCache8), binding.KvCache4.__new__(binding.KvCache4)
+    p, t = binding.Planner, torch.zeros(1)
+    for call, match in ((lambda: p.rope_append_kv4(_NoLibrary(), None, t, t, None, t, t, eight, None), "KvCache8"),
+                        (lambda: p.rope_append_kv8(_NoLibrary(), None, t, t, None, t, t, four, None), "KvCache4"),
+                        (lambda: p.kv4_read(_NoLibrary(), eight, t, t, t, t), "KvCache8"),
+                        (lambda: p.kv8_read(_NoLibrary(), four, t, t, t, t), "KvCache4"),
+                        (lambda: p.attention_kv4(_NoLibrary(), t, eight, t, t, 0.1, t), "KvCache8"),
+                        (lambda: p.kv4_evict(_NoLibrary(), four, t, t, 1, 0, eight, t, t, t), "KvCache8")):
+        with pytest.raises(binding.JepaError, match=match):
+            call()
+
+
 def test_rows_refuse():
     x = torch.zeros(4, 32)
     binding._sized(x, "x")
