@@ -11,7 +11,7 @@
 //     smallest weight kept is found in four passes of eight bits over order-preserving integers, each CTA's
 //     counts read by the others through distributed shared memory; then every CTA knows how many it
 //     keeps and writes their places. No atomics across CTAs: the result does not depend on their order.
-//   * k_evict_move: 16 bytes a lane, four tokens in flight.
+//   * k_evict_move: 16 bytes a lane, two tokens in flight.
 #include "kv4.cuh"
 
 #include <cooperative_groups.h>
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
 template <int D>
 __global__ void __launch_bounds__(256) k_evict_move(Kv4View c, Kv4View to, const int* kv_len, int keep,
                                                     const int* places, int* err_flag) {
-  constexpr int LPT = D / 16, RPW = 32 / LPT, AHEAD = 4;   // lanes a token, half of them K's, half V's
+  constexpr int LPT = D / 16, RPW = 32 / LPT, AHEAD = 2;   // lanes a token, half of them K's, half V's
   constexpr int KB = D / 2, SB = D / 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the places are there
   const int s = blockIdx.z, head = blockIdx.y, lane = threadIdx.x & 31;
@@ -310,7 +310,7 @@ cudaError_t kv4_evict(const Kv4View& c, const int* kv_len, const float* mass, in
   cudaError_t e = cudaLaunchKernelEx(&cfg, k_evict_select, c, a, to.max_pages << to.page_log2, err_flag);
   if (e != cudaSuccess) return e;
   const int most = (int)(reach < keep ? reach : keep);
-  const int per = 8 * (32 / (c.dim / 16)) * 4;             // tokens a CTA moves
+  const int per = 8 * (32 / (c.dim / 16)) * 2;             // tokens a CTA moves
   cfg.attrs = attr + 1;                  // no clusters
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((most + per - 1) / per, c.heads, c.batch);
