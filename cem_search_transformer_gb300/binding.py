@@ -261,9 +261,10 @@ def _rows(t, name: str, device: Optional[int] = None):
     st = t.stride()
     if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
         raise JepaError(1, f"{name}: the heads of a token must be contiguous")
-    if not t.is_cuda:
+    at = t.get_device()                  # -1: host memory
+    if at < 0:
         raise JepaError(1, f"{name} must be a CUDA tensor")
-    if device is not None and t.get_device() != device:
+    if device is not None and at != device:
         raise JepaError(1, f"{name} is on {t.device}, the planner on cuda:{device}")
     return t.data_ptr(), (st[0] if n > 1 else heads * dim), n, heads, dim
 

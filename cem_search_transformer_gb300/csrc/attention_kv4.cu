@@ -40,12 +40,11 @@ struct Shape {
   static constexpr int UNIT = SHARERS * KS;        // keys of a unit
   static constexpr int KB = D / 2, SB = D / 16;    // bytes of a key's codes, and of its scales
   static constexpr int KW = D / 32;                // 32-bit words of a key a lane takes
-  [[maybe_unused]] static constexpr int VW = D / 64;   // 32-bit words of a V row a lane takes
-  [[maybe_unused]] static constexpr int MT = D / 16;   // output tiles of 16 columns
+  static constexpr int VW = D / 64;   // 32-bit words of a V row a lane takes
   static constexpr int KINDS = KIND == WEIGHTS ? 1 : 2;        // K, or K and V
   static constexpr int OFF_V = KS * KB, OFF_SC = KINDS * KS * KB;   // of a stage: K, V codes, K, V scales
   static constexpr int STAGE = OFF_SC + KINDS * KS * SB;
-  [[maybe_unused]] static constexpr int OUT_LD = OUT_ROW<D>;
+  static constexpr int OUT_LD = OUT_ROW<D>;
   static constexpr int OFF_OUT = WARPS * NST * STAGE;
   static constexpr int SMEM = OFF_OUT + (KIND == BY_CTA ? WARPS * ROWS * OUT_LD * 4 : 0);
   static_assert(2 * KS * SB / 16 <= 32, "a step's scales are a chunk a lane at most");
@@ -121,6 +120,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
     k_attention_kv4(Kv4View c, Args a, MassArgs ma, int whole, int* err_flag) {
   using S = Shape<D, NR, KIND>;
   constexpr int ROWS = S::ROWS, NST = S::NST;
+  [[maybe_unused]] constexpr int MT = D / 16;          // output tiles of 16 columns
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // worker of the line: the CTA, or the warp
@@ -263,20 +263,20 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
   const int tiles = KIND == WEIGHTS ? (rows + ROWS - 1) / ROWS : 1;   // row tiles of an item of the weights
   // scores of a stage's 16-key group p: keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
   auto scores = [&](const uint8_t* kb, int p, const Queries<D, NR>& qr, float (&x)[NR][4]) {
-            uint32_t w[2][S::KW], f[2][S::VW];
+    uint32_t w[2][S::KW], f[2][S::VW];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = 16 * p + 8 * h;
-              if (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4*>(kb + at_k + row * S::KB);
-                w[h][0] = x.x; w[h][1] = x.y; w[h][S::KW - 2] = x.z; w[h][S::KW - 1] = x.w;
-                key_scales<D>(*reinterpret_cast<const uint16_t*>(kb + at_ks + row * S::SB), f[h]);
-              } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(kb + at_k + row * S::KB);
-                w[h][0] = x.x; w[h][1] = x.y;
-                key_scales<D>(kb[at_ks + row * S::SB], f[h]);
-              }
-            }
+    for (int h = 0; h < 2; ++h) {
+      const int row = 16 * p + 8 * h;
+      if (D == 128) {
+        const uint4 y = *reinterpret_cast<const uint4*>(kb + at_k + row * S::KB);
+        w[h][0] = y.x; w[h][1] = y.y; w[h][S::KW - 2] = y.z; w[h][S::KW - 1] = y.w;
+        key_scales<D>(*reinterpret_cast<const uint16_t*>(kb + at_ks + row * S::SB), f[h]);
+      } else {
+        const uint2 y = *reinterpret_cast<const uint2*>(kb + at_k + row * S::KB);
+        w[h][0] = y.x; w[h][1] = y.y;
+        key_scales<D>(kb[at_ks + row * S::SB], f[h]);
+      }
+    }
     scores_of<D, NR>(w, f, qr.qf, x);
   };
   int stage = 0;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
     } else {
     qr.load(a, s, head, r0, rows, len);
     scale_queries(qr, k_unit);
-    float o[NR][S::MT][4];
+    float o[NR][MT][4];
     float m[NR][2], ref[NR][2], l[NR][2];        // ref: m - P_SHIFT, 0 before the first key
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
       ref[nr][0] = ref[nr][1] = 0.f;
       l[nr][0] = l[nr][1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < S::MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
+      for (int i = 0; i < MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
     }
 
     for (int k = sg.k0; k < sg.k1; ++k) {
@@ -382,9 +382,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
 
       float sc[S::GROUPS][NR][4];
 #pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) {
-        scores(kb, p, qr, sc[p]);
-      }
+      for (int p = 0; p < S::GROUPS; ++p) scores(kb, p, qr, sc[p]);
       const bool edge = key0 + S::KS > qr.lim_min;   // some row does not see some key (warp-uniform)
       bool move = false;
       float top[NR][2];
@@ -422,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
             ref[nr][e] = mn == -INFINITY ? 0.f : mn - P_SHIFT;
             l[nr][e] *= al;
 #pragma unroll
-            for (int d = 0; d < S::MT; ++d) {
+            for (int d = 0; d < MT; ++d) {
               o[nr][d][e] *= al;
               o[nr][d][2 + e] *= al;
             }
@@ -500,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
             float hit[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(hit, n0, n0, n1, n1, see[0], see[1]);
 #pragma unroll
-            for (int d = 0; d < S::MT; ++d)
+            for (int d = 0; d < MT; ++d)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 if (hit[e] > 0.f) o[nr][d][e] = __int_as_float(0x7fc00000);
@@ -524,15 +522,15 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
           const bool none = m[nr][e] == -INFINITY && x == 0.f;   // no key was seen (scores of NaN: a NaN sum)
           const float f = none ? 0.f : unit / x;
           const long long at = row_at(a, s, head, r);
-          uint32_t w[S::MT];
+          uint32_t w[MT];
 #pragma unroll
-          for (int d = 0; d < S::MT; ++d) {
+          for (int d = 0; d < MT; ++d) {
             const __nv_bfloat162 y = __floats2bfloat162_rn(o[nr][d][e] * f, o[nr][d][2 + e] * f);
             w[d] = *reinterpret_cast<const uint32_t*>(&y);
           }
           uint4* to = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
 #pragma unroll
-          for (int d = 0; d < S::MT; d += 4) to[d / 4] = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
+          for (int d = 0; d < MT; d += 4) to[d / 4] = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
           if (a.lse && g == 0) a.lse[at] = none ? -INFINITY : (ref[nr][e] + log2f(x)) * 0.69314718055994531f;
         }
     } else {
@@ -557,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
           }
           float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * (D / 8);
 #pragma unroll
-          for (int d = 0; d < S::MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
+          for (int d = 0; d < MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
             *reinterpret_cast<float4*>(to + 2 * d) =
                 make_float4(o[nr][d][e] * unit, o[nr][d][2 + e] * unit, o[nr][d + 1][e] * unit,
                             o[nr][d + 1][2 + e] * unit);
