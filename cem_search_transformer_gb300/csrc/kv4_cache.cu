@@ -300,39 +300,45 @@ __device__ __forceinline__ void read_token(const Kv4View& c, const int* __restri
     if (lane == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
   }
-  const int off = pos & (c.page - 1), chunks = c.heads * (D / 8);
-  constexpr int AHEAD = 8;                 // loads a lane has in flight
-  for (int i0 = lane; i0 < 2 * chunks; i0 += 32 * AHEAD) {
-    uint32_t u[AHEAD], scale[AHEAD];
+  // A lane's place in a head stays the same from turn to turn: its addresses move on by constants.
+  constexpr int CH = D / 8, TURN = 32 / CH, AHEAD = 4;   // chunks a head, heads of a turn, turns in flight
+  const int chunk = lane % CH, h0 = lane / CH;
+  const long long row = (((long long)pg * c.heads + h0) << c.page_log2) + (pos & (c.page - 1));
+  const long long codes = row * (D / 2) + 4 * chunk, scales = row * (D / 16) + (chunk >> 1);
+  const long long out = (t * c.heads + h0) * D + 8 * chunk;
+  const int step = TURN << c.page_log2;
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int i = i0 + 32 * k;
-      if (i >= 2 * chunks) break;
-      const bool is_v = i >= chunks;
-      const int j = is_v ? i - chunks : i, head = j / (D / 8), b = j % (D / 8);
-      const long long row = (((long long)pg * c.heads + head) << c.page_log2) + off;
-      u[k] = *reinterpret_cast<const uint32_t*>((is_v ? c.v : c.k) + row * (D / 2) + 4 * b);
-      scale[k] = (is_v ? c.v_scale : c.k_scale)[row * (D / 16) + (b >> 1)];
-    }
+  for (int kind = 0; kind < 2; ++kind) {
+    const uint8_t *from = (kind ? c.v : c.k) + codes, *sc_from = (kind ? c.v_scale : c.k_scale) + scales;
+    const float* units = kind ? c.v_unit : c.k_unit;
+    bf16* to = (kind ? v_out : k_out) + out;
+    for (int h = h0; h < c.heads; h += TURN * AHEAD) {
+      uint32_t u[AHEAD], sc[AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int i = i0 + 32 * k;
-      if (i >= 2 * chunks) break;
-      const bool is_v = i >= chunks;
-      const int j = is_v ? i - chunks : i;
-      const float unit = kv4_unit(is_v ? c.v_unit : c.k_unit, j / (D / 8));
-      const uint32_t sc = f16x2_of_e4m3_pair(scale[k] * 0x101u);
-      const uint32_t x[4] = {f16x2_of_e2m1x2<0>(u[k]), f16x2_of_e2m1x2<1>(u[k]), f16x2_of_e2m1x2<2>(u[k]),
-                             f16x2_of_e2m1x2<3>(u[k])};
-      float z[8];
+      for (int k = 0; k < AHEAD; ++k)
+        if (h + TURN * k < c.heads) {
+          u[k] = *reinterpret_cast<const uint32_t*>(from + (long long)(step * k) * (D / 2));
+          sc[k] = sc_from[(long long)(step * k) * (D / 16)];
+        }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[q]), *reinterpret_cast<const __half2*>(&sc));
-        const float2 f = __half22float2(y);
-        z[2 * q] = f.x * unit;
-        z[2 * q + 1] = f.y * unit;
-      }
-      store8((is_v ? v_out : k_out) + (t * chunks + j) * 8, z);
+      for (int k = 0; k < AHEAD; ++k)
+        if (h + TURN * k < c.heads) {
+          const uint32_t f2 = f16x2_of_e4m3_pair(sc[k]);
+          const float f = __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu))) * kv4_unit(units, h + TURN * k);
+          const uint32_t x[4] = {f16x2_of_e2m1x2<0>(u[k]), f16x2_of_e2m1x2<1>(u[k]), f16x2_of_e2m1x2<2>(u[k]),
+                                 f16x2_of_e2m1x2<3>(u[k])};
+          float z[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[q]));
+            z[2 * q] = y.x * f;
+            z[2 * q + 1] = y.y * f;
+          }
+          store8(to + TURN * k * D, z);
+        }
+      from += (long long)(step * AHEAD) * (D / 2);
+      sc_from += (long long)(step * AHEAD) * (D / 16);
+      to += TURN * AHEAD * D;
     }
   }
 }

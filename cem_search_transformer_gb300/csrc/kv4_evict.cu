@@ -96,9 +96,15 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
   const int pieces = size * WARPS, each = ((old + pieces - 1) / pieces + 31) & ~31;
   const int begin = min((long long)old, (long long)(rank * WARPS + warp) * each), end = min(old, begin + each);
   const int first = warp * each;         // of its piece among the CTA's
-  auto key = [&](int i) {
-    const int at = first + i - begin;
-    return at < HELD ? held[at] : ordered(__ldg(mass + i));
+  // f(i, weight) for the lane's tokens: those that are held, then those that are not
+  static_assert(HELD % 32 == 0, "a warp's turns are held or not as a whole");
+  const int held_end = min(end, begin + max(0, HELD - first));
+  const uint32_t* const mine_held = held + (first - begin);
+  auto each_token = [&](auto f) {
+    int i = begin + lane;
+#pragma unroll 4
+    for (; i < held_end; i += 32) f(i, mine_held[i]);
+    for (; i < end; i += 32) f(i, ordered(__ldg(mass + i)));
   };
   for (int b = threadIdx.x; b < BINS; b += THREADS) hist[0][b] = 0;
   __syncthreads();
@@ -131,11 +137,9 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     if (pass > 0) {
       for (int b = threadIdx.x; b < BINS; b += THREADS) mine[b] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int i = begin + lane; i < end; i += 32) {
-        const uint32_t u = key(i);
+      each_token([&](int, uint32_t u) {
         if ((u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(mine + ((u >> shift) & 255), 1);
-      }
+      });
     }
     cluster.sync();
     if (threadIdx.x < BINS) {
@@ -176,12 +180,10 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
   }
   // ---- where the kept ones go: all above the border, and the first `need` equal to it ----
   uint32_t above = 0, equal = 0;
-#pragma unroll 4
-  for (int i = begin + lane; i < end; i += 32) {
-    const uint32_t u = key(i);
+  each_token([&](int, uint32_t u) {
     above += u > prefix;
     equal += u == prefix;
-  }
+  });
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) warp_counts[warp] = make_uint2(above, equal);
@@ -209,9 +211,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     }
   cluster.sync();                        // every CTA's counts have been read before it ends
   const uint32_t below = (1u << lane) - 1, last = (uint32_t)need;
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t u = i < end ? key(i) : 0u;
+  auto place = [&](int i, uint32_t u) {
     const bool gt = i < end && u > prefix, eq = i < end && u == prefix;
     const uint32_t gts = __ballot_sync(0xffffffffu, gt), eqs = __ballot_sync(0xffffffffu, eq);
     const uint32_t e = equal + __popc(eqs & below);
@@ -222,7 +222,11 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     }
     above += __popc(gts);
     equal += __popc(eqs);
-  }
+  };
+  int i0 = begin;
+#pragma unroll 2
+  for (; i0 < held_end; i0 += 32) place(i0 + lane, i0 + lane < end ? mine_held[i0 + lane] : 0u);
+  for (; i0 < end; i0 += 32) place(i0 + lane, i0 + lane < end ? ordered(__ldg(mass + i0 + lane)) : 0u);
 }
 
 // A warp takes RPW kept tokens of a head at a time, AHEAD times.
