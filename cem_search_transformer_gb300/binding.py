@@ -123,7 +123,7 @@ def load(path: str = _LIB_PATH):
         "jepa_attention_packed": ([P, P, I64, P, I64, P, I64, I, I, I, I, I, I, P, P, F, I, P, P, P],
                                   I),
         "jepa_rope_append_kv4": ([P, CACHE4, P, I64, P, I64, P, I64, I, I, P, P, F, P, I, I, I, P, P,
-                                  P, P, P], I),
+                                  P, P, P, P], I),
         "jepa_kv4_read": ([P, CACHE4, P, P, I, P, P, P], I),
         "jepa_attention_kv4_workspace": ([P, CACHE4, ctypes.POINTER(Z)], I),
         "jepa_attention_kv4": ([P, CACHE4, P, I, I, P, F, I, P, P, P, P, F, P, Z, P], I),
@@ -426,12 +426,14 @@ def _refuse(cache, other, what: str):
 
 def _append_method(name: str):
     """Planner's append to one of the paged caches (jepa_<name> of the C header)."""
-    call, other = "jepa_" + name, KvCache4 if name.endswith("8") else KvCache8
+    eight = name.endswith("8")
+    call, other = "jepa_" + name, KvCache4 if eight else KvCache8
 
     def append(self, q, k, v, rope_table, cu, start, cache, q_out, q_norm=None, k_norm=None,
-               norm_eps=1e-6, interleaved=False, k_out=None, stream=None):
+               norm_eps=1e-6, interleaved=False, k_out=None, stream=None, rope_start=None):
         """Norm, rotate and append packed tokens: q [tokens, q_heads, head_dim] (or None with
-        q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None."""
+        q_out None), k and v [tokens, kv_heads, head_dim]; rope_table [positions, rot] or None;
+        rope_start [batch] (4-bit cache only): positions for the rotation where they are not start."""
         _refuse(cache, other, name)
         dev = self.device
         kp, ks, tokens, heads, dim = _rows(k, "k", dev)
@@ -455,12 +457,17 @@ def _append_method(name: str):
         cache.check(dev)
         if tokens < 1:
             raise JepaError(1, "tokens must be >= 1 (got 0)")
+        apart = ()
+        if not eight:
+            apart = (_opt(rope_start, "rope_start", "i32", cache.batch, dev),)
+        elif rope_start is not None:
+            raise JepaError(1, f"{name} takes no rope_start")
         st = getattr(self.lib, call)(
             self.h, cache.ref, qp, qs, kp, ks, vp, vs, tokens, q_heads,
             _opt(q_norm, "q_norm", "f32", dim, dev), _opt(k_norm, "k_norm", "f32", dim, dev), norm_eps,
             _opt(rope_table, "rope_table", "f32", positions * rot, dev), positions, rot,
             int(interleaved), _dev(cu, "cu", "i32", cache.batch + 1, dev),
-            _dev(start, "start", "i32", cache.batch, dev), qo,
+            _dev(start, "start", "i32", cache.batch, dev), *apart, qo,
             _opt(k_out, "k_out", "bf16", tokens * heads * dim, dev), _stream_on(stream, dev))
         if st:
             self._check(st, name)

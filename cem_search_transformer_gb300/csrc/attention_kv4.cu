@@ -17,6 +17,15 @@
 //     element in a byte), so that a conversion gives a register of the fragment.
 //   * No scale varies within what a warp accumulates, as pages' scales do in 8 bits: the units
 //     of a head multiply the scores and the outputs once.
+//   * The weights need the rows' sums, so their keys are read and multiplied a second time, by the same kernel
+//     without values. Holding the scores of short items in shared memory instead gained 1 to 7 us of 110
+//     (256 candidates of 776 tokens) and cost every other call half a microsecond.
+// Measured, inputs behind L2: two sequences of 100001 to 130001 tokens, 64 query heads over 8 of 128, 62 us
+// (4.5 TB/s; the kernel alone 57, 0.73 of the copy rate); 32 of 100 to 8000 tokens 40 us; 16 of 4000 to 30000
+// with weights 111 us, of which the weights' pass is 42; 256 of 776 tokens with 16 heads of 64, two queries and weights 110;
+// one of 517 tokens 8 us (latency). Bound by issue: 64 conversions and 64 products a 16-key group of 128 columns
+// share the SM's dispatch (a loop of the two alone issues 0.73 a cycle, this kernel 0.58 to 0.64), and no single part
+// that is left out of it (copies, products, exponentials, scales) makes it more than an eighth faster.
 #include "decode_line.cuh"
 
 #include "kv4.cuh"
@@ -32,15 +41,19 @@ enum Kind { BY_CTA, BY_WARP, WEIGHTS };
 template <int D, int NR, int KIND>
 struct Shape {
   static constexpr int ROWS = 8 * NR;              // query rows of an item
-  static constexpr int KS = D == 64 && NR == 1 ? 64 : 32;   // keys a warp takes in a step
-  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;    // cp.async stages of a warp
+  // Keys a warp takes in a step, cp.async stages of a warp and CTAs a SM. Heads of 64: steps of 64 keys in two
+  // stages 76 us (256 of 776 tokens), of 32 in three 78; four groups side by side hide more of each other's
+  // latency than turns of two (12% more). Heads of 128: three CTAs with three stages 57 us (the two long sequences),
+  // four with two 59.
+  static constexpr int KS = D == 64 && NR == 1 ? 64 : 32;
+  static constexpr int NST = D == 64 && NR == 1 ? 2 : 3;
   static constexpr int CTAS = (D == 64 ? 4 : 3) - (NR == 2);
   static constexpr int GROUPS = KS / 16;           // 16-key groups
   static constexpr int SHARERS = KIND == BY_CTA ? WARPS : 1;   // warps that share an item's keys
   static constexpr int UNIT = SHARERS * KS;        // keys of a unit
   static constexpr int KB = D / 2, SB = D / 16;    // bytes of a key's codes, and of its scales
   static constexpr int KW = D / 32;                // 32-bit words of a key a lane takes
-  static constexpr int VW = D / 64;   // 32-bit words of a V row a lane takes
+  static constexpr int VW = D / 64;                // 32-bit words of a V row a lane takes
   static constexpr int KINDS = KIND == WEIGHTS ? 1 : 2;        // K, or K and V
   static constexpr int OFF_V = KS * KB, OFF_SC = KINDS * KS * KB;   // of a stage: K, V codes, K, V scales
   static constexpr int STAGE = OFF_SC + KINDS * KS * SB;
@@ -607,7 +620,8 @@ cudaError_t launch(const Kv4View& c, Args a, const MassArgs* w, int* err_flag, i
   const long long slots = (long long)(num_sms < MAX_SMS ? num_sms : MAX_SMS) * S::CTAS;
   const long long items = (long long)c.batch * c.heads * a.tiles;
   const int whole = max_units <= WHOLE_UNITS;
-  // Short items a warp each, without barriers and joining, where their rounds fill the warps to four fifths.
+  // Short items a warp each, without barriers and joining, where their rounds fill the warps to four fifths: 4096 items of 776
+  // keys (84% of the rounds) 110 us with the weights, shared by four warps each 157.
   const long long warps = slots * WARPS, rounds = (items + warps - 1) / warps;
   cudaError_t e;
   if (whole && 5 * items >= 4 * rounds * warps) {
@@ -649,6 +663,7 @@ cudaError_t attention_kv4(const Kv4View& c, const bf16* q, int q_tokens, int q_h
   a.group = q_heads / c.heads;
   a.tiles = 0;
   a.causal = causal;
+  // up to 8 rows in one 8-wide tile: two long sequences with 8 rows 62 us, in the shape for 16 rows 79
   const bool narrow = q_tokens * a.group <= 8;
   if (c.dim == 64)
     return narrow ? launch<64, 1>(c, a, mass, err_flag, num_sms, s) : launch<64, 2>(c, a, mass, err_flag, num_sms, s);

@@ -44,6 +44,7 @@ struct AppendArgs {
   const float* rope;                         // [positions][rot]
   int positions, rot, interleaved;
   const int *cu, *start;                     // [batch + 1], [batch]
+  const int* rope_start = nullptr;           // [batch]: positions for the rotation where they are not the places
   bf16 *q_out, *k_out;                       // dense; k_out may be null
 };
 cudaError_t rope_append_kv8(const Kv8View& c, const AppendArgs& a, int* err_flag,

@@ -139,6 +139,19 @@ __device__ __forceinline__ int positions_of(const PageView& c, const AppendArgs&
   return min(a.positions, c.max_pages << c.page_log2);
 }
 
+// Place of packed token t of the sequence `at` in the cache, and its row of the rotary table (the same number
+// but where APART). False where either is out of range.
+template <bool APART>
+__device__ __forceinline__ bool place_of(const PageView& c, const AppendArgs& a, const Place& at, int t, int& pos,
+                                         int& row) {
+  pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
+  row = pos;
+  if (!APART || !a.rope_start) return at.first >= 0 && pos >= 0 && pos < positions_of(c, a);
+  const int from = __ldg(a.rope_start + at.s);
+  row = (int)((unsigned)from + (unsigned)(t - at.begin));
+  return at.first >= 0 && pos >= 0 && pos < (c.max_pages << c.page_log2) && from >= 0 && row >= 0 && row < a.positions;
+}
+
 // Launch that, with `early`, begins while the kernel before it in the stream still runs: what may
 // not overlap stands behind a griddepcontrol.wait, which lasts until that kernel's end.
 template <class... P, class... A>
@@ -192,7 +205,7 @@ __device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>
 // loads of the rows and of the token's sequence go out together.
 constexpr int Q_HEADS = 8;
 
-template <int D, bool INTER>
+template <int D, bool INTER, bool APART = false>
 __device__ __forceinline__ void rotate_queries(const PageView& c, const AppendArgs& a,
                                                long long unit, int* err_flag) {
   constexpr int L = D / 16, ROWS = 32 / L, PASSES = Q_HEADS / ROWS;
@@ -210,13 +223,13 @@ __device__ __forceinline__ void rotate_queries(const PageView& c, const AppendAr
   }
   const Place at = locate(a.cu, a.start, c.batch, t);
   if (!holds(at, t, a.tokens)) return;            // left as it is
-  const int pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
-  if (at.first < 0 || pos < 0 || pos >= positions_of(c, a)) {
+  int pos, row;
+  if (!place_of<APART>(c, a, at, t, pos, row)) {
     if ((threadIdx.x & 31) == 0) atomicOr(err_flag, DEV_ERR_INDEX);
     return;
   }
   float an[16];
-  if (ln.rotates) load_angles(an, a.rope + (long long)pos * a.rot, a.rot, ln.p);
+  if (ln.rotates) load_angles(an, a.rope + (long long)row * a.rot, a.rot, ln.p);
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     float y[16];

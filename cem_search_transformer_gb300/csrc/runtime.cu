@@ -1488,8 +1488,8 @@ jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, con
                                  const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
                                  const float* q_norm, const float* k_norm, float norm_eps,
                                  const float* rope_table, int positions, int rot, int interleaved,
-                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
-                                 uint16_t* k_out, void* stream) {
+                                 const int32_t* cu, const int32_t* start, const int32_t* rope_start,
+                                 uint16_t* q_out, uint16_t* k_out, void* stream) {
   if (!ctx) return JEPA_ERR_INVALID_ARG;
   Kv4View c;
   const jepa_status st = kv4_view(ctx, "rope_append_kv4", cache, &c);
@@ -1499,6 +1499,8 @@ jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, con
                                       q_heads, q_norm, k_norm, norm_eps, rope_table, positions, rot,
                                       interleaved, cu, start, q_out, k_out, &a);
   if (bad) return bad;
+  if (!aligned(rope_start, 4)) return fail(ctx, JEPA_ERR_INVALID_ARG, "rope_append_kv4: bad argument");
+  a.rope_start = rope_start;
   OnDevice on(ctx->device);
   CK(on.status);
   CK(rope_append_kv4(c, a, ctx->dev_err, (cudaStream_t)stream));
@@ -1587,12 +1589,14 @@ jepa_status jepa_kv4_evict(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int
     return fail(ctx, JEPA_ERR_SHAPE, "kv4_evict: the caches differ in batch, heads or head_dim");
   if (t.k_unit != c.k_unit || t.v_unit != c.v_unit)
     return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_evict: the caches must have the same units");
-  if ((long long)t.max_pages * t.page < keep)
-    return fail(ctx, JEPA_ERR_SHAPE, "kv4_evict: the target's table names fewer than keep tokens");
   if (workspace_bytes < kv4_evict_workspace(c, keep))
     return fail(ctx, JEPA_ERR_INVALID_ARG, "kv4_evict: the workspace is too small");
   OnDevice on(ctx->device);
   CK(on.status);
+  // a budget beyond what the target's table can name is that
+  const long long room = (long long)t.max_pages * t.page;
+  if (keep > room) keep = (int)room;
+  if (recent > keep) recent = keep;
   CK(kv4_evict(c, kv_len, mass, keep, recent, t, len_out, mass_out, workspace, ctx->dev_err,
                ctx->num_sms, (cudaStream_t)stream));
   return JEPA_OK;

@@ -435,14 +435,16 @@ typedef struct {
  * e4m3(max|x| / 6 / unit), nearest even, at least 2^-9 and at most 448; codes = e2m1(x / (scale * unit)),
  * nearest even, saturating. A block that holds a NaN or an infinity gets a NaN scale and reads as NaN. For
  * keys the norm's factor 1 / sqrt(mean(x^2) + norm_eps) is rounded once to fp32 and multiplied by the
- * weight first, and each product and sum of the rotation is rounded to fp32. */
+ * weight first, and each product and sum of the rotation is rounded to fp32. rope_start [batch] int32 dev or
+ * NULL: token i of sequence b lies at place start[b] + i - cu[b] and is rotated for position rope_start[b] + i -
+ * cu[b], as it has to be behind an eviction; NULL: both are start. */
 jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
                                  int64_t q_stride, const uint16_t* k, int64_t k_stride,
                                  const uint16_t* v, int64_t v_stride, int tokens, int q_heads,
                                  const float* q_norm, const float* k_norm, float norm_eps,
                                  const float* rope_table, int positions, int rot, int interleaved,
-                                 const int32_t* cu, const int32_t* start, uint16_t* q_out,
-                                 uint16_t* k_out, void* stream);
+                                 const int32_t* cu, const int32_t* start, const int32_t* rope_start,
+                                 uint16_t* q_out, uint16_t* k_out, void* stream);
 
 /* Read cached tokens back as bf16 (exact), as jepa_kv8_read. */
 jepa_status jepa_kv4_read(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int32_t* cu,
@@ -482,7 +484,8 @@ jepa_status jepa_kv4_evict_workspace(jepa_ctx* ctx, const jepa_kv4_cache* cache,
  *   one sequence and hold no token that `cache` names (shared pages are thus never written), but for
  *   sequences with n <= keep, which may name the same pages in both tables where the page sizes are equal.
  *   kv_len, len_out [batch] int32 dev; mass [batch][kv_heads][max_pages * page_size] float32 dev;
- *   0 <= recent <= keep, 1 <= keep <= to->max_pages * to->page_size; workspace as above, 256-byte
+ *   0 <= recent <= keep, 1 <= keep <= 2^30; where to's table names fewer than keep tokens it counts as so many
+ *   (recent too); workspace as above, 256-byte
  *   aligned. Calls that may overlap on the device need a workspace each. */
 jepa_status jepa_kv4_evict(jepa_ctx* ctx, const jepa_kv4_cache* cache, const int32_t* kv_len,
                            const float* mass, int keep, int recent, const jepa_kv4_cache* to,

@@ -198,6 +198,45 @@ def test_in_place_and_again(planner):
         assert torch.equal(a, b)
 
 
+def test_positions_apart_from_places(planner):
+    """rope_start: tokens are rotated for other positions than their places, which may lie behind the table's end."""
+    from cem_search_transformer_gb300 import binding
+    n, old, at, page, dim = [3, 0, 70], [60, 5, 0], [900, 7, 130], 32, 128
+    lens = [a + b for a, b in zip(n, old)]
+    rng = np.random.default_rng(4)
+    rows = [bf16(rng.standard_normal((73, h, dim))).cuda() for h in (4, 2, 2)]
+    table = planner.rope_table(1000, 64)
+    got = []
+    for first, apart in ((old, at), (at, None)):
+        pool = Pool4([a + b for a, b in zip(n, first)], 2, page, dim, seed=1)
+        q_out, k_out = torch.empty_like(rows[0]), torch.empty_like(rows[1])
+        planner.rope_append_kv4(*rows, table, cu_of(n), i32(first), pool.cache, q_out, k_out=k_out, interleaved=True,
+                                rope_start=None if apart is None else i32(apart))
+        k_read, v_read = torch.empty_like(rows[1]), torch.empty_like(rows[2])
+        planner.kv4_read(pool.cache, cu_of(n), i32(first), k_read, v_read)
+        planner.sync_check()
+        got.append((q_out, k_out, k_read, v_read))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    pool = Pool4(lens, 2, page, dim, seed=1)
+    short = planner.rope_table(40, 64)                                # places may pass the table's end, positions may not
+    q_out = torch.full_like(rows[0], 5.0)
+    planner.rope_append_kv4(*rows, short, cu_of(n), i32(old), pool.cache, q_out, rope_start=i32([37, 0, 38]))
+    with pytest.raises(binding.JepaError, match="outside"):
+        planner.sync_check()
+    assert not torch.any(torch.all(q_out[:5].reshape(5, -1) == 5.0, 1)) and torch.all(q_out[5:] == 5.0)
+    planner.rope_append_kv4(*rows, short, cu_of(n), i32(old), pool.cache, q_out, rope_start=i32([-1, 0, 2 ** 31 - 3]))
+    with pytest.raises(binding.JepaError, match="outside"):
+        planner.sync_check()
+    with pytest.raises(binding.JepaError, match="elements"):
+        planner.rope_append_kv4(*rows, short, cu_of(n), i32(old), pool.cache, q_out, rope_start=i32([0, 0]))
+    u8 = torch.zeros(8, 2, 32, 128, dtype=torch.uint8, device="cuda")
+    ones = torch.ones(8, 2, device="cuda")
+    eight = binding.KvCache8(u8, u8.clone(), ones, ones.clone(), i32(np.arange(9).reshape(3, 3) % 8))
+    with pytest.raises(binding.JepaError, match="rope_start"):
+        planner.rope_append_kv8(*rows, short, cu_of(n), i32(old), eight, q_out, rope_start=i32(old))
+
+
 def test_bad_pages_positions_and_offsets_are_skipped_and_reported(planner):
     from cem_search_transformer_gb300 import binding
     n, page, dim = [20, 20, 20, 20], 16, 64

@@ -125,6 +125,25 @@ def test_same_buffers_and_sequences_that_stay(planner):
         assert torch.equal(t[others], b[others])
 
 
+def test_budgets_beyond_the_targets_room(planner):
+    """keep above what the target's table names counts as that; above a sequence's length all stay."""
+    lens, heads, page, dim = [300, 40], 2, 16, 64
+    pool = Pool4(lens, heads, page, dim, seed=2)
+    pool.fill(lens, 3)
+    m = masses(np.random.default_rng(8), 2, heads, pool.table.shape[1] * page, "plain")
+    for keep, recent in ((48, 48), (1000, 7), (1000, 999)):
+        to = Target(pool, 2, 48)
+        mass_out, len_out = torch.empty(2, heads, 48, device="cuda"), i32([0, 0])
+        ws = torch.empty(planner.kv4_evict_workspace(pool.cache, keep), dtype=torch.uint8, device="cuda")
+        planner.kv4_evict(pool.cache, i32(lens), torch.from_numpy(m).cuda(), keep, recent, to.cache, len_out, mass_out, ws)
+        planner.sync_check()
+        assert len_out.tolist() == [48, 40]
+        for s, n in enumerate(lens):
+            for h in range(heads):
+                at = four_bit.kept(m[s, h, :n], 48, min(recent, 48))
+                assert np.array_equal(mass_out[s, h, :len(at)].cpu().numpy(), m[s, h, at]) and not mass_out[s, h, len(at):].any()
+
+
 def test_captured_and_on_two_streams(planner):
     lens, keep, recent = [5000, 300], 512, 64
     pool = Pool4(lens, 2, 64, 64)
@@ -200,7 +219,7 @@ def test_refusals(planner):
     other = Pool4([64], 2, 16, 64)                           # units of its own
     wide = Pool4([64], 2, 16, 128)
     for change, match in ((dict(recent=33), "bad argument"), (dict(recent=-1), "bad argument"), (dict(keep=0), "bad argument"),
-                          (dict(keep=33), "fewer"), (dict(workspace=ws[:n - 4]), "small"), (dict(len_out=kv_len), "bad argument"),
+                          (dict(workspace=ws[:n - 4]), "small"), (dict(len_out=kv_len), "bad argument"),
                           (dict(to=other.cache, mass_out=None), "units"), (dict(to=wide.cache, mass_out=None), "differ"), (dict(mass=mass[:, :, :63].contiguous()), "elements"),
                           (dict(mass=None), "required"), (dict(mass_out=mass[:, :1, :16].contiguous()), "elements")):
         with pytest.raises(binding.JepaError, match=match):
@@ -243,13 +262,12 @@ def test_a_decoder_layer_step_by_step(planner):
         planner.linear_fp8(codes, scales, wq, sq, None, batch, n_out, width, 0, proj)
         qkv = proj.to(torch.bfloat16).view(batch, -1, dim)
         q_out = torch.empty(batch, q_heads, dim, dtype=torch.bfloat16, device="cuda")
-        # rotated for its position, stored behind the cached tokens: after an eviction these differ, so the
-        # rotation is a call of its own on a table that begins at the position
-        tables = torch.stack([rope[p - n:p - n + 128] for p, n in zip(seen, lens)])
-        for s in range(batch):
-            one = type(pool.cache)(now.k, now.v, now.ks, now.vs, now.table[s:s + 1], *pool.units)
-            planner.rope_append_kv4(qkv[s:s + 1, :q_heads], qkv[s:s + 1, q_heads:q_heads + heads], qkv[s:s + 1, q_heads + heads:],
-                                    tables[s], cu_of([1]), i32([lens[s]]), one, q_out[s:s + 1])
+        # stored behind the cached tokens, rotated for its position: after an eviction these differ
+        k_out = torch.empty(batch, heads, dim, dtype=torch.bfloat16, device="cuda")
+        planner.rope_append_kv4(qkv[:, :q_heads], qkv[:, q_heads:q_heads + heads], qkv[:, q_heads + heads:], rope, cu_of([1] * batch),
+                                i32(lens), now.cache, q_out, k_out=k_out, rope_start=i32(seen) if step >= 4 else None)
+        want = four_bit.norm_rotate(f64(qkv[:, q_heads:q_heads + heads]), None, rope.cpu().numpy(), np.array(seen), False)
+        assert np.all(np.abs(f64(k_out) - want) <= 2.0 ** -8 * np.abs(want))
         lens, seen = [n + 1 for n in lens], [p + 1 for p in seen]
         before = mass.clone()
         out, lse = torch.empty(batch, 1, q_heads, dim, dtype=torch.bfloat16, device="cuda"), torch.empty(batch, 1, q_heads, device="cuda")

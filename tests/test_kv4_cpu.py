@@ -144,7 +144,7 @@ def test_null_contexts_are_refused_by_the_library():
     c, n = binding.Kv4Struct(), ctypes.c_size_t()
     r = ctypes.byref(c)
     assert lib.jepa_rope_append_kv4(None, r, *([None, 0] * 3), 1, 1, None, None, 0.0, None, 0, 0, 0,
-                                    None, None, None, None, None) == 1
+                                    None, None, None, None, None, None) == 1
     assert lib.jepa_kv4_read(None, r, None, None, 1, None, None, None) == 1
     assert lib.jepa_attention_kv4_workspace(None, r, ctypes.byref(n)) == 1
     assert lib.jepa_attention_kv4(None, r, None, 1, 1, None, 1.0, 1, None, None, None, None, 1.0, None, 0, None) == 1
