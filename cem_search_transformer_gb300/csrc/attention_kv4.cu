@@ -371,211 +371,211 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
         }
       }
     } else {
-    qr.load(a, s, head, r0, rows, len);
-    scale_queries(qr, k_unit);
-    float o[NR][MT][4];
-    float m[NR][2], ref[NR][2], l[NR][2];        // ref: m - P_SHIFT, 0 before the first key
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      m[nr][0] = m[nr][1] = -INFINITY;
-      ref[nr][0] = ref[nr][1] = 0.f;
-      l[nr][0] = l[nr][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
-    }
-
-    for (int k = sg.k0; k < sg.k1; ++k) {
-      cp_wait<NST - 2>();
-      __syncwarp();
-      issue();                         // into the stage that the step before this one has read
-      const int key0 = k * S::UNIT + first_key;
-      const uint8_t* kb = ring_ptr + stage * S::STAGE;
-      stage = stage + 1 == NST ? 0 : stage + 1;
-      if (key0 >= len) continue;
-
-      float sc[S::GROUPS][NR][4];
-#pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) scores(kb, p, qr, sc[p]);
-      const bool edge = key0 + S::KS > qr.lim_min;   // some row does not see some key (warp-uniform)
-      bool move = false;
-      float top[NR][2];
+      qr.load(a, s, head, r0, rows, len);
+      scale_queries(qr, k_unit);
+      float o[NR][MT][4];
+      float m[NR][2], ref[NR][2], l[NR][2];        // ref: m - P_SHIFT, 0 before the first key
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
-        if (edge) {
+        m[nr][0] = m[nr][1] = -INFINITY;
+        ref[nr][0] = ref[nr][1] = 0.f;
+        l[nr][0] = l[nr][1] = 0.f;
 #pragma unroll
-          for (int p = 0; p < S::GROUPS; ++p)
+        for (int i = 0; i < MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
+      }
+
+      for (int k = sg.k0; k < sg.k1; ++k) {
+        cp_wait<NST - 2>();
+        __syncwarp();
+        issue();                         // into the stage that the step before this one has read
+        const int key0 = k * S::UNIT + first_key;
+        const uint8_t* kb = ring_ptr + stage * S::STAGE;
+        stage = stage + 1 == NST ? 0 : stage + 1;
+        if (key0 >= len) continue;
+
+        float sc[S::GROUPS][NR][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key0 + 16 * p + 8 * (e >> 1) + g >= qr.lim[nr][e & 1]) sc[p][nr][e] = -INFINITY;
+        for (int p = 0; p < S::GROUPS; ++p) scores(kb, p, qr, sc[p]);
+        const bool edge = key0 + S::KS > qr.lim_min;   // some row does not see some key (warp-uniform)
+        bool move = false;
+        float top[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          if (edge) {
+#pragma unroll
+            for (int p = 0; p < S::GROUPS; ++p)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 16 * p + 8 * (e >> 1) + g >= qr.lim[nr][e & 1]) sc[p][nr][e] = -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(sc[0][nr][e], sc[0][nr][2 + e]);
+#pragma unroll
+            for (int p = 1; p < S::GROUPS; ++p) x = fmaxf(x, fmaxf(sc[p][nr][e], sc[p][nr][2 + e]));
+            top[nr][e] = x * qr.qs[nr][e];
+            move = move || top[nr][e] > m[nr][e] + P_SLACK;   // a first score is larger than -inf
+          }
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          // the maxima over all keys of the step; the reference moves where it has to
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = top[nr][e];
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              const float mn = fmaxf(m[nr][e], x);
+              const float al = mn == -INFINITY ? 1.f : ex2f(m[nr][e] - mn);
+              m[nr][e] = mn;
+              ref[nr][e] = mn == -INFINITY ? 0.f : mn - P_SHIFT;
+              l[nr][e] *= al;
+#pragma unroll
+              for (int d = 0; d < MT; ++d) {
+                o[nr][d][e] *= al;
+                o[nr][d][2 + e] *= al;
+              }
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(sc[0][nr][e], sc[0][nr][2 + e]);
+        for (int p = 0; p < S::GROUPS; ++p) {
+          uint32_t b[NR][2];
 #pragma unroll
-          for (int p = 1; p < S::GROUPS; ++p) x = fmaxf(x, fmaxf(sc[p][nr][e], sc[p][nr][2 + e]));
-          top[nr][e] = x * qr.qs[nr][e];
-          move = move || top[nr][e] > m[nr][e] + P_SLACK;   // a first score is larger than -inf
+          for (int nr = 0; nr < NR; ++nr) {
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pr[e] = ex2f(fmaf(sc[p][nr][e], qr.qs[nr][e & 1], -ref[nr][e & 1]));
+              l[nr][e & 1] += pr[e];
+            }
+            b[nr][0] = transposed(pack_f16(pr[0], pr[1]));
+            b[nr][1] = transposed(pack_f16(pr[2], pr[3]));
+          }
+          // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group, D/8 values each, and their scales
+          uint32_t w[4][S::VW], vs[4];
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int row = 16 * p + 8 * (k4 >> 1);
+            const uint8_t* from = kb + ((k4 & 1) ? at_v1 : at_v) + row * S::KB;
+            if (D == 128) {
+              const uint2 x = *reinterpret_cast<const uint2*>(from);
+              w[k4][0] = x.x; w[k4][S::VW - 1] = x.y;
+            } else {
+              w[k4][0] = *reinterpret_cast<const uint32_t*>(from);
+            }
+            vs[k4] = kb[at_vs + (row + (k4 & 1)) * S::SB];
+          }
+          // A block that reads as NaN reaches only rows that see its key: a product with a masked
+          // probability of 0 would spread it. Rows can differ in what they see only at the causal edge.
+          uint32_t nan = 0;                      // bit k4: this lane's block of key k4 is NaN
+          if (edge) {
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4)
+              if ((vs[k4] & 0x7fu) == 0x7fu) {
+                nan |= 1u << k4;
+                vs[k4] = 0;
+              }
+          }
+          const uint32_t sa = f16x2_of_e4m3_pair(vs[0] | (vs[1] << 8)), sb = f16x2_of_e4m3_pair(vs[2] | (vs[3] << 8));
+#pragma unroll
+          for (int q = 0; q < S::VW; ++q) {
+            // bytes (even element of the first key, of the second), and the odd elements
+            const uint32_t x0 = (w[0][q] & 0x0f0f0f0fu) | ((w[1][q] << 4) & 0xf0f0f0f0u);
+            const uint32_t x1 = ((w[0][q] >> 4) & 0x0f0f0f0fu) | (w[1][q] & 0xf0f0f0f0u);
+            const uint32_t y0 = (w[2][q] & 0x0f0f0f0fu) | ((w[3][q] << 4) & 0xf0f0f0f0u);
+            const uint32_t y1 = ((w[2][q] >> 4) & 0x0f0f0f0fu) | (w[3][q] & 0xf0f0f0f0u);
+            auto tile = [&](int d, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+              const uint32_t a0 = mul2(c0, sa), a1 = mul2(c1, sa), a2 = mul2(c2, sb), a3 = mul2(c3, sb);
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][d], a0, a1, a2, a3, b[nr][0], b[nr][1]);
+            };
+            tile(4 * q, f16x2_of_e2m1x2<0>(x0), f16x2_of_e2m1x2<0>(x1), f16x2_of_e2m1x2<0>(y0), f16x2_of_e2m1x2<0>(y1));
+            tile(4 * q + 1, f16x2_of_e2m1x2<1>(x0), f16x2_of_e2m1x2<1>(x1), f16x2_of_e2m1x2<1>(y0), f16x2_of_e2m1x2<1>(y1));
+            tile(4 * q + 2, f16x2_of_e2m1x2<2>(x0), f16x2_of_e2m1x2<2>(x1), f16x2_of_e2m1x2<2>(y0), f16x2_of_e2m1x2<2>(y1));
+            tile(4 * q + 3, f16x2_of_e2m1x2<3>(x0), f16x2_of_e2m1x2<3>(x1), f16x2_of_e2m1x2<3>(y0), f16x2_of_e2m1x2<3>(y1));
+          }
+          if (edge && __any_sync(0xffffffffu, nan != 0)) {
+            // how many NaN blocks of a lane's elements each row sees
+            const uint32_t n0 = ((nan & 1u) ? 0x3c00u : 0u) | ((nan & 2u) ? 0x3c000000u : 0u);
+            const uint32_t n1 = ((nan & 4u) ? 0x3c00u : 0u) | ((nan & 8u) ? 0x3c000000u : 0u);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              uint32_t see[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int key = key0 + 16 * p + 8 * h + 2 * t;
+                see[h] = pack_f16(key < qr.lim_g[nr] ? 1.f : 0.f, key + 1 < qr.lim_g[nr] ? 1.f : 0.f);
+              }
+              float hit[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(hit, n0, n0, n1, n1, see[0], see[1]);
+#pragma unroll
+              for (int d = 0; d < MT; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (hit[e] > 0.f) o[nr][d][e] = __int_as_float(0x7fc00000);
+            }
+          }
         }
       }
-      if (__any_sync(0xffffffffu, move)) {
-        // the maxima over all keys of the step; the reference moves where it has to
+      const float unit = kv4_unit(c.v_unit, head);
+      if constexpr (KIND == BY_WARP) {
+        // ---- the warp has all of the item ----
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = top[nr][e];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[nr][e], x);
-            const float al = mn == -INFINITY ? 1.f : ex2f(m[nr][e] - mn);
-            m[nr][e] = mn;
-            ref[nr][e] = mn == -INFINITY ? 0.f : mn - P_SHIFT;
-            l[nr][e] *= al;
+            float x = l[nr][e];
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            const int r = r0 + 8 * nr + 2 * t + e;
+            if (r >= rows) continue;
+            const bool none = m[nr][e] == -INFINITY && x == 0.f;   // no key was seen (scores of NaN: a NaN sum)
+            const float f = none ? 0.f : unit / x;
+            const long long at = row_at(a, s, head, r);
+            uint32_t w[MT];
 #pragma unroll
             for (int d = 0; d < MT; ++d) {
-              o[nr][d][e] *= al;
-              o[nr][d][2 + e] *= al;
+              const __nv_bfloat162 y = __floats2bfloat162_rn(o[nr][d][e] * f, o[nr][d][2 + e] * f);
+              w[d] = *reinterpret_cast<const uint32_t*>(&y);
             }
+            uint4* to = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
+#pragma unroll
+            for (int d = 0; d < MT; d += 4) to[d / 4] = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
+            if (a.lse && g == 0) a.lse[at] = none ? -INFINITY : (ref[nr][e] + log2f(x)) * 0.69314718055994531f;
           }
+      } else {
+        // ---- join the four warps ----
+        __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
+        float* const sm_o = reinterpret_cast<float*>(smem + S::OFF_OUT);
+        __syncthreads();   // the joining before this one has been read
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = l[nr][e];
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            const int row = 8 * nr + 2 * t + e;
+            if (g == 0) {
+              // from here on m is the exponent's reference; -inf only where no key was seen (scores
+              // that are all NaN leave the maximum at -inf, but a NaN sum)
+              sm_m[warp][row] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
+              sm_l[warp][row] = x;
+            }
+            float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * (D / 8);
+#pragma unroll
+            for (int d = 0; d < MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
+              *reinterpret_cast<float4*>(to + 2 * d) =
+                  make_float4(o[nr][d][e] * unit, o[nr][d][2 + e] * unit, o[nr][d + 1][e] * unit,
+                              o[nr][d + 1][2 + e] * unit);
+          }
+        __syncthreads();
+        join_warps<D, NR>(a, sg, rows, total, workers, sm_o, sm_m, sm_l, begun);
       }
-#pragma unroll
-      for (int p = 0; p < S::GROUPS; ++p) {
-        uint32_t b[NR][2];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          float pr[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            pr[e] = ex2f(fmaf(sc[p][nr][e], qr.qs[nr][e & 1], -ref[nr][e & 1]));
-            l[nr][e & 1] += pr[e];
-          }
-          b[nr][0] = transposed(pack_f16(pr[0], pr[1]));
-          b[nr][1] = transposed(pack_f16(pr[2], pr[3]));
-        }
-        // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the group, D/8 values each, and their scales
-        uint32_t w[4][S::VW], vs[4];
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-          const int row = 16 * p + 8 * (k4 >> 1);
-          const uint8_t* from = kb + ((k4 & 1) ? at_v1 : at_v) + row * S::KB;
-          if (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(from);
-            w[k4][0] = x.x; w[k4][S::VW - 1] = x.y;
-          } else {
-            w[k4][0] = *reinterpret_cast<const uint32_t*>(from);
-          }
-          vs[k4] = kb[at_vs + (row + (k4 & 1)) * S::SB];
-        }
-        // A block that reads as NaN reaches only rows that see its key: a product with a masked
-        // probability of 0 would spread it. Rows can differ in what they see only at the causal edge.
-        uint32_t nan = 0;                      // bit k4: this lane's block of key k4 is NaN
-        if (edge) {
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4)
-            if ((vs[k4] & 0x7fu) == 0x7fu) {
-              nan |= 1u << k4;
-              vs[k4] = 0;
-            }
-        }
-        const uint32_t sa = f16x2_of_e4m3_pair(vs[0] | (vs[1] << 8)), sb = f16x2_of_e4m3_pair(vs[2] | (vs[3] << 8));
-#pragma unroll
-        for (int q = 0; q < S::VW; ++q) {
-          // bytes (even element of the first key, of the second), and the odd elements
-          const uint32_t x0 = (w[0][q] & 0x0f0f0f0fu) | ((w[1][q] << 4) & 0xf0f0f0f0u);
-          const uint32_t x1 = ((w[0][q] >> 4) & 0x0f0f0f0fu) | (w[1][q] & 0xf0f0f0f0u);
-          const uint32_t y0 = (w[2][q] & 0x0f0f0f0fu) | ((w[3][q] << 4) & 0xf0f0f0f0u);
-          const uint32_t y1 = ((w[2][q] >> 4) & 0x0f0f0f0fu) | (w[3][q] & 0xf0f0f0f0u);
-          auto tile = [&](int d, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
-            const uint32_t a0 = mul2(c0, sa), a1 = mul2(c1, sa), a2 = mul2(c2, sb), a3 = mul2(c3, sb);
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][d], a0, a1, a2, a3, b[nr][0], b[nr][1]);
-          };
-          tile(4 * q, f16x2_of_e2m1x2<0>(x0), f16x2_of_e2m1x2<0>(x1), f16x2_of_e2m1x2<0>(y0), f16x2_of_e2m1x2<0>(y1));
-          tile(4 * q + 1, f16x2_of_e2m1x2<1>(x0), f16x2_of_e2m1x2<1>(x1), f16x2_of_e2m1x2<1>(y0), f16x2_of_e2m1x2<1>(y1));
-          tile(4 * q + 2, f16x2_of_e2m1x2<2>(x0), f16x2_of_e2m1x2<2>(x1), f16x2_of_e2m1x2<2>(y0), f16x2_of_e2m1x2<2>(y1));
-          tile(4 * q + 3, f16x2_of_e2m1x2<3>(x0), f16x2_of_e2m1x2<3>(x1), f16x2_of_e2m1x2<3>(y0), f16x2_of_e2m1x2<3>(y1));
-        }
-        if (edge && __any_sync(0xffffffffu, nan != 0)) {
-          // how many NaN blocks of a lane's elements each row sees
-          const uint32_t n0 = ((nan & 1u) ? 0x3c00u : 0u) | ((nan & 2u) ? 0x3c000000u : 0u);
-          const uint32_t n1 = ((nan & 4u) ? 0x3c00u : 0u) | ((nan & 8u) ? 0x3c000000u : 0u);
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            uint32_t see[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int key = key0 + 16 * p + 8 * h + 2 * t;
-              see[h] = pack_f16(key < qr.lim_g[nr] ? 1.f : 0.f, key + 1 < qr.lim_g[nr] ? 1.f : 0.f);
-            }
-            float hit[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(hit, n0, n0, n1, n1, see[0], see[1]);
-#pragma unroll
-            for (int d = 0; d < MT; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (hit[e] > 0.f) o[nr][d][e] = __int_as_float(0x7fc00000);
-          }
-        }
-      }
-    }
-    const float unit = kv4_unit(c.v_unit, head);
-    if constexpr (KIND == BY_WARP) {
-      // ---- the warp has all of the item ----
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = l[nr][e];
-          x += __shfl_xor_sync(0xffffffffu, x, 4);
-          x += __shfl_xor_sync(0xffffffffu, x, 8);
-          x += __shfl_xor_sync(0xffffffffu, x, 16);
-          const int r = r0 + 8 * nr + 2 * t + e;
-          if (r >= rows) continue;
-          const bool none = m[nr][e] == -INFINITY && x == 0.f;   // no key was seen (scores of NaN: a NaN sum)
-          const float f = none ? 0.f : unit / x;
-          const long long at = row_at(a, s, head, r);
-          uint32_t w[MT];
-#pragma unroll
-          for (int d = 0; d < MT; ++d) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(o[nr][d][e] * f, o[nr][d][2 + e] * f);
-            w[d] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          uint4* to = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
-#pragma unroll
-          for (int d = 0; d < MT; d += 4) to[d / 4] = make_uint4(w[d], w[d + 1], w[d + 2], w[d + 3]);
-          if (a.lse && g == 0) a.lse[at] = none ? -INFINITY : (ref[nr][e] + log2f(x)) * 0.69314718055994531f;
-        }
-    } else {
-      // ---- join the four warps ----
-      __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
-      float* const sm_o = reinterpret_cast<float*>(smem + S::OFF_OUT);
-      __syncthreads();   // the joining before this one has been read
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = l[nr][e];
-          x += __shfl_xor_sync(0xffffffffu, x, 4);
-          x += __shfl_xor_sync(0xffffffffu, x, 8);
-          x += __shfl_xor_sync(0xffffffffu, x, 16);
-          const int row = 8 * nr + 2 * t + e;
-          if (g == 0) {
-            // from here on m is the exponent's reference; -inf only where no key was seen (scores
-            // that are all NaN leave the maximum at -inf, but a NaN sum)
-            sm_m[warp][row] = m[nr][e] != -INFINITY ? m[nr][e] - P_SHIFT : x == 0.f ? -INFINITY : 0.f;
-            sm_l[warp][row] = x;
-          }
-          float* to = sm_o + (warp * ROWS + row) * S::OUT_LD + g * (D / 8);
-#pragma unroll
-          for (int d = 0; d < MT; d += 2)   // tile d: columns 2d and 2d + 1 of the lane's
-            *reinterpret_cast<float4*>(to + 2 * d) =
-                make_float4(o[nr][d][e] * unit, o[nr][d][2 + e] * unit, o[nr][d + 1][e] * unit,
-                            o[nr][d + 1][2 + e] * unit);
-        }
-      __syncthreads();
-      join_warps<D, NR>(a, sg, rows, total, workers, sm_o, sm_m, sm_l, begun);
-    }
     }
   }
   cp_wait<0>();
