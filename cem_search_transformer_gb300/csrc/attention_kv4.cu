@@ -177,6 +177,9 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
   const int chunk = lane % CPR, sub = lane / CPR;
   Cursor load_cur{0, 0, 0, 0};
   Segment ld;
+  // row tiles of an item of the weights: its keys are gone through once for each
+  [[maybe_unused]] const int tiles = KIND == WEIGHTS ? (rows + ROWS - 1) / ROWS : 1;
+  [[maybe_unused]] int ld_tile = 0;
   int ld_left = 0, ld_stage = 0;               // steps left of the segment
   bool ld_more = plan<S::UNIT, ROWS>(c, a, whole, u_begin, u_end, load_cur, ld);
   uint32_t lane_to[16 / RPI];                  // of a lane's chunks of a 16-key group
@@ -257,8 +260,11 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
     ld_stage = ld_stage + 1 == NST ? 0 : ld_stage + 1;
     ld_key += S::UNIT;
     if (ld_more && --ld_left == 0) {
-      ld_more = plan<S::UNIT, ROWS>(c, a, whole, ld.next, u_end, load_cur, ld);
-      begin_segment();
+      if (KIND != WEIGHTS || ++ld_tile == tiles) {
+        ld_more = plan<S::UNIT, ROWS>(c, a, whole, ld.next, u_end, load_cur, ld);
+        ld_tile = 0;
+      }
+      begin_segment();                         // of the next, or again for the next tile of rows
     }
     fetch_pages();
   };
@@ -273,7 +279,6 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
   const uint32_t at_v1 = S::OFF_V + (D == 128 ? code_at<D>(2 * t + 1, g >> 1) + 8 * (g & 1) : code_at<D>(2 * t + 1, g >> 2) + 4 * (g & 3));
   const uint32_t at_ks = S::OFF_SC + g * S::SB + (D == 128 ? 2 * t : t);
   const uint32_t at_vs = S::OFF_SC + S::KS * S::SB + 2 * t * S::SB + (D == 128 ? g : g >> 1);
-  const int tiles = KIND == WEIGHTS ? (rows + ROWS - 1) / ROWS : 1;   // row tiles of an item of the weights
   // scores of a stage's 16-key group p: keys g, g + 8 (c0 c1, c2 c3) and query rows 2t, 2t + 1
   auto scores = [&](const uint8_t* kb, int p, const Queries<D, NR>& qr, float (&x)[NR][4]) {
     uint32_t w[2][S::KW], f[2][S::VW];
@@ -318,28 +323,30 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
             if (r >= rows) qr.lim[nr][e] = 0;  // no weight
           }
       };
-      if (tiles == 1) load_rows(0);
-      for (int k = sg.k0; k < sg.k1; ++k) {
-        const int key0 = k * S::UNIT;
-        // This lane writes keys (16 p + 8 h + g) of its share of the pairs (p, h): with four groups p = t, with
-        // two p = t / 2 and h = t % 2. What they had is loaded ahead of its use.
-        constexpr int OWN = S::GROUPS / 2;
-        float old[OWN];
+      for (int tile = 0; tile < tiles; ++tile) {
+        load_rows(tile * ROWS);
+        // what a key has so far: from the call's input, then from the tiles before, by the same lane
+        const float* const before = tile ? ma.out : ma.mass;
+        const float decay = tile ? 1.f : ma.decay;
+        for (int k = sg.k0; k < sg.k1; ++k) {
+          const int key0 = k * S::UNIT;
+          // This lane writes keys (16 p + 8 h + g) of its share of the pairs (p, h): with four groups p = t, with
+          // two p = t / 2 and h = t % 2. What they had is loaded ahead of its use.
+          constexpr int OWN = S::GROUPS / 2;
+          float old[OWN];
 #pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-          const int key = key0 + (OWN == 2 ? 16 * t + 8 * j : 8 * t) + g;
-          old[j] = ma.mass && key < len ? ma.mass[at + key] : 0.f;
-        }
-        cp_wait<NST - 2>();
-        __syncwarp();
-        issue();
-        const uint8_t* kb = ring_ptr + stage * S::STAGE;
-        stage = stage + 1 == NST ? 0 : stage + 1;
-        float sum[S::GROUPS][2];
+          for (int j = 0; j < OWN; ++j) {
+            const int key = key0 + (OWN == 2 ? 16 * t + 8 * j : 8 * t) + g;
+            old[j] = before && key < len ? before[at + key] : 0.f;
+          }
+          cp_wait<NST - 2>();
+          __syncwarp();
+          issue();
+          const uint8_t* kb = ring_ptr + stage * S::STAGE;
+          stage = stage + 1 == NST ? 0 : stage + 1;
+          float sum[S::GROUPS][2];
 #pragma unroll
-        for (int p = 0; p < S::GROUPS; ++p) sum[p][0] = sum[p][1] = 0.f;
-        for (int tile = 0; tile < tiles; ++tile) {
-          if (tiles > 1) load_rows(tile * ROWS);
+          for (int p = 0; p < S::GROUPS; ++p) sum[p][0] = sum[p][1] = 0.f;
           const bool inside = full && key0 + S::KS <= qr.lim_min;   // every row sees every key (warp-uniform)
 #pragma unroll
           for (int p = 0; p < S::GROUPS; ++p) {
@@ -353,21 +360,21 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
                 if (inside || key0 + 16 * p + 8 * (e >> 1) + g < qr.lim[nr][e & 1]) sum[p][e >> 1] += y;
               }
           }
-        }
-        // sums over the four lanes t of a key, each of which ends with its share: half of the values go
-        // to the lane 2 away and half of what is left to the neighbour
-        float half[S::GROUPS];                 // pairs (p, h) in order, those of this lane's half
+          // sums over the four lanes t of a key, each of which ends with its share: half of the values go
+          // to the lane 2 away and half of what is left to the neighbour
+          float half[S::GROUPS];                 // pairs (p, h) in order, those of this lane's half
 #pragma unroll
-        for (int i = 0; i < S::GROUPS; ++i) {
-          const float lo = sum[i / 2][i & 1], hi = sum[(S::GROUPS + i) / 2][i & 1];
-          half[i] = ((t & 2) ? hi : lo) + __shfl_xor_sync(0xffffffffu, (t & 2) ? lo : hi, 2);
-        }
+          for (int i = 0; i < S::GROUPS; ++i) {
+            const float lo = sum[i / 2][i & 1], hi = sum[(S::GROUPS + i) / 2][i & 1];
+            half[i] = ((t & 2) ? hi : lo) + __shfl_xor_sync(0xffffffffu, (t & 2) ? lo : hi, 2);
+          }
 #pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-          const float lo = half[j], hi = half[OWN + j];
-          const float x = ((t & 1) ? hi : lo) + __shfl_xor_sync(0xffffffffu, (t & 1) ? lo : hi, 1);
-          const int key = key0 + (OWN == 2 ? 16 * t + 8 * j : 8 * t) + g;
-          if (key < len) ma.out[at + key] = ma.mass ? fmaf(ma.decay, old[j], x) : x;
+          for (int j = 0; j < OWN; ++j) {
+            const float lo = half[j], hi = half[OWN + j];
+            const float x = ((t & 1) ? hi : lo) + __shfl_xor_sync(0xffffffffu, (t & 1) ? lo : hi, 1);
+            const int key = key0 + (OWN == 2 ? 16 * t + 8 * j : 8 * t) + g;
+            if (key < len) ma.out[at + key] = before ? fmaf(decay, old[j], x) : x;
+          }
         }
       }
     } else {
