@@ -18,11 +18,12 @@
 //   * No scale varies within what a warp accumulates, as pages' scales do in 8 bits: the units
 //     of a head multiply the scores and the outputs once.
 //   * The weights need the rows' sums, so their keys are read and multiplied a second time, by the same kernel
-//     without values. Holding the scores of short items in shared memory instead gained 1 to 7 us of 110
+//     without values, once for each tile of query rows (64 rows of 32 sequences of 4000 tokens: 111 us; a tile's
+//     queries loaded anew in each step instead 228). Holding the scores of short items in shared memory instead gained 1 to 7 us of 110
 //     (256 candidates of 776 tokens) and cost every other call half a microsecond.
 // Measured, inputs behind L2: two sequences of 100001 to 130001 tokens, 64 query heads over 8 of 128, 62 us
 // (4.5 TB/s; the kernel alone 57, 0.73 of the copy rate); 32 of 100 to 8000 tokens 40 us; 16 of 4000 to 30000
-// with weights 111 us, of which the weights' pass is 42; 256 of 776 tokens with 16 heads of 64, two queries and weights 110;
+// with weights 109 us, of which the weights' pass is 41; 256 of 776 tokens with 16 heads of 64, two queries and weights 107;
 // one of 517 tokens 8 us (latency). Bound by issue: 64 conversions and 64 products a 16-key group of 128 columns
 // share the SM's dispatch (a loop of the two alone issues 0.73 a cycle, this kernel 0.58 to 0.64), and no single part
 // that is left out of it (copies, products, exponentials, scales) makes it more than an eighth faster.
@@ -670,7 +671,8 @@ cudaError_t attention_kv4(const Kv4View& c, const bf16* q, int q_tokens, int q_h
   a.group = q_heads / c.heads;
   a.tiles = 0;
   a.causal = causal;
-  // up to 8 rows in one 8-wide tile: two long sequences with 8 rows 62 us, in the shape for 16 rows 79
+  // Up to 8 rows in one 8-wide tile: two long sequences with 8 rows 62 us, in the shape for 16 rows 79. A shape for 32 rows
+  // (heads of 64) took 110 us for 64 rows of 64 sequences of 2000 tokens against 119, but 15 against 12 for one of 1000.
   const bool narrow = q_tokens * a.group <= 8;
   if (c.dim == 64)
     return narrow ? launch<64, 1>(c, a, mass, err_flag, num_sms, s) : launch<64, 2>(c, a, mass, err_flag, num_sms, s);
