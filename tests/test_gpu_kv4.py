@@ -280,6 +280,24 @@ def test_bad_pages_positions_and_offsets_are_skipped_and_reported(planner):
                 planner.sync_check()
 
 
+def test_rows_ahead_of_the_first_sequence_and_behind_the_last_are_left(planner):
+    cu, old = [7, 7, 30, 64], [3, 0, 40]
+    n = np.diff(cu)
+    pool = Pool4([a + b for a, b in zip(n, old)], 3, 32, 64, seed=1)
+    rng = np.random.default_rng(1)
+    q, k, v = (bf16(rng.standard_normal((80, h, 64))).cuda() for h in (6, 3, 3))
+    q_out, k_out, k_read, v_read = (torch.full_like(t, 5.0) for t in (q, k, k, v))
+    planner.rope_append_kv4(q, k, v, None, i32(cu), i32(old), pool.cache, q_out, k_out=k_out)
+    planner.kv4_read(pool.cache, i32(cu), i32(old), k_read, v_read)
+    planner.sync_check()
+    for t in (q_out, k_out, k_read, v_read):
+        assert torch.all(t[:7] == 5.0) and torch.all(t[64:] == 5.0)
+    assert torch.equal(q_out[7:64], q[7:64]) and torch.equal(k_out[7:64], k[7:64])
+    for got, rows, unit in ((k_read, k, pool.unit_np[0]), (v_read, v, pool.unit_np[1])):
+        want = four_bit.values(*four_bit.quantise(f64(rows), unit[None, :, None]), unit[None, :, None])
+        assert np.array_equal(f64(got)[7:64], want[7:64])
+
+
 # ---- attention and weights ----
 
 def weights_of(q, k, lim, scale):

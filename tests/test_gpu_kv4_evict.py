@@ -125,6 +125,34 @@ def test_same_buffers_and_sequences_that_stay(planner):
         assert torch.equal(t[others], b[others])
 
 
+def test_shared_pages_stay_as_they_are(planner):
+    """Three sequences that name the same pages choose for themselves; the pages themselves are not written."""
+    from cem_search_transformer_gb300 import binding
+    n, heads, page, dim, keep = 150, 2, 32, 128, 40
+    pool = Pool4([n], heads, page, dim, seed=2, spare=7)
+    pool.fill([n], 3)
+    held = pool.held(0, n)
+    before = [t.clone() for t in (pool.k, pool.v, pool.ks, pool.vs)]
+    shared = binding.KvCache4(pool.k, pool.v, pool.ks, pool.vs, i32(np.repeat(pool.table_np, 3, 0)), *pool.units)
+    table = pool.spare[:6].reshape(3, 2)
+    to = binding.KvCache4(pool.k, pool.v, pool.ks, pool.vs, i32(table), *pool.units)
+    m = masses(np.random.default_rng(3), 3, heads, shared.max_pages * page, "ties")
+    ws = torch.empty(planner.kv4_evict_workspace(shared, keep), dtype=torch.uint8, device="cuda")
+    len_out = i32([0] * 3)
+    planner.kv4_evict(shared, i32([n, n, 90]), torch.from_numpy(m).cuda(), keep, 9, to, len_out, None, ws)
+    planner.sync_check()
+    pages = pool.table_np[0]
+    for t, b in zip((pool.k, pool.v, pool.ks, pool.vs), before):
+        assert torch.equal(t[pages], b[pages])
+    pool.table_np = table
+    for s, length in enumerate((n, n, 90)):
+        got = pool.held(s, keep)
+        for h in range(heads):
+            at = four_bit.kept(m[s, h, :length], keep, 9)
+            for g, w in zip(got, held):
+                assert np.array_equal(g[:, h], w[at, h])
+
+
 def test_budgets_beyond_the_targets_room(planner):
     """keep above what the target's table names counts as that; above a sequence's length all stay."""
     lens, heads, page, dim = [300, 40], 2, 16, 64
