@@ -158,8 +158,9 @@ __device__ __forceinline__ uint32_t scale_code(float top, float inv_unit) {
   return p & 0xffu;
 }
 
-// Codes of 8 elements, the first in the lowest bits.
-__device__ __forceinline__ uint32_t e2m1x8(const pair (&y)[8], int from, float scale) {
+// Codes of 8 elements, the first in the lowest bits. `most`: the scale is e4m3's largest, so that quotients may
+// lie far beyond 6.
+__device__ __forceinline__ uint32_t e2m1x8(const pair (&y)[8], int from, float scale, bool most) {
   float inv1;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv1) : "f"(scale));
   const pair inv = f2_both(inv1), neg = f2_both(-scale);
@@ -170,6 +171,15 @@ __device__ __forceinline__ uint32_t e2m1x8(const pair (&y)[8], int from, float s
     const float2 f = f2_unpack(f2_fma(f2_fma(z, neg, x), inv, z));   // the quotients, correctly rounded
     q[2 * i] = f.x;
     q[2 * i + 1] = f.y;
+  }
+  if (most) {
+    // a quotient past fp32 has no remainder: infinity less infinity. Its code is that of 8, as of all beyond 6
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = f2_unpack(y[from + i / 2]);
+      const float one = i & 1 ? x.y : x.x;
+      if (fabsf(one) > 8.f * scale) q[i] = copysignf(8.f, one);
+    }
   }
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -197,7 +207,7 @@ __device__ __forceinline__ void quantise_store(uint8_t* codes, uint8_t* scales, 
     const uint32_t f = f16x2_of_e4m3_pair(sc);
     const float scale = __half2float(__ushort_as_half((unsigned short)(f & 0xffffu))) * unit;
     *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + 4 * chunk) =
-        sc == 0x7f ? 0u : e2m1x8(y, 4 * h, scale);
+        sc == 0x7f ? 0u : e2m1x8(y, 4 * h, scale, sc == 0x7e);
     if (!(chunk & 1)) scales[at * (D / 16) + (chunk >> 1)] = (uint8_t)sc;
   }
 }
