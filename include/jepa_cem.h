@@ -434,8 +434,8 @@ typedef struct {
  * jepa_rope_append_kv8. Each 16 elements of a rotated key or of a value are quantised from fp32: scale =
  * e4m3(max|x| / 6 / unit), nearest even, at least 2^-9 and at most 448; codes = e2m1(x / (scale * unit)),
  * nearest even, saturating. A block that holds a NaN or an infinity gets a NaN scale and reads as NaN. For
- * keys the norm's factor 1 / sqrt(mean(x^2) + norm_eps) is rounded once to fp32 and multiplied by the
- * weight first, and each product and sum of the rotation is rounded to fp32. rope_start [batch] int32 dev or
+ * keys the norm's factor 1 / sqrt(mean(x^2) + norm_eps) is rounded once to fp32 (of any finite head: its squares may
+ * leave fp32) and multiplied by the weight first, and each product and sum of the rotation is rounded to fp32. rope_start [batch] int32 dev or
  * NULL: token i of sequence b lies at place start[b] + i - cu[b] and is rotated for position rope_start[b] + i -
  * cu[b], as it has to be behind an eviction; NULL: both are start. */
 jepa_status jepa_rope_append_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,

@@ -52,13 +52,20 @@ def unpack(data):
     return np.where(n & 8, -1.0, 1.0) * E2M1[n & 7]
 
 
+def round_to_24_bits(x) -> np.ndarray:
+    """Nearest value with fp32's 24 bits (ties to even), of any exponent."""
+    m, e = np.frexp(np.asarray(x, np.float64))
+    return np.ldexp(np.round(m * 2.0 ** 24), e - 24)
+
+
 def norm_rotate(x, weight, table, pos, interleaved: bool, eps: float = 1e-6) -> np.ndarray:
     """``oracle.paged.norm_rotate`` in fp32: the norm's factor rounded once, then every product
-    and sum."""
+    and sum. The factor and its product with the weight are no results: they have fp32's bits and no ends."""
     y = np.asarray(x, np.float32).copy()
     if weight is not None:
         r = (1 / np.sqrt(np.mean(y.astype(np.float64) ** 2, -1, keepdims=True) + np.float64(np.float32(eps))))
-        y = y * (r.astype(np.float32) * np.asarray(weight, np.float32))
+        r = round_to_24_bits(round_to_24_bits(r) * np.asarray(weight, np.float32).astype(np.float64))
+        y = (y * r).astype(np.float32)
     rot = 0 if table is None else table.shape[1]
     if rot:
         t = np.asarray(table, np.float32)[pos]

@@ -50,3 +50,70 @@ def test_elements_beyond_the_largest_scale_keep_their_sign(planner, dim, unit):
             same_codes(scales, sc, 0)
             same_codes(codes, c, 0)
             assert np.array_equal(f64(out), four_bit.values(c, sc, unit))
+
+
+def far_heads(rng, n, heads, dim):
+    """Finite head rows whose squares, or their sum, leave fp32: above, and (with no epsilon) below."""
+    x = rng.standard_normal((n, heads, dim))
+    x /= np.abs(x).max(-1, keepdims=True)
+    size = np.array([2.0 ** 64, 1.8e19, 1e19, 3e19, 1e25, 1e38, 3.3e38, 1.0])
+    x = x * np.resize(size, n)[:, None, None]
+    x[5, 0, 1:] = 1.0                                              # one far element among ordinary ones
+    x[6, -1, :] = 3.3e38 * (-1.0) ** np.arange(dim)                # the factor is subnormal
+    return np.clip(x, -3.38e38, 3.38e38)
+
+
+@pytest.mark.parametrize("dim,heads,rot,interleaved", [(64, 2, 64, False), (128, 3, 48, False), (64, 5, 32, True), (128, 8, 128, True)])
+@pytest.mark.parametrize("size,eps", [(1.0, 1e-6), (2.0 ** -140, 0.0), (2.0 ** -100, 0.0)])
+def test_norm_of_keys_whose_squares_leave_fp32(planner, dim, heads, rot, interleaved, size, eps):
+    """The norm's factor is that of the definition: only rows of zeros without an epsilon are 0 / 0, codes and scales
+    are equal but for a code in one row, and k_out is half a bf16 step off (test_gpu_kv4.py)."""
+    rng = np.random.default_rng(dim + heads)
+    n = 24
+    x = far_heads(rng, n, heads, dim) * size
+    pool = Pool4([n], heads, 16, dim)
+    k, v = bf16(x).cuda(), bf16(rng.standard_normal((n, heads, dim))).cuda()
+    w = torch.rand(dim, device="cuda") + 0.5
+    table = planner.rope_table(n, rot)
+    k_out = torch.empty_like(k)
+    planner.rope_append_kv4(None, k, v, table, cu_of([n]), i32([0]), pool.cache, None, k_norm=w, norm_eps=eps,
+                            interleaved=interleaved, k_out=k_out)
+    planner.sync_check()
+    with np.errstate(divide="ignore", invalid="ignore"):
+        want = four_bit.norm_rotate(f64(k), w.cpu().numpy(), table.cpu().numpy(), np.arange(n), interleaved, eps)
+    some = (f64(k) != 0).any(-1)                                     # bf16 ends at 2^-133
+    assert np.array_equal(np.isfinite(want).all(-1), some) and some.mean() > 0.8
+    got = f64(k_out)
+    assert np.isnan(got[~some]).all()
+    assert np.all(np.abs(got - want)[some] <= (2.0 ** -8 + 2.0 ** -23) * np.abs(want[some]) + 2.0 ** -22)
+    codes, scales, _, _ = pool.held(0, n)
+    c, sc = four_bit.quantise(want, pool.unit_np[0][None, :, None])
+    same_codes(scales, sc, 1)
+    same_codes(codes, c, 1)
+
+
+def test_infinities_and_nan_under_the_norm_stay_in_their_head(planner):
+    """inf / inf is NaN in its block and x / inf zero in the others; a NaN is all of its head; heads beside them, in
+    the same warp, are as without them."""
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((6, 4, 64))
+    w = torch.rand(64, device="cuda") + 0.5
+    v = bf16(rng.standard_normal((6, 4, 64))).cuda()
+    got = []
+    for bad in (False, True):
+        if bad:
+            x[1, 2, 20], x[4, 0, 63], x[2, 3, 5], x[5, 1, 0] = np.inf, -np.inf, np.nan, 2e38
+        k = bf16(x).cuda()
+        pool = Pool4([6], 4, 16, 64)
+        planner.rope_append_kv4(None, k, v, None, cu_of([6]), i32([0]), pool.cache, None, k_norm=w)
+        planner.sync_check()
+        got.append(pool.held(0, 6))
+        with np.errstate(invalid="ignore"):
+            c, sc = four_bit.quantise(four_bit.norm_rotate(f64(k), w.cpu().numpy(), None, None, False), pool.unit_np[0][None, :, None])
+        same_codes(got[-1][1], sc, 1)
+        same_codes(got[-1][0], c, 1)
+    touched = np.zeros((6, 4), bool)
+    touched[[1, 4, 2, 5], [2, 0, 3, 1]] = True
+    for a, b in zip(*got):
+        assert np.array_equal(a[~touched], b[~touched])
+    assert np.isnan(got[1][1][2, 3]).all() and np.isnan(got[1][1][1, 2]).sum() == 1 and not got[1][0][1, 2].any()
