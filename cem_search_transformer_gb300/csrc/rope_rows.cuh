@@ -182,6 +182,29 @@ __device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>
     float ss = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // Heads whose squares leave fp32, or vanish where no epsilon holds their mean up, come to where they do not by a power of
+    // two, and the epsilon by its square. Nine prompts: 1 us of 114 for the look.
+    const bool far = !(ss < 0x1p120f && ss >= (eps < 0x1p-106f ? 0x1p-96f : 0.f));
+    if (__any_sync(0xffffffffu, far)) {
+      float top = 0.f;                    // drops NaN, which reach the sum all the same
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float f = 1.f;
+      if (far && top >= 0x1p50f && top < INFINITY) f = pow2(50 - (int)(__float_as_uint(top) >> 23) + 127);
+      if (far && top < 0x1p-40f) f = 0x1p75f;
+      eps = eps * f * f;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        y[i] *= f;
+        sum = fmaf(y[i], y[i], sum);
+      }
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (far) ss = sum;
+    }
     const float r = __frsqrt_rn(ss * (1.0f / D) + eps);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {

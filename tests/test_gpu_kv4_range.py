@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import four_bit
+from oracle import four_bit, paged
 from test_gpu_kv4 import Pool4, same_codes
 from test_gpu_kv8 import bf16, cu_of, f64, i32
 
@@ -117,3 +117,40 @@ def test_infinities_and_nan_under_the_norm_stay_in_their_head(planner):
     for a, b in zip(*got):
         assert np.array_equal(a[~touched], b[~touched])
     assert np.isnan(got[1][1][2, 3]).all() and np.isnan(got[1][1][1, 2]).sum() == 1 and not got[1][0][1, 2].any()
+
+
+@pytest.mark.parametrize("dim,heads,rot,interleaved", [(64, 2, 64, False), (128, 3, 48, False), (64, 5, 32, True), (128, 8, 128, True)])
+@pytest.mark.parametrize("size,eps", [(1.0, 1e-6), (1.0, 1e25), (2.0 ** -140, 0.0), (2.0 ** -100, 0.0), (2.0 ** -100, 1e-35)])
+@pytest.mark.parametrize("batch", [1, 12])
+def test_norm_of_queries_and_of_the_8_bit_caches_keys_whose_squares_leave_fp32(planner, dim, heads, rot, interleaved, size, eps, batch):
+    """Both appends' queries and the 8-bit one's keys, in both its launch shapes, against 64 bits: half a bf16 step, and
+    16 * 2^-24 (|a| + |b|) for the rotated fp32 values (test_gpu_kv8.py)."""
+    from cem_search_transformer_gb300 import binding
+    rng = np.random.default_rng(dim + heads)
+    n = 24
+    x = far_heads(rng, n, heads, dim) * size
+    new = [n] + [0] * (batch - 1)
+    pool = Pool4([n] * batch, heads, 16, dim)
+    q, v = bf16(x).cuda(), bf16(rng.standard_normal((n, heads, dim))).cuda()
+    w = torch.rand(dim, device="cuda") + 0.5
+    table = planner.rope_table(n, rot)
+    u8 = torch.zeros(2 * batch, heads, 16, dim, dtype=torch.uint8, device="cuda")
+    scale = torch.ones(2 * batch, heads, device="cuda")
+    eight = binding.KvCache8(u8, u8.clone(), scale, scale.clone(), i32(np.arange(2 * batch).reshape(batch, 2)))
+    got = [torch.empty_like(q) for _ in range(3)]
+    args = dict(q_norm=w, k_norm=w, norm_eps=eps, interleaved=interleaved)
+    planner.rope_append_kv4(q, v, v, table, cu_of(new), i32([0] * batch), pool.cache, got[0], **args)
+    planner.rope_append_kv8(q, q, v, table, cu_of(new), i32([0] * batch), eight, got[1], k_out=got[2], **args)
+    planner.sync_check()
+    e32 = float(np.float32(eps))
+    some = (f64(q) != 0).any(-1) | (e32 > 0)
+    for t in got:
+        for i in range(n):
+            for h in range(heads):
+                if not some[i, h]:
+                    assert torch.isnan(t[i, h]).all()
+                    continue
+                a = f64(q)[i:i + 1, h:h + 1]
+                want = paged.norm_rotate(a, w.cpu().numpy(), table.cpu().numpy(), np.array([i]), interleaved, e32)
+                both = 2 * np.abs(paged.norm_rotate(a, w.cpu().numpy(), None, None, interleaved, e32)).max()
+                assert np.all(np.abs(f64(t)[i, h] - want[0, 0]) <= 2.0 ** -8 * np.abs(want[0, 0]) + 16 * 2.0 ** -24 * both + 2.0 ** -133), (i, h)
