@@ -65,16 +65,24 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float f) {
   return make_uint2((uint32_t)p[0] | ((uint32_t)p[1] << 16), (uint32_t)p[2] | ((uint32_t)p[3] << 16));
 }
 
-// Sum of `v` and maximum of `m` over the T threads of a row. `sm`: two floats a warp of the row.
+// Elements whose squares leave fp32: a warp that holds some has its elements times 2^-75, its sum of squares by the
+// square of that. `far`: this warp's are so. Rows of which one warp is far become so as a whole.
+constexpr float DOWN = 0x1p-75f;
+
+// Sum of `v` and maximum of `m` over the T threads of a row. `sm`: two floats a warp of the row, and one more.
+// Returns whether the row is far: sum and maximum are then those of elements times 2^-75.
 template <int T>
-__device__ __forceinline__ void over_row(float& v, float& m, float2* sm) {
+__device__ __forceinline__ bool over_row(float& v, float& m, bool far, float2* sm, float* sm_far) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     v += __shfl_xor_sync(0xffffffffu, v, o);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-  if (T == 32) return;
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x % T >> 5] = make_float2(v, m);
+  if (T == 32) return far;
+  if ((threadIdx.x & 31) == 0) {
+    sm[threadIdx.x % T >> 5] = make_float2(far ? INFINITY : v, m);
+    if (far) sm_far[threadIdx.x % T >> 5] = v;
+  }
   __syncthreads();
   v = m = 0.f;
 #pragma unroll
@@ -83,14 +91,39 @@ __device__ __forceinline__ void over_row(float& v, float& m, float2* sm) {
     v += x.x;
     m = fmaxf(m, x.y);
   }
+  if (v < INFINITY) return false;
+  v = m = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < T / 32; ++i) {
+    const float2 x = sm[i];
+    const bool near = x.x < INFINITY;
+    v += near ? x.x * DOWN * DOWN : sm_far[i];
+    m = fmaxf(m, near ? x.y * DOWN : x.y);
+  }
+  return true;
+}
+
+// Largest of `top` over the T threads of a row. `sm`: a float a warp of the row.
+template <int T>
+__device__ __forceinline__ float top_of_row(float top, float* sm) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (T == 32) return top;
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x % T >> 5] = top;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < T / 32; ++i) top = fmaxf(top, sm[i]);
+  return top;
 }
 
 constexpr float MOST = 0x1p126f;         // the largest factor of the codes
 
-// T threads a row, V vectors of 8 elements a thread, R rows a CTA.
-template <int T, int V, int R, bool XH, bool DH>
+// T threads a row, V vectors of 8 elements a thread, R rows a CTA. BARE: an epsilon that does not hold up the mean of
+// squares that vanish (one kernel with a branch for both: 6192 rows of 1024 15.4 us instead of 14.0).
+template <int T, int V, int R, bool XH, bool DH, bool BARE>
 __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
   __shared__ float2 sm[T * R / 32];
+  __shared__ float sm_far[T * R / 32], sm_top[T * R / 32];
   static_assert(T == 32 || T * R <= 1024, "rows of several warps meet at the CTA's barrier");
   const long long row = (long long)blockIdx.x * R + threadIdx.x / T;
   const int tid = threadIdx.x % T, vecs = a.cols >> 3;
@@ -123,8 +156,47 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
   for (int k = 0; k < V; ++k) {
     const int i = tid + k * T;
     if (on && a.x_out && i < vecs) store8<XH>(a.x_out, row * a.out_stride + 8 * i, s[k]);
+    if (!BARE)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[j & 3] = fmaf(s[k][j], s[k][j], part[j & 3]);
+      for (int j = 0; j < 8; ++j) part[j & 3] = fmaf(s[k][j], s[k][j], part[j & 3]);
+  }
+  float eps = a.eps;
+  const int warp0 = threadIdx.x / T * (T / 32);        // of the row
+  if (BARE) {
+    // rows of small elements come near 1, by a power of two
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(s[k][j]));
+    top = top_of_row<T>(top, sm_top + warp0);
+    if (top < 0x1p-40f) {
+      // the larger of the row and the epsilon's root
+      const int e = max((int)(__float_as_uint(top) >> 23), (int)(__float_as_uint(eps) >> 24) + 64) - 127;
+      const float f = __uint_as_float((uint32_t)(127 - max(e, -120)) << 23);
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[k][j] *= f;
+      eps = eps * f * f;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part[j & 3] = fmaf(s[k][j], s[k][j], part[j & 3]);
+  }
+  float sum = (part[0] + part[1]) + (part[2] + part[3]);
+  // 1024 threads' sums below 2^110 stay in fp32; NaN and infinities count as far
+  const bool far = __any_sync(0xffffffffu, !(sum < 0x1p110f));
+  if (far) {
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[k][j] *= DOWN;
+        sum = fmaf(s[k][j], s[k][j], sum);
+      }
   }
   // z = s w takes s's place; its maximum goes through the CTA together with the sum
   float m = 0.f;
@@ -140,17 +212,20 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
       m = fmaxf(m, fabsf(s[k][j]));      // drops NaN
     }
   }
-  float sum = (part[0] + part[1]) + (part[2] + part[3]);
-  over_row<T>(sum, m, sm + threadIdx.x / T * (T / 32));
+  const bool far_row = over_row<T>(sum, m, far, sm + warp0, sm_far + warp0);
   if (!on) return;
-  const float r = 1.f / sqrtf(sum / (float)a.cols + a.eps);
+  if (far_row) eps = eps * DOWN * DOWN;
+  // brings this warp's elements to where the row's are; taken into the factors (the elements themselves: 4 us of 55 for
+  // 4099 rows of 8192)
+  const float g = far_row && !far ? DOWN : 1.f;
+  const float r = 1.f / sqrtf(sum / (float)a.cols + eps);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int i = tid + k * T;
     if (a.y && i < vecs) {
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = s[k][j] * r;
+      for (int j = 0; j < 8; ++j) y[j] = s[k][j] * (r * g);
       store8<true>(a.y, row * a.cols + 8 * i, y);
     }
   }
@@ -163,14 +238,14 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int i = tid + k * T;
-    if (i < vecs) *reinterpret_cast<uint2*>(a.codes + row * a.cols + 8 * i) = e4m3x8(s[k], f);
+    if (i < vecs) *reinterpret_cast<uint2*>(a.codes + row * a.cols + 8 * i) = e4m3x8(s[k], f * g);
   }
 }
 
-template <int T, int V, int R>
-cudaError_t launch(const Args& a, int x_bf16, int delta_bf16, cudaStream_t s) {
-  auto* kernel = x_bf16 ? (delta_bf16 ? k_add_rmsnorm<T, V, R, true, true> : k_add_rmsnorm<T, V, R, true, false>)
-                        : (delta_bf16 ? k_add_rmsnorm<T, V, R, false, true> : k_add_rmsnorm<T, V, R, false, false>);
+template <int T, int V, int R, bool BARE>
+cudaError_t start(const Args& a, int x_bf16, int delta_bf16, cudaStream_t s) {
+  auto* kernel = x_bf16 ? (delta_bf16 ? k_add_rmsnorm<T, V, R, true, true, BARE> : k_add_rmsnorm<T, V, R, true, false, BARE>)
+                        : (delta_bf16 ? k_add_rmsnorm<T, V, R, false, true, BARE> : k_add_rmsnorm<T, V, R, false, false, BARE>);
   cudaLaunchAttribute attr;                // begins while the kernel before it ends
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -181,6 +256,11 @@ cudaError_t launch(const Args& a, int x_bf16, int delta_bf16, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+template <int T, int V, int R>
+cudaError_t launch(const Args& a, int x_bf16, int delta_bf16, cudaStream_t s) {
+  return a.eps < 0x1p-106f ? start<T, V, R, true>(a, x_bf16, delta_bf16, s)
+                           : start<T, V, R, false>(a, x_bf16, delta_bf16, s);
 }
 
 }  // namespace
