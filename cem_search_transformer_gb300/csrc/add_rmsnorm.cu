@@ -24,10 +24,11 @@ struct Args {
   bf16* y;
 };
 
+// Rows by plain loads: x is written where the sum goes back in place, and __ldg is for what no one writes.
 template <bool HALF>
 __device__ __forceinline__ void load8(const void* base, long long at, float (&v)[8]) {
   if (HALF) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(base) + at));
+    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(base) + at);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -36,7 +37,7 @@ __device__ __forceinline__ void load8(const void* base, long long at, float (&v)
     }
   } else {
     const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = p[0], b = p[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
@@ -204,8 +205,9 @@ __global__ void __launch_bounds__(T * R) k_add_rmsnorm(Args a) {
   for (int k = 0; k < V; ++k) {
     const int i = tid + k * T;
     if (i >= vecs) continue;
-    float w[8];
-    load8<false>(a.w, 8 * i, w);
+    const float4* wp = reinterpret_cast<const float4*>(a.w + 8 * i);
+    const float4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
+    const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       s[k][j] *= w[j];

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<D, NR, KIND>::CTAS))
     const int* at = ld_pages;
 #pragma unroll
     for (int p = 0; p < S::GROUPS; ++p)
-      pg_next[p] = ld_more && key + 16 * p < ld.len ? __ldg(at + ((key + 16 * p) >> c.page_log2)) : -1;
+      pg_next[p] = ld_more && key + 16 * p < ld.len ? at[(key + 16 * p) >> c.page_log2] : -1;
   };
   auto issue = [&]() {                         // the next step of the stream into the next stage
     const int key0 = ld_key;

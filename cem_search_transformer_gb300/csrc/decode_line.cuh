@@ -74,7 +74,7 @@ struct Args {
 
 // Cached length of sequence s, clamped to what the table can name.
 __device__ __forceinline__ int length_of(const PageView& c, const Args& a, int s, int* err_flag) {
-  const int n = __ldg(a.kv_len + s), most = c.max_pages << c.page_log2;
+  const int n = a.kv_len[s], most = c.max_pages << c.page_log2;
   if (n < 0 || n > most) {
     if (err_flag) atomicOr(err_flag, DEV_ERR_INDEX);
     return n < 0 ? 0 : most;

@@ -333,8 +333,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_append_kv4(Kv4View c, AppendArgs
 // Cached tokens back as bf16 (code * scale has at most six significant bits: exact). A warp per
 // packed token; a lane moves 8 elements at a time, so that a warp's stores are whole lines.
 template <int D>
-__device__ __forceinline__ void read_token(const Kv4View& c, const int* __restrict__ cu,
-                                           const int* __restrict__ first, int tokens,
+__device__ __forceinline__ void read_token(const Kv4View& c, const int* cu, const int* first, int tokens,
                                            bf16* __restrict__ k_out, bf16* __restrict__ v_out,
                                            int* err_flag) {
   const long long t = ((long long)blockIdx.x * THREADS + threadIdx.x) >> 5;
@@ -394,7 +393,7 @@ __device__ __forceinline__ void read_token(const Kv4View& c, const int* __restri
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 5)
-    k_kv4_read(Kv4View c, const int* __restrict__ cu, const int* __restrict__ first, int tokens,
+    k_kv4_read(Kv4View c, const int* cu, const int* first, int tokens,
                bf16* __restrict__ k_out, bf16* __restrict__ v_out, int* err_flag) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   read_token<D>(c, cu, first, tokens, k_out, v_out, err_flag);

@@ -32,22 +32,22 @@ struct Place {
 };
 // The largest s with cu[s] <= t (cu ascending), by the whole warp: 32-way probes, the last of
 // which brings the bounds and the start along.
-__device__ __forceinline__ Place locate(const int* __restrict__ cu, const int* __restrict__ start,
-                                        int batch, int t) {
+// Offsets and starts are read by plain loads: the kernel stands by while the one before it may still write them.
+__device__ __forceinline__ Place locate(const int* cu, const int* start, int batch, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = batch;
   while (n > 32) {
     const int step = (n + 31) >> 5, at = lane * step;
-    const bool le = at < n && __ldg(cu + lo + at) <= t;
+    const bool le = at < n && cu[lo + at] <= t;
     const int last = 31 - __clz((int)(__ballot_sync(0xffffffffu, le) | 1u));
     lo += last * step;
     n = min(step, n - last * step);
   }
   int b = 0x7fffffff, e = 0, f = 0;
   if (lane < n) {
-    b = __ldg(cu + lo + lane);
-    e = __ldg(cu + lo + lane + 1);
-    f = __ldg(start + lo + lane);
+    b = cu[lo + lane];
+    e = cu[lo + lane + 1];
+    f = start[lo + lane];
   }
   const uint32_t le = __ballot_sync(0xffffffffu, b <= t);
   const int last = le ? 31 - __clz((int)le) : 0;
@@ -67,10 +67,10 @@ __device__ __forceinline__ bool holds(const Place& p, int t, int tokens) {
 
 // Reports the sequences that are skipped, empty ones too, each by one thread of the grid (which has a
 // thread for each). Stands at a kernel's end, where the offsets are in the cache.
-__device__ __forceinline__ void report_offsets(const int* __restrict__ cu, int batch, int tokens,
+__device__ __forceinline__ void report_offsets(const int* cu, int batch, int tokens,
                                                int* err_flag) {
   const long long s = (long long)blockIdx.x * THREADS + threadIdx.x;
-  if (s < batch && !kv8_span_ok(__ldg(cu + s), __ldg(cu + s + 1), tokens)) atomicOr(err_flag, DEV_ERR_INDEX);
+  if (s < batch && !kv8_span_ok(cu[s], cu[s + 1], tokens)) atomicOr(err_flag, DEV_ERR_INDEX);
 }
 // Blocks for `threads` of work and at least one thread a sequence.
 long long blocks_for(long long threads, int batch) {
@@ -147,7 +147,7 @@ __device__ __forceinline__ bool place_of(const PageView& c, const AppendArgs& a,
   pos = (int)((unsigned)at.first + (unsigned)(t - at.begin));
   row = pos;
   if (!APART || !a.rope_start) return at.first >= 0 && pos >= 0 && pos < positions_of(c, a);
-  const int from = __ldg(a.rope_start + at.s);
+  const int from = a.rope_start[at.s];
   row = (int)((unsigned)from + (unsigned)(t - at.begin));
   return at.first >= 0 && pos >= 0 && pos < (c.max_pages << c.page_log2) && from >= 0 && row >= 0 && row < a.positions;
 }
