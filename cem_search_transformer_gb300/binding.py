@@ -247,6 +247,13 @@ def _sized(t, name: str):
     return t
 
 
+def _int32(n, name: str) -> int:
+    """`n` itself, which the library takes as 32 bits (ctypes would cut off what is above them)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise JepaError(1, f"{name} out of range ({n})")
+    return n
+
+
 def _rows(t, name: str, device: Optional[int] = None):
     """(address, elements between tokens, tokens, heads, head_dim) of token rows [tokens, heads,
     head_dim]: a bf16 CUDA tensor whose heads lie back to back (a slice of a wider projection's
@@ -802,7 +809,7 @@ class Planner:
     def kv4_evict_workspace(self, cache: KvCache4, keep: int) -> int:
         """Bytes of workspace that kv4_evict needs."""
         n = ctypes.c_size_t()
-        self._check(self.lib.jepa_kv4_evict_workspace(self.h, cache.ref, keep, ctypes.byref(n)),
+        self._check(self.lib.jepa_kv4_evict_workspace(self.h, cache.ref, _int32(keep, "keep"), ctypes.byref(n)),
                     "kv4_evict_workspace")
         return n.value
 
@@ -819,8 +826,8 @@ class Planner:
         heads = cache.batch * cache.kv_heads
         st = self.lib.jepa_kv4_evict(
             self.h, cache.ref, _dev(_sized(kv_len, "kv_len"), "kv_len", "i32", cache.batch, dev),
-            _dev(mass, "mass", "f32", heads * cache.max_pages * cache.page_size, dev), keep, recent,
-            to.ref, _dev(len_out, "len_out", "i32", cache.batch, dev),
+            _dev(mass, "mass", "f32", heads * cache.max_pages * cache.page_size, dev), _int32(keep, "keep"),
+            _int32(recent, "recent"), to.ref, _dev(len_out, "len_out", "i32", cache.batch, dev),
             _opt(mass_out, "mass_out", "f32", heads * to.max_pages * to.page_size, dev),
             _dev(_sized(workspace, "workspace"), "workspace", "u8", 0, dev), workspace.numel(),
             _stream_on(stream, dev))
@@ -843,6 +850,7 @@ class Planner:
             raise JepaError(1, "x_out must have x's type")
         if rows < 1 or cols < 1:
             raise JepaError(1, "rows and cols must be >= 1")
+        _int32(rows, "rows")
         n = rows * cols
         st = self.lib.jepa_add_rmsnorm_fp8(
             self.h, xp, xh, xs, dp, dh, ds, _dev(weight, "weight", "f32", cols, dev), eps, rows, cols, op,
