@@ -1552,6 +1552,10 @@ jepa_status jepa_attention_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const
   if ((long long)q_tokens * (q_heads / c.heads) > 65536 ||
       (long long)c.batch * q_tokens * q_heads > (1LL << 30))
     return fail(ctx, JEPA_ERR_SHAPE, "attention_kv4: too many query rows");
+  // the weights' pass reads the queries after out has been written
+  const uintptr_t bytes = (uintptr_t)c.batch * q_tokens * q_heads * c.dim * sizeof(bf16);
+  if (mass_out && (uintptr_t)q < (uintptr_t)out + bytes && (uintptr_t)out < (uintptr_t)q + bytes)
+    return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv4: weights need an out that does not overlap q");
   if (workspace_bytes < attention_kv4_workspace(c.dim, ctx->num_sms))
     return fail(ctx, JEPA_ERR_INVALID_ARG, "attention_kv4: the workspace is too small");
   OnDevice on(ctx->device);

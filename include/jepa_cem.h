@@ -463,7 +463,7 @@ jepa_status jepa_attention_kv4_workspace(jepa_ctx* ctx, const jepa_kv4_cache* ca
  * for j < kv_len[b]; what lies behind is left as it was. mass, mass_out [batch][kv_heads][max_pages *
  * page_size] float32 dev; mass NULL: zeros; mass_out may be mass. A token that is appended starts
  * with what mass holds at its place, so fill it with zeros at first (jepa_kv4_evict does so behind what it
- * keeps). decay finite. The sums' order is fixed. */
+ * keeps). decay finite, and out apart from q (the weights come after out). The sums' order is fixed. */
 jepa_status jepa_attention_kv4(jepa_ctx* ctx, const jepa_kv4_cache* cache, const uint16_t* q,
                                int q_tokens, int q_heads, const int32_t* kv_len, float scale,
                                int causal, uint16_t* out, float* lse, const float* mass,
