@@ -154,3 +154,33 @@ def test_norm_of_queries_and_of_the_8_bit_caches_keys_whose_squares_leave_fp32(p
                 want = paged.norm_rotate(a, w.cpu().numpy(), table.cpu().numpy(), np.array([i]), interleaved, e32)
                 both = 2 * np.abs(paged.norm_rotate(a, w.cpu().numpy(), None, None, interleaved, e32)).max()
                 assert np.all(np.abs(f64(t)[i, h] - want[0, 0]) <= 2.0 ** -8 * np.abs(want[0, 0]) + 16 * 2.0 ** -24 * both + 2.0 ** -133), (i, h)
+
+
+@pytest.mark.parametrize("given,read", [(0.3, 0.25), (3.99, 2.0), (float("nan"), 2.0 ** -40), (0.0, 2.0 ** -40), (-2.0, 2.0 ** -40),
+                                        (2.0 ** 50, 2.0 ** 40), (float("inf"), 2.0 ** 40), (2.0 ** -60, 2.0 ** -40)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_units_that_are_no_powers_of_two_or_beyond_their_ends(planner, given, read, dim):
+    """Read as the power of two at or below or the nearer end, NaN as the least, by the append, the read-back and the
+    attention alike: the same bytes and outputs as with that unit."""
+    rng = np.random.default_rng(dim)
+    x = bf16(rng.standard_normal((40, 2, dim)) * read).cuda()
+    q = bf16(rng.standard_normal((1, 1, 4, dim)) * max(2.0 ** -20, min(1.0, 1 / read))).cuda()
+    got = []
+    for unit in (given, read):
+        pool = Pool4([40], 2, 16, dim)
+        for t in pool.units:
+            t.fill_(unit)
+        planner.rope_append_kv4(None, x, x, None, cu_of([40]), i32([0]), pool.cache, None)
+        k_read, v_read, out, lse = torch.empty_like(x), torch.empty_like(x), torch.empty_like(q), torch.empty(1, 1, 4, device="cuda")
+        planner.kv4_read(pool.cache, cu_of([40]), i32([0]), k_read, v_read)
+        ws = torch.empty(planner.attention_kv4_workspace(pool.cache), dtype=torch.uint8, device="cuda")
+        mass = torch.zeros(1, 2, pool.table.shape[1] * 16, device="cuda")
+        planner.attention_kv4(q, pool.cache, i32([40]), out, 0.125, ws, lse=lse, mass_out=mass)
+        planner.sync_check()
+        pgs = pool.table_np[0]
+        got.append([t[pgs].cpu() for t in (pool.k, pool.v, pool.ks, pool.vs)] + [k_read, v_read, out, lse, mass])
+    # (slots behind the 40 tokens keep the pool's filling in both)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    c, sc = four_bit.quantise(f64(x), np.float32(read))
+    assert np.array_equal(f64(got[0][5]), four_bit.values(c, sc, read))
