@@ -4,8 +4,8 @@
 //
 // with s to x_out, codes and scales as the fp8 linear layers take them and, where asked for, y as
 // bf16. Bound by the bytes of x, delta and the outputs, each touched once: a row stays in registers
-// between its sum of squares, its maximum and its codes. Measured: 6192 rows of 1024 in fp32 13.7 us (6 TB/s,
-// 0.90 of the copy rate), 4099 of 8192 in bf16 with a bf16 output 57 us (5.3 TB/s), one row 4 us.
+// between its sum of squares, its maximum and its codes. Measured: 6192 rows of 1024 in fp32 14.0 us (5.9 TB/s,
+// 0.88 of the copy rate), 4099 of 8192 in bf16 with a bf16 output 55 us (5.5 TB/s), one row 2 us (4 by itself).
 #include "add_rmsnorm.cuh"
 
 namespace jepa {
@@ -273,10 +273,10 @@ cudaError_t add_rmsnorm(const void* x, int x_bf16, long long x_stride, const voi
                         bf16* y, cudaStream_t s) {
   const Args a{x, delta, x_stride, delta_stride, out_stride, w, eps, rows, cols, x_out, codes, scales, y};
   // One vector a thread while that leaves few warps a row: more of a SM's rows in flight, and a short
-  // chain for a single one. Wider rows take more, as their barriers cost more than the registers. Measured, us:
-  // 6192 x 1024 fp32: 128 threads 16.4, 64 with two vectors 18.1, a warp with four 18.5; 1000 x 4096
-  // bf16: 256 with two 10.2, 128 with four 11.0; 4099 x 8192 bf16: 256 with four 55, 512 with two 58, 1024 68;
-  // 1000 x 16384: 1024 with two 37, 512 with four 41.
+  // chain for a single one. Wider rows take more, as their barriers cost more than the registers. Measured in this
+  // form, us: 6192 x 1024 fp32: 128 threads 14.0, 64 with two vectors 16.0, a warp with four 16.3; 1000 x 4096
+  // bf16: 256 with two 8.6, 128 with four 9.6; 4099 x 8192 bf16 and bf16 rows: 256 with four 55, 512 with two 57,
+  // 1024 69; 1000 x 16384 bf16: 1024 with two 32.0, 512 with four 32.8.
   if (cols <= 256) return launch<32, 1, 8>(a, x_bf16, delta_bf16, s);
   if (cols <= 512) return launch<64, 1, 2>(a, x_bf16, delta_bf16, s);
   if (cols <= 1024) return launch<128, 1, 1>(a, x_bf16, delta_bf16, s);

@@ -6,8 +6,8 @@
 // written a token) and by latency on short ones. No token's codes depend on another token: a warp
 // takes a token and up to eight heads of its queries, keys or values, which share the angles.
 //
-// Measured: nine prompts of 100 to 4500 tokens, 32 query heads over 8 of 128: append 93 us (5 TB/s; issue 65% of the
-// slots), read-back 20 (4.5 TB/s); one token for each of 64 sequences 4 us each (latency).
+// Measured: nine prompts of 100 to 4500 tokens, 32 query heads over 8 of 128: append 97 us (4.5 TB/s; issue 65% of the
+// slots), read-back 20 (4.5 TB/s), both 115; one token for each of 64 sequences 4 us each (latency).
 //
 // A code is the nearest e2m1 value to x / (scale * unit), and neighbours are a third apart, so what
 // decides between them is computed as the definition has it: the norm's factor is correctly rounded (sum of
@@ -317,7 +317,8 @@ __device__ __forceinline__ void append_unit(const Kv4View& c, const AppendArgs& 
 }
 
 // Key / value warps, then query warps, in one grid. Four CTAs a SM in 64 registers: nine prompts of 100 to
-// 4500 tokens 93 us, three in 80 registers 103, queries and the rest in a kernel each 99.
+// 4500 tokens 93 us, three in 80 registers 103, queries and the rest in a kernel each 99 (all of them without the
+// looks for heads whose squares leave fp32, 2 us).
 template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS, 4) k_append_kv4(Kv4View c, AppendArgs a, long long kv_units, int* err_flag) {
   asm volatile("griddepcontrol.launch_dependents;");

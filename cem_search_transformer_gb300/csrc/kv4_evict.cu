@@ -12,8 +12,8 @@
 //     counts read by the others through distributed shared memory; then every CTA knows how many it
 //     keeps and writes their places. No atomics across CTAs: the result does not depend on their order.
 //   * k_evict_move: 16 bytes a lane, two tokens in flight.
-// Measured: 8 heads of 128 of six sequences of 5001 to 70001 tokens back to 8192: selection 27 us (issue 59%: the six
-// looks at each weight), moving 31 (130 MB read for 53: a token's 8 bytes of scales cost a 32-byte sector each), the
+// Measured: 8 heads of 128 of six sequences of 34648 to 70001 tokens back to 8192: selection 27 us (issue 57%: the six
+// looks at each weight), moving 31 (130 MB read for 57: a token's 8 bytes of scales cost a 32-byte sector each), the
 // read-back that follows 43. Slower: moving by the clusters that chose (16% of the whole), digits of eleven bits (the
 // clusters' counts then are eight times the traffic between SMs: 43%).
 #include "kv4.cuh"
@@ -308,8 +308,8 @@ cudaError_t kv4_evict(const Kv4View& c, const int* kv_len, const float* mass, in
   const long long items = (long long)c.batch * c.heads;
   EvictArgs a{kv_len, mass, keep, recent, len_out, mass_out, (int*)workspace};
   // CTAs a (sequence, head): pieces of two thousand tokens or more, up to the portable cluster size, while the machine has
-  // room. Six sequences of up to 70001 tokens and 8 heads, with the read-back: one CTA 277 us, two 186, four 140,
-  // eight 102; eight of up to 2001 and 16 heads (128 items): one 19, two 23, four 30, eight 45.
+  // room. Six sequences of up to 70001 tokens and 8 heads, with the read-back: one CTA 249 us, two 170, four 129,
+  // eight 102; eight of up to 2001 and 16 heads (128 items): one 19, two 21, four 28, eight 43.
   const long long reach = (long long)c.max_pages << c.page_log2;
   int size = 1;
   while (size < MAX_CLUSTER && reach > 2048LL * size && items * size < 2LL * num_sms) size *= 2;

@@ -169,7 +169,9 @@ cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, bool early, cuda
 }
 
 // y = x * w / sqrt(mean(x^2) + eps), then (a, b) -> (a cos - b sin, b cos + a sin) for the pairs
-// (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1), i < rot / 2. All lanes of the warp call it.
+// (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1), i < rot / 2. All lanes of the warp call it. Products are
+// fused and sums plain fp32: what goes to bf16 or to 8 bits behind it can differ by a step from another order's where
+// a rotation nearly cancels or a value lies next to a border (4-bit keys, whose steps are wide, are taken exactly).
 template <int D, bool INTER>
 __device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>& ln,
                                             const float* __restrict__ w, float eps,
