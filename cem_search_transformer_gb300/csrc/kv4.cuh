@@ -24,7 +24,7 @@ struct Kv4View : PageView {
 // what is given.
 __device__ __forceinline__ float kv4_unit(const float* units, int head) {
   if (!units) return 1.f;
-  const float u = __ldg(units + head);
+  const float u = load_late(units + head);
   const float sane = u >= KV8_SCALE_MIN ? fminf(u, KV8_SCALE_MAX) : KV8_SCALE_MIN;
   return __uint_as_float(__float_as_uint(sane) & 0x7f800000u);
 }

@@ -117,7 +117,7 @@ __device__ __forceinline__ void norm_rotate_exact(pair (&y)[8], const Lane<D, IN
     const pair r = f2_both(norm_factor<D>(y, eps));
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float4 g = __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 4 ? ln.c0 : ln.c1) + 2 * (i & 3)));
+      const float4 g = load_late(reinterpret_cast<const float4*>(w + 8 * (i < 4 ? ln.c0 : ln.c1) + 2 * (i & 3)));
       y[i] = f2_mul(y[i], f2_mul(r, f2_pack(g.x, g.y)));
       y[i + 1] = f2_mul(y[i + 1], f2_mul(r, f2_pack(g.z, g.w)));
     }

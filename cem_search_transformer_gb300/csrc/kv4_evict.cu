@@ -30,14 +30,6 @@ constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int BINS = 256;
 constexpr int MAX_CLUSTER = 8;           // the portable size
 
-// A weight. Not by __ldg, which is for what no one writes while the kernel lives: k_evict_select stands by while the
-// call before may still write them. A volatile load of global memory stays behind the griddepcontrol.wait; an
-// ordinary one, which stores to shared memory hold back as well, took a microsecond more (20 and 103).
-__device__ __forceinline__ float weight_at(const float* p) {
-  float x;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(p));
-  return x;
-}
 // Weights as integers in the same order: NaN the least, -0 as 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
   if (x != x) return 0;
@@ -116,7 +108,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
     int i = begin + lane;
 #pragma unroll 4
     for (; i < held_end; i += 32) f(i, mine_held[i]);
-    for (; i < end; i += 32) f(i, ordered(weight_at(mass + i)));
+    for (; i < end; i += 32) f(i, ordered(load_late(mass + i)));
   };
   for (int b = threadIdx.x; b < BINS; b += THREADS) hist[0][b] = 0;
   __syncthreads();
@@ -127,7 +119,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const int i = i0 + 32 * k + lane;
-      x[k] = i < end ? weight_at(mass + i) : 0.f;
+      x[k] = i < end ? load_late(mass + i) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
@@ -238,7 +230,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(Kv4View c, EvictArgs a
   int i0 = begin;
 #pragma unroll 2
   for (; i0 < held_end; i0 += 32) place(i0 + lane, i0 + lane < end ? mine_held[i0 + lane] : 0u);
-  for (; i0 < end; i0 += 32) place(i0 + lane, i0 + lane < end ? ordered(weight_at(mass + i0 + lane)) : 0u);
+  for (; i0 < end; i0 += 32) place(i0 + lane, i0 + lane < end ? ordered(load_late(mass + i0 + lane)) : 0u);
 }
 
 // A warp takes RPW kept tokens of a head at a time, AHEAD times.

@@ -30,6 +30,20 @@ struct Kv8View : PageView {
   float *k_scale, *v_scale;
 };
 
+// Loads that stay behind a griddepcontrol.wait, being volatile like it: __ldg is for what no one writes while the kernel
+// lives, and may be moved ahead of the wait. Stores to elsewhere hold them back as little as __ldg (plain loads of an
+// eviction's weights took a microsecond more, 20 and 103).
+__device__ __forceinline__ float load_late(const float* p) {
+  float x;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float4 load_late(const float4* p) {
+  float4 x;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p));
+  return x;
+}
+
 // ---- launchers (each returns the launch's error) ----
 
 cudaError_t rope_table(int positions, int rot, double base, double factor, float* table,

@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_angles(float (&an)[16], const float* row, i
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(row + h * (rot >> 1) + 8 * p + i));
+      const float4 x = load_late(reinterpret_cast<const float4*>(row + h * (rot >> 1) + 8 * p + i));
       an[8 * h + i] = x.x; an[8 * h + i + 1] = x.y; an[8 * h + i + 2] = x.z; an[8 * h + i + 3] = x.w;
     }
 }
@@ -211,7 +211,7 @@ __device__ __forceinline__ void norm_rotate(float (&y)[16], const Lane<D, INTER>
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const float4 g =
-          __ldg(reinterpret_cast<const float4*>(w + 8 * (i < 8 ? ln.c0 : ln.c1) + (i & 7)));
+          load_late(reinterpret_cast<const float4*>(w + 8 * (i < 8 ? ln.c0 : ln.c1) + (i & 7)));
       y[i] *= r * g.x; y[i + 1] *= r * g.y; y[i + 2] *= r * g.z; y[i + 3] *= r * g.w;
     }
   }

@@ -107,3 +107,72 @@ def test_norm_in_place_on_rows_that_share_sectors(planner, cols, pitch):
         planner.add_rmsnorm_fp8(wide[:, :cols], delta, w, wide[:, :cols], None, None, y=y[1])
         assert torch.equal(y[0], y[1]) and torch.equal(wide[:, :cols], x) and torch.equal(wide[:, cols:], behind)
     planner.sync_check()
+
+
+def test_weights_units_and_tables_written_by_the_kernel_before(planner):
+    """A copy into the weights, units, offsets or tables directly ahead of the call that goes by them."""
+    heads, dim, page, n, times = 4, 64, 16, 50, 6
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.rand(*s, device="cuda", generator=g) + 0.5  # noqa: E731
+    rows = (torch.randn(700, 256, device="cuda", generator=g)).to(torch.bfloat16)
+    gains, norms, ropes = [rand(256) for _ in range(times)], [rand(dim) for _ in range(times)], [rand(64, dim) for _ in range(times)]
+    units = [2.0 ** torch.randint(-3, 3, (heads,), device="cuda", generator=g).float() for _ in range(times)]
+    k = torch.randn(n, heads, dim, device="cuda", generator=g).to(torch.bfloat16)
+    orders = [torch.randperm(4, device="cuda", generator=g).to(torch.int32)[None] for _ in range(times)]
+    firsts = [i32([i]) for i in range(times)]
+
+    def state():
+        pool = Pool4([64], heads, page, dim, spare=0)
+        s = dict(pool=pool, gain=torch.empty(256, device="cuda"), norm=torch.empty(dim, device="cuda"), rope=torch.empty(64, dim, device="cuda"),
+                 first=i32([0]), q=torch.empty_like(k), out=[])
+        for _ in range(times):
+            s["out"].append([torch.empty_like(rows), torch.empty_like(k), torch.empty_like(k), torch.empty_like(k),
+                             torch.empty(1, n, heads, dim, dtype=torch.bfloat16, device="cuda")])
+        s["ws"] = torch.empty(planner.attention_kv4_workspace(pool.cache), dtype=torch.uint8, device="cuda")
+        return s
+    cu = cu_of([n])
+
+    def run(s, behind):
+        stream, pool = torch.cuda.current_stream(), s["pool"]
+        for i in range(times):
+            y, q, kr, vr, att = s["out"][i]
+            s["gain"].copy_(gains[i])
+            behind()
+            planner.add_rmsnorm_fp8(rows, None, s["gain"], None, None, None, y=y, stream=stream)
+            behind()
+            for a, b in ((s["rope"], ropes[i]), (s["first"], firsts[i]), (pool.table, orders[i]), (pool.units[0], units[i]), (pool.units[1], units[i])):
+                a.copy_(b)
+            s["norm"].copy_(norms[i])
+            behind()
+            planner.rope_append_kv4(k, k, k, s["rope"], cu, s["first"], pool.cache, q, q_norm=s["norm"], k_norm=s["norm"], stream=stream)
+            behind()
+            pool.units[1].copy_(units[i - 1])
+            behind()
+            planner.kv4_read(pool.cache, cu, s["first"], kr, vr, stream=stream)
+            behind()
+            s["first"].add_(n)
+            behind()
+            planner.attention_kv4(q.unsqueeze(0), pool.cache, s["first"], att, 0.125, s["ws"], stream=stream)
+            behind()
+    apart, chain = state(), state()
+    run(apart, torch.cuda.synchronize)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(chain, lambda: None)
+    for _ in range(20):
+        # (slots ahead of a round's first token may hold what the last replay left: both start from the same bytes)
+        for t in ("k", "v", "ks", "vs"):
+            getattr(chain["pool"], t).zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+    for t in ("k", "v", "ks", "vs"):
+        getattr(apart["pool"], t).zero_()
+    run(apart, torch.cuda.synchronize)
+    planner.sync_check()
+    for a, b in zip(chain["out"], apart["out"]):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
